@@ -23,6 +23,8 @@ __all__ = [
     "DEVERR_SLOT_OUT_OF_RANGE", "library_path", "load_library", "dsa_status_string",
     "dsa_packed_row_bytes", "dsa_cache_row_bytes", "dsa_quant_k_cache", "dsa_gather_dequant", "dsa_gather_requant",
     "dsa_sparse_attn_workspace_size", "dsa_sparse_attn", "dsa_sparse_attn_static_ws", "dsa_topk_select", "DsaAttnArgs",
+    "DEVERR_REQUEST_ORDER", "DsaPagedArgs", "DsaEvictArgs", "dsa_paged_attn_workspace_size", "dsa_paged_attn",
+    "dsa_paged_attn_mass", "dsa_cache_evict_workspace_size", "dsa_cache_evict",
 ]
 
 CACHE_BF16 = 0
@@ -30,6 +32,7 @@ CACHE_FP8_SCALED = 1
 DEVERR_INDEX_OUT_OF_RANGE = 0x1
 DEVERR_TIMEOUT = 0x2
 DEVERR_SLOT_OUT_OF_RANGE = 0x4
+DEVERR_REQUEST_ORDER = 0x8
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lock = threading.Lock()
@@ -60,6 +63,45 @@ class DsaAttnArgs(ctypes.Structure):
         ("req_of_token", ctypes.c_void_p), ("sm_scale", ctypes.c_float),
         ("out", ctypes.c_void_p), ("out_stride_t", ctypes.c_int64), ("out_stride_h", ctypes.c_int64),
         ("lse", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+        ("error_word", ctypes.c_void_p),
+    ]
+
+
+class DsaPagedArgs(ctypes.Structure):
+    """ctypes mirror of ``dsa_paged_args_t``."""
+
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("q_stride_t", ctypes.c_int64), ("q_stride_h", ctypes.c_int64),
+        ("T", ctypes.c_int64), ("H", ctypes.c_int),
+        ("cache", ctypes.c_void_p), ("kind", ctypes.c_int), ("num_slots", ctypes.c_int64),
+        ("d_nope", ctypes.c_int), ("d_rope", ctypes.c_int), ("d_v", ctypes.c_int),
+        ("block_table", ctypes.c_void_p), ("bt_stride", ctypes.c_int64),
+        ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int), ("num_requests", ctypes.c_int64),
+        ("req_of_token", ctypes.c_void_p), ("starts", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
+        ("q_positions", ctypes.c_void_p), ("key_positions", ctypes.c_void_p),
+        ("kp_stride", ctypes.c_int64), ("kp_width", ctypes.c_int64),
+        ("sm_scale", ctypes.c_float), ("logit_cap", ctypes.c_float), ("slopes", ctypes.c_void_p),
+        ("out", ctypes.c_void_p), ("out_stride_t", ctypes.c_int64), ("out_stride_h", ctypes.c_int64),
+        ("lse", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+        ("error_word", ctypes.c_void_p),
+    ]
+
+
+class DsaEvictArgs(ctypes.Structure):
+    """ctypes mirror of ``dsa_evict_args_t``."""
+
+    _fields_ = [
+        ("cache", ctypes.c_void_p), ("kind", ctypes.c_int), ("num_slots", ctypes.c_int64),
+        ("d_nope", ctypes.c_int), ("d_rope", ctypes.c_int),
+        ("block_table", ctypes.c_void_p), ("bt_stride", ctypes.c_int64),
+        ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int), ("num_requests", ctypes.c_int64),
+        ("lengths", ctypes.c_void_p), ("budgets", ctypes.c_void_p), ("budget", ctypes.c_int),
+        ("sink", ctypes.c_int), ("recent", ctypes.c_int), ("width", ctypes.c_int64),
+        ("mass", ctypes.c_void_p), ("mass_stride", ctypes.c_int64),
+        ("positions", ctypes.c_void_p), ("positions_stride", ctypes.c_int64),
+        ("mass_out", ctypes.c_void_p), ("mass_out_stride", ctypes.c_int64),
+        ("positions_out", ctypes.c_void_p), ("positions_out_stride", ctypes.c_int64),
+        ("lengths_out", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
         ("error_word", ctypes.c_void_p),
     ]
 
@@ -103,6 +145,16 @@ def load_library():
         lib.dsa_quant_fp8_blockscale.restype = i32
         lib.dsa_proj_gemm.argtypes = [P, P, P, P, i64, i64, i64, P, i64, P, ctypes.c_size_t, P]
         lib.dsa_proj_gemm.restype = i32
+        lib.dsa_paged_attn_workspace_size.argtypes = [ctypes.POINTER(DsaPagedArgs), ctypes.POINTER(ctypes.c_size_t)]
+        lib.dsa_paged_attn_workspace_size.restype = i32
+        lib.dsa_paged_attn.argtypes = [ctypes.POINTER(DsaPagedArgs), P]
+        lib.dsa_paged_attn.restype = i32
+        lib.dsa_paged_attn_mass.argtypes = [ctypes.POINTER(DsaPagedArgs), P, i64, P, i64, i64, P]
+        lib.dsa_paged_attn_mass.restype = i32
+        lib.dsa_cache_evict_workspace_size.argtypes = [i64, i64, ctypes.POINTER(ctypes.c_size_t)]
+        lib.dsa_cache_evict_workspace_size.restype = i32
+        lib.dsa_cache_evict.argtypes = [ctypes.POINTER(DsaEvictArgs), P]
+        lib.dsa_cache_evict.restype = i32
         _LIB = lib
         return lib
 
@@ -458,3 +510,254 @@ def dsa_proj_gemm(x_codes, x_scales, w_codes, w_scales, *, out=None, workspace=N
                                       out.stride(0), _ptr(workspace), workspace.numel(), _stream(x_codes.device))
     _check(st, "dsa_proj_gemm")
     return out
+
+
+# ------------------------------------------------------- dense attention over the paged cache --
+def _need_on(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}: every tensor must be on one device")
+
+
+def _need_vector(name, t, n):
+    """A contiguous int32 CUDA tensor of n entries (or None)."""
+    import torch
+
+    _need_cuda(name, t, torch.int32)
+    if t is not None and (t.dim() != 1 or t.numel() != n or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous tensor of {n} entries")
+
+
+def _need_rows(name, t, rows=None, cols=None):
+    if t is not None and (t.dim() != 2 or t.stride(1) != 1 or (rows is not None and t.shape[0] != rows) or
+                          (cols is not None and t.shape[1] < cols)):
+        raise ValueError(f"{name} must be [{rows if rows is not None else 'rows'}, "
+                         f"{'>=' + str(cols) if cols is not None else 'columns'}], contiguous along its last dimension")
+
+
+def _cache_rows(cache, kind, d):
+    """The cache as [num_slots, row] rows, checked."""
+    import torch
+
+    if kind not in (CACHE_BF16, CACHE_FP8_SCALED):
+        raise ValueError("kind must be CACHE_BF16 or CACHE_FP8_SCALED")
+    _need_cuda("cache", cache, torch.uint8 if kind == CACHE_FP8_SCALED else torch.bfloat16)
+    if cache.dim() == 3 and cache.shape[1] == 1:
+        cache = cache.view(cache.shape[0], -1)
+    if cache.dim() != 2 or not cache.is_contiguous() or cache.shape[1] != d:
+        raise ValueError(f"cache must be contiguous [num_slots, {d}]")
+    return cache
+
+
+def _row_stride(t):
+    # a single row has no second one to step to: any stride is as good, and torch may report 1
+    return t.shape[1] if t.shape[0] <= 1 else t.stride(0)
+
+
+def _paged_args(q, cache, kind, block_table, lengths, sm_scale, page_size, starts, req_of_token, logit_cap, slopes,
+                q_positions, key_positions, lse, error_word):
+    import torch
+
+    _need_cuda("q", q, torch.bfloat16)
+    if q.dim() != 3 or q.shape[2] != 256 or q.stride(2) != 1:
+        raise ValueError("q must be [T, H, 256], contiguous along its last dimension")
+    T, H = q.shape[0], q.shape[1]
+    cache = _cache_rows(cache, kind, 264 if kind == CACHE_FP8_SCALED else 256)
+    _need_vector("lengths", lengths, T)
+    _need_vector("starts", starts, T)
+    _need_vector("req_of_token", req_of_token, T)
+    _need_vector("q_positions", q_positions, T)
+    _need_cuda("block_table", block_table, torch.int32)
+    _need_rows("block_table", block_table)
+    _need_cuda("key_positions", key_positions, torch.int32)
+    _need_rows("key_positions", key_positions, None if block_table is None else block_table.shape[0])
+    _need_cuda("slopes", slopes, torch.float32)
+    if slopes is not None and (slopes.dim() != 1 or slopes.numel() != H or not slopes.is_contiguous()):
+        raise ValueError("slopes must be a contiguous tensor of H entries")
+    _need_cuda("lse", lse, torch.float32)
+    if lse is not None and (tuple(lse.shape) != (T, H) or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous [T, H] tensor")
+    _need_cuda("error_word", error_word, torch.int32)
+    _need_on(q.device, cache=cache, block_table=block_table, lengths=lengths, starts=starts, req_of_token=req_of_token,
+             slopes=slopes, q_positions=q_positions, key_positions=key_positions, lse=lse, error_word=error_word)
+    a = DsaPagedArgs()
+    a.q = q.data_ptr()
+    a.q_stride_t, a.q_stride_h = (q.stride(0) if T > 1 else 0), (q.stride(1) if H > 1 else 0)
+    a.T, a.H = T, H
+    a.cache, a.kind, a.num_slots = cache.data_ptr(), kind, cache.shape[0]
+    a.d_nope, a.d_rope, a.d_v = 256, 0, 256
+    a.lengths = lengths.data_ptr()
+    # without a table or key positions every request reads the same slots: no row to run out of
+    a.num_requests = 1 << 31
+    if block_table is not None:
+        a.block_table, a.bt_stride = block_table.data_ptr(), _row_stride(block_table)
+        a.page_size, a.max_pages = page_size, block_table.shape[1]
+        a.num_requests = block_table.shape[0]
+    if key_positions is not None:
+        a.key_positions, a.kp_stride = key_positions.data_ptr(), _row_stride(key_positions)
+        a.kp_width = key_positions.shape[1]
+        a.num_requests = key_positions.shape[0]
+    if starts is not None:
+        a.starts = starts.data_ptr()
+    if req_of_token is not None:
+        a.req_of_token = req_of_token.data_ptr()
+    if q_positions is not None:
+        a.q_positions = q_positions.data_ptr()
+    a.sm_scale, a.logit_cap = float(sm_scale), float(logit_cap)
+    if slopes is not None:
+        a.slopes = slopes.data_ptr()
+    if lse is not None:
+        a.lse = lse.data_ptr()
+    if error_word is not None:
+        a.error_word = error_word.data_ptr()
+    return a
+
+
+def _give_workspace(a, workspace, nbytes, device):
+    """``workspace``, or memory of the current stream for this call: the caching allocator orders
+    its reuse with the stream, and inside a graph capture it belongs to the graph."""
+    import torch
+
+    _need_cuda("workspace", workspace, torch.uint8)
+    if workspace is None:
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    _need_on(device, workspace=workspace)
+    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
+    return workspace
+
+
+def dsa_paged_attn_workspace_size(T: int, H: int = 64) -> int:
+    """Workspace bytes dsa_paged_attn needs on the current device."""
+    a = DsaPagedArgs()
+    a.T, a.H = T, H
+    n = ctypes.c_size_t(0)
+    _check(load_library().dsa_paged_attn_workspace_size(ctypes.byref(a), ctypes.byref(n)),
+           "dsa_paged_attn_workspace_size")
+    return int(n.value)
+
+
+def dsa_paged_attn(q, cache, kind: int, block_table, lengths, sm_scale: float, *, page_size: int = 0, starts=None,
+                   req_of_token=None, logit_cap: float = 0.0, slopes=None, q_positions=None, key_positions=None,
+                   out=None, lse=None, workspace=None, error_word=None):
+    """Dense attention of q [T, H, 256] over positions starts[t] .. lengths[t] - 1 of each token's
+    request (token t's own request t without ``req_of_token``): bf16 [T, H, 256].
+
+    ``block_table`` int32 [R, pages], or None: position j is slot j. ``logit_cap`` > 0 caps scores
+    by a tanh; ``slopes`` fp32 [H] subtracts slopes[h] * |q_position - key_position|. ``lse`` fp32
+    [T, H] receives the natural log sum of exp(score)."""
+    import torch
+
+    a = _paged_args(q, cache, kind, block_table, lengths, sm_scale, page_size, starts, req_of_token, logit_cap, slopes,
+                    q_positions, key_positions, lse, error_word)
+    if out is None:
+        out = torch.empty((a.T, a.H, 256), dtype=torch.bfloat16, device=q.device)
+    _need_cuda("out", out, torch.bfloat16)
+    _need_on(q.device, out=out)
+    if tuple(out.shape) != (a.T, a.H, 256) or out.stride(2) != 1:
+        raise ValueError("out must be [T, H, 256], contiguous along its last dimension")
+    a.out = out.data_ptr()
+    a.out_stride_t = out.stride(0) if a.T > 1 else 256 * a.H
+    a.out_stride_h = out.stride(1) if a.H > 1 else 256
+    with torch.cuda.device(q.device):
+        need = 0 if workspace is not None else dsa_paged_attn_workspace_size(a.T, a.H)
+        workspace = _give_workspace(a, workspace, need, q.device)
+        _check(load_library().dsa_paged_attn(ctypes.byref(a), _stream(q.device)), "dsa_paged_attn")
+    return out
+
+
+def dsa_paged_attn_mass(q, cache, kind: int, block_table, lengths, sm_scale: float, lse, mass, *, page_size: int = 0,
+                        starts=None, req_of_token=None, logit_cap: float = 0.0, slopes=None, q_positions=None,
+                        key_positions=None, mass_out=None, error_word=None):
+    """Adds each position's attention weight, summed over heads, to ``mass`` fp32 [R, S]: in place,
+    or into ``mass_out`` (entries outside the tokens' ranges are left as they are). ``lse`` is
+    dsa_paged_attn's on the same arguments. Requests must be strictly ascending. Returns mass_out."""
+    import torch
+
+    if lse is None:
+        raise ValueError("lse is required")
+    a = _paged_args(q, cache, kind, block_table, lengths, sm_scale, page_size, starts, req_of_token, logit_cap, slopes,
+                    q_positions, key_positions, lse, error_word)
+    if mass_out is None:
+        mass_out = mass
+    for name, t in (("mass", mass), ("mass_out", mass_out)):
+        _need_cuda(name, t, torch.float32)
+        _need_rows(name, t, None if block_table is None and key_positions is None else a.num_requests)
+    _need_on(q.device, mass=mass, mass_out=mass_out)
+    if mass_out.shape != mass.shape:
+        raise ValueError("mass_out must have mass's shape")
+    a.num_requests = mass.shape[0]
+    with torch.cuda.device(q.device):
+        _check(load_library().dsa_paged_attn_mass(ctypes.byref(a), _ptr(mass), _row_stride(mass), _ptr(mass_out),
+                                                  _row_stride(mass_out), mass.shape[1], _stream(q.device)),
+               "dsa_paged_attn_mass")
+    return mass_out
+
+
+def dsa_cache_evict_workspace_size(num_requests: int, width: int) -> int:
+    """Workspace bytes dsa_cache_evict needs for mass rows of ``width`` entries."""
+    n = ctypes.c_size_t(0)
+    _check(load_library().dsa_cache_evict_workspace_size(num_requests, width, ctypes.byref(n)),
+           "dsa_cache_evict_workspace_size")
+    return int(n.value)
+
+
+def dsa_cache_evict(cache, kind: int, block_table, lengths, mass, budget: int = 0, *, page_size: int = 0, sink: int = 0,
+                    recent: int = 0, budgets=None, positions=None, mass_out=None, positions_out=None, lengths_out=None,
+                    d_nope: int = 256, d_rope: int = 0, workspace=None, error_word=None):
+    """Shrinks request r from lengths[r] to at most budgets[r] (``budget`` without them) positions,
+    in place in the paged cache: the positions of largest ``mass`` fp32 [R, S] stay, the first
+    ``sink`` and ``recent`` newest token positions always. Kept rows past the budget move into the
+    evicted places below it; ``mass``, ``positions`` int32 [R, S] (each entry's token position; its
+    index without them) and ``lengths`` follow, in place or into the ``_out`` tensors. Returns
+    (lengths_out, mass_out, positions_out)."""
+    import torch
+
+    row = dsa_cache_row_bytes(kind, d_nope, d_rope)
+    cache = _cache_rows(cache, kind, row if kind == CACHE_FP8_SCALED else row // 2)
+    _need_cuda("mass", mass, torch.float32)
+    _need_rows("mass", mass)
+    R, S = mass.shape
+    lengths_out = lengths if lengths_out is None else lengths_out
+    mass_out = mass if mass_out is None else mass_out
+    positions_out = positions if positions_out is None else positions_out
+    for name, t in (("lengths", lengths), ("budgets", budgets), ("lengths_out", lengths_out)):
+        _need_vector(name, t, R)
+    _need_cuda("block_table", block_table, torch.int32)
+    _need_rows("block_table", block_table, R)
+    _need_cuda("mass_out", mass_out, torch.float32)
+    for name, t in (("positions", positions), ("positions_out", positions_out)):
+        _need_cuda(name, t, torch.int32)
+    for name, t in (("mass_out", mass_out), ("positions", positions), ("positions_out", positions_out)):
+        _need_rows(name, t, R, S)
+    _need_cuda("error_word", error_word, torch.int32)
+    _need_on(cache.device, block_table=block_table, lengths=lengths, budgets=budgets, mass=mass, positions=positions,
+             mass_out=mass_out, positions_out=positions_out, lengths_out=lengths_out, error_word=error_word)
+    a = DsaEvictArgs()
+    a.cache, a.kind, a.num_slots = cache.data_ptr(), kind, cache.shape[0]
+    a.d_nope, a.d_rope = d_nope, d_rope
+    if block_table is not None:
+        a.block_table, a.bt_stride = block_table.data_ptr(), _row_stride(block_table)
+        a.page_size, a.max_pages = page_size, block_table.shape[1]
+    a.num_requests, a.width = R, S
+    a.lengths, a.lengths_out = lengths.data_ptr(), lengths_out.data_ptr()
+    if budgets is not None:
+        a.budgets = budgets.data_ptr()
+    a.budget, a.sink, a.recent = int(budget), int(sink), int(recent)
+
+    # a single row's stride says nothing; one that is at least the width passes the library's check
+    def stride(t):
+        return S if R == 1 else t.stride(0)
+
+    a.mass, a.mass_stride = mass.data_ptr(), stride(mass)
+    a.mass_out, a.mass_out_stride = mass_out.data_ptr(), stride(mass_out)
+    if positions is not None:
+        a.positions, a.positions_stride = positions.data_ptr(), stride(positions)
+    if positions_out is not None:
+        a.positions_out, a.positions_out_stride = positions_out.data_ptr(), stride(positions_out)
+    if error_word is not None:
+        a.error_word = error_word.data_ptr()
+    with torch.cuda.device(cache.device):
+        need = 0 if workspace is not None else dsa_cache_evict_workspace_size(R, S)
+        workspace = _give_workspace(a, workspace, need, cache.device)
+        _check(load_library().dsa_cache_evict(ctypes.byref(a), _stream(cache.device)), "dsa_cache_evict")
+    return lengths_out, mass_out, positions_out

@@ -54,6 +54,7 @@ typedef enum {
 #define DSA_DEVERR_INDEX_OUT_OF_RANGE 0x1  /* an index / page addressed no slot: entry masked */
 #define DSA_DEVERR_TIMEOUT 0x2             /* a bounded device-side wait gave up */
 #define DSA_DEVERR_SLOT_OUT_OF_RANGE 0x4   /* quant_k_cache: out_loc outside [0, num_slots): row skipped */
+#define DSA_DEVERR_REQUEST_ORDER 0x8       /* paged_attn_mass: a request named twice or out of order: token skipped */
 
 typedef enum {
   DSA_CACHE_BF16 = 0,        /* bf16 latent rows [num_slots, d_nope + d_rope] */
@@ -274,6 +275,145 @@ DSA_API dsa_status_t dsa_quant_fp8_blockscale(const void* x, int64_t rows, int64
 DSA_API dsa_status_t dsa_proj_gemm(const void* x_codes, const void* x_scales, const void* w_codes,
                                    const void* w_scales, int64_t M, int64_t N, int64_t K, void* y, int64_t y_stride,
                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Dense attention over the paged latent cache: one new token per request (decode), over every
+ * position of a range instead of a top-k list, with the two operators that shrink a cache by the
+ * attention its positions receive. Geometry 256+0 (d_nope = d_v = 256), both cache kinds.
+ *
+ * Positions. Request r's position j is the cache row slot(r, j) = block_table[r, j / page_size] *
+ * page_size + j % page_size, or slot j when block_table is NULL (direct mode). Token t reads the
+ * positions starts[t] <= j < lengths[t] of request req_of_token[t]. A range past the addressable
+ * positions (max_pages * page_size; num_slots in direct mode; the row width of key_positions or
+ * of the mass), a page that addresses no slot, or a request outside [0, num_requests) sets
+ * DSA_DEVERR_INDEX_OUT_OF_RANGE, and the positions concerned are masked. Rows outside the range
+ * are never used, whatever they hold.
+ *
+ * Scores, natural units, for head h and position j:
+ *   u = sm_scale * dot(q[t,h,:], k_j)
+ *   u = logit_cap * tanh(u / logit_cap)                       when logit_cap > 0
+ *   u = u - slopes[h] * |qpos_t - kpos_rj|                    when slopes != NULL
+ * with qpos_t = q_positions[t] (lengths[t] - 1 when NULL) and kpos_rj = key_positions[r, j] (j
+ * when NULL; a cache that evicted positions keeps them out of order, dsa_cache_evict).
+ * A document mask is a range (starts[t] = the document's first position); a causal or a prefix
+ * mask over several tokens of a request is lengths[t].
+ * Arithmetic: keys are exact (bf16 as stored; FP8 code * tile scale, the codes exact in the
+ * products and the fp32 scales applied to the fp32 accumulators); scores, softmax statistics and
+ * sums in fp32; the probabilities (FP8: times the key's tile scale) enter the value product as
+ * bf16. Results are bit-identical across repeated calls with the same inputs on one device.
+ */
+typedef struct dsa_paged_args {
+  const void* q;                 /* bf16 [T, H, 256], 16-byte aligned, strides multiples of 8 */
+  int64_t q_stride_t, q_stride_h;
+  int64_t T;                     /* query tokens, at most 2^24 (0 = no-op) */
+  int H;                         /* heads: 1 .. 128 */
+  const void* cache;
+  dsa_cache_kind_t kind;
+  int64_t num_slots;
+  int d_nope, d_rope, d_v;       /* (256, 0, 256) */
+  const int32_t* block_table;    /* int32 [num_requests, bt_stride] or NULL (direct slots) */
+  int64_t bt_stride;
+  int page_size, max_pages;
+  int64_t num_requests;          /* rows of block_table, key_positions and mass */
+  const int32_t* req_of_token;   /* int32 [T], or NULL: token t belongs to request t */
+  const int32_t* starts;         /* int32 [T], or NULL: 0; a negative entry counts as 0 */
+  const int32_t* lengths;        /* int32 [T]; lengths[t] <= starts[t]: nothing to read */
+  const int32_t* q_positions;    /* int32 [T] or NULL */
+  const int32_t* key_positions;  /* int32 [num_requests, kp_stride] or NULL */
+  int64_t kp_stride;
+  int64_t kp_width;              /* entries of a key_positions row */
+  float sm_scale;                /* any finite value */
+  float logit_cap;               /* 0: none; else positive and finite */
+  const float* slopes;           /* fp32 [H] or NULL */
+  void* out;                     /* bf16 [T, H, 256], 16-byte aligned, strides multiples of 8 */
+  int64_t out_stride_t, out_stride_h;
+  float* lse;                    /* fp32 [T, H] natural log sum of exp(u): optional output of
+                                    dsa_paged_attn, input of dsa_paged_attn_mass */
+  void* workspace;               /* device scratch of dsa_paged_attn_workspace_size bytes, 256-byte
+                                    aligned, of any content. Calls whose kernels may overlap on
+                                    the GPU need separate ones (two captured graphs included). */
+  size_t workspace_bytes;
+  int32_t* error_word;           /* optional device int32; DSA_DEVERR_* bits are OR-ed in */
+} dsa_paged_args_t;
+
+/* Bytes of workspace dsa_paged_attn needs on the current device (T and H of the args count). */
+DSA_API dsa_status_t dsa_paged_attn_workspace_size(const dsa_paged_args_t* args, size_t* bytes);
+
+/*
+ * dsa_paged_attn - out[t,h,:] = sum_j softmax_j(u) k_j over the token's range, and lse[t,h] when
+ * asked for. A token with nothing to read gets out = 0 and lse = -inf. Tokens may share a request.
+ */
+DSA_API dsa_status_t dsa_paged_attn(const dsa_paged_args_t* args, void* stream);
+
+/*
+ * dsa_paged_attn_mass - the attention weight each cached position received, summed over heads:
+ *   mass_out[r, j] = mass[r, j] + sum_h exp(u[h, j] - lse[t, h])   for the positions j of token t's range,
+ * r its request; every other entry of mass_out is left as it is. args->lse [T, H] is the input
+ * (dsa_paged_attn's on the same arguments); out and workspace are not used.
+ *   mass          fp32 [num_requests, mass_width], row stride mass_stride
+ *   mass_out      the same shape, row stride mass_out_stride: equal to mass (in place) or disjoint
+ * Each request at most once and in ascending order (req_of_token strictly ascending, or NULL):
+ * a token whose request does not exceed every earlier one is skipped and sets
+ * DSA_DEVERR_REQUEST_ORDER. Masked positions add nothing, but are copied.
+ */
+DSA_API dsa_status_t dsa_paged_attn_mass(const dsa_paged_args_t* args, const float* mass, int64_t mass_stride,
+                                         float* mass_out, int64_t mass_out_stride, int64_t mass_width, void* stream);
+
+/*
+ * dsa_cache_evict - shrink every request to its budget, keeping the positions of largest mass, in
+ * place in the paged cache. For request r with n = lengths[r] and b = budgets[r] (budget when
+ * budgets is NULL; a negative one counts as 0), n > b:
+ *   kept        the b positions of the largest mass, ties to the lower position; the first `sink`
+ *               token positions (kpos < sink) and the `recent` newest (kpos > max kpos - recent)
+ *               rank as +inf. kpos_j = positions[r, j], j when positions is NULL. NaN is outside
+ *               the contract (any order, but b are kept).
+ *   moved       the i-th kept position >= b, in ascending order, moves to the i-th evicted
+ *               position < b: its cache row, mass and kpos. Nothing else moves, so the rows of
+ *               [0, b) hold the kept positions, not in order of age.
+ *   mass_out    [r, 0 .. b): the kept masses; [r, b .. n): 0
+ *   positions_out [r, 0 .. b): the kept kpos (optional when positions is NULL)
+ *   lengths_out [r] = b
+ * A request with n <= b keeps all: mass_out and positions_out [r, 0 .. n) are copies, lengths_out
+ * n. Entries at or past n are left as they are. Each output may be its input (in place) or disjoint.
+ * A request whose n exceeds `width` or the addressable positions, or with a page among its n
+ * positions that addresses no slot, keeps all as well and sets DSA_DEVERR_INDEX_OUT_OF_RANGE
+ * (only its first min(n, width) entries are copied).
+ * The pages of a request that is shrunk must be its own: a page that another request also names
+ * would change under it (give such a request a budget of at least its length).
+ * Cache rows of both kinds and both geometries (256+0, 512+64). Direct mode (block_table NULL)
+ * takes one request. Bit-identical across repeated calls.
+ */
+typedef struct dsa_evict_args {
+  void* cache;
+  dsa_cache_kind_t kind;
+  int64_t num_slots;
+  int d_nope, d_rope;
+  const int32_t* block_table;    /* int32 [num_requests, bt_stride] or NULL (direct slots) */
+  int64_t bt_stride;
+  int page_size, max_pages;
+  int64_t num_requests;          /* 0 = no-op */
+  const int32_t* lengths;        /* int32 [num_requests] */
+  const int32_t* budgets;        /* int32 [num_requests] or NULL */
+  int budget;                    /* used when budgets is NULL: >= 0 */
+  int sink, recent;              /* >= 0 */
+  int64_t width;                 /* entries of a row of mass and positions: 1 .. 2^30 */
+  const float* mass;             /* fp32 [num_requests, width] */
+  int64_t mass_stride;
+  const int32_t* positions;      /* int32 [num_requests, width] or NULL */
+  int64_t positions_stride;
+  float* mass_out;
+  int64_t mass_out_stride;
+  int32_t* positions_out;
+  int64_t positions_out_stride;
+  int32_t* lengths_out;          /* int32 [num_requests] */
+  void* workspace;               /* dsa_cache_evict_workspace_size bytes, any content; one call at
+                                    a time per workspace */
+  size_t workspace_bytes;
+  int32_t* error_word;
+} dsa_evict_args_t;
+
+DSA_API dsa_status_t dsa_cache_evict_workspace_size(int64_t num_requests, int64_t width, size_t* bytes);
+DSA_API dsa_status_t dsa_cache_evict(const dsa_evict_args_t* args, void* stream);
 
 #ifdef __cplusplus
 }
