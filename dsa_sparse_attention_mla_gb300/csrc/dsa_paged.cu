@@ -14,11 +14,13 @@
 //    O^T[column, head] += V^T P^T in two M = 128 halves of the 256 columns, V^T read MN-major from
 //    the same K tile (tcgen05 kind::f16, bf16 operands, fp32 accumulators in tensor memory). A
 //    token has at most 64 heads per pass: heads as M would leave half of the tensor core idle.
-//  * FP8 rows: the e4m3 codes are widened to bf16 exactly on their way into shared memory. The two
-//    tile scales of a row never touch them: S keeps one accumulator per scale tile and they are
-//    multiplied there in fp32, and the value product takes one weight matrix per scale tile,
-//    p * scale, so the keys are the exact products code * scale.
-//  * Softmax with one thread per key and 16 heads (four warps per lane quarter). The running maximum
+//  * FP8 rows: scores run on the e4m3 codes as they are (kind::f8f6f4), the bf16 query split into two
+//    e4m3 terms per head and 128-column tile, scaled by a power of two: hi + lo is the bf16 component
+//    for every component within 2^9 of its tile's largest. S keeps one accumulator per scale tile and
+//    the fp32 scales multiply there. The value product takes the codes widened to bf16, which is exact,
+//    and one bf16 weight matrix per scale tile, p * scale: e4m3 weights would lose what many far
+//    positions add up to beside one strong one. So the keys are the exact products code * scale.
+//  * Softmax with one thread per key and 32 heads (two warps per lane quarter). The running maximum
 //    of a head is raised, and O and the sums rescaled, only when some score exceeds it by 2^20: p
 //    and its sums are floating point, so a stale maximum costs no precision, and the exact path runs
 //    for a segment's first tile and almost never again.
@@ -26,11 +28,16 @@
 //    device): rows (token, group of 64 heads) cost their 128-position tiles plus a constant, and
 //    CTA c takes the c-th of G equal parts of the total. A row cut by a border leaves unnormalised
 //    parts in the workspace, which a second, dependent launch joins in the order of the parts.
-//  * Warp roles: 0-15 softmax, 16 scheduler (walks the CTA's rows), 17 score products, 18 value
-//    products, 19 query loads, 20-27 row loads. Every wait is bounded.
+//  * Warp roles: 0-7 softmax, 8 scheduler (walks the CTA's rows, finds the slots of each tile's
+//    positions and prefetches them into L2, up to eight tiles ahead), 9 score products, 10 value
+//    products, 11 query loads, 12-15 row loads. Every wait is bounded.
+//    512 threads leave 128 registers each: with 16 softmax warps and 72, spills of 200 to 450 bytes a
+//    thread were more than the L1 beside the tiles holds, and a tile took 9500 cycles.
+//  * Rows go straight from global memory to their swizzled place with cp.async, so every free stage of
+//    the ring holds loads in flight and no register does. FP8: the warp that copied a row widens it
+//    into a second ring while the softmax of its tile runs.
 //  * The mass kernel is the same without the value product: with the lse given, each key's thread
-//    adds the weights of all 64 heads; four warp groups take tiles in turn, with an accumulator
-//    buffer each.
+//    adds the weights of all 64 heads; two groups of four warps take tiles in turn.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -47,19 +54,50 @@ constexpr int kD = 256;
 constexpr int kMaxHeads = 128;
 constexpr int kHG = 64;    // heads per row (MMA N)
 constexpr int kBN = 128;   // positions per tile (MMA M)
-constexpr int kSoftmaxWarps = 16;
-constexpr int kWarpSched = 16, kWarpScore = 17, kWarpValue = 18, kWarpQuery = 19, kWarpLoad0 = 20;
-constexpr int kLoadWarps = 8;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kWarpSched = 8, kWarpScore = 9, kWarpValue = 10, kWarpQuery = 11, kWarpLoad0 = 12;
+constexpr int kLoadWarps = 4;
+constexpr int kLoadRows = kBN / kLoadWarps;
 constexpr int kWarps = kWarpLoad0 + kLoadWarps;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCtas = 192;      // the join's lists
 constexpr int kSegs = 8;           // segment ring depth
+constexpr int kMaps = 8;           // tiles whose slots are known ahead
+constexpr int kPrefetchPage = 16;  // smallest page prefetched into L2: an eighth of a tile per request
 constexpr int kRowOverhead = 1;    // a row's start and end, in tiles
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -1e30f;   // running maximum before the first valid score
 constexpr float kStale = 20.0f;    // a score may exceed the running maximum by 2^20
+
+// Bounded wait for the phase of the given parity. The hint lets the hardware park the warp for up to
+// a millisecond: some twenty warps wait at any time, and polling took a third of the issue slots.
+__device__ __forceinline__ bool try_wait_parked(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n"
+      "selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(1000000u)
+      : "memory");
+  return ok != 0;
+}
+// Waits for the phase for about half a microsecond.
+__device__ __forceinline__ void park(uint32_t bar, uint32_t parity) {
+  asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%0], %1, %2;\n}" ::"r"(bar),
+               "r"(parity), "r"(500u)
+               : "memory");
+}
+static __device__ __noinline__ bool bar_wait_retry(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!try_wait_parked(bar, parity))
+    if (globaltimer_ns() - t0 > kWaitNs) return false;
+  return true;
+}
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+  return try_wait_parked(bar, parity) || bar_wait_retry(bar, parity);
+}
 
 struct Params {
   const uint16_t* q;
@@ -120,26 +158,32 @@ struct Cfg {
   static constexpr int O_COL = NSB * S_COLS;          // O^T halves at O_COL and O_COL + 64
   static constexpr int TMEM_USED = O_COL + (MASS ? 0 : 128);
   static constexpr int TMEM_COLS = TMEM_USED <= 256 ? 256 : 512;
-  // rings of a tile's valid mask and scales: a load warp may run this far ahead of the tile's reader
+  // FP8: ring of tile scales; a load warp may run this far ahead of the tile's reader
   static constexpr int NV = MASS ? 8 : 4;
-  static constexpr int NST = 4;                       // K ring: halves of a tile (128 keys x 128 columns)
-  static constexpr int HALF_BYTES = kBN * 256;
+  static constexpr bool WIDEN = F8 && !MASS;
+  // K ring: halves of a tile (128 keys x 128 columns), as stored; FP8 values: a ring of widened halves
+  static constexpr int HALF_BYTES = kBN * (F8 ? 128 : 256);
+  static constexpr int NST = F8 ? (MASS ? 8 : 5) : 4;
+  static constexpr int NW = 2;
+  static constexpr int WIDE_BYTES = WIDEN ? kBN * 256 : 0;
   static constexpr int PBUF = F8 ? 1 : 2;
   static constexpr int PN = F8 ? 2 : 1;               // weight matrices per tile
   static constexpr int P_BYTES = MASS ? 0 : PN * kBN * 128;
-  static constexpr int Q_OFF = 0, Q_BYTES = kHG * kD * 2;
+  static constexpr int Q_OFF = 0, Q_BYTES = kHG * kD * 2;  // FP8: hi terms of both tiles, then lo
   static constexpr int K_OFF = Q_OFF + Q_BYTES;
-  static constexpr int P_OFF = K_OFF + NST * HALF_BYTES;
+  static constexpr int W_OFF = K_OFF + NST * HALF_BYTES;
+  static constexpr int P_OFF = W_OFF + NW * WIDE_BYTES;
   static constexpr int SEG_OFF = P_OFF + PBUF * P_BYTES;
-  static constexpr int VM_OFF = SEG_OFF + kSegs * 64;         // [NV] valid masks of a tile, 128 bits
-  static constexpr int SC_OFF = VM_OFF + 16 * NV;             // FP8: [NV][128][2] tile scales
-  static constexpr int NL_OFF = SC_OFF + (F8 ? NV * 1024 : 0); // mass: [kSegs][64] -lse, exp2 domain
+  static constexpr int MAP_OFF = SEG_OFF + kSegs * 64;        // [kMaps][128] slots, -1: masked
+  static constexpr int SC_OFF = MAP_OFF + kMaps * 512;        // FP8: [NV][128][2] tile scales
+  static constexpr int SQ_OFF = SC_OFF + (F8 ? NV * 1024 : 0); // FP8: [kSegs][64][2] query scales
+  static constexpr int NL_OFF = SQ_OFF + (F8 ? kSegs * 512 : 0);  // mass: [kSegs][64] -lse, exp2 domain
   static constexpr int SL_OFF = NL_OFF + (MASS ? kSegs * 256 : 0);  // slopes [128]
-  static constexpr int RED_OFF = SL_OFF + 512;  // m [2][64], alpha [64], part [4][64], inverse sums [64]
-  static constexpr int VOTE_OFF = RED_OFF + 8 * 256;
-  static constexpr int PLAN_OFF = VOTE_OFF + 128;  // block scans: 2 x kWarps int64; start row, its cost
+  // -m [2][64], alpha [64], part [4][64], inverse sums [64], raise of m [64]
+  static constexpr int RED_OFF = SL_OFF + 512;
+  static constexpr int PLAN_OFF = RED_OFF + 9 * 256;  // block scans: 2 x kWarps int64; start row, its cost
   static constexpr int BAR_OFF = PLAN_OFF + 2 * 8 * kWarps + 64;
-  static constexpr int NBARS = 2 + 2 * NST + 3 * kSegs + NV + 2 * NSB + 2 * 2 + 1 + 2;
+  static constexpr int NBARS = 2 + 2 * NST + 3 * kSegs + NV + 2 * kMaps + 2 * NSB + 2 * 2 + 2 + 2 * NW;
   static constexpr int MISC_OFF = BAR_OFF + 8 * NBARS;
   static constexpr int SMEM_BYTES = MISC_OFF + 16 + 1024;
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
@@ -190,7 +234,7 @@ __device__ __forceinline__ float modify(float u, float cap, float inv_cap2, floa
   return (u - bias) * kLog2e;
 }
 
-// Sums over the block, exclusive per thread (v), and in total; `buf` holds kWarps values.
+// Exclusive sum over the block, and its total; `buf` holds kWarps values.
 __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* buf, int64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t x = v;
@@ -201,14 +245,15 @@ __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* buf, int64_t* t
   }
   if (lane == 31) buf[warp] = x;
   __syncthreads();
-  int64_t base = 0, sum = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    const int64_t s = buf[w];
-    if (w < warp) base += s;
-    sum += s;
+  int64_t w = lane < kWarps ? buf[lane] : 0;  // every warp sums up the warps
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
   }
-  *total = sum;
-  return base + x - v;
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  const int64_t before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+  return (warp > 0 ? before : 0) + x - v;
 }
 // Exclusive running maximum over the block.
 __device__ __forceinline__ int block_max(int v, int64_t* buf) {
@@ -223,26 +268,77 @@ __device__ __forceinline__ int block_max(int v, int64_t* buf) {
   int ex = __shfl_up_sync(0xffffffffu, x, 1);
   if (lane == 0) ex = INT32_MIN;
   __syncthreads();
-  for (int w = 0; w < warp; ++w) ex = max(ex, (int)buf[w]);
-  return ex;
+  int w = lane < warp ? (int)buf[lane] : INT32_MIN;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) w = max(w, __shfl_xor_sync(0xffffffffu, w, o));
+  return max(ex, w);
 }
+static_assert(kWarps <= 32, "one lane per warp in the block scans");
 
-// Exchange among the softmax warps (one arrival each on `xbar`, phase `n` of it): returns the OR
-// of `v` over the warps, with every warp's earlier shared-memory writes visible, or -1 when a warp
-// did not arrive within the time limit.
-static __device__ __forceinline__ int exchange(uint32_t xbar, int* votes, uint32_t n, bool v) {
+// Barrier of the softmax warps that returns the OR of `v`. All of them take the same path through
+// the tiles: a warp whose wait runs out goes on with what it has, waiting no more, and all leave
+// together between two segments, so none is left behind at a barrier.
+__device__ __forceinline__ bool softmax_any(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.or.pred q, 1, 256, p;\nselp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
+static_assert(32 * kSoftmaxWarps == 256, "the barriers' thread count");
+
+// Splits query rows h0 .. h0 + 15 of a row (zero past `heads`) into e4m3 hi and lo terms, lane l
+// columns 8 l .. 8 l + 7, per head and 128-column tile scaled by 2^-e so that the largest component
+// lies in [128, 256); sq[h][tile] = f * 2^e.
+__device__ __forceinline__ void split_query(const uint16_t* q, int64_t q_sh, int h0, int heads, float f, uint8_t* qbuf,
+                                            float* sq) {
   const int lane = threadIdx.x & 31;
-  const int slot = n & 1;
-  const bool any = __any_sync(0xffffffffu, v);
-  __syncwarp();
-  if (lane == 0) {
-    votes[slot * kSoftmaxWarps + (threadIdx.x >> 5)] = any ? 1 : 0;
-    mbar_arrive(xbar);
+  const int gl = lane & 15, tile = lane >> 4;
+#pragma unroll
+  for (int part = 0; part < kHG / kLoadWarps / 4; ++part) {
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int h = h0 + 4 * part + i;
+      v[i] = h < heads ? *reinterpret_cast<const uint4*>(q + h * q_sh + 8 * lane) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int h = h0 + 4 * part + i;
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      uint32_t a = 0u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) a = max(a, max((w[j] << 16) & 0x7FFFFFFFu, w[j] & 0x7FFF0000u));
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));  // within the tile's lanes
+      int e = (int)(a >> 23) - 127 - 7;
+      e = a == 0u ? 0 : (e < -126 ? -126 : e);
+      const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+      uint32_t hi[2], lo[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float x[4], r[4];
+        x[0] = __uint_as_float(w[2 * j] << 16) * inv;
+        x[1] = __uint_as_float(w[2 * j] & 0xFFFF0000u) * inv;
+        x[2] = __uint_as_float(w[2 * j + 1] << 16) * inv;
+        x[3] = __uint_as_float(w[2 * j + 1] & 0xFFFF0000u) * inv;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) r[c] = __uint_as_float(__float_as_uint(x[c]) & 0xFFF00000u);  // four significant bits
+        hi[j] = (uint32_t)f32x2_to_e4m3x2(r[0], r[1]) | ((uint32_t)f32x2_to_e4m3x2(r[2], r[3]) << 16);
+        lo[j] = (uint32_t)f32x2_to_e4m3x2(x[0] - r[0], x[1] - r[1]) |
+                ((uint32_t)f32x2_to_e4m3x2(x[2] - r[2], x[3] - r[3]) << 16);
+      }
+      uint8_t* d = qbuf + tile * (kHG * 128) + h * 128 + (((gl >> 1) ^ (h & 7)) << 4) + 8 * (gl & 1);
+      *reinterpret_cast<uint2*>(d) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(d + 2 * kHG * 128) = make_uint2(lo[0], lo[1]);
+      // an infinite or NaN component makes the head's scores NaN
+      if (gl == 0)
+        sq[2 * h + tile] = a >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : f * __uint_as_float((uint32_t)(127 + e) << 23);
+    }
   }
-  const bool ok = mbar_wait(xbar, n & 1, kWaitNs);
-  if (!__all_sync(0xffffffffu, ok)) return -1;
-  const int mine = votes[slot * kSoftmaxWarps + (lane & (kSoftmaxWarps - 1))];
-  return __any_sync(0xffffffffu, mine != 0) ? 1 : 0;
 }
 
 template <int KIND, bool MASS, bool MODS>
@@ -262,16 +358,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
   const uint32_t b1 = bar0 + 16 + 16 * C::NST;
   auto g_full = [&](uint32_t s) { return b1 + 8 * s; };                 // segment ring
   auto g_empty = [&](uint32_t s) { return b1 + 8 * (kSegs + s); };
-  auto nl_full = [&](uint32_t s) { return b1 + 8 * (2 * kSegs + s); };  // mass: the segment's -lse
+  auto aux_full = [&](uint32_t s) { return b1 + 8 * (2 * kSegs + s); };  // the segment's -lse, query scales
   const uint32_t b2 = b1 + 24 * kSegs;
-  auto v_full = [&](uint32_t s) { return b2 + 8 * s; };                 // valid mask and scales of a tile
-  auto s_full = [&](uint32_t s) { return b2 + 8 * (C::NV + s); };
-  auto s_empty = [&](uint32_t s) { return b2 + 8 * (C::NV + C::NSB + s); };
-  const uint32_t b3 = b2 + 8 * C::NV + 16 * C::NSB;
+  auto v_full = [&](uint32_t s) { return b2 + 8 * s; };                 // FP8: scales of a tile
+  auto map_full = [&](uint32_t s) { return b2 + 8 * (C::NV + s); };     // slots of a tile
+  auto map_empty = [&](uint32_t s) { return b2 + 8 * (C::NV + kMaps + s); };
+  const uint32_t b2s = b2 + 8 * (C::NV + 2 * kMaps);
+  auto s_full = [&](uint32_t s) { return b2s + 8 * s; };
+  auto s_empty = [&](uint32_t s) { return b2s + 8 * (C::NSB + s); };
+  const uint32_t b3 = b2s + 16 * C::NSB;
   auto p_full = [&](uint32_t s) { return b3 + 8 * s; };
   auto pv_done = [&](uint32_t s) { return b3 + 16 + 8 * s; };
-  const uint32_t xbar = b3 + 32;
-  auto drain = [&](uint32_t s) { return b3 + 40 + 8 * s; };
+  auto drain = [&](uint32_t s) { return b3 + 32 + 8 * s; };
+  auto w_full = [&](uint32_t s) { return b3 + 48 + 8 * s; };  // widened halves
+  auto w_empty = [&](uint32_t s) { return b3 + 48 + 8 * (C::NW + s); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
   Seg* segs = reinterpret_cast<Seg*>(smem + C::SEG_OFF);
@@ -279,19 +379,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
 
   asm volatile("griddepcontrol.launch_dependents;");
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 32);
+    mbar_init(q_full, F8 ? kLoadWarps : 32);  // bf16: one asynchronous arrival per thread
     mbar_init(q_empty, 1);
     for (int s = 0; s < C::NST; ++s) {
-      mbar_init(k_full(s), F8 ? kLoadWarps : 32 * kLoadWarps);  // bf16: one asynchronous arrival per thread
+      mbar_init(k_full(s), 32 * kLoadWarps);  // one asynchronous arrival per thread
       mbar_init(k_empty(s), 1);
     }
     for (int s = 0; s < kSegs; ++s) {
       mbar_init(g_full(s), 1);
-      // softmax warps, load warps, query warp, score issuer, value issuer
-      mbar_init(g_empty(s), kSoftmaxWarps + kLoadWarps + 2 + (MASS ? 0 : 1));
-      mbar_init(nl_full(s), 1);
+      // softmax warps, score issuer, value issuer, query warp, FP8: load warps
+      mbar_init(g_empty(s), kSoftmaxWarps + 1 + (MASS ? 0 : 1) + (C::WIDEN ? 0 : 1) + (F8 ? kLoadWarps : 0));
+      mbar_init(aux_full(s), (MASS ? 1 : 0) + (F8 ? kLoadWarps : 0) + (!MASS && !F8 ? 1 : 0));
     }
-    for (int s = 0; s < C::NV; ++s) mbar_init(v_full(s), kLoadWarps);
+    for (int s = 0; s < C::NV; ++s) mbar_init(v_full(s), 32 * kLoadWarps);
+    for (int s = 0; s < kMaps; ++s) {
+      mbar_init(map_full(s), 1);
+      mbar_init(map_empty(s), MASS ? 4 : kSoftmaxWarps);
+    }
     for (int s = 0; s < C::NSB; ++s) {
       mbar_init(s_full(s), 1);
       mbar_init(s_empty(s), MASS ? 4 : kSoftmaxWarps);
@@ -301,7 +405,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       mbar_init(pv_done(s), 1);
       mbar_init(drain(s), 1);
     }
-    mbar_init(xbar, kSoftmaxWarps);
+    for (int s = 0; s < C::NW; ++s) {
+      mbar_init(w_full(s), kLoadWarps);
+      mbar_init(w_empty(s), 1);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -340,8 +447,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     for (int64_t i = i0; i < i1; ++i) sum += cost_of(i, run);
     int64_t total;
     const int64_t pre = block_sum(sum, plan + kWarps, &total);
-    c0 = cta * total / p.G;
-    c1 = (cta + 1) * total / p.G;
+    if (total < (1 << 22)) {  // G is at most kMaxCtas < 2^9: 32-bit divisions
+      c0 = (uint32_t)cta * (uint32_t)total / (uint32_t)p.G;
+      c1 = (uint32_t)(cta + 1) * (uint32_t)total / (uint32_t)p.G;
+    } else {
+      c0 = cta * total / p.G;
+      c1 = (cta + 1) * total / p.G;
+    }
     if (c0 < c1 && pre <= c0 && c0 < pre + sum) {
       int64_t at = pre, i = i0;
       run = mx;
@@ -367,13 +479,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     *abort_flag = 1;
   };
   auto wait = [&](uint32_t bar, uint32_t par) -> bool {
-    if (mbar_wait(bar, par, kWaitNs)) return true;
+    if (bar_wait(bar, par)) return true;
     fail();
     return false;
   };
   // the whole warp waits, and agrees on the outcome
   auto wait_warp = [&](uint32_t bar, uint32_t par) -> bool {
-    if (__all_sync(0xffffffffu, mbar_wait(bar, par, kWaitNs))) return true;
+    if (__all_sync(0xffffffffu, bar_wait(bar, par))) return true;
     fail();
     return false;
   };
@@ -381,9 +493,68 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
   if (warp == kWarpSched) {
     // ================================================================== scheduler ====
     uint32_t sc = 0;
+    uint32_t g = 0;  // tiles mapped
     int64_t tail = -1;
     int head = 0;
     bool ok = true;
+    auto map_slot = [&](bool& good) -> int4* {
+      const uint32_t m = g % kMaps;
+      good = g < kMaps || wait_warp(map_empty(m), ((g / kMaps) & 1) ^ 1);
+      return reinterpret_cast<int4*>(smem + C::MAP_OFF + m * 512) + lane;
+    };
+    auto map_done = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(map_full(g % kMaps));
+      ++g;
+    };
+    // the slots of `n` tiles from position `base` of the range [a, b): lane l rows 4 l .. 4 l + 3
+    auto map_tiles = [&](int req, uint32_t a, uint32_t b, uint32_t base, int n) -> bool {
+      const int32_t* bt = p.bt ? p.bt + req * p.bt_stride : nullptr;
+      for (int k = 0; k < n; ++k, base += kBN) {
+        bool good;
+        int4* dst = map_slot(good);
+        if (!good) return false;
+        int sl[4];
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t pos = base + 4 * lane + i;
+          sl[i] = -1;
+          if (pos >= a && pos < b) {
+            if (bt) {
+              const uint32_t pg = (uint32_t)(((uint64_t)pos * p.pg_mul) >> p.pg_shift);
+              const int64_t page = bt[pg];
+              const int64_t slot = page * p.page_size + (pos - pg * (uint32_t)p.page_size);
+              if (page < 0 || slot >= p.num_slots) bad = true;
+              else sl[i] = (int)slot;
+            } else {
+              sl[i] = (int)pos;
+            }
+          }
+        }
+        if (bad) set_err(p.err, DSA_DEVERR_INDEX_OUT_OF_RANGE);
+        *dst = make_int4(sl[0], sl[1], sl[2], sl[3]);
+        // the tile's rows into L2, one request per page: the copies then wait for L2 only
+        if (bt && p.page_size >= kPrefetchPage) {
+          const uint32_t lo = max(base, a), hi = min(base + (uint32_t)kBN, b);
+          const uint32_t pg = (uint32_t)(((uint64_t)lo * p.pg_mul) >> p.pg_shift) + lane;
+          const uint64_t first = (uint64_t)pg * (uint32_t)p.page_size;
+          if (first < hi) {
+            const uint64_t from = first > lo ? first : lo;
+            const uint64_t to = first + p.page_size < hi ? first + p.page_size : hi;
+            const int64_t s0 = (int64_t)bt[pg] * p.page_size + (int64_t)(from - first);
+            if (s0 >= 0 && s0 + (int64_t)(to - from) <= p.num_slots) {
+              const uint64_t b0 = (uint64_t)(s0 * C::RB) & ~15ull;
+              const uint32_t bytes = (uint32_t)((uint64_t)((s0 + (int64_t)(to - from)) * C::RB) - b0) & ~15u;
+              if (bytes)
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.cache + b0), "r"(bytes) : "memory");
+            }
+          }
+        }
+        map_done();
+      }
+      return true;
+    };
     if (c0 < c1) {
       int64_t row = plan_start[0], cost = plan_start[1];
       int run = (int)plan_start[2];
@@ -457,6 +628,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
           __syncwarp();
           if (lane == 0) mbar_arrive(g_full(slot));
           ++sc;
+          const int a = __shfl_sync(0xffffffffu, r.a, src), b = __shfl_sync(0xffffffffu, r.b, src);
+          const int t0 = __shfl_sync(0xffffffffu, (int)lo, src);
+          const int nt = __shfl_sync(0xffffffffu, n > 0 ? (int)(hi - lo) : 0, src);
+          const int req = __shfl_sync(0xffffffffu, r.req, src);
+          if (!map_tiles(req, (uint32_t)a, (uint32_t)b, (uint32_t)(a & ~127) + 128u * (uint32_t)t0, nt)) {
+            ok = false;
+            break;
+          }
         }
         row += 32;
         cost += __shfl_sync(0xffffffffu, cum, 31);
@@ -467,6 +646,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       p.ws_head[cta] = head;
     }
     if (ok) {
+      bool good;
+      int4* dst = map_slot(good);
+      if (good) {  // no more tiles
+        *dst = make_int4(-2, -2, -2, -2);
+        map_done();
+      }
       const uint32_t slot = sc % kSegs;
       if (sc < kSegs || wait_warp(g_empty(slot), ((sc / kSegs) & 1) ^ 1)) {
         if (lane == 0) {
@@ -478,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
   } else if (warp == kWarpScore) {
     // ============================================================= score products ====
     if (lane == 0) {
-      constexpr uint32_t idS = idesc_bf16(kBN, kHG, 0, 0);
+      constexpr uint32_t idS = F8 ? idesc_e4m3(kBN, kHG, 0, 0) : idesc_bf16(kBN, kHG, 0, 0);
       const uint64_t dq = sw128_desc(sbase + C::Q_OFF, 16, 1024);
       const uint32_t q_lo = (uint32_t)dq, q_hi = (uint32_t)(dq >> 32);
       const uint32_t k_hi = (uint32_t)(sw128_desc(0, 16, 1024) >> 32);
@@ -512,21 +697,32 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
             tc_fence_after();
             const uint32_t k_lo = (uint32_t)sw128_desc(sbase + C::K_OFF + st * C::HALF_BYTES, 16, 1024);
             const uint32_t d = F8 ? d0 + 64 * h : d0;
+            if constexpr (F8) {
+              // 32 columns per step, hi term then lo term (two chunks further)
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              const uint32_t ka = (uint32_t)((kk >> 2) * ((kBN * 128) >> 4) + (kk & 3) * 2);
-              const uint32_t qa = (uint32_t)((2 * h + (kk >> 2)) * ((kHG * 128) >> 4) + (kk & 3) * 2);
-              if (kk == 0 && (F8 || h == 0)) mma_bf16_lohi<0>(d, k_lo + ka, k_hi, q_lo + qa, q_hi, idS);
-              else mma_bf16_lohi<1>(d, k_lo + ka, k_hi, q_lo + qa, q_hi, idS);
+              for (int kk = 0; kk < 4; ++kk) {
+                const uint32_t qa = q_lo + (uint32_t)((h * (kHG * 128) + 32 * kk) >> 4);
+                if (kk == 0) mma_f8_lohi<0>(d, k_lo, k_hi, qa, q_hi, idS);
+                else mma_f8_lohi<1>(d, k_lo + 2 * kk, k_hi, qa, q_hi, idS);
+                mma_f8_lohi<1>(d, k_lo + 2 * kk, k_hi, qa + ((2 * kHG * 128) >> 4), q_hi, idS);
+              }
+            } else {
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk) {
+                const uint32_t ka = (uint32_t)((kk >> 2) * ((kBN * 128) >> 4) + (kk & 3) * 2);
+                const uint32_t qa = (uint32_t)((2 * h + (kk >> 2)) * ((kHG * 128) >> 4) + (kk & 3) * 2);
+                if (kk == 0 && h == 0) mma_bf16_lohi<0>(d, k_lo + ka, k_hi, q_lo + qa, q_hi, idS);
+                else mma_bf16_lohi<1>(d, k_lo + ka, k_hi, q_lo + qa, q_hi, idS);
+              }
             }
-            if (MASS) mma_commit(k_empty(st));
+            if (MASS || F8) mma_commit(k_empty(st));
           }
           if (ok) mma_commit(s_full(sb));
         }
         if (ok) mma_commit(q_empty);
       }
       mma_commit(drain(0));
-      mbar_wait(drain(0), 0, kWaitNs);
+      bar_wait(drain(0), 0);
     }
     __syncwarp();
   } else if (warp == kWarpValue) {
@@ -548,11 +744,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
             ok = false;
             break;
           }
+          // weights and rows were written through the generic proxy: ordered here, by the thread that
+          // has waited for them (a writer's fence would also wait for its copies in flight)
+          fence_proxy_async_smem();
           tc_fence_after();
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t st = (2 * g + h) % C::NST;
-            const uint32_t v_lo = (uint32_t)sw128_desc(sbase + C::K_OFF + st * C::HALF_BYTES, kBN * 128, 1024);
+            const uint32_t hs = 2 * g + h, st = hs % (C::WIDEN ? C::NW : C::NST);
+            if (C::WIDEN) {
+              if (!wait(w_full(st), (hs / C::NW) & 1)) {
+                ok = false;
+                break;
+              }
+              fence_proxy_async_smem();
+              tc_fence_after();
+            }
+            const uint32_t v_lo = (uint32_t)sw128_desc(
+                sbase + (C::WIDEN ? C::W_OFF + st * C::WIDE_BYTES : C::K_OFF + st * C::HALF_BYTES), kBN * 128, 1024);
             const uint32_t p_lo = (uint32_t)sw128_desc(
                 sbase + C::P_OFF + pb * C::P_BYTES + (F8 ? h * kBN * 128 : 0), kBN * 128, 1024);
             const uint32_t d = tmem + C::O_COL + 64 * h;
@@ -561,20 +769,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
 #pragma unroll
             for (int j = 1; j < kBN / 16; ++j)
               mma_bf16_lohi<1>(d, v_lo + 128 * j, mn_hi, p_lo + 128 * j, mn_hi, idPV);
-            mma_commit(k_empty(st));
+            mma_commit(C::WIDEN ? w_empty(st) : k_empty(st));
           }
+          if (!ok) break;
           mma_commit(pv_done(g & 1));
         }
       }
       mma_commit(drain(1));
-      mbar_wait(drain(1), 0, kWaitNs);
+      bar_wait(drain(1), 0);
     }
     __syncwarp();
   } else if (warp == kWarpQuery) {
     // ================================================================ query loads ====
     // 64 heads x 256 columns in four 128-byte-swizzled chunks; heads past the row's are zero.
+    // FP8: the load warps split the query, and for the attention nothing is left to do here.
     uint32_t qc = 0;
-    for (uint32_t sc = 0;; ++sc) {
+    for (uint32_t sc = 0; !C::WIDEN; ++sc) {
       const uint32_t slot = sc % kSegs;
       if (!wait_warp(g_full(slot), (sc / kSegs) & 1)) break;
       const Seg s = segs[slot];
@@ -590,8 +800,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
           for (int h = lane; h < kHG; h += 32)
             nl[h] = h < heads ? -p.lse[s.t * p.lse_st + s.hg * kHG + h] * kLog2e : -INFINITY;
           __syncwarp();
-          if (lane == 0) mbar_arrive(nl_full(slot));
+          if (lane == 0) mbar_arrive(aux_full(slot));
         }
+      }
+      if (!F8 && s.ntiles > 0) {
         if (qc > 0 && !wait_warp(q_empty, (qc - 1) & 1)) break;
         ++qc;
         const uint16_t* q = p.q + (int64_t)s.t * p.q_st + (int64_t)s.hg * kHG * p.q_sh;
@@ -611,161 +823,182 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp >= kWarpLoad0) {
     // ================================================================== row loads ====
-    // Warp w takes rows 16 w .. 16 w + 15 of every tile, in two column halves. Lane l < 16 finds
-    // row l's slot, one tile ahead of the copies.
+    // Warp w takes rows 32 w .. 32 w + 31 of every tile, in two column halves; the 16 lanes of a half
+    // warp share a row.
     const int lw = warp - kWarpLoad0;
-    uint32_t g = 0;  // tiles so far, and the segment being read
-    uint32_t sc = 0;
-    int k = 0;
-    Seg s{};
-    s.ntiles = 0;
-    bool ok = true, more = true;
-    int64_t slot_n = -1;      // slot of this lane's row in the next tile
-    float2 scale_n = make_float2(0.0f, 0.0f);
-    // finds the next tile's slots; false when there is none
-    auto advance = [&]() -> bool {
-      while (k >= s.ntiles) {
-        const uint32_t ring = sc % kSegs;
-        if (!wait_warp(g_full(ring), (sc / kSegs) & 1)) {
-          ok = false;
-          return false;
-        }
-        s = segs[ring];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(g_empty(ring));
-        ++sc;
-        k = 0;
-        if (s.type == 0) return false;
-      }
-      const uint32_t pos = (uint32_t)(s.a & ~127) + 128u * (uint32_t)(s.tile0 + k) + 16 * lw + (lane & 15);
-      int64_t slot = -1;
-      if (pos >= (uint32_t)s.a && pos < (uint32_t)s.b) {
-        if (p.bt) {
-          const uint32_t pg = (uint32_t)(((uint64_t)pos * p.pg_mul) >> p.pg_shift);
-          const int64_t page = p.bt[s.req * p.bt_stride + pg];
-          slot = page * p.page_size + (pos - pg * (uint32_t)p.page_size);
-          if (page < 0 || slot >= p.num_slots) slot = -2;
-        } else {
-          slot = pos;
-        }
-      }
-      if (slot == -2) {
-        if (lane < 16) set_err(p.err, DSA_DEVERR_INDEX_OUT_OF_RANGE);
-        slot = -1;
-      }
-      slot_n = slot;
-      if (F8) {
-        scale_n = make_float2(0.0f, 0.0f);
-        if (slot >= 0 && lane < 16) scale_n = *reinterpret_cast<const float2*>(p.cache + slot * C::RB + 256);
-      }
-      ++k;
-      return true;
-    };
     const int gl = lane & 15, hi16 = lane >> 4;
-    // FP8: the 16 lanes of a half warp read one row's 128 codes of a half
-    auto load_half = [&](uint2 (&v)[8], int64_t slot, int h) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int64_t sl = __shfl_sync(0xffffffffu, slot, 2 * i + hi16);
-        v[i] = make_uint2(0u, 0u);
-        if (sl >= 0) v[i] = __ldcs(reinterpret_cast<const uint2*>(p.cache + sl * C::RB + 128 * h + 8 * gl));
-      }
+    const int r0 = kLoadRows * lw + hi16;
+    // byte offset of row r's 16-byte granule gl in a half's two 128-byte-swizzled chunks
+    auto place = [&](int r) -> uint32_t {
+      return (uint32_t)((gl >> 3) * (kBN * 128) + r * 128 + (((gl & 7) ^ (r & 7)) << 4));
     };
-    auto store_half = [&](const uint2 (&v)[8], uint32_t st) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = 16 * lw + 2 * i + hi16;
-        const uint32_t c[2] = {v[i].x, v[i].y};
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float2 a = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)(c[j] & 0xFFFFu)));
-          const float2 b = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)(c[j] >> 16)));
-          w[2 * j] = f32x2_to_bf16x2(a.x, a.y);
-          w[2 * j + 1] = f32x2_to_bf16x2(b.x, b.y);
-        }
-        uint8_t* d = smem + C::K_OFF + st * C::HALF_BYTES + (gl >> 3) * (kBN * 128) + r * 128 + (((gl & 7) ^ (r & 7)) << 4);
-        *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    };
-    // the tile's valid rows and scales, for the softmax warps
-    auto publish = [&](int64_t slot, float2 scale) {
-      const uint32_t m = __ballot_sync(0xffffffffu, slot >= 0) & 0xFFFFu;
-      if (lane == 0) reinterpret_cast<uint16_t*>(smem + C::VM_OFF + 16 * (g % C::NV))[lw] = (uint16_t)m;
-      if (F8 && lane < 16)
-        reinterpret_cast<float2*>(smem + C::SC_OFF + 1024 * (g % C::NV))[16 * lw + lane] = scale;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(v_full(g % C::NV));
-    };
-    more = advance();
     if constexpr (F8) {
-      uint2 va[8], vb[8];
-      int64_t slot = slot_n;
-      float2 scale = scale_n;
-      if (more) load_half(va, slot, 0);
-      while (more) {
-        load_half(vb, slot, 1);
-        const int64_t cur = slot;
-        const float2 cur_scale = scale;
-        more = advance();
-        slot = slot_n;
-        scale = scale_n;
-        {
-          const uint32_t hs = 2 * g, st = hs % C::NST;
-          if (hs >= C::NST && !wait_warp(k_empty(st), ((hs / C::NST) & 1) ^ 1)) break;
-          publish(cur, cur_scale);
-          store_half(va, st);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(k_full(st));
+      // Three kinds of work, taken as they become possible: the split of a segment's query (16 heads
+      // per warp), the copy of a half into a free stage, and the widening of a half that has
+      // landed. A lane widens the 8-byte pieces it copied. Copies come first, so they run ahead.
+      uint32_t hi_ = 0, hw = 0;  // halves copied, halves widened
+      uint32_t sc = 0, qn = 0;   // segments seen, queries split
+      bool end = false, q_end = false;
+      uint32_t idle = 0;
+      uint64_t since = 0;
+      auto test = [&](uint32_t bar, uint32_t par) -> bool { return __all_sync(0xffffffffu, mbar_test(bar, par)); };
+      // byte offset of the lane's piece of row r in a half as stored
+      auto piece = [&](int r) -> uint32_t {
+        return (uint32_t)(r * 128 + (((gl >> 1) ^ (r & 7)) << 4) + 8 * (gl & 1));
+      };
+      while (!(end && q_end && (MASS || hw == hi_))) {
+        bool did = false;
+        if (!end && (MASS || hi_ - hw < C::NST)) {
+          const uint32_t st = hi_ % C::NST, gi = hi_ >> 1;
+          const int h = hi_ & 1;
+          bool go = hi_ < C::NST || test(k_empty(st), ((hi_ / C::NST) & 1) ^ 1);
+          if (go && h == 0) go = test(map_full(gi % kMaps), (gi / kMaps) & 1);
+          if (go) {
+            did = true;
+            const int* slots = reinterpret_cast<const int*>(smem + C::MAP_OFF + (gi % kMaps) * 512);
+            if (h == 0 && slots[0] == -2) {
+              end = true;
+            } else {
+              if (h == 0) {
+                // the two scales of this lane's row
+                const int r = kLoadRows * lw + lane;
+                const int sl = slots[r];
+                const uint32_t dst = sbase + C::SC_OFF + 1024 * (gi % C::NV) + 8 * r;
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst),
+                             "l"(p.cache + (sl >= 0 ? (int64_t)sl * C::RB + 256 : 0)), "r"(sl >= 0 ? 8 : 0)
+                             : "memory");
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(v_full(gi % C::NV)) : "memory");
+              }
+              const uint32_t dst = sbase + C::K_OFF + st * C::HALF_BYTES;
+#pragma unroll
+              for (int part = 0; part < kLoadRows / 16; ++part) {
+                int sl[8];  // read before the first copy: the copies are ordered with memory accesses
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sl[i] = slots[r0 + 16 * part + 2 * i];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst + piece(r0 + 16 * part + 2 * i)),
+                               "l"(p.cache + (sl[i] >= 0 ? (int64_t)sl[i] * C::RB + 128 * h + 8 * gl : 0)),
+                               "r"(sl[i] >= 0 ? 8 : 0)
+                               : "memory");
+              }
+              asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(k_full(st)) : "memory");
+              asm volatile("cp.async.commit_group;" ::: "memory");
+              ++hi_;
+            }
+          }
         }
-        if (more) load_half(va, slot, 0);
-        {
-          const uint32_t hs = 2 * g + 1, st = hs % C::NST;
-          if (hs >= C::NST && !wait_warp(k_empty(st), ((hs / C::NST) & 1) ^ 1)) break;
-          store_half(vb, st);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(k_full(st));
+        if (!did && !q_end && test(g_full(sc % kSegs), (sc / kSegs) & 1)) {
+          const uint32_t slot = sc % kSegs;
+          const Seg& s = segs[slot];
+          if (s.type == 0) {
+            q_end = did = true;
+          } else if (s.ntiles == 0 || qn == 0 || test(q_empty, (qn - 1) & 1)) {
+            did = true;
+            if (s.ntiles > 0) {
+              const int heads = min(kHG, p.H - s.hg * kHG);
+              split_query(p.q + (int64_t)s.t * p.q_st + (int64_t)s.hg * kHG * p.q_sh, p.q_sh, kHG / kLoadWarps * lw, heads,
+                          MODS ? p.sm_scale : p.sm_scale * kLog2e, smem + C::Q_OFF,
+                          reinterpret_cast<float*>(smem + C::SQ_OFF) + 128 * slot);
+              ++qn;
+            }
+            __syncwarp();
+            if (lane == 0) {
+              if (s.ntiles > 0) mbar_arrive(q_full);
+              mbar_arrive(aux_full(slot));
+              mbar_arrive(g_empty(slot));
+            }
+            __syncwarp();
+            ++sc;
+          }
         }
-        ++g;
+        if constexpr (C::WIDEN) {
+          const uint32_t sw = hw % C::NW;
+          if (!did && hw < hi_ && (hw < C::NW || test(w_empty(sw), ((hw / C::NW) & 1) ^ 1))) {
+            did = true;
+            // the copies of the halves after it may still be in flight
+            const uint32_t ahead = hi_ - hw - 1;
+            if (ahead == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+            else if (ahead == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+            else if (ahead == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+            else if (ahead == 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+            else asm volatile("cp.async.wait_group 4;" ::: "memory");
+            const uint8_t* raw = smem + C::K_OFF + (hw % C::NST) * C::HALF_BYTES;
+            uint8_t* wide = smem + C::W_OFF + sw * C::WIDE_BYTES;
+#pragma unroll
+            for (int part = 0; part < kLoadRows / 16; ++part) {
+              uint2 v[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint2*>(raw + piece(r0 + 16 * part + 2 * i));
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint32_t c[2] = {v[i].x, v[i].y};
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  const float2 a = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)(c[j] & 0xFFFFu)));
+                  const float2 b = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)(c[j] >> 16)));
+                  w[2 * j] = f32x2_to_bf16x2(a.x, a.y);
+                  w[2 * j + 1] = f32x2_to_bf16x2(b.x, b.y);
+                }
+                *reinterpret_cast<uint4*>(wide + place(r0 + 16 * part + 2 * i)) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(w_full(sw));
+            ++hw;
+          }
+        }
+        if (did) {
+          idle = 0;
+        } else {
+          // nothing possible now: park for a while on the likeliest of the events, then look again
+          const uint32_t st = hi_ % C::NST, gi = hi_ >> 1;
+          const bool fill = !end && (MASS || hi_ - hw < C::NST);
+          if (C::WIDEN && hw < hi_) park(w_empty(hw % C::NW), ((hw / C::NW) & 1) ^ 1);
+          else if (fill && hi_ >= C::NST && !mbar_test(k_empty(st), ((hi_ / C::NST) & 1) ^ 1))
+            park(k_empty(st), ((hi_ / C::NST) & 1) ^ 1);
+          else if (fill && (hi_ & 1) == 0) park(map_full(gi % kMaps), (gi / kMaps) & 1);
+          else park(g_full(sc % kSegs), (sc / kSegs) & 1);
+          if ((++idle & 15) == 0) {
+            const uint64_t now = globaltimer_ns();
+            if (idle == 16) since = now;
+            else if (__any_sync(0xffffffffu, now - since > kWaitNs)) {
+              fail();
+              break;
+            }
+          }
+        }
       }
     } else {
-      while (more) {
-        const int64_t slot = slot_n;
-        bool stop = false;
+      for (uint32_t hs = 0;; ++hs) {
+        const uint32_t st = hs % C::NST, g = hs >> 1;
+        if (hs >= C::NST && !wait_warp(k_empty(st), ((hs / C::NST) & 1) ^ 1)) break;
+        const int h = hs & 1;
+        if (h == 0 && !wait_warp(map_full(g % kMaps), (g / kMaps) & 1)) break;
+        const int* slots = reinterpret_cast<const int*>(smem + C::MAP_OFF + (g % kMaps) * 512);
+        if (h == 0 && slots[0] == -2) break;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t hs = 2 * g + h, st = hs % C::NST;
-          if (hs >= C::NST && !wait_warp(k_empty(st), ((hs / C::NST) & 1) ^ 1)) {
-            stop = true;
-            break;
-          }
-          if (h == 0) publish(slot, scale_n);
+        for (int part = 0; part < kLoadRows / 16; ++part) {
+          int sl[8];  // read before the first copy: the copies are ordered with memory accesses
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sl[i] = slots[r0 + 16 * part + 2 * i];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int64_t sl = __shfl_sync(0xffffffffu, slot, 2 * i + hi16);
-            const int r = 16 * lw + 2 * i + hi16;
-            const uint32_t dst = sbase + C::K_OFF + st * C::HALF_BYTES + (gl >> 3) * (kBN * 128) + r * 128 +
-                                 (((gl & 7) ^ (r & 7)) << 4);
-            const uint8_t* src = p.cache + (sl >= 0 ? sl * C::RB + 256 * h + 16 * gl : 0);
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(sl >= 0 ? 16 : 0)
+            const uint32_t dst = sbase + C::K_OFF + st * C::HALF_BYTES + place(r0 + 16 * part + 2 * i);
+            const uint8_t* src = p.cache + (sl[i] >= 0 ? (int64_t)sl[i] * C::RB + 256 * h + 16 * gl : 0);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(sl[i] >= 0 ? 16 : 0)
                          : "memory");
           }
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(k_full(st)) : "memory");
-          if (h == 0) more = advance();
         }
-        if (stop) break;
-        ++g;
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(k_full(st)) : "memory");
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
     }
-    (void)ok;
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if constexpr (MASS) {
-    // ================================================= weights of a key, 16 warps ====
+    // ================================================== weights of a key, 8 warps ====
     const int qd = warp & 3, gi = warp >> 2;
     const int tr = 32 * qd + lane;
-    const uint32_t tl = tmem + ((uint32_t)(32 * qd) << 16) + gi * C::S_COLS;
     const float inv_cap2 = MODS && p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
     const float c_log2 = p.sm_scale * kLog2e;
     uint32_t g = 0;
@@ -775,12 +1008,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       if (!wait_warp(g_full(slot), (sc / kSegs) & 1)) break;
       const Seg s = segs[slot];
       if (s.type == 0) break;
-      if (s.ntiles > 0 && !wait_warp(nl_full(slot), (sc / kSegs) & 1)) break;
+      if (!wait_warp(aux_full(slot), (sc / kSegs) & 1)) break;
+      const float* sq = reinterpret_cast<const float*>(smem + C::SQ_OFF) + 128 * slot;
       const float* nl = reinterpret_cast<const float*>(smem + C::NL_OFF) + slot * kHG;
       const float* slopes = s_slopes + s.hg * kHG;
       const int64_t qp = MODS && p.qpos ? p.qpos[s.t] : (int64_t)p.lengths[s.t] - 1;
       for (int k = 0; k < s.ntiles; ++k, ++g) {
-        if ((g & 3) != (uint32_t)gi) continue;
+        if ((g & 1) != (uint32_t)gi) continue;
+        const uint32_t sb = g % C::NSB;
+        const uint32_t tl = tmem + ((uint32_t)(32 * qd) << 16) + sb * C::S_COLS;
         const uint32_t pos = (uint32_t)(s.a & ~127) + 128u * (uint32_t)(s.tile0 + k) + tr;
         const bool in = pos >= (uint32_t)s.a && pos < (uint32_t)s.b;
         float old = 0.0f, dist = 0.0f;
@@ -791,16 +1027,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
             dist = fabsf((float)(qp - kp));
           }
         }
-        if (!wait_warp(v_full(g % C::NV), (g / C::NV) & 1) || !wait_warp(s_full(gi), (g >> 2) & 1)) {
+        if (!wait_warp(map_full(g % kMaps), (g / kMaps) & 1) || !wait_warp(s_full(sb), (g / C::NSB) & 1) ||
+            (F8 && !wait_warp(v_full(g % C::NV), (g / C::NV) & 1))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const bool valid = (reinterpret_cast<const uint32_t*>(smem + C::VM_OFF + 16 * (g % C::NV))[qd] >> lane) & 1;
+        const bool valid = reinterpret_cast<const int*>(smem + C::MAP_OFF + (g % kMaps) * 512)[tr] >= 0;
         float2 scl = make_float2(1.0f, 1.0f);
         if (F8) scl = reinterpret_cast<const float2*>(smem + C::SC_OFF + 1024 * (g % C::NV))[tr];
         const float f = MODS ? p.sm_scale : c_log2;
-        const float f0 = F8 ? scl.x * f : f, f1 = scl.y * f;
         float w = 0.0f;
 #pragma unroll
         for (int ch = 0; ch < kHG / 16; ++ch) {
@@ -810,59 +1046,73 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
           tc_wait_ld();
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            float x = u2f(x0[i]) * f0;
-            if (F8) x = fmaf(u2f(x1[i]), f1, x);
+            float x;
+            if (F8) {
+              const float2 qs = *reinterpret_cast<const float2*>(sq + 2 * (16 * ch + i));
+              x = fmaf(u2f(x1[i]), scl.y * qs.y, u2f(x0[i]) * (scl.x * qs.x));
+            } else {
+              x = u2f(x0[i]) * f;
+            }
             if (MODS) x = modify(x, p.cap, inv_cap2, slopes[16 * ch + i] * dist);
             w += ex2_approx(x + nl[16 * ch + i]);
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(s_empty(gi));
+        if (lane == 0) {
+          mbar_arrive(s_empty(sb));
+          mbar_arrive(map_empty(g % kMaps));
+        }
         if (in) p.mass_out[s.req * p.mass_out_st + pos] = valid ? old + w : old;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(g_empty(slot));
     }
   } else {
-    // ==================================================== softmax and outputs, 16 warps ====
-    // Warp = lane quarter qd (keys 32 qd ..; output columns 32 qd .. of both halves), heads 16 hq ..
+    // ===================================================== softmax and outputs, 8 warps ====
+    // Warp = lane quarter qd (keys 32 qd ..; output columns 32 qd .. of the 128 of half hq), heads
+    // 32 hq .. of the scores.
     const int qd = warp & 3, hq = warp >> 2;
+    const int hb = 32 * hq;
     const int tr = 32 * qd + lane;
-    const int sid = threadIdx.x;  // 0 .. 511
+    const int sid = threadIdx.x;  // 0 .. 255
     const uint32_t tl = tmem + ((uint32_t)(32 * qd) << 16);
-    float* red = reinterpret_cast<float*>(smem + C::RED_OFF);
+    float* red = reinterpret_cast<float*>(smem + C::RED_OFF);  // -m, two buffers
     float* red_alpha = red + 128;
     float* red_part = red + 192;  // [4 quarters][64 heads]
     float* red_inv = red + 448;
-    int* votes = reinterpret_cast<int*>(smem + C::VOTE_OFF);
+    float* red_raise = red + 512;
     const float inv_cap2 = MODS && p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
     const float c_log2 = p.sm_scale * kLog2e;
-    uint32_t g = 0, xc = 0, mb = 0;
-    auto xsync = [&](bool v) -> int {
-      const int r = exchange(xbar, votes, xc++, v);
-      if (r < 0) fail();
-      return r;
+    uint32_t g = 0, mb = 0;
+    bool failed = false;  // a wait ran out: go on without waiting, and leave with the others
+    auto await = [&](uint32_t bar, uint32_t par) {
+      if (failed || __all_sync(0xffffffffu, bar_wait(bar, par))) return;
+      fail();
+      failed = true;
     };
-    auto pv_wait = [&](uint32_t last) -> bool { return wait_warp(pv_done(last & 1), (last >> 1) & 1); };
-    // O^T columns this warp handles: half oh, heads 32 * (hq & 1) ..
-    const int oh = hq >> 1, ob = 32 * (hq & 1);
-    const uint32_t o_addr = tl + C::O_COL + 64 * oh + ob;
-    bool ok = true;
-    for (uint32_t sc = 0; ok; ++sc) {
+    auto pv_wait = [&](uint32_t last) { await(pv_done(last & 1), (last >> 1) & 1); };
+    const uint32_t o_addr = tl + C::O_COL + 64 * hq;  // O^T half hq, all heads
+    for (uint32_t sc = 0;; ++sc) {
       const uint32_t slot = sc % kSegs;
-      if (!wait_warp(g_full(slot), (sc / kSegs) & 1)) break;
+      await(g_full(slot), (sc / kSegs) & 1);
+      if (F8 && !failed && segs[slot].type != 0) await(aux_full(slot), (sc / kSegs) & 1);
+      if (softmax_any(failed)) break;
       const Seg s = segs[slot];
       __syncwarp();
       if (lane == 0) mbar_arrive(g_empty(slot));
       if (s.type == 0) break;
       const int heads = min(kHG, p.H - s.hg * kHG);
-      const float* slopes = s_slopes + s.hg * kHG + 16 * hq;
+      // chunks of 16 heads in use: the weights of the others meet only unused columns of O^T
+      const int nch = max(0, min(2, (heads - hb + 15) >> 4));
+      const float* slopes = s_slopes + s.hg * kHG + hb;
+      const float* sq = reinterpret_cast<const float*>(smem + C::SQ_OFF) + 128 * slot + 2 * hb;
       int64_t qp = 0;
       if (MODS) qp = p.qpos ? p.qpos[s.t] : (int64_t)p.lengths[s.t] - 1;
-      float lsum[16];
+      float lsum[32];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) lsum[i] = 0.0f;
+      for (int i = 0; i < 32; ++i) lsum[i] = 0.0f;
+      bool fresh = true;  // no valid key so far: m counts as 0
       for (int k = 0; k < s.ntiles; ++k, ++g) {
         const uint32_t sb = g % C::NSB;
         float dist = 0.0f;
@@ -872,162 +1122,169 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
           if (p.kpos && pos >= (uint32_t)s.a && pos < (uint32_t)s.b) kp = p.kpos[s.req * p.kp_stride + pos];
           dist = fabsf((float)(qp - kp));
         }
-        if (!wait_warp(v_full(g % C::NV), (g / C::NV) & 1) || !wait_warp(s_full(sb), (g / C::NSB) & 1)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const bool valid = (reinterpret_cast<const uint32_t*>(smem + C::VM_OFF + 16 * (g % C::NV))[qd] >> lane) & 1;
+        await(map_full(g % kMaps), (g / kMaps) & 1);
+        if (F8) await(v_full(g % C::NV), (g / C::NV) & 1);
+        const bool valid = reinterpret_cast<const int*>(smem + C::MAP_OFF + (g % kMaps) * 512)[tr] >= 0;
         float2 scl = make_float2(1.0f, 1.0f);
         if (F8) scl = reinterpret_cast<const float2*>(smem + C::SC_OFF + 1024 * (g % C::NV))[tr];
-        float x[16];
-        {
+        await(s_full(sb), (g / C::NSB) & 1);
+        tc_fence_after();
+        // y = score - m, exp2 domain
+        float y[32], top = -INFINITY;
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch) {
+          if (ch >= nch) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[16 * ch + i] = -INFINITY;
+            continue;
+          }
           uint32_t x0[16], x1[16];
-          tmem_ld32_x16(tl + sb * C::S_COLS + 16 * hq, x0);
-          if (F8) tmem_ld32_x16(tl + sb * C::S_COLS + 64 + 16 * hq, x1);
+          tmem_ld32_x16(tl + sb * C::S_COLS + hb + 16 * ch, x0);
+          if (F8) tmem_ld32_x16(tl + sb * C::S_COLS + 64 + hb + 16 * ch, x1);
+          float nm[16];
+          const float* m = red + 64 * mb + hb + 16 * ch;
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            float4 v = *reinterpret_cast<const float4*>(m + i);
+            if (fresh) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            nm[i] = v.x;
+            nm[i + 1] = v.y;
+            nm[i + 2] = v.z;
+            nm[i + 3] = v.w;
+          }
           tc_wait_ld();
-          const float f = MODS ? p.sm_scale : c_log2;
-          const float f0 = F8 ? scl.x * f : f, f1 = scl.y * f;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            x[i] = u2f(x0[i]) * f0;
-            if (F8) x[i] = fmaf(u2f(x1[i]), f1, x[i]);
-            if (MODS) x[i] = modify(x[i], p.cap, inv_cap2, slopes[i] * dist);
-            if (!valid) x[i] = -INFINITY;
+            float v;
+            if (F8) {
+              const float2 qs = *reinterpret_cast<const float2*>(sq + 2 * (16 * ch + i));
+              const float2 a = __fmul2_rn(scl, qs);
+              if (MODS)
+                v = modify(fmaf(u2f(x0[i]), a.x, u2f(x1[i]) * a.y), p.cap, inv_cap2, slopes[16 * ch + i] * dist) + nm[i];
+              else
+                v = fmaf(u2f(x0[i]), a.x, fmaf(u2f(x1[i]), a.y, nm[i]));
+            } else {
+              if (MODS) v = modify(u2f(x0[i]) * p.sm_scale, p.cap, inv_cap2, slopes[16 * ch + i] * dist) + nm[i];
+              else v = fmaf(u2f(x0[i]), c_log2, nm[i]);
+            }
+            y[16 * ch + i] = valid ? v : -INFINITY;
+            top = fmaxf(top, y[16 * ch + i]);
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(s_empty(sb));
-        bool exact = k == 0;
-        if (!exact) {
-          float top = -INFINITY;
-          const float* m = red + 64 * mb + 16 * hq;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) top = fmaxf(top, x[i] - m[i]);
-          const int r = xsync(top > kStale);
-          if (r < 0) {
-            ok = false;
-            break;
-          }
-          exact = r != 0;
+        if (lane == 0) {
+          mbar_arrive(s_empty(sb));
+          mbar_arrive(map_empty(g % kMaps));
         }
+        bool exact = fresh;
+        if (!exact) exact = softmax_any(top > kStale);
         if (exact) {
           // exact maximum of the tile per head; the running maxima are raised to it
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int mx = redux_max_s32(f2ord(x[i]));
-            if (lane == i) red_part[64 * qd + 16 * hq + i] = ord2f(mx);
+          for (int i = 0; i < 32; ++i) {
+            const int mx = redux_max_s32(f2ord(y[i]));
+            if (lane == i) red_part[64 * qd + hb + i] = ord2f(mx);
           }
-          if (xsync(false) < 0) {
-            ok = false;
-            break;
-          }
+          const bool some = softmax_any(valid);
           if (sid < kHG) {
-            const float mo = k == 0 ? kNoMax : red[64 * mb + sid];
-            const float mt = fmaxf(fmaxf(red_part[sid], red_part[64 + sid]), fmaxf(red_part[128 + sid], red_part[192 + sid]));
-            const float mn = fmaxf(mo, mt);
-            red[64 * (mb ^ 1) + sid] = mn;
-            red_alpha[sid] = ex2_approx(mo - mn);
+            // relative to the m that y was taken from; a first maximum may be below it
+            const float up = fmaxf(fmaxf(red_part[sid], red_part[64 + sid]), fmaxf(red_part[128 + sid], red_part[192 + sid]));
+            const float mo = fresh ? 0.0f : -red[64 * mb + sid];
+            const float raise = fresh ? (up > kNoMax ? up : 0.0f) : fmaxf(up, 0.0f);
+            red[64 * (mb ^ 1) + sid] = -(mo + raise);
+            red_raise[sid] = raise;
+            red_alpha[sid] = ex2_approx(-raise);
           }
-          if (xsync(false) < 0) {
-            ok = false;
-            break;
-          }
+          softmax_sync();
           mb ^= 1;
-          if (k > 0) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) lsum[i] *= red_alpha[16 * hq + i];
-            if (!pv_wait(g - 1)) {
-              ok = false;
-              break;
-            }
+          for (int i = 0; i < 32; ++i) y[i] -= red_raise[hb + i];
+          if (!fresh) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) lsum[i] *= red_alpha[hb + i];
+            pv_wait(g - 1);
             tc_fence_after();
 #pragma unroll 1
-            for (int ch = 0; ch < 2; ++ch) {
+            for (int ch = 0; ch < 4; ++ch) {
               uint32_t o[16];
               tmem_ld32_x16(o_addr + 16 * ch, o);
               tc_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = f2u(u2f(o[i]) * red_alpha[ob + 16 * ch + i]);
+              for (int i = 0; i < 16; ++i) o[i] = f2u(u2f(o[i]) * red_alpha[16 * ch + i]);
               tmem_st32_x16(o_addr + 16 * ch, o);
             }
             tc_wait_st();
           }
+          fresh = fresh && !some;
         }
-        {
-          const float* m = red + 64 * mb + 16 * hq;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            x[i] = ex2_approx(x[i] - m[i]);
-            lsum[i] += x[i];
-          }
+        for (int i = 0; i < 32; ++i) {
+          if (16 * nch <= (i & 16)) continue;
+          y[i] = ex2_approx(y[i]);
+          lsum[i] += y[i];
         }
         // the weights' buffer is free once the value product that read it is complete
-        if (g >= C::PBUF && !pv_wait(g - C::PBUF)) {
-          ok = false;
-          break;
-        }
+        if (g >= C::PBUF) pv_wait(g - C::PBUF);
         uint8_t* prow = smem + C::P_OFF + (g % C::PBUF) * C::P_BYTES + tr * 128;
         const int sw = tr & 7;
 #pragma unroll
         for (int h = 0; h < C::PN; ++h) {
           const float f = F8 ? (h == 0 ? scl.x : scl.y) : 1.0f;
-          uint32_t w[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            w[i] = F8 ? f32x2_to_bf16x2(x[2 * i] * f, x[2 * i + 1] * f) : f32x2_to_bf16x2(x[2 * i], x[2 * i + 1]);
-          *reinterpret_cast<uint4*>(prow + h * (kBN * 128) + (((2 * hq) ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-          *reinterpret_cast<uint4*>(prow + h * (kBN * 128) + (((2 * hq + 1) ^ sw) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+          for (int ch = 0; ch < 2; ++ch) {
+            if (ch >= nch) continue;
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float a = y[16 * ch + 2 * i], b = y[16 * ch + 2 * i + 1];
+              w[i] = F8 ? f32x2_to_bf16x2(a * f, b * f) : f32x2_to_bf16x2(a, b);
+            }
+            const int gr = 4 * hq + 2 * ch;
+            *reinterpret_cast<uint4*>(prow + h * (kBN * 128) + ((gr ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(prow + h * (kBN * 128) + (((gr + 1) ^ sw) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
         }
-        fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full(g % C::PBUF));
       }
-      if (!ok) break;
       // ---- the segment's end: sums over the keys, then this warp's columns of O^T
       {
-        // reduce-scatter over the lanes: lanes 2i and 2i + 1 end with the warp's sum of head i
-        float v8[8], v4[4], v2[2];
-        const bool b4 = lane & 16, b3_ = lane & 8, b2_ = lane & 4, b1_ = lane & 2;
+        // reduce-scatter over the lanes: lane i ends with the warp's sum of head i
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          v8[i] = (b4 ? lsum[i + 8] : lsum[i]) + __shfl_xor_sync(0xffffffffu, b4 ? lsum[i] : lsum[i + 8], 16);
+        for (int w = 16; w > 0; w >>= 1) {
+          const bool upper = lane & w;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v4[i] = (b3_ ? v8[i + 4] : v8[i]) + __shfl_xor_sync(0xffffffffu, b3_ ? v8[i] : v8[i + 4], 8);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) v2[i] = (b2_ ? v4[i + 2] : v4[i]) + __shfl_xor_sync(0xffffffffu, b2_ ? v4[i] : v4[i + 2], 4);
-        float v1 = (b1_ ? v2[1] : v2[0]) + __shfl_xor_sync(0xffffffffu, b1_ ? v2[0] : v2[1], 2);
-        v1 += __shfl_xor_sync(0xffffffffu, v1, 1);
-        if ((lane & 1) == 0) red_part[64 * qd + 16 * hq + (lane >> 1)] = v1;
+          for (int i = 0; i < w; ++i)
+            lsum[i] = (upper ? lsum[i + w] : lsum[i]) + __shfl_xor_sync(0xffffffffu, upper ? lsum[i] : lsum[i + w], w);
+        }
+        red_part[64 * qd + hb + lane] = lsum[0];
       }
-      if (xsync(false) < 0) break;
+      softmax_sync();
       const int part = 2 * cta + (s.kind == 1 ? 1 : 0);
       if (sid < kHG) {
         const float L = (red_part[sid] + red_part[64 + sid]) + (red_part[128 + sid] + red_part[192 + sid]);
-        const float m = red[64 * mb + sid];
+        const float m = -red[64 * mb + sid];
         red_inv[sid] = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);
         if (s.kind != 0) {
-          p.ws_ml[(int64_t)part * 2 * kHG + sid] = s.ntiles > 0 ? m : kNoMax;
+          p.ws_ml[(int64_t)part * 2 * kHG + sid] = L == 0.0f ? kNoMax : m;
           p.ws_ml[(int64_t)part * 2 * kHG + kHG + sid] = L;
         } else if (p.lse && sid < heads) {
           p.lse[s.t * p.lse_st + s.hg * kHG + sid] = L == 0.0f ? -INFINITY : (m + log2f(L)) * kLn2;
         }
       }
-      if (xsync(false) < 0) break;
-      if (s.ntiles > 0 && !pv_wait(g - 1)) break;
+      softmax_sync();
+      if (s.ntiles > 0) pv_wait(g - 1);
       tc_fence_after();
-      const int dv = 128 * oh + tr;
+      const int dv = 128 * hq + tr;
       uint16_t* orow = p.out + (int64_t)s.t * p.out_st + (int64_t)s.hg * kHG * p.out_sh;
       float* prt = p.ws_o + (int64_t)part * kHG * kD + dv;
 #pragma unroll 1
-      for (int ch = 0; ch < 2; ++ch) {
-        const int h0 = ob + 16 * ch;
-        if (h0 >= heads) break;
+      for (int h0 = 0; h0 < heads; h0 += 16) {
         uint32_t o[16];
         if (s.ntiles > 0) {
-          tmem_ld32_x16(o_addr + 16 * ch, o);
+          tmem_ld32_x16(o_addr + h0, o);
           tc_wait_ld();
         } else {
 #pragma unroll
@@ -1051,9 +1308,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
           }
         }
       }
+      // (the barrier at the next segment's start keeps it from rewriting sums still being read)
       tc_fence_before();
-      // the sums and weights of this segment are read before the next one rewrites them
-      if (xsync(false) < 0) break;
     }
   }
   tc_fence_before();
@@ -1173,6 +1429,8 @@ dsa_status_t check(const dsa_paged_args_t* a, bool mass) {
   if (a->H > kMaxHeads || a->T > (1 << 24) || a->d_nope != kD || a->d_rope != 0 || a->d_v != kD)
     return DSA_ERR_UNSUPPORTED;
   if (a->T == 0) return DSA_OK;
+  // more rows than any device holds: slots fit 31 bits
+  if (a->num_slots > 0x7FFFFFFF) return DSA_ERR_UNSUPPORTED;
   if (!a->q || !a->cache || !a->lengths || a->num_slots < 0 || a->num_requests < 1) return DSA_ERR_INVALID_ARGUMENT;
   if (!a->req_of_token && a->T > a->num_requests) return DSA_ERR_INVALID_ARGUMENT;
   if (!aligned(a->q, 16) || a->q_stride_t % 8 || a->q_stride_h % 8 || a->q_stride_t < 0 || a->q_stride_h < 0)

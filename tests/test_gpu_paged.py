@@ -4,7 +4,9 @@ definitions (oracle/paged.py).
 Tolerances, per element, from the arithmetic the header states (u = 2^-24 fp32, 2^-8 bf16 half steps):
   score    d = 256 * 2^-23 * B + 2^-21 * (|cap| + |bias| + |u|), B = max_j |sm_scale| sum |q k|
            (an fp32 sum of 256 exact products in any order, one step of slack for the tensor core's
-           truncation; then a few fp32 operations, the tanh from one exponential)
+           truncation; then a few fp32 operations, the tanh from one exponential); with an FP8 cache
+           + 2^-17 |sm_scale| max |q| max_j sum |k| (the query's second e4m3 term: its smallest step
+           is 2^-9 where the tile's largest component is at least 2^7, half a step is 2^-17 of it)
   lse      d + n 2^-23 + 2^-20 (each exponential 2^-21 relative, their fp32 sum, the logarithm)
   out      2^-8 |out| (its own rounding) + 5 * 2^-8 sqrt(sum (p k)^2) (the weights rounded to bf16:
            independent errors of at most 2^-8 relative each, whose standard deviation is below
@@ -86,7 +88,10 @@ class Case:
             kp = pos if kpos is None else kpos[r][pos]
             bias = np.abs(slopes).max() * np.abs(qp - kp).max()
         umax = np.abs(u).max(axis=1) if u.shape[1] else np.zeros(self.H)
-        return u, k, pos, 256 * 2.0 ** -23 * bound + 2.0 ** -21 * (abs(cap) + bias + umax)
+        d = 256 * 2.0 ** -23 * bound + 2.0 ** -21 * (abs(cap) + bias + umax)
+        if self.kind == FP8 and len(pos):
+            d = d + 2.0 ** -17 * abs(self.sm_scale) * np.abs(P.bf16_to_f64(self.q[t])).max(axis=1) * np.abs(k).sum(1).max()
+        return u, k, pos, d
 
 
 def dev_t(x, dev):
@@ -342,6 +347,17 @@ def test_repeats_streams_and_graphs(gpu, kind):
     g1.replay()
     torch.cuda.synchronize()
     assert torch.equal(o1, ref)
+
+
+@pytest.mark.parametrize("kind", [BF16, FP8])
+def test_tiles_without_a_valid_key(gpu, kind):
+    """Whole tiles of bad pages before, between and after valid ones, scores far from zero."""
+    c = Case(gpu, kind, [1200, 5000], 24, seed=37, q_scale=20.0)
+    c.bt[0, 0:4] = -1
+    c.bt[0, 8:11] = -5
+    c.bt[1, 2:40] = -1
+    c.bt[1, 70:79] = c.cache.shape[0]
+    run_and_check(c, want_err=dsa.DEVERR_INDEX_OUT_OF_RANGE)
 
 
 def test_mass_refuses_repeated_and_unordered_requests(gpu):
