@@ -15,14 +15,16 @@
 //    the same K tile (tcgen05 kind::f16, bf16 operands, fp32 accumulators in tensor memory). A
 //    token has at most 64 heads per pass: heads as M would leave half of the tensor core idle.
 //  * FP8 rows: scores run on the e4m3 codes as they are (kind::f8f6f4), the bf16 query split into two
-//    e4m3 terms per head and 128-column tile, scaled by a power of two: hi + lo is the bf16 component
-//    for every component within 2^9 of its tile's largest. S keeps one accumulator per scale tile and
-//    the fp32 scales multiply there. The value product takes the codes widened to bf16, which is exact,
-//    and one bf16 weight matrix per scale tile, p * scale: e4m3 weights would lose what many far
-//    positions add up to beside one strong one. So the keys are the exact products code * scale.
+//    e4m3 terms per head, scaled by a power of two: hi + lo is the bf16 component for every component
+//    within 2^9 of the head's largest. S keeps one accumulator per scale tile and the fp32 scales
+//    multiply there. The value product takes the codes widened to f16, which is exact and one
+//    conversion per two codes (to bf16 it is four instructions), and one f16 weight matrix per scale
+//    tile: p * scale relative to the largest scale so far, 2^22 of normal range below the strongest
+//    position. e4m3 weights (as two terms) would need no widening but lose what many far positions add
+//    up to beside one strong one. So the keys are the exact products code * scale.
 //  * Softmax with one thread per key and 32 heads (two warps per lane quarter). The running maximum
-//    of a head is raised, and O and the sums rescaled, only when some score exceeds it by 2^20: p
-//    and its sums are floating point, so a stale maximum costs no precision, and the exact path runs
+//    of a head is raised, and O and the sums rescaled, only when some score exceeds it by 2^20 (FP8:
+//    2^6): p and its sums are floating point, so a stale maximum costs no precision, and the exact path runs
 //    for a segment's first tile and almost never again.
 //  * Persistent CTAs, one per SM. Each computes the same split from the lengths (they live on the
 //    device): rows (token, group of 64 heads) cost their 128-position tiles plus a constant, and
@@ -33,11 +35,14 @@
 //    products, 11 query loads, 12-15 row loads. Every wait is bounded.
 //    512 threads leave 128 registers each: with 16 softmax warps and 72, spills of 200 to 450 bytes a
 //    thread were more than the L1 beside the tiles holds, and a tile took 9500 cycles.
-//  * Rows go straight from global memory to their swizzled place with cp.async, so every free stage of
-//    the ring holds loads in flight and no register does. FP8: the warp that copied a row widens it
-//    into a second ring while the softmax of its tile runs.
+//  * bf16 tiles without a masked position come by TMA, in boxes of as many rows as a page and a tile
+//    share; other bf16 tiles and FP8 rows (264 bytes: no tensor map takes that pitch) by cp.async
+//    straight to their swizzled place. Either way every free stage of the ring holds loads in flight
+//    and no register does. FP8: the warp that copied a row widens it into a second ring while the
+//    softmax of its tile runs.
 //  * The mass kernel is the same without the value product: with the lse given, each key's thread
 //    adds the weights of all 64 heads; two groups of four warps take tiles in turn.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -69,7 +74,10 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -1e30f;   // running maximum before the first valid score
-constexpr float kStale = 20.0f;    // a score may exceed the running maximum by 2^20
+// A score may exceed the running maximum by 2^20; FP8: by 2^6, so that an f16 weight is at most
+// 2^(6 + kWeightShift) < 65504.
+constexpr float kStale = 20.0f, kStaleF8 = 6.0f;
+constexpr int kWeightShift = 8;
 
 // Bounded wait for the phase of the given parity. The hint lets the hardware park the warp for up to
 // a millisecond: some twenty warps wait at any time, and polling took a third of the issue slots.
@@ -112,6 +120,7 @@ struct Params {
   uint32_t pg_mul;  // x / page_size == (x * pg_mul) >> pg_shift for 0 <= x < 2^31
   int pg_shift;
   int64_t pos_limit;  // addressable positions of a request
+  int box_rows;       // bf16: rows of a TMA box (0: none, a page and a tile share fewer than eight)
   int64_t num_requests;
   const int32_t* req;
   const int32_t* starts;
@@ -175,13 +184,15 @@ struct Cfg {
   static constexpr int P_OFF = W_OFF + NW * WIDE_BYTES;
   static constexpr int SEG_OFF = P_OFF + PBUF * P_BYTES;
   static constexpr int MAP_OFF = SEG_OFF + kSegs * 64;        // [kMaps][128] slots, -1: masked
-  static constexpr int SC_OFF = MAP_OFF + kMaps * 512;        // FP8: [NV][128][2] tile scales
-  static constexpr int SQ_OFF = SC_OFF + (F8 ? NV * 1024 : 0); // FP8: [kSegs][64][2] query scales
-  static constexpr int NL_OFF = SQ_OFF + (F8 ? kSegs * 512 : 0);  // mass: [kSegs][64] -lse, exp2 domain
+  static constexpr int FULL_OFF = MAP_OFF + kMaps * 512;      // [kMaps] no position of the tile is masked
+  static constexpr int SC_OFF = FULL_OFF + kMaps * 4;        // FP8: [NV][128][2] tile scales
+  static constexpr int SQ_OFF = SC_OFF + (F8 ? NV * 1024 : 0); // FP8: [kSegs][64] query scales
+  static constexpr int NL_OFF = SQ_OFF + (F8 ? kSegs * 256 : 0);  // mass: [kSegs][64] -lse, exp2 domain
   static constexpr int SL_OFF = NL_OFF + (MASS ? kSegs * 256 : 0);  // slopes [128]
-  // -m [2][64], alpha [64], part [4][64], inverse sums [64], raise of m [64]
+  // -m [2][64], alpha [64], part [4][64], inverse sums [64], raise of m [64]; FP8: largest scales of
+  // the tile [8][2], reference scales [2][2] and their inverses [2][2]
   static constexpr int RED_OFF = SL_OFF + 512;
-  static constexpr int PLAN_OFF = RED_OFF + 9 * 256;  // block scans: 2 x kWarps int64; start row, its cost
+  static constexpr int PLAN_OFF = RED_OFF + 9 * 256 + 128;  // block scans: 2 x kWarps int64; start row, its cost
   static constexpr int BAR_OFF = PLAN_OFF + 2 * 8 * kWarps + 64;
   static constexpr int NBARS = 2 + 2 * NST + 3 * kSegs + NV + 2 * kMaps + 2 * NSB + 2 * 2 + 2 + 2 * NW;
   static constexpr int MISC_OFF = BAR_OFF + 8 * NBARS;
@@ -189,6 +200,24 @@ struct Cfg {
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
   static_assert(TMEM_USED <= 512, "TMEM budget");
 };
+
+// Instruction descriptor, kind::f16 with f16 A/B and fp32 accumulation.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn_major, int b_mn_major) {
+  return (1u << 4) | ((uint32_t)a_mn_major << 15) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t f32x2_to_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// 2-D tiled tensor load (coordinates innermost first).
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
 
 __device__ __forceinline__ void set_err(int32_t* err, int bits) {
   if (err) atomicOr(err, bits);
@@ -291,13 +320,13 @@ __device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 
 static_assert(32 * kSoftmaxWarps == 256, "the barriers' thread count");
 
 // Splits query rows h0 .. h0 + 15 of a row (zero past `heads`) into e4m3 hi and lo terms, lane l
-// columns 8 l .. 8 l + 7, per head and 128-column tile scaled by 2^-e so that the largest component
-// lies in [128, 256); sq[h][tile] = f * 2^e.
+// columns 8 l .. 8 l + 7, per head scaled by 2^-e so that the largest component lies in
+// [128, 256); sq[h] = f * 2^e.
 __device__ __forceinline__ void split_query(const uint16_t* q, int64_t q_sh, int h0, int heads, float f, uint8_t* qbuf,
                                             float* sq) {
   const int lane = threadIdx.x & 31;
   const int gl = lane & 15, tile = lane >> 4;
-#pragma unroll
+#pragma unroll 1
   for (int part = 0; part < kHG / kLoadWarps / 4; ++part) {
     uint4 v[4];
 #pragma unroll
@@ -312,8 +341,7 @@ __device__ __forceinline__ void split_query(const uint16_t* q, int64_t q_sh, int
       uint32_t a = 0u;
 #pragma unroll
       for (int j = 0; j < 4; ++j) a = max(a, max((w[j] << 16) & 0x7FFFFFFFu, w[j] & 0x7FFF0000u));
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));  // within the tile's lanes
+      a = __reduce_max_sync(0xffffffffu, a);
       int e = (int)(a >> 23) - 127 - 7;
       e = a == 0u ? 0 : (e < -126 ? -126 : e);
       const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
@@ -335,14 +363,14 @@ __device__ __forceinline__ void split_query(const uint16_t* q, int64_t q_sh, int
       *reinterpret_cast<uint2*>(d) = make_uint2(hi[0], hi[1]);
       *reinterpret_cast<uint2*>(d + 2 * kHG * 128) = make_uint2(lo[0], lo[1]);
       // an infinite or NaN component makes the head's scores NaN
-      if (gl == 0)
-        sq[2 * h + tile] = a >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : f * __uint_as_float((uint32_t)(127 + e) << 23);
+      if (lane == 0)
+        sq[h] = a >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : f * __uint_as_float((uint32_t)(127 + e) << 23);
     }
   }
 }
 
 template <int KIND, bool MASS, bool MODS>
-__global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tmap) {
   using C = Cfg<KIND, MASS>;
   constexpr bool F8 = C::F8;
   extern __shared__ uint8_t smem_raw[];
@@ -534,6 +562,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         }
         if (bad) set_err(p.err, DSA_DEVERR_INDEX_OUT_OF_RANGE);
         *dst = make_int4(sl[0], sl[1], sl[2], sl[3]);
+        const bool full = __all_sync(0xffffffffu, sl[0] >= 0 && sl[1] >= 0 && sl[2] >= 0 && sl[3] >= 0);
+        if (lane == 0) reinterpret_cast<int*>(smem + C::FULL_OFF)[g % kMaps] = full;
         // the tile's rows into L2, one request per page: the copies then wait for L2 only
         if (bt && p.page_size >= kPrefetchPage) {
           const uint32_t lo = max(base, a), hi = min(base + (uint32_t)kBN, b);
@@ -728,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
   } else if (warp == kWarpValue) {
     // ============================================================= value products ====
     if (!MASS && lane == 0) {
-      constexpr uint32_t idPV = idesc_bf16(kBN, kHG, 1, 1);
+      constexpr uint32_t idPV = F8 ? idesc_f16(kBN, kHG, 1, 1) : idesc_bf16(kBN, kHG, 1, 1);
       const uint32_t mn_hi = (uint32_t)(sw128_desc(0, kBN * 128, 1024) >> 32);
       uint32_t g = 0;
       bool ok = true;
@@ -828,9 +858,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     const int lw = warp - kWarpLoad0;
     const int gl = lane & 15, hi16 = lane >> 4;
     const int r0 = kLoadRows * lw + hi16;
-    // byte offset of row r's 16-byte granule gl in a half's two 128-byte-swizzled chunks
-    auto place = [&](int r) -> uint32_t {
-      return (uint32_t)((gl >> 3) * (kBN * 128) + r * 128 + (((gl & 7) ^ (r & 7)) << 4));
+    // byte offset of row r's 16-byte granule gl in a half's two 128-byte-swizzled chunks; the swizzle of
+    // rows r0 + 2 i repeats every four i
+    uint32_t place4[4], piece4[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = r0 + 2 * i;
+      place4[i] = (uint32_t)((gl >> 3) * (kBN * 128) + r * 128 + (((gl & 7) ^ (r & 7)) << 4));
+      // FP8: of the lane's 8-byte piece of row r in a half as stored
+      piece4[i] = (uint32_t)(r * 128 + (((gl >> 1) ^ (r & 7)) << 4) + 8 * (gl & 1));
+    }
+    // The warp's rows of a tile: the lane's own row's slot, and, when all 32 follow one another, the
+    // first one's (else -1).
+    auto rows_of = [&](uint32_t tile, int& own) -> int {
+      own = reinterpret_cast<const int*>(smem + C::MAP_OFF + (tile % kMaps) * 512)[kLoadRows * lw + lane];
+      const int first = __shfl_sync(0xffffffffu, own, 0);
+      return __all_sync(0xffffffffu, first >= 0 && own == first + lane) ? first : -1;
     };
     if constexpr (F8) {
       // Three kinds of work, taken as they become possible: the split of a segment's query (16 heads
@@ -839,13 +882,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       uint32_t hi_ = 0, hw = 0;  // halves copied, halves widened
       uint32_t sc = 0, qn = 0;   // segments seen, queries split
       bool end = false, q_end = false;
+      int own = -1, first = -1;  // slots of the tile being copied
       uint32_t idle = 0;
       uint64_t since = 0;
       auto test = [&](uint32_t bar, uint32_t par) -> bool { return __all_sync(0xffffffffu, mbar_test(bar, par)); };
-      // byte offset of the lane's piece of row r in a half as stored
-      auto piece = [&](int r) -> uint32_t {
-        return (uint32_t)(r * 128 + (((gl >> 1) ^ (r & 7)) << 4) + 8 * (gl & 1));
-      };
       while (!(end && q_end && (MASS || hw == hi_))) {
         bool did = false;
         if (!end && (MASS || hi_ - hw < C::NST)) {
@@ -855,32 +895,34 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
           if (go && h == 0) go = test(map_full(gi % kMaps), (gi / kMaps) & 1);
           if (go) {
             did = true;
-            const int* slots = reinterpret_cast<const int*>(smem + C::MAP_OFF + (gi % kMaps) * 512);
-            if (h == 0 && slots[0] == -2) {
+            if (h == 0) first = rows_of(gi, own);
+            if (h == 0 && own == -2) {
               end = true;
             } else {
               if (h == 0) {
                 // the two scales of this lane's row
-                const int r = kLoadRows * lw + lane;
-                const int sl = slots[r];
-                const uint32_t dst = sbase + C::SC_OFF + 1024 * (gi % C::NV) + 8 * r;
+                const uint32_t dst = sbase + C::SC_OFF + 1024 * (gi % C::NV) + 8 * (kLoadRows * lw + lane);
                 asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst),
-                             "l"(p.cache + (sl >= 0 ? (int64_t)sl * C::RB + 256 : 0)), "r"(sl >= 0 ? 8 : 0)
+                             "l"(p.cache + (own >= 0 ? (int64_t)own * C::RB + 256 : 0)), "r"(own >= 0 ? 8 : 0)
                              : "memory");
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(v_full(gi % C::NV)) : "memory");
               }
               const uint32_t dst = sbase + C::K_OFF + st * C::HALF_BYTES;
+              if (first >= 0) {
+                const uint8_t* src = p.cache + (int64_t)(first + hi16) * C::RB + 128 * h + 8 * gl;
 #pragma unroll
-              for (int part = 0; part < kLoadRows / 16; ++part) {
-                int sl[8];  // read before the first copy: the copies are ordered with memory accesses
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sl[i] = slots[r0 + 16 * part + 2 * i];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst + piece(r0 + 16 * part + 2 * i)),
-                               "l"(p.cache + (sl[i] >= 0 ? (int64_t)sl[i] * C::RB + 128 * h + 8 * gl : 0)),
-                               "r"(sl[i] >= 0 ? 8 : 0)
+                for (int i = 0; i < kLoadRows / 2; ++i)
+                  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst + piece4[i & 3] + 1024 * (i >> 2)),
+                               "l"(src + 2 * C::RB * i)
                                : "memory");
+              } else {
+#pragma unroll 4
+                for (int i = 0; i < kLoadRows / 2; ++i) {
+                  const int sl = __shfl_sync(0xffffffffu, own, 2 * i + hi16);
+                  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst + piece4[i & 3] + 1024 * (i >> 2)),
+                               "l"(p.cache + (sl >= 0 ? (int64_t)sl * C::RB + 128 * h + 8 * gl : 0)), "r"(sl >= 0 ? 8 : 0)
+                               : "memory");
+                }
               }
               asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(k_full(st)) : "memory");
               asm volatile("cp.async.commit_group;" ::: "memory");
@@ -899,7 +941,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
               const int heads = min(kHG, p.H - s.hg * kHG);
               split_query(p.q + (int64_t)s.t * p.q_st + (int64_t)s.hg * kHG * p.q_sh, p.q_sh, kHG / kLoadWarps * lw, heads,
                           MODS ? p.sm_scale : p.sm_scale * kLog2e, smem + C::Q_OFF,
-                          reinterpret_cast<float*>(smem + C::SQ_OFF) + 128 * slot);
+                          reinterpret_cast<float*>(smem + C::SQ_OFF) + kHG * slot);
               ++qn;
             }
             __syncwarp();
@@ -929,20 +971,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
             for (int part = 0; part < kLoadRows / 16; ++part) {
               uint2 v[8];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint2*>(raw + piece(r0 + 16 * part + 2 * i));
+              for (int i = 0; i < 8; ++i)
+                v[i] = *reinterpret_cast<const uint2*>(raw + piece4[i & 3] + 1024 * (i >> 2) + 2048 * part);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const uint32_t c[2] = {v[i].x, v[i].y};
-                uint32_t w[4];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  const float2 a = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)(c[j] & 0xFFFFu)));
-                  const float2 b = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)(c[j] >> 16)));
-                  w[2 * j] = f32x2_to_bf16x2(a.x, a.y);
-                  w[2 * j + 1] = f32x2_to_bf16x2(b.x, b.y);
-                }
-                *reinterpret_cast<uint4*>(wide + place(r0 + 16 * part + 2 * i)) = make_uint4(w[0], w[1], w[2], w[3]);
-              }
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4*>(wide + place4[i & 3] + 1024 * (i >> 2) + 2048 * part) =
+                    make_uint4(e4m3x2_to_f16x2((uint16_t)v[i].x), e4m3x2_to_f16x2((uint16_t)(v[i].x >> 16)),
+                               e4m3x2_to_f16x2((uint16_t)v[i].y), e4m3x2_to_f16x2((uint16_t)(v[i].y >> 16)));
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(w_full(sw));
@@ -971,27 +1006,51 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         }
       }
     } else {
+      int own = -1, first = -1;
+      bool boxes = false;
       for (uint32_t hs = 0;; ++hs) {
         const uint32_t st = hs % C::NST, g = hs >> 1;
         if (hs >= C::NST && !wait_warp(k_empty(st), ((hs / C::NST) & 1) ^ 1)) break;
         const int h = hs & 1;
-        if (h == 0 && !wait_warp(map_full(g % kMaps), (g / kMaps) & 1)) break;
-        const int* slots = reinterpret_cast<const int*>(smem + C::MAP_OFF + (g % kMaps) * 512);
-        if (h == 0 && slots[0] == -2) break;
-#pragma unroll
-        for (int part = 0; part < kLoadRows / 16; ++part) {
-          int sl[8];  // read before the first copy: the copies are ordered with memory accesses
-#pragma unroll
-          for (int i = 0; i < 8; ++i) sl[i] = slots[r0 + 16 * part + 2 * i];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t dst = sbase + C::K_OFF + st * C::HALF_BYTES + place(r0 + 16 * part + 2 * i);
-            const uint8_t* src = p.cache + (sl[i] >= 0 ? (int64_t)sl[i] * C::RB + 256 * h + 16 * gl : 0);
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(sl[i] >= 0 ? 16 : 0)
-                         : "memory");
-          }
+        if (h == 0) {
+          if (!wait_warp(map_full(g % kMaps), (g / kMaps) & 1)) break;
+          first = rows_of(g, own);
+          if (own == -2) break;
+          boxes = p.box_rows > 0 && reinterpret_cast<const int*>(smem + C::FULL_OFF)[g % kMaps];
         }
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(k_full(st)) : "memory");
+        const uint32_t dst = sbase + C::K_OFF + st * C::HALF_BYTES;
+        if (boxes) {
+          // boxes of 64 columns x box_rows rows, a box by the warp its first row belongs to
+          const int per = p.box_rows < kLoadRows ? kLoadRows / p.box_rows : 1;
+          const bool mine = (kLoadRows * lw) % p.box_rows == 0 || p.box_rows < kLoadRows;
+          const int bytes = p.box_rows * 128;
+          if (mine && lane == 0) mbar_arrive_expect_tx(k_full(st), 2 * per * bytes);
+          else mbar_arrive(k_full(st));
+          __syncwarp();
+          if (mine && lane < 2 * per) {
+            const int c = lane / per, r = (lane % per) * p.box_rows;
+            const int y = reinterpret_cast<const int*>(smem + C::MAP_OFF + (g % kMaps) * 512)[kLoadRows * lw + r];
+            tma_load_2d(dst + c * (kBN * 128) + (kLoadRows * lw + r) * 128, &tmap, 128 * h + 64 * c, y, k_full(st));
+          }
+        } else {
+          if (first >= 0) {
+            const uint8_t* src = p.cache + (int64_t)(first + hi16) * C::RB + 256 * h + 16 * gl;
+#pragma unroll
+            for (int i = 0; i < kLoadRows / 2; ++i)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + place4[i & 3] + 1024 * (i >> 2)),
+                           "l"(src + 2 * C::RB * i)
+                           : "memory");
+          } else {
+#pragma unroll 4
+            for (int i = 0; i < kLoadRows / 2; ++i) {
+              const int sl = __shfl_sync(0xffffffffu, own, 2 * i + hi16);
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + place4[i & 3] + 1024 * (i >> 2)),
+                           "l"(p.cache + (sl >= 0 ? (int64_t)sl * C::RB + 256 * h + 16 * gl : 0)), "r"(sl >= 0 ? 16 : 0)
+                           : "memory");
+            }
+          }
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(k_full(st)) : "memory");
+        }
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -1009,7 +1068,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       const Seg s = segs[slot];
       if (s.type == 0) break;
       if (!wait_warp(aux_full(slot), (sc / kSegs) & 1)) break;
-      const float* sq = reinterpret_cast<const float*>(smem + C::SQ_OFF) + 128 * slot;
+      const float* sq = reinterpret_cast<const float*>(smem + C::SQ_OFF) + kHG * slot;
+      const int heads = min(kHG, p.H - s.hg * kHG);
       const float* nl = reinterpret_cast<const float*>(smem + C::NL_OFF) + slot * kHG;
       const float* slopes = s_slopes + s.hg * kHG;
       const int64_t qp = MODS && p.qpos ? p.qpos[s.t] : (int64_t)p.lengths[s.t] - 1;
@@ -1037,26 +1097,34 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         float2 scl = make_float2(1.0f, 1.0f);
         if (F8) scl = reinterpret_cast<const float2*>(smem + C::SC_OFF + 1024 * (g % C::NV))[tr];
         const float f = MODS ? p.sm_scale : c_log2;
-        float w = 0.0f;
-#pragma unroll
-        for (int ch = 0; ch < kHG / 16; ++ch) {
+        const float2 s0 = make_float2(scl.x, scl.x), s1 = make_float2(scl.y, scl.y), f2 = make_float2(f, f);
+        float2 w2 = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+        for (int ch = 0; ch < (heads + 15) >> 4; ++ch) {
           uint32_t x0[16], x1[16];
           tmem_ld32_x16(tl + 16 * ch, x0);
           if (F8) tmem_ld32_x16(tl + 64 + 16 * ch, x1);
           tc_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float x;
+          for (int i = 0; i < 16; i += 2) {
+            const float2 n = *reinterpret_cast<const float2*>(nl + 16 * ch + i);
+            float2 x = make_float2(u2f(x0[i]), u2f(x0[i + 1]));
+            float2 q = f2;
             if (F8) {
-              const float2 qs = *reinterpret_cast<const float2*>(sq + 2 * (16 * ch + i));
-              x = fmaf(u2f(x1[i]), scl.y * qs.y, u2f(x0[i]) * (scl.x * qs.x));
-            } else {
-              x = u2f(x0[i]) * f;
+              x = __ffma2_rn(make_float2(u2f(x1[i]), u2f(x1[i + 1])), s1, __fmul2_rn(x, s0));
+              q = *reinterpret_cast<const float2*>(sq + 16 * ch + i);
             }
-            if (MODS) x = modify(x, p.cap, inv_cap2, slopes[16 * ch + i] * dist);
-            w += ex2_approx(x + nl[16 * ch + i]);
+            if (MODS) {
+              x = __fmul2_rn(x, q);
+              x.x = modify(x.x, p.cap, inv_cap2, slopes[16 * ch + i] * dist) + n.x;
+              x.y = modify(x.y, p.cap, inv_cap2, slopes[16 * ch + i + 1] * dist) + n.y;
+            } else {
+              x = __ffma2_rn(x, q, n);
+            }
+            w2 = __fadd2_rn(w2, make_float2(ex2_approx(x.x), ex2_approx(x.y)));
           }
         }
+        const float w = w2.x + w2.y;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -1082,6 +1150,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     float* red_part = red + 192;  // [4 quarters][64 heads]
     float* red_inv = red + 448;
     float* red_raise = red + 512;
+    float* red_sc = red + 576;   // FP8: largest |scale| of the tile, [8 warps][2]
+    float* red_ref = red + 592;  // FP8: [2 buffers][2] reference scales (powers of two)
+    float* red_wf = red + 596;   // FP8: [2 buffers][2] 2^kWeightShift / reference
     const float inv_cap2 = MODS && p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
     const float c_log2 = p.sm_scale * kLog2e;
     uint32_t g = 0, mb = 0;
@@ -1106,13 +1177,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       // chunks of 16 heads in use: the weights of the others meet only unused columns of O^T
       const int nch = max(0, min(2, (heads - hb + 15) >> 4));
       const float* slopes = s_slopes + s.hg * kHG + hb;
-      const float* sq = reinterpret_cast<const float*>(smem + C::SQ_OFF) + 128 * slot + 2 * hb;
+      const float* sq = reinterpret_cast<const float*>(smem + C::SQ_OFF) + kHG * slot + hb;
       int64_t qp = 0;
       if (MODS) qp = p.qpos ? p.qpos[s.t] : (int64_t)p.lengths[s.t] - 1;
-      float lsum[32];
+      float2 lsum[16];  // heads 2 i, 2 i + 1 of the warp
 #pragma unroll
-      for (int i = 0; i < 32; ++i) lsum[i] = 0.0f;
-      bool fresh = true;  // no valid key so far: m counts as 0
+      for (int i = 0; i < 16; ++i) lsum[i] = make_float2(0.0f, 0.0f);
+      bool fresh = true;  // no valid key so far: m counts as 0, no reference scale
       for (int k = 0; k < s.ntiles; ++k, ++g) {
         const uint32_t sb = g % C::NSB;
         float dist = 0.0f;
@@ -1125,50 +1196,53 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         await(map_full(g % kMaps), (g / kMaps) & 1);
         if (F8) await(v_full(g % C::NV), (g / C::NV) & 1);
         const bool valid = reinterpret_cast<const int*>(smem + C::MAP_OFF + (g % kMaps) * 512)[tr] >= 0;
-        float2 scl = make_float2(1.0f, 1.0f);
+        float2 scl = make_float2(0.0f, 0.0f);
         if (F8) scl = reinterpret_cast<const float2*>(smem + C::SC_OFF + 1024 * (g % C::NV))[tr];
         await(s_full(sb), (g / C::NSB) & 1);
         tc_fence_after();
         // y = score - m, exp2 domain
-        float y[32], top = -INFINITY;
+        float2 y[16];
+        float top = -INFINITY;
+        const float f = MODS ? p.sm_scale : c_log2;
+        const float2 s0 = make_float2(scl.x, scl.x), s1 = make_float2(scl.y, scl.y), f2 = make_float2(f, f);
+        const float* m = red + 64 * mb + hb;
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch) {
-          if (ch >= nch) {
+          if (ch < nch) {
+            uint32_t x0[16], x1[16];
+            tmem_ld32_x16(tl + sb * C::S_COLS + hb + 16 * ch, x0);
+            if (F8) tmem_ld32_x16(tl + sb * C::S_COLS + 64 + hb + 16 * ch, x1);
+            tc_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) y[16 * ch + i] = -INFINITY;
-            continue;
-          }
-          uint32_t x0[16], x1[16];
-          tmem_ld32_x16(tl + sb * C::S_COLS + hb + 16 * ch, x0);
-          if (F8) tmem_ld32_x16(tl + sb * C::S_COLS + 64 + hb + 16 * ch, x1);
-          float nm[16];
-          const float* m = red + 64 * mb + hb + 16 * ch;
-#pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            float4 v = *reinterpret_cast<const float4*>(m + i);
-            if (fresh) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            nm[i] = v.x;
-            nm[i + 1] = v.y;
-            nm[i + 2] = v.z;
-            nm[i + 3] = v.w;
-          }
-          tc_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float v;
-            if (F8) {
-              const float2 qs = *reinterpret_cast<const float2*>(sq + 2 * (16 * ch + i));
-              const float2 a = __fmul2_rn(scl, qs);
-              if (MODS)
-                v = modify(fmaf(u2f(x0[i]), a.x, u2f(x1[i]) * a.y), p.cap, inv_cap2, slopes[16 * ch + i] * dist) + nm[i];
-              else
-                v = fmaf(u2f(x0[i]), a.x, fmaf(u2f(x1[i]), a.y, nm[i]));
-            } else {
-              if (MODS) v = modify(u2f(x0[i]) * p.sm_scale, p.cap, inv_cap2, slopes[16 * ch + i] * dist) + nm[i];
-              else v = fmaf(u2f(x0[i]), c_log2, nm[i]);
+            for (int i = 0; i < 16; i += 2) {
+              float2 n = *reinterpret_cast<const float2*>(m + 16 * ch + i);
+              if (fresh) n = make_float2(0.0f, 0.0f);
+              float2 x = make_float2(u2f(x0[i]), u2f(x0[i + 1]));
+              float2 q = f2;
+              if (F8) {
+                x = __ffma2_rn(make_float2(u2f(x1[i]), u2f(x1[i + 1])), s1, __fmul2_rn(x, s0));
+                q = *reinterpret_cast<const float2*>(sq + 16 * ch + i);
+              }
+              if (MODS) {
+                x = __fmul2_rn(x, q);
+                x.x = modify(x.x, p.cap, inv_cap2, slopes[16 * ch + i] * dist) + n.x;
+                x.y = modify(x.y, p.cap, inv_cap2, slopes[16 * ch + i + 1] * dist) + n.y;
+              } else {
+                x = __ffma2_rn(x, q, n);
+              }
+              y[8 * ch + i / 2] = x;
+              top = fmaxf(top, fmaxf(x.x, x.y));
             }
-            y[16 * ch + i] = valid ? v : -INFINITY;
-            top = fmaxf(top, y[16 * ch + i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[8 * ch + i] = make_float2(-INFINITY, -INFINITY);
+          }
+        }
+        if (__any_sync(0xffffffffu, !valid)) {
+          if (!valid) {
+            top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] = make_float2(-INFINITY, -INFINITY);
           }
         }
         tc_fence_before();
@@ -1178,13 +1252,28 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
           mbar_arrive(map_empty(g % kMaps));
         }
         bool exact = fresh;
-        if (!exact) exact = softmax_any(top > kStale);
+        if (!exact) {
+          bool stale = top > (F8 ? kStaleF8 : kStale);
+          if (F8) stale = stale || fabsf(scl.x) > red_ref[2 * mb] || fabsf(scl.y) > red_ref[2 * mb + 1];
+          exact = softmax_any(stale);
+        }
+        float rescale = 1.0f;  // FP8: of this warp's half of O^T, beside the heads' factors
         if (exact) {
           // exact maximum of the tile per head; the running maxima are raised to it
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int mx = redux_max_s32(f2ord(y[i]));
-            if (lane == i) red_part[64 * qd + hb + i] = ord2f(mx);
+          for (int i = 0; i < 16; ++i) {
+            const int m0 = redux_max_s32(f2ord(y[i].x)), m1 = redux_max_s32(f2ord(y[i].y));
+            if (lane == 2 * i) red_part[64 * qd + hb + 2 * i] = ord2f(m0);
+            if (lane == 2 * i + 1) red_part[64 * qd + hb + 2 * i + 1] = ord2f(m1);
+          }
+          if (F8) {
+            // magnitudes order like their bits
+            const uint32_t a0 = __reduce_max_sync(0xffffffffu, f2u(fabsf(scl.x)));
+            const uint32_t a1 = __reduce_max_sync(0xffffffffu, f2u(fabsf(scl.y)));
+            if (lane == 0) {
+              red_sc[2 * warp] = u2f(a0);
+              red_sc[2 * warp + 1] = u2f(a1);
+            }
           }
           const bool some = softmax_any(valid);
           if (sid < kHG) {
@@ -1195,14 +1284,30 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
             red[64 * (mb ^ 1) + sid] = -(mo + raise);
             red_raise[sid] = raise;
             red_alpha[sid] = ex2_approx(-raise);
+          } else if (F8 && sid < kHG + 2) {
+            const int t = sid - kHG;
+            float top_sc = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) top_sc = fmaxf(top_sc, red_sc[2 * w + t]);  // warps 0 - 3: all keys
+            // the power of two at or above it, 2^-100 at least: its inverse is finite
+            uint32_t e = (f2u(top_sc) + 0x7FFFFFu) >> 23;
+            e = e < 27u ? 27u : (e > 254u ? 254u : e);
+            const float old = fresh ? 0.0f : red_ref[2 * mb + t];
+            const float ref = fmaxf(old, u2f(e << 23));
+            red_ref[2 * (mb ^ 1) + t] = ref;
+            red_wf[2 * (mb ^ 1) + t] = (float)(1 << kWeightShift) / ref;
           }
           softmax_sync();
+          if (F8 && !fresh) rescale = red_ref[2 * mb + hq] / red_ref[2 * (mb ^ 1) + hq];
           mb ^= 1;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) y[i] -= red_raise[hb + i];
+          for (int i = 0; i < 16; ++i) {
+            const float2 up = *reinterpret_cast<const float2*>(red_raise + hb + 2 * i);
+            y[i] = make_float2(y[i].x - up.x, y[i].y - up.y);
+          }
           if (!fresh) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) lsum[i] *= red_alpha[hb + i];
+            for (int i = 0; i < 16; ++i) lsum[i] = __fmul2_rn(lsum[i], *reinterpret_cast<const float2*>(red_alpha + hb + 2 * i));
             pv_wait(g - 1);
             tc_fence_after();
 #pragma unroll 1
@@ -1211,38 +1316,50 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
               tmem_ld32_x16(o_addr + 16 * ch, o);
               tc_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = f2u(u2f(o[i]) * red_alpha[16 * ch + i]);
+              for (int i = 0; i < 16; ++i) o[i] = f2u(u2f(o[i]) * (red_alpha[16 * ch + i] * rescale));
               tmem_st32_x16(o_addr + 16 * ch, o);
             }
             tc_wait_st();
           }
           fresh = fresh && !some;
         }
+        float2 wf = make_float2(1.0f, 1.0f);  // FP8: the key's scales relative to the references
+        if (F8) wf = __fmul2_rn(scl, *reinterpret_cast<const float2*>(red_wf + 2 * mb));
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          if (16 * nch <= (i & 16)) continue;
-          y[i] = ex2_approx(y[i]);
-          lsum[i] += y[i];
+        for (int ch = 0; ch < 2; ++ch) {
+          if (ch < nch) {
+#pragma unroll
+            for (int i = 8 * ch; i < 8 * ch + 8; ++i) {
+              y[i] = make_float2(ex2_approx(y[i].x), ex2_approx(y[i].y));
+              lsum[i] = __fadd2_rn(lsum[i], y[i]);
+            }
+          }
         }
         // the weights' buffer is free once the value product that read it is complete
         if (g >= C::PBUF) pv_wait(g - C::PBUF);
         uint8_t* prow = smem + C::P_OFF + (g % C::PBUF) * C::P_BYTES + tr * 128;
         const int sw = tr & 7;
 #pragma unroll
-        for (int h = 0; h < C::PN; ++h) {
-          const float f = F8 ? (h == 0 ? scl.x : scl.y) : 1.0f;
+        for (int ch = 0; ch < 2; ++ch) {
+          if (ch < nch) {
 #pragma unroll
-          for (int ch = 0; ch < 2; ++ch) {
-            if (ch >= nch) continue;
-            uint32_t w[8];
+            for (int h = 0; h < C::PN; ++h) {
+              uint32_t w[8];
+              const float wh = h == 0 ? wf.x : wf.y;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float a = y[16 * ch + 2 * i], b = y[16 * ch + 2 * i + 1];
-              w[i] = F8 ? f32x2_to_bf16x2(a * f, b * f) : f32x2_to_bf16x2(a, b);
+              for (int i = 0; i < 8; ++i) {
+                if (F8) {
+                  const float2 v = __fmul2_rn(y[8 * ch + i], make_float2(wh, wh));
+                  w[i] = f32x2_to_f16x2(v.x, v.y);
+                } else {
+                  w[i] = f32x2_to_bf16x2(y[8 * ch + i].x, y[8 * ch + i].y);
+                }
+              }
+              uint8_t* d = prow + h * (kBN * 128);
+              const int gr = 4 * hq + 2 * ch;
+              *reinterpret_cast<uint4*>(d + ((gr ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(d + (((gr + 1) ^ sw) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
             }
-            const int gr = 4 * hq + 2 * ch;
-            *reinterpret_cast<uint4*>(prow + h * (kBN * 128) + ((gr ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4*>(prow + h * (kBN * 128) + (((gr + 1) ^ sw) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
           }
         }
         tc_fence_before();
@@ -1252,14 +1369,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       // ---- the segment's end: sums over the keys, then this warp's columns of O^T
       {
         // reduce-scatter over the lanes: lane i ends with the warp's sum of head i
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          v[2 * i] = lsum[i].x;
+          v[2 * i + 1] = lsum[i].y;
+        }
 #pragma unroll
         for (int w = 16; w > 0; w >>= 1) {
           const bool upper = lane & w;
 #pragma unroll
           for (int i = 0; i < w; ++i)
-            lsum[i] = (upper ? lsum[i + w] : lsum[i]) + __shfl_xor_sync(0xffffffffu, upper ? lsum[i] : lsum[i + w], w);
+            v[i] = (upper ? v[i + w] : v[i]) + __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[i + w], w);
         }
-        red_part[64 * qd + hb + lane] = lsum[0];
+        red_part[64 * qd + hb + lane] = v[0];
       }
       softmax_sync();
       const int part = 2 * cta + (s.kind == 1 ? 1 : 0);
@@ -1277,6 +1400,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       softmax_sync();
       if (s.ntiles > 0) pv_wait(g - 1);
       tc_fence_after();
+      // FP8: weights were relative to the half's reference scale
+      const float back = F8 && !fresh ? red_ref[2 * mb + hq] * (1.0f / (1 << kWeightShift)) : 1.0f;
       const int dv = 128 * hq + tr;
       uint16_t* orow = p.out + (int64_t)s.t * p.out_st + (int64_t)s.hg * kHG * p.out_sh;
       float* prt = p.ws_o + (int64_t)part * kHG * kD + dv;
@@ -1293,13 +1418,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         if (s.kind != 0) {
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (h0 + i < heads) prt[(h0 + i) * kD] = u2f(o[i]);
+            if (h0 + i < heads) prt[(h0 + i) * kD] = u2f(o[i]) * back;
         } else {
           // lanes 2i and 2i + 1 hold neighbouring columns: they swap heads, so that each writes
           // two columns of one head
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float e = u2f(o[2 * i]) * red_inv[h0 + 2 * i], f = u2f(o[2 * i + 1]) * red_inv[h0 + 2 * i + 1];
+            const float e = u2f(o[2 * i]) * back * red_inv[h0 + 2 * i];
+            const float f = u2f(o[2 * i + 1]) * back * red_inv[h0 + 2 * i + 1];
             const bool odd = lane & 1;
             const float other = __shfl_xor_sync(0xffffffffu, odd ? e : f, 1);
             const uint32_t w = odd ? f32x2_to_bf16x2(other, f) : f32x2_to_bf16x2(e, other);
@@ -1514,18 +1640,64 @@ int grid_of(const Params& p, const DeviceInfo& dev) {
   return (int)(most < sms ? most : sms);
 }
 
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// 2-D map over the bf16 rows, box 64 columns x p->box_rows rows, 128-byte swizzle: the K-major layout
+// the products read. box_rows is what a page and a tile share, a power of two; the swizzle repeats
+// every eight rows, so smaller shares go without a map.
+dsa_status_t encode_rows(Params* p, CUtensorMap* map) {
+  int box = kBN;
+  if (p->bt)
+    while (p->page_size % box) box >>= 1;
+  p->box_rows = 0;
+  if (box < 8 || p->num_slots < box) return DSA_OK;
+  static std::mutex mu;
+  static EncodeFn fn = nullptr;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!fn) {
+      void* f = nullptr;
+      cudaDriverEntryPointQueryResult qres;
+      const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &qres);
+      if (e != cudaSuccess) return cuda_fail(e);
+      if (!f || qres != cudaDriverEntryPointSuccess) return cuda_fail(cudaErrorSymbolNotFound);
+      fn = reinterpret_cast<EncodeFn>(f);
+    }
+  }
+  const cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)p->num_slots};
+  const cuuint64_t strides[1] = {(cuuint64_t)kD * 2};
+  const cuuint32_t boxes[2] = {64, (cuuint32_t)box};
+  const cuuint32_t es[2] = {1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint8_t*>(p->cache), dims, strides, boxes, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
+  p->box_rows = box;
+  return DSA_OK;
+}
+
 template <int KIND, bool MASS, bool MODS>
-cudaError_t launch_one(const Params& p, cudaStream_t s) {
-  paged_kernel<KIND, MASS, MODS><<<(unsigned)p.G, kThreads, Cfg<KIND, MASS>::SMEM_BYTES, s>>>(p);
+cudaError_t launch_one(const Params& p, const CUtensorMap& map, cudaStream_t s) {
+  paged_kernel<KIND, MASS, MODS><<<(unsigned)p.G, kThreads, Cfg<KIND, MASS>::SMEM_BYTES, s>>>(p, map);
   return cudaGetLastError();
 }
 
 template <bool MASS>
-cudaError_t launch(const Params& p, int kind, cudaStream_t s) {
+dsa_status_t launch(Params p, int kind, cudaStream_t s) {
   const bool mods = p.cap > 0.0f || p.slopes;
-  if (kind == DSA_CACHE_BF16)
-    return mods ? launch_one<DSA_CACHE_BF16, MASS, true>(p, s) : launch_one<DSA_CACHE_BF16, MASS, false>(p, s);
-  return mods ? launch_one<DSA_CACHE_FP8_SCALED, MASS, true>(p, s) : launch_one<DSA_CACHE_FP8_SCALED, MASS, false>(p, s);
+  CUtensorMap map{};
+  cudaError_t e;
+  if (kind == DSA_CACHE_BF16) {
+    const dsa_status_t st = encode_rows(&p, &map);
+    if (st != DSA_OK) return st;
+    e = mods ? launch_one<DSA_CACHE_BF16, MASS, true>(p, map, s) : launch_one<DSA_CACHE_BF16, MASS, false>(p, map, s);
+  } else {
+    e = mods ? launch_one<DSA_CACHE_FP8_SCALED, MASS, true>(p, map, s)
+             : launch_one<DSA_CACHE_FP8_SCALED, MASS, false>(p, map, s);
+  }
+  return e == cudaSuccess ? DSA_OK : cuda_fail(e);
 }
 
 template <int KIND, bool MASS, bool MODS>
@@ -1586,8 +1758,7 @@ extern "C" dsa_status_t dsa_paged_attn(const dsa_paged_args_t* a, void* stream) 
   p.ws_first = reinterpret_cast<int*>(ws + w.first);
   if ((st = paged::prepare_kernels(dev.device)) != DSA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = paged::launch<false>(p, a->kind, s);
-  if (e != cudaSuccess) return cuda_fail(e);
+  if ((st = paged::launch<false>(p, a->kind, s)) != DSA_OK) return st;
   if (p.G == 1) return DSA_OK;  // no border, nothing to join
   // the join's blocks: a row (or CTA) each, its heads over as many blocks as fill the device
   const int64_t nrows = p.T * p.HG;
@@ -1603,7 +1774,7 @@ extern "C" dsa_status_t dsa_paged_attn(const dsa_paged_args_t* a, void* stream) 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, paged::join_kernel, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged::join_kernel, p);
   return e == cudaSuccess ? DSA_OK : cuda_fail(e);
 }
 
@@ -1632,8 +1803,7 @@ extern "C" dsa_status_t dsa_paged_attn_mass(const dsa_paged_args_t* a, const flo
     p.lse = a->lse + h;
     p.slopes = a->slopes ? a->slopes + h : nullptr;
     p.H = a->H - h < paged::kHG ? a->H - h : paged::kHG;
-    const cudaError_t e = paged::launch<true>(p, a->kind, static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return cuda_fail(e);
+    if ((st = paged::launch<true>(p, a->kind, static_cast<cudaStream_t>(stream))) != DSA_OK) return st;
     p.mass = mass_out;
     p.mass_st = mass_out_stride;
   }

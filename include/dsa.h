@@ -299,11 +299,11 @@ DSA_API dsa_status_t dsa_proj_gemm(const void* x_codes, const void* x_scales, co
  * mask over several tokens of a request is lengths[t].
  * Arithmetic: keys are exact (bf16 as stored; FP8 code * tile scale, the codes exact in the
  * products and the fp32 scales applied to the fp32 accumulators); with an FP8 cache the bf16 query
- * enters as two e4m3 terms per head and 128-column tile (a power-of-two scale each; exact for every
- * component within 2^9 of the tile's largest, and within 2^-17 of the largest otherwise); scores,
- * softmax statistics and sums in fp32; the probabilities (FP8: times the key's tile scale) enter the
- * value product as bf16. Results are bit-identical across repeated calls with the same inputs on
- * one device.
+ * enters as two e4m3 terms per head (a power-of-two scale each; exact for every component within 2^9
+ * of the head's largest, and within 2^-17 of the largest otherwise); scores, softmax statistics and
+ * sums in fp32; the probabilities enter the value product as bf16 (FP8: times the key's tile scale,
+ * relative to the largest so far, as f16: 11 bits down to 2^-22 of the largest weight). Results are
+ * bit-identical across repeated calls with the same inputs on one device.
  */
 typedef struct dsa_paged_args {
   const void* q;                 /* bf16 [T, H, 256], 16-byte aligned, strides multiples of 8 */

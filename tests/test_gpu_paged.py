@@ -6,7 +6,7 @@ Tolerances, per element, from the arithmetic the header states (u = 2^-24 fp32, 
            (an fp32 sum of 256 exact products in any order, one step of slack for the tensor core's
            truncation; then a few fp32 operations, the tanh from one exponential); with an FP8 cache
            + 2^-17 |sm_scale| max |q| max_j sum |k| (the query's second e4m3 term: its smallest step
-           is 2^-9 where the tile's largest component is at least 2^7, half a step is 2^-17 of it)
+           is 2^-9 where the head's largest component is at least 2^7, half a step is 2^-17 of it)
   lse      d + n 2^-23 + 2^-20 (each exponential 2^-21 relative, their fp32 sum, the logarithm)
   out      2^-8 |out| (its own rounding) + 5 * 2^-8 sqrt(sum (p k)^2) (the weights rounded to bf16:
            independent errors of at most 2^-8 relative each, whose standard deviation is below
