@@ -22,7 +22,7 @@
 //    tile: p * scale relative to the largest scale so far, 2^22 of normal range below the strongest
 //    position. e4m3 weights (as two terms) would need no widening but lose what many far positions add
 //    up to beside one strong one. So the keys are the exact products code * scale.
-//  * Softmax with one thread per key and 32 heads (two warps per lane quarter). The running maximum
+//  * Softmax with one thread per key and 16 heads (four warps per lane quarter). The running maximum
 //    of a head is raised, and O and the sums rescaled, only when some score exceeds it by 2^20 (FP8:
 //    2^6): p and its sums are floating point, so a stale maximum costs no precision, and the exact path runs
 //    for a segment's first tile and almost never again.
@@ -30,18 +30,20 @@
 //    device): rows (token, group of 64 heads) cost their 128-position tiles plus a constant, and
 //    CTA c takes the c-th of G equal parts of the total. A row cut by a border leaves unnormalised
 //    parts in the workspace, which a second, dependent launch joins in the order of the parts.
-//  * Warp roles: 0-7 softmax, 8 scheduler (walks the CTA's rows, finds the slots of each tile's
-//    positions and prefetches them into L2, up to eight tiles ahead), 9 score products, 10 value
-//    products, 11 query loads, 12-15 row loads. Every wait is bounded.
-//    512 threads leave 128 registers each: with 16 softmax warps and 72, spills of 200 to 450 bytes a
-//    thread were more than the L1 beside the tiles holds, and a tile took 9500 cycles.
+//  * Warp roles: 0-15 softmax, 16 scheduler (walks the CTA's rows, finds the slots of each tile's
+//    positions and prefetches them into L2, up to eight tiles ahead), 17 score products, 18 value
+//    products, 19 query loads, 20-23 row loads, 24-27 FP8: query split and widening. Every wait is
+//    bounded. A warp of such a kernel issues about every sixth cycle whatever its role, so the time
+//    of a tile is the instructions a warp spends on it: hence sixteen softmax warps of 16 heads each,
+//    one job per warp and no polling between jobs. The registers are split anew after the start (a
+//    spill would leave the L1 that the tiles leave over: a tile took 9500 cycles with spills).
 //  * bf16 tiles without a masked position come by TMA, in boxes of as many rows as a page and a tile
 //    share; other bf16 tiles and FP8 rows (264 bytes: no tensor map takes that pitch) by cp.async
 //    straight to their swizzled place. Either way every free stage of the ring holds loads in flight
-//    and no register does. FP8: the warp that copied a row widens it into a second ring while the
-//    softmax of its tile runs.
+//    and no register does. FP8: other warps widen the rows into a second ring while the softmax
+//    of their tile runs.
 //  * The mass kernel is the same without the value product: with the lse given, each key's thread
-//    adds the weights of all 64 heads; two groups of four warps take tiles in turn.
+//    adds the weights of all 64 heads; four groups of four warps take tiles in turn.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -59,11 +61,11 @@ constexpr int kD = 256;
 constexpr int kMaxHeads = 128;
 constexpr int kHG = 64;    // heads per row (MMA N)
 constexpr int kBN = 128;   // positions per tile (MMA M)
-constexpr int kSoftmaxWarps = 8;
-constexpr int kWarpSched = 8, kWarpScore = 9, kWarpValue = 10, kWarpQuery = 11, kWarpLoad0 = 12;
-constexpr int kLoadWarps = 4;
+constexpr int kSoftmaxWarps = 16;
+constexpr int kWarpSched = 16, kWarpScore = 17, kWarpValue = 18, kWarpQuery = 19, kWarpLoad0 = 20, kWarpWiden0 = 24;
+constexpr int kLoadWarps = 4, kWidenWarps = 4;
 constexpr int kLoadRows = kBN / kLoadWarps;
-constexpr int kWarps = kWarpLoad0 + kLoadWarps;
+constexpr int kWarps = kWarpWiden0 + kWidenWarps;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCtas = 192;      // the join's lists
 constexpr int kSegs = 8;           // segment ring depth
@@ -97,7 +99,7 @@ __device__ __forceinline__ void park(uint32_t bar, uint32_t parity) {
                "r"(parity), "r"(500u)
                : "memory");
 }
-static __device__ __noinline__ bool bar_wait_retry(uint32_t bar, uint32_t parity) {
+static __device__ __forceinline__ bool bar_wait_retry(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = globaltimer_ns();
   while (!try_wait_parked(bar, parity))
     if (globaltimer_ns() - t0 > kWaitNs) return false;
@@ -310,16 +312,16 @@ static_assert(kWarps <= 32, "one lane per warp in the block scans");
 __device__ __forceinline__ bool softmax_any(bool v) {
   uint32_t r;
   asm volatile(
-      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.or.pred q, 1, 256, p;\nselp.u32 %0, 1, 0, q;\n}"
+      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.or.pred q, 1, 512, p;\nselp.u32 %0, 1, 0, q;\n}"
       : "=r"(r)
       : "r"((uint32_t)v)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
-static_assert(32 * kSoftmaxWarps == 256, "the barriers' thread count");
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 512;" ::: "memory"); }
+static_assert(32 * kSoftmaxWarps == 512, "the barriers' thread count");
 
-// Splits query rows h0 .. h0 + 15 of a row (zero past `heads`) into e4m3 hi and lo terms, lane l
+// Splits query rows h0 .. of a widening warp's share of a row (zero past `heads`) into e4m3 hi and lo terms, lane l
 // columns 8 l .. 8 l + 7, per head scaled by 2^-e so that the largest component lies in
 // [128, 256); sq[h] = f * 2^e.
 __device__ __forceinline__ void split_query(const uint16_t* q, int64_t q_sh, int h0, int heads, float f, uint8_t* qbuf,
@@ -327,7 +329,7 @@ __device__ __forceinline__ void split_query(const uint16_t* q, int64_t q_sh, int
   const int lane = threadIdx.x & 31;
   const int gl = lane & 15, tile = lane >> 4;
 #pragma unroll 1
-  for (int part = 0; part < kHG / kLoadWarps / 4; ++part) {
+  for (int part = 0; part < kHG / kWidenWarps / 4; ++part) {
     uint4 v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -407,17 +409,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
 
   asm volatile("griddepcontrol.launch_dependents;");
   if (threadIdx.x == 0) {
-    mbar_init(q_full, F8 ? kLoadWarps : 32);  // bf16: one asynchronous arrival per thread
+    mbar_init(q_full, F8 ? kWidenWarps : 32);  // bf16: one asynchronous arrival per thread
     mbar_init(q_empty, 1);
     for (int s = 0; s < C::NST; ++s) {
       mbar_init(k_full(s), 32 * kLoadWarps);  // one asynchronous arrival per thread
-      mbar_init(k_empty(s), 1);
+      mbar_init(k_empty(s), 1 + (C::WIDEN ? kWidenWarps : 0));  // the last product to read it, the widening
     }
     for (int s = 0; s < kSegs; ++s) {
       mbar_init(g_full(s), 1);
-      // softmax warps, score issuer, value issuer, query warp, FP8: load warps
-      mbar_init(g_empty(s), kSoftmaxWarps + 1 + (MASS ? 0 : 1) + (C::WIDEN ? 0 : 1) + (F8 ? kLoadWarps : 0));
-      mbar_init(aux_full(s), (MASS ? 1 : 0) + (F8 ? kLoadWarps : 0) + (!MASS && !F8 ? 1 : 0));
+      // softmax warps, score issuer, value issuer, query warp, FP8: widening warps
+      mbar_init(g_empty(s), kSoftmaxWarps + 1 + (MASS ? 0 : 1) + (C::WIDEN ? 0 : 1) + (F8 ? kWidenWarps : 0));
+      mbar_init(aux_full(s), (MASS ? 1 : 0) + (F8 ? kWidenWarps : 0) + (!MASS && !F8 ? 1 : 0));
     }
     for (int s = 0; s < C::NV; ++s) mbar_init(v_full(s), 32 * kLoadWarps);
     for (int s = 0; s < kMaps; ++s) {
@@ -434,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       mbar_init(drain(s), 1);
     }
     for (int s = 0; s < C::NW; ++s) {
-      mbar_init(w_full(s), kLoadWarps);
+      mbar_init(w_full(s), kWidenWarps);
       mbar_init(w_empty(s), 1);
     }
     *abort_flag = 0;
@@ -518,6 +520,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     return false;
   };
 
+  // 896 threads x 72 registers at launch; 512 x 80 + 384 x 56 is within that total. (No function is
+  // called from here on: ptxas allocates past the launch's 72 only without calls.)
+  static_assert(32 * kWarps * 72 >= 512 * 80 + 384 * 56 && 32 * kWarps == 896, "register split");
+  if (warp >= kSoftmaxWarps) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (warp == kWarpSched) {
     // ================================================================== scheduler ====
     uint32_t sc = 0;
@@ -851,211 +858,160 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       if (lane == 0) mbar_arrive(g_empty(slot));
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp >= kWarpLoad0) {
+  } else if (warp < kWarpWiden0) {
     // ================================================================== row loads ====
-    // Warp w takes rows 32 w .. 32 w + 31 of every tile, in two column halves; the 16 lanes of a half
-    // warp share a row.
+    // Warp w takes rows 32 w .. 32 w + 31 of every tile, in two column halves; by cp.async the 16 lanes of
+    // a half warp share a row.
     const int lw = warp - kWarpLoad0;
     const int gl = lane & 15, hi16 = lane >> 4;
     const int r0 = kLoadRows * lw + hi16;
-    // byte offset of row r's 16-byte granule gl in a half's two 128-byte-swizzled chunks; the swizzle of
-    // rows r0 + 2 i repeats every four i
-    uint32_t place4[4], piece4[4];
+    // byte offset of the lane's piece (16 bytes; FP8: 8) of row r0 + 2 i in a half as stored: rows of
+    // 128 bytes, 16-byte granules swizzled by the row, which repeats every four i
+    uint32_t piece[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = r0 + 2 * i;
-      place4[i] = (uint32_t)((gl >> 3) * (kBN * 128) + r * 128 + (((gl & 7) ^ (r & 7)) << 4));
-      // FP8: of the lane's 8-byte piece of row r in a half as stored
-      piece4[i] = (uint32_t)(r * 128 + (((gl >> 1) ^ (r & 7)) << 4) + 8 * (gl & 1));
+      piece[i] = F8 ? (uint32_t)(r * 128 + (((gl >> 1) ^ (r & 7)) << 4) + 8 * (gl & 1))
+                    : (uint32_t)((gl >> 3) * (kBN * 128) + r * 128 + (((gl & 7) ^ (r & 7)) << 4));
     }
-    // The warp's rows of a tile: the lane's own row's slot, and, when all 32 follow one another, the
-    // first one's (else -1).
-    auto rows_of = [&](uint32_t tile, int& own) -> int {
-      own = reinterpret_cast<const int*>(smem + C::MAP_OFF + (tile % kMaps) * 512)[kLoadRows * lw + lane];
+    constexpr int PIECE = F8 ? 8 : 16, HALF_ROW = F8 ? 128 : 256;
+    for (uint32_t g = 0;; ++g) {
+      if (!wait_warp(map_full(g % kMaps), (g / kMaps) & 1)) break;
+      const int own = reinterpret_cast<const int*>(smem + C::MAP_OFF + (g % kMaps) * 512)[kLoadRows * lw + lane];
+      if (__any_sync(0xffffffffu, own == -2)) break;
       const int first = __shfl_sync(0xffffffffu, own, 0);
-      return __all_sync(0xffffffffu, first >= 0 && own == first + lane) ? first : -1;
-    };
-    if constexpr (F8) {
-      // Three kinds of work, taken as they become possible: the split of a segment's query (16 heads
-      // per warp), the copy of a half into a free stage, and the widening of a half that has
-      // landed. A lane widens the 8-byte pieces it copied. Copies come first, so they run ahead.
-      uint32_t hi_ = 0, hw = 0;  // halves copied, halves widened
-      uint32_t sc = 0, qn = 0;   // segments seen, queries split
-      bool end = false, q_end = false;
-      int own = -1, first = -1;  // slots of the tile being copied
-      uint32_t idle = 0;
-      uint64_t since = 0;
-      auto test = [&](uint32_t bar, uint32_t par) -> bool { return __all_sync(0xffffffffu, mbar_test(bar, par)); };
-      while (!(end && q_end && (MASS || hw == hi_))) {
-        bool did = false;
-        if (!end && (MASS || hi_ - hw < C::NST)) {
-          const uint32_t st = hi_ % C::NST, gi = hi_ >> 1;
-          const int h = hi_ & 1;
-          bool go = hi_ < C::NST || test(k_empty(st), ((hi_ / C::NST) & 1) ^ 1);
-          if (go && h == 0) go = test(map_full(gi % kMaps), (gi / kMaps) & 1);
-          if (go) {
-            did = true;
-            if (h == 0) first = rows_of(gi, own);
-            if (h == 0 && own == -2) {
-              end = true;
-            } else {
-              if (h == 0) {
-                // the two scales of this lane's row
-                const uint32_t dst = sbase + C::SC_OFF + 1024 * (gi % C::NV) + 8 * (kLoadRows * lw + lane);
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst),
-                             "l"(p.cache + (own >= 0 ? (int64_t)own * C::RB + 256 : 0)), "r"(own >= 0 ? 8 : 0)
-                             : "memory");
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(v_full(gi % C::NV)) : "memory");
-              }
-              const uint32_t dst = sbase + C::K_OFF + st * C::HALF_BYTES;
-              if (first >= 0) {
-                const uint8_t* src = p.cache + (int64_t)(first + hi16) * C::RB + 128 * h + 8 * gl;
-#pragma unroll
-                for (int i = 0; i < kLoadRows / 2; ++i)
-                  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst + piece4[i & 3] + 1024 * (i >> 2)),
-                               "l"(src + 2 * C::RB * i)
-                               : "memory");
-              } else {
-#pragma unroll 4
-                for (int i = 0; i < kLoadRows / 2; ++i) {
-                  const int sl = __shfl_sync(0xffffffffu, own, 2 * i + hi16);
-                  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst + piece4[i & 3] + 1024 * (i >> 2)),
-                               "l"(p.cache + (sl >= 0 ? (int64_t)sl * C::RB + 128 * h + 8 * gl : 0)), "r"(sl >= 0 ? 8 : 0)
-                               : "memory");
-                }
-              }
-              asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(k_full(st)) : "memory");
-              asm volatile("cp.async.commit_group;" ::: "memory");
-              ++hi_;
-            }
-          }
+      const bool run = __all_sync(0xffffffffu, first >= 0 && own == first + lane);  // rows that follow one another
+      const bool boxes = !F8 && p.box_rows > 0 && reinterpret_cast<const int*>(smem + C::FULL_OFF)[g % kMaps];
+      bool stop = false;
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t hs = 2 * g + h, st = hs % C::NST;
+        if (hs >= C::NST && !wait_warp(k_empty(st), ((hs / C::NST) & 1) ^ 1)) {
+          stop = true;
+          break;
         }
-        if (!did && !q_end && test(g_full(sc % kSegs), (sc / kSegs) & 1)) {
-          const uint32_t slot = sc % kSegs;
-          const Seg& s = segs[slot];
-          if (s.type == 0) {
-            q_end = did = true;
-          } else if (s.ntiles == 0 || qn == 0 || test(q_empty, (qn - 1) & 1)) {
-            did = true;
-            if (s.ntiles > 0) {
-              const int heads = min(kHG, p.H - s.hg * kHG);
-              split_query(p.q + (int64_t)s.t * p.q_st + (int64_t)s.hg * kHG * p.q_sh, p.q_sh, kHG / kLoadWarps * lw, heads,
-                          MODS ? p.sm_scale : p.sm_scale * kLog2e, smem + C::Q_OFF,
-                          reinterpret_cast<float*>(smem + C::SQ_OFF) + kHG * slot);
-              ++qn;
-            }
-            __syncwarp();
-            if (lane == 0) {
-              if (s.ntiles > 0) mbar_arrive(q_full);
-              mbar_arrive(aux_full(slot));
-              mbar_arrive(g_empty(slot));
-            }
-            __syncwarp();
-            ++sc;
-          }
-        }
-        if constexpr (C::WIDEN) {
-          const uint32_t sw = hw % C::NW;
-          if (!did && hw < hi_ && (hw < C::NW || test(w_empty(sw), ((hw / C::NW) & 1) ^ 1))) {
-            did = true;
-            // the copies of the halves after it may still be in flight
-            const uint32_t ahead = hi_ - hw - 1;
-            if (ahead == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
-            else if (ahead == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-            else if (ahead == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
-            else if (ahead == 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
-            else asm volatile("cp.async.wait_group 4;" ::: "memory");
-            const uint8_t* raw = smem + C::K_OFF + (hw % C::NST) * C::HALF_BYTES;
-            uint8_t* wide = smem + C::W_OFF + sw * C::WIDE_BYTES;
-#pragma unroll
-            for (int part = 0; part < kLoadRows / 16; ++part) {
-              uint2 v[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                v[i] = *reinterpret_cast<const uint2*>(raw + piece4[i & 3] + 1024 * (i >> 2) + 2048 * part);
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint4*>(wide + place4[i & 3] + 1024 * (i >> 2) + 2048 * part) =
-                    make_uint4(e4m3x2_to_f16x2((uint16_t)v[i].x), e4m3x2_to_f16x2((uint16_t)(v[i].x >> 16)),
-                               e4m3x2_to_f16x2((uint16_t)v[i].y), e4m3x2_to_f16x2((uint16_t)(v[i].y >> 16)));
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(w_full(sw));
-            ++hw;
-          }
-        }
-        if (did) {
-          idle = 0;
-        } else {
-          // nothing possible now: park for a while on the likeliest of the events, then look again
-          const uint32_t st = hi_ % C::NST, gi = hi_ >> 1;
-          const bool fill = !end && (MASS || hi_ - hw < C::NST);
-          if (C::WIDEN && hw < hi_) park(w_empty(hw % C::NW), ((hw / C::NW) & 1) ^ 1);
-          else if (fill && hi_ >= C::NST && !mbar_test(k_empty(st), ((hi_ / C::NST) & 1) ^ 1))
-            park(k_empty(st), ((hi_ / C::NST) & 1) ^ 1);
-          else if (fill && (hi_ & 1) == 0) park(map_full(gi % kMaps), (gi / kMaps) & 1);
-          else park(g_full(sc % kSegs), (sc / kSegs) & 1);
-          if ((++idle & 15) == 0) {
-            const uint64_t now = globaltimer_ns();
-            if (idle == 16) since = now;
-            else if (__any_sync(0xffffffffu, now - since > kWaitNs)) {
-              fail();
-              break;
-            }
-          }
-        }
-      }
-    } else {
-      int own = -1, first = -1;
-      bool boxes = false;
-      for (uint32_t hs = 0;; ++hs) {
-        const uint32_t st = hs % C::NST, g = hs >> 1;
-        if (hs >= C::NST && !wait_warp(k_empty(st), ((hs / C::NST) & 1) ^ 1)) break;
-        const int h = hs & 1;
-        if (h == 0) {
-          if (!wait_warp(map_full(g % kMaps), (g / kMaps) & 1)) break;
-          first = rows_of(g, own);
-          if (own == -2) break;
-          boxes = p.box_rows > 0 && reinterpret_cast<const int*>(smem + C::FULL_OFF)[g % kMaps];
+        if (F8 && h == 0) {
+          // the two scales of the lane's row
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(sbase + C::SC_OFF + 1024 * (g % C::NV) +
+                                                                            8 * (kLoadRows * lw + lane)),
+                       "l"(p.cache + (own >= 0 ? (int64_t)own * C::RB + 256 : 0)), "r"(own >= 0 ? 8 : 0)
+                       : "memory");
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(v_full(g % C::NV)) : "memory");
         }
         const uint32_t dst = sbase + C::K_OFF + st * C::HALF_BYTES;
         if (boxes) {
           // boxes of 64 columns x box_rows rows, a box by the warp its first row belongs to
           const int per = p.box_rows < kLoadRows ? kLoadRows / p.box_rows : 1;
-          const bool mine = (kLoadRows * lw) % p.box_rows == 0 || p.box_rows < kLoadRows;
-          const int bytes = p.box_rows * 128;
-          if (mine && lane == 0) mbar_arrive_expect_tx(k_full(st), 2 * per * bytes);
+          const bool mine = p.box_rows < kLoadRows || (kLoadRows * lw) % p.box_rows == 0;
+          if (mine && lane == 0) mbar_arrive_expect_tx(k_full(st), 2 * per * p.box_rows * 128);
           else mbar_arrive(k_full(st));
           __syncwarp();
-          if (mine && lane < 2 * per) {
-            const int c = lane / per, r = (lane % per) * p.box_rows;
-            const int y = reinterpret_cast<const int*>(smem + C::MAP_OFF + (g % kMaps) * 512)[kLoadRows * lw + r];
+          const int c = lane & 1, r = (lane >> 1) * p.box_rows;
+          const int y = __shfl_sync(0xffffffffu, own, r & 31);
+          if (mine && lane < 2 * per)
             tma_load_2d(dst + c * (kBN * 128) + (kLoadRows * lw + r) * 128, &tmap, 128 * h + 64 * c, y, k_full(st));
-          }
-        } else {
-          if (first >= 0) {
-            const uint8_t* src = p.cache + (int64_t)(first + hi16) * C::RB + 256 * h + 16 * gl;
+          continue;
+        }
+        if (run) {
+          const uint8_t* src = p.cache + (int64_t)(first + hi16) * C::RB + HALF_ROW * h + PIECE * gl;
 #pragma unroll
-            for (int i = 0; i < kLoadRows / 2; ++i)
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + place4[i & 3] + 1024 * (i >> 2)),
+          for (int i = 0; i < kLoadRows / 2; ++i) {
+            if constexpr (F8)
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst + piece[i & 3] + 1024 * (i >> 2)),
                            "l"(src + 2 * C::RB * i)
                            : "memory");
-          } else {
-#pragma unroll 4
-            for (int i = 0; i < kLoadRows / 2; ++i) {
-              const int sl = __shfl_sync(0xffffffffu, own, 2 * i + hi16);
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + place4[i & 3] + 1024 * (i >> 2)),
-                           "l"(p.cache + (sl >= 0 ? (int64_t)sl * C::RB + 256 * h + 16 * gl : 0)), "r"(sl >= 0 ? 16 : 0)
+            else
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + piece[i & 3] + 1024 * (i >> 2)),
+                           "l"(src + 2 * C::RB * i)
                            : "memory");
-            }
           }
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(k_full(st)) : "memory");
+        } else {
+#pragma unroll 4
+          for (int i = 0; i < kLoadRows / 2; ++i) {
+            const int sl = __shfl_sync(0xffffffffu, own, 2 * i + hi16);
+            const uint8_t* src = p.cache + (sl >= 0 ? (int64_t)sl * C::RB + HALF_ROW * h + PIECE * gl : 0);
+            if constexpr (F8)
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst + piece[i & 3] + 1024 * (i >> 2)),
+                           "l"(src), "r"(sl >= 0 ? 8 : 0)
+                           : "memory");
+            else
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + piece[i & 3] + 1024 * (i >> 2)),
+                           "l"(src), "r"(sl >= 0 ? 16 : 0)
+                           : "memory");
+          }
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(k_full(st)) : "memory");
+      }
+      if (stop) break;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if constexpr (F8) {
+    // ================================================= FP8: query split and widening ====
+    // Warp w splits heads 16 w .. of a segment's query, then widens rows 32 w .. 32 w + 31 of its tiles.
+    const int ww = warp - kWarpWiden0;
+    const int gl = lane & 15, r0 = 32 * ww + (lane >> 4);
+    uint32_t from[4], to[4];  // offsets of row r0 + 2 i's piece as stored, and of its 16-byte granule widened
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = r0 + 2 * i;
+      from[i] = (uint32_t)(r * 128 + (((gl >> 1) ^ (r & 7)) << 4) + 8 * (gl & 1));
+      to[i] = (uint32_t)((gl >> 3) * (kBN * 128) + r * 128 + (((gl & 7) ^ (r & 7)) << 4));
+    }
+    uint32_t hs = 0, qn = 0;  // halves widened, queries split
+    bool ok = true;
+    for (uint32_t sc = 0; ok; ++sc) {
+      const uint32_t slot = sc % kSegs;
+      if (!wait_warp(g_full(slot), (sc / kSegs) & 1)) break;
+      const Seg s = segs[slot];
+      if (s.type == 0) break;
+      if (s.ntiles > 0) {
+        if (qn > 0 && !wait_warp(q_empty, (qn - 1) & 1)) break;
+        ++qn;
+        split_query(p.q + (int64_t)s.t * p.q_st + (int64_t)s.hg * kHG * p.q_sh, p.q_sh, kHG / kWidenWarps * ww,
+                    min(kHG, p.H - s.hg * kHG), MODS ? p.sm_scale : p.sm_scale * kLog2e, smem + C::Q_OFF,
+                    reinterpret_cast<float*>(smem + C::SQ_OFF) + kHG * slot);
+      }
+      __syncwarp();
+      if (lane == 0) {
+        if (s.ntiles > 0) mbar_arrive(q_full);
+        mbar_arrive(aux_full(slot));
+        mbar_arrive(g_empty(slot));
+      }
+      if constexpr (C::WIDEN) {
+        const uint32_t end = hs + 2 * (uint32_t)s.ntiles;
+        for (; hs < end; ++hs) {
+          const uint32_t st = hs % C::NST, sw = hs % C::NW;
+          if (!wait_warp(k_full(st), (hs / C::NST) & 1) ||
+              (hs >= C::NW && !wait_warp(w_empty(sw), ((hs / C::NW) & 1) ^ 1))) {
+            ok = false;
+            break;
+          }
+          const uint8_t* raw = smem + C::K_OFF + st * C::HALF_BYTES;
+          uint8_t* wide = smem + C::W_OFF + sw * C::WIDE_BYTES;
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            uint2 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint2*>(raw + from[i & 3] + 1024 * (i >> 2) + 2048 * part);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(wide + to[i & 3] + 1024 * (i >> 2) + 2048 * part) =
+                  make_uint4(e4m3x2_to_f16x2((uint16_t)v[i].x), e4m3x2_to_f16x2((uint16_t)(v[i].x >> 16)),
+                             e4m3x2_to_f16x2((uint16_t)v[i].y), e4m3x2_to_f16x2((uint16_t)(v[i].y >> 16)));
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(w_full(sw));
+            mbar_arrive(k_empty(st));
+          }
         }
       }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if constexpr (MASS) {
-    // ================================================== weights of a key, 8 warps ====
+  }
+  } else {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
+  if constexpr (MASS) {
+    // ================================================= weights of a key, 16 warps ====
     const int qd = warp & 3, gi = warp >> 2;
     const int tr = 32 * qd + lane;
     const float inv_cap2 = MODS && p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
@@ -1074,7 +1030,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       const float* slopes = s_slopes + s.hg * kHG;
       const int64_t qp = MODS && p.qpos ? p.qpos[s.t] : (int64_t)p.lengths[s.t] - 1;
       for (int k = 0; k < s.ntiles; ++k, ++g) {
-        if ((g & 1) != (uint32_t)gi) continue;
+        if ((g & 3) != (uint32_t)gi) continue;
         const uint32_t sb = g % C::NSB;
         const uint32_t tl = tmem + ((uint32_t)(32 * qd) << 16) + sb * C::S_COLS;
         const uint32_t pos = (uint32_t)(s.a & ~127) + 128u * (uint32_t)(s.tile0 + k) + tr;
@@ -1137,20 +1093,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       if (lane == 0) mbar_arrive(g_empty(slot));
     }
   } else {
-    // ===================================================== softmax and outputs, 8 warps ====
-    // Warp = lane quarter qd (keys 32 qd ..; output columns 32 qd .. of the 128 of half hq), heads
-    // 32 hq .. of the scores.
+    // ==================================================== softmax and outputs, 16 warps ====
+    // Warp = lane quarter qd (keys 32 qd ..; output columns 32 qd .. of the 128 of half oh), heads
+    // 16 hq .. of the scores, 32 (hq & 1) .. of the output.
     const int qd = warp & 3, hq = warp >> 2;
-    const int hb = 32 * hq;
+    const int hb = 16 * hq, oh = hq >> 1, ob = 32 * (hq & 1);
     const int tr = 32 * qd + lane;
-    const int sid = threadIdx.x;  // 0 .. 255
+    const int sid = threadIdx.x;  // 0 .. 511
     const uint32_t tl = tmem + ((uint32_t)(32 * qd) << 16);
     float* red = reinterpret_cast<float*>(smem + C::RED_OFF);  // -m, two buffers
     float* red_alpha = red + 128;
     float* red_part = red + 192;  // [4 quarters][64 heads]
     float* red_inv = red + 448;
     float* red_raise = red + 512;
-    float* red_sc = red + 576;   // FP8: largest |scale| of the tile, [8 warps][2]
+    float* red_sc = red + 576;   // FP8: largest |scale| of the tile, [4 quarters][2]
     float* red_ref = red + 592;  // FP8: [2 buffers][2] reference scales (powers of two)
     float* red_wf = red + 596;   // FP8: [2 buffers][2] 2^kWeightShift / reference
     const float inv_cap2 = MODS && p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
@@ -1163,7 +1119,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       failed = true;
     };
     auto pv_wait = [&](uint32_t last) { await(pv_done(last & 1), (last >> 1) & 1); };
-    const uint32_t o_addr = tl + C::O_COL + 64 * hq;  // O^T half hq, all heads
+    const uint32_t o_addr = tl + C::O_COL + 64 * oh + ob;
+    // -m of a segment without a valid key so far is 0
+    if (sid < kHG) red[sid] = 0.0f;
     for (uint32_t sc = 0;; ++sc) {
       const uint32_t slot = sc % kSegs;
       await(g_full(slot), (sc / kSegs) & 1);
@@ -1174,15 +1132,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       if (lane == 0) mbar_arrive(g_empty(slot));
       if (s.type == 0) break;
       const int heads = min(kHG, p.H - s.hg * kHG);
-      // chunks of 16 heads in use: the weights of the others meet only unused columns of O^T
-      const int nch = max(0, min(2, (heads - hb + 15) >> 4));
+      const bool used = hb < heads;  // (the weights of unused heads meet only unused columns of O^T)
       const float* slopes = s_slopes + s.hg * kHG + hb;
       const float* sq = reinterpret_cast<const float*>(smem + C::SQ_OFF) + kHG * slot + hb;
       int64_t qp = 0;
       if (MODS) qp = p.qpos ? p.qpos[s.t] : (int64_t)p.lengths[s.t] - 1;
-      float2 lsum[16];  // heads 2 i, 2 i + 1 of the warp
+      float2 lsum[8];  // heads 2 i, 2 i + 1 of the warp
 #pragma unroll
-      for (int i = 0; i < 16; ++i) lsum[i] = make_float2(0.0f, 0.0f);
+      for (int i = 0; i < 8; ++i) lsum[i] = make_float2(0.0f, 0.0f);
       bool fresh = true;  // no valid key so far: m counts as 0, no reference scale
       for (int k = 0; k < s.ntiles; ++k, ++g) {
         const uint32_t sb = g % C::NSB;
@@ -1201,48 +1158,52 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         await(s_full(sb), (g / C::NSB) & 1);
         tc_fence_after();
         // y = score - m, exp2 domain
-        float2 y[16];
+        float2 y[8];
         float top = -INFINITY;
-        const float f = MODS ? p.sm_scale : c_log2;
-        const float2 s0 = make_float2(scl.x, scl.x), s1 = make_float2(scl.y, scl.y), f2 = make_float2(f, f);
-        const float* m = red + 64 * mb + hb;
+        if (used) {
+          uint32_t x0[16], x1[16];
+          tmem_ld32_x16(tl + sb * C::S_COLS + hb, x0);
+          if (F8) tmem_ld32_x16(tl + sb * C::S_COLS + 64 + hb, x1);
+          const float f = MODS ? p.sm_scale : c_log2;
+          const float2 s0 = make_float2(scl.x, scl.x), s1 = make_float2(scl.y, scl.y), f2 = make_float2(f, f);
+          const float* m = red + 64 * mb + hb;
+          tc_wait_ld();
 #pragma unroll
-        for (int ch = 0; ch < 2; ++ch) {
-          if (ch < nch) {
-            uint32_t x0[16], x1[16];
-            tmem_ld32_x16(tl + sb * C::S_COLS + hb + 16 * ch, x0);
-            if (F8) tmem_ld32_x16(tl + sb * C::S_COLS + 64 + hb + 16 * ch, x1);
-            tc_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              float2 n = *reinterpret_cast<const float2*>(m + 16 * ch + i);
-              if (fresh) n = make_float2(0.0f, 0.0f);
-              float2 x = make_float2(u2f(x0[i]), u2f(x0[i + 1]));
-              float2 q = f2;
-              if (F8) {
-                x = __ffma2_rn(make_float2(u2f(x1[i]), u2f(x1[i + 1])), s1, __fmul2_rn(x, s0));
-                q = *reinterpret_cast<const float2*>(sq + 16 * ch + i);
-              }
-              if (MODS) {
-                x = __fmul2_rn(x, q);
-                x.x = modify(x.x, p.cap, inv_cap2, slopes[16 * ch + i] * dist) + n.x;
-                x.y = modify(x.y, p.cap, inv_cap2, slopes[16 * ch + i + 1] * dist) + n.y;
-              } else {
-                x = __ffma2_rn(x, q, n);
-              }
-              y[8 * ch + i / 2] = x;
-              top = fmaxf(top, fmaxf(x.x, x.y));
+          for (int i = 0; i < 16; i += 4) {
+            const float4 n = *reinterpret_cast<const float4*>(m + i);
+            float2 xa = make_float2(u2f(x0[i]), u2f(x0[i + 1])), xb = make_float2(u2f(x0[i + 2]), u2f(x0[i + 3]));
+            float2 qa = f2, qb = f2;
+            if (F8) {
+              xa = __ffma2_rn(make_float2(u2f(x1[i]), u2f(x1[i + 1])), s1, __fmul2_rn(xa, s0));
+              xb = __ffma2_rn(make_float2(u2f(x1[i + 2]), u2f(x1[i + 3])), s1, __fmul2_rn(xb, s0));
+              const float4 q = *reinterpret_cast<const float4*>(sq + i);
+              qa = make_float2(q.x, q.y);
+              qb = make_float2(q.z, q.w);
             }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[8 * ch + i] = make_float2(-INFINITY, -INFINITY);
+            if (MODS) {
+              xa = __fmul2_rn(xa, qa);
+              xb = __fmul2_rn(xb, qb);
+              xa.x = modify(xa.x, p.cap, inv_cap2, slopes[i] * dist) + n.x;
+              xa.y = modify(xa.y, p.cap, inv_cap2, slopes[i + 1] * dist) + n.y;
+              xb.x = modify(xb.x, p.cap, inv_cap2, slopes[i + 2] * dist) + n.z;
+              xb.y = modify(xb.y, p.cap, inv_cap2, slopes[i + 3] * dist) + n.w;
+            } else {
+              xa = __ffma2_rn(xa, qa, make_float2(n.x, n.y));
+              xb = __ffma2_rn(xb, qb, make_float2(n.z, n.w));
+            }
+            y[i / 2] = xa;
+            y[i / 2 + 1] = xb;
+            top = fmaxf(fmaxf(fmaxf(top, xa.x), fmaxf(xa.y, xb.x)), xb.y);
           }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = make_float2(-INFINITY, -INFINITY);
         }
         if (__any_sync(0xffffffffu, !valid)) {
           if (!valid) {
             top = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = make_float2(-INFINITY, -INFINITY);
+            for (int i = 0; i < 8; ++i) y[i] = make_float2(-INFINITY, -INFINITY);
           }
         }
         tc_fence_before();
@@ -1261,7 +1222,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         if (exact) {
           // exact maximum of the tile per head; the running maxima are raised to it
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < 8; ++i) {
             const int m0 = redux_max_s32(f2ord(y[i].x)), m1 = redux_max_s32(f2ord(y[i].y));
             if (lane == 2 * i) red_part[64 * qd + hb + 2 * i] = ord2f(m0);
             if (lane == 2 * i + 1) red_part[64 * qd + hb + 2 * i + 1] = ord2f(m1);
@@ -1270,9 +1231,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
             // magnitudes order like their bits
             const uint32_t a0 = __reduce_max_sync(0xffffffffu, f2u(fabsf(scl.x)));
             const uint32_t a1 = __reduce_max_sync(0xffffffffu, f2u(fabsf(scl.y)));
-            if (lane == 0) {
-              red_sc[2 * warp] = u2f(a0);
-              red_sc[2 * warp + 1] = u2f(a1);
+            if (lane == 0 && hq == 0) {
+              red_sc[2 * qd] = u2f(a0);
+              red_sc[2 * qd + 1] = u2f(a1);
             }
           }
           const bool some = softmax_any(valid);
@@ -1288,7 +1249,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
             const int t = sid - kHG;
             float top_sc = 0.0f;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) top_sc = fmaxf(top_sc, red_sc[2 * w + t]);  // warps 0 - 3: all keys
+            for (int w = 0; w < 4; ++w) top_sc = fmaxf(top_sc, red_sc[2 * w + t]);
             // the power of two at or above it, 2^-100 at least: its inverse is finite
             uint32_t e = (f2u(top_sc) + 0x7FFFFFu) >> 23;
             e = e < 27u ? 27u : (e > 254u ? 254u : e);
@@ -1298,25 +1259,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
             red_wf[2 * (mb ^ 1) + t] = (float)(1 << kWeightShift) / ref;
           }
           softmax_sync();
-          if (F8 && !fresh) rescale = red_ref[2 * mb + hq] / red_ref[2 * (mb ^ 1) + hq];
+          if (F8 && !fresh) rescale = red_ref[2 * mb + oh] / red_ref[2 * (mb ^ 1) + oh];
           mb ^= 1;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < 8; ++i) {
             const float2 up = *reinterpret_cast<const float2*>(red_raise + hb + 2 * i);
             y[i] = make_float2(y[i].x - up.x, y[i].y - up.y);
           }
           if (!fresh) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) lsum[i] = __fmul2_rn(lsum[i], *reinterpret_cast<const float2*>(red_alpha + hb + 2 * i));
+            for (int i = 0; i < 8; ++i) lsum[i] = __fmul2_rn(lsum[i], *reinterpret_cast<const float2*>(red_alpha + hb + 2 * i));
             pv_wait(g - 1);
             tc_fence_after();
 #pragma unroll 1
-            for (int ch = 0; ch < 4; ++ch) {
+            for (int ch = 0; ch < 2; ++ch) {
               uint32_t o[16];
               tmem_ld32_x16(o_addr + 16 * ch, o);
               tc_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = f2u(u2f(o[i]) * (red_alpha[16 * ch + i] * rescale));
+              for (int i = 0; i < 16; ++i) o[i] = f2u(u2f(o[i]) * (red_alpha[ob + 16 * ch + i] * rescale));
               tmem_st32_x16(o_addr + 16 * ch, o);
             }
             tc_wait_st();
@@ -1325,41 +1286,34 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         }
         float2 wf = make_float2(1.0f, 1.0f);  // FP8: the key's scales relative to the references
         if (F8) wf = __fmul2_rn(scl, *reinterpret_cast<const float2*>(red_wf + 2 * mb));
+        if (used) {
 #pragma unroll
-        for (int ch = 0; ch < 2; ++ch) {
-          if (ch < nch) {
-#pragma unroll
-            for (int i = 8 * ch; i < 8 * ch + 8; ++i) {
-              y[i] = make_float2(ex2_approx(y[i].x), ex2_approx(y[i].y));
-              lsum[i] = __fadd2_rn(lsum[i], y[i]);
-            }
+          for (int i = 0; i < 8; ++i) {
+            y[i] = make_float2(ex2_approx(y[i].x), ex2_approx(y[i].y));
+            lsum[i] = __fadd2_rn(lsum[i], y[i]);
           }
         }
         // the weights' buffer is free once the value product that read it is complete
         if (g >= C::PBUF) pv_wait(g - C::PBUF);
         uint8_t* prow = smem + C::P_OFF + (g % C::PBUF) * C::P_BYTES + tr * 128;
         const int sw = tr & 7;
+        if (used) {
 #pragma unroll
-        for (int ch = 0; ch < 2; ++ch) {
-          if (ch < nch) {
+          for (int h = 0; h < C::PN; ++h) {
+            uint32_t w[8];
+            const float wh = h == 0 ? wf.x : wf.y;
 #pragma unroll
-            for (int h = 0; h < C::PN; ++h) {
-              uint32_t w[8];
-              const float wh = h == 0 ? wf.x : wf.y;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                if (F8) {
-                  const float2 v = __fmul2_rn(y[8 * ch + i], make_float2(wh, wh));
-                  w[i] = f32x2_to_f16x2(v.x, v.y);
-                } else {
-                  w[i] = f32x2_to_bf16x2(y[8 * ch + i].x, y[8 * ch + i].y);
-                }
+            for (int i = 0; i < 8; ++i) {
+              if (F8) {
+                const float2 v = __fmul2_rn(y[i], make_float2(wh, wh));
+                w[i] = f32x2_to_f16x2(v.x, v.y);
+              } else {
+                w[i] = f32x2_to_bf16x2(y[i].x, y[i].y);
               }
-              uint8_t* d = prow + h * (kBN * 128);
-              const int gr = 4 * hq + 2 * ch;
-              *reinterpret_cast<uint4*>(d + ((gr ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-              *reinterpret_cast<uint4*>(d + (((gr + 1) ^ sw) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
             }
+            uint8_t* d = prow + h * (kBN * 128);
+            *reinterpret_cast<uint4*>(d + (((2 * hq) ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(d + (((2 * hq + 1) ^ sw) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
           }
         }
         tc_fence_before();
@@ -1368,27 +1322,29 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       }
       // ---- the segment's end: sums over the keys, then this warp's columns of O^T
       {
-        // reduce-scatter over the lanes: lane i ends with the warp's sum of head i
-        float v[32];
+        // reduce-scatter over the lanes: lanes 2i and 2i + 1 end with the warp's sum of head i
+        float v[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 8; ++i) {
           v[2 * i] = lsum[i].x;
           v[2 * i + 1] = lsum[i].y;
         }
 #pragma unroll
-        for (int w = 16; w > 0; w >>= 1) {
-          const bool upper = lane & w;
+        for (int w = 8; w > 0; w >>= 1) {
+          const bool upper = lane & (2 * w);
 #pragma unroll
           for (int i = 0; i < w; ++i)
-            v[i] = (upper ? v[i + w] : v[i]) + __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[i + w], w);
+            v[i] = (upper ? v[i + w] : v[i]) + __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[i + w], 2 * w);
         }
-        red_part[64 * qd + hb + lane] = v[0];
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+        if ((lane & 1) == 0) red_part[64 * qd + hb + (lane >> 1)] = v[0];
       }
       softmax_sync();
       const int part = 2 * cta + (s.kind == 1 ? 1 : 0);
       if (sid < kHG) {
         const float L = (red_part[sid] + red_part[64 + sid]) + (red_part[128 + sid] + red_part[192 + sid]);
         const float m = -red[64 * mb + sid];
+        red[64 * mb + sid] = 0.0f;  // for the next segment
         red_inv[sid] = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);
         if (s.kind != 0) {
           p.ws_ml[(int64_t)part * 2 * kHG + sid] = L == 0.0f ? kNoMax : m;
@@ -1401,15 +1357,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       if (s.ntiles > 0) pv_wait(g - 1);
       tc_fence_after();
       // FP8: weights were relative to the half's reference scale
-      const float back = F8 && !fresh ? red_ref[2 * mb + hq] * (1.0f / (1 << kWeightShift)) : 1.0f;
-      const int dv = 128 * hq + tr;
+      const float back = F8 && !fresh ? red_ref[2 * mb + oh] * (1.0f / (1 << kWeightShift)) : 1.0f;
+      const int dv = 128 * oh + tr;
       uint16_t* orow = p.out + (int64_t)s.t * p.out_st + (int64_t)s.hg * kHG * p.out_sh;
       float* prt = p.ws_o + (int64_t)part * kHG * kD + dv;
 #pragma unroll 1
-      for (int h0 = 0; h0 < heads; h0 += 16) {
+      for (int h0 = ob; h0 < min(heads, ob + 32); h0 += 16) {
         uint32_t o[16];
         if (s.ntiles > 0) {
-          tmem_ld32_x16(o_addr + h0, o);
+          tmem_ld32_x16(o_addr + h0 - ob, o);
           tc_wait_ld();
         } else {
 #pragma unroll
@@ -1437,6 +1393,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       // (the barrier at the next segment's start keeps it from rewriting sums still being read)
       tc_fence_before();
     }
+  }
   }
   tc_fence_before();
   __syncthreads();
