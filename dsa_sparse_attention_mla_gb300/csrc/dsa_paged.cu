@@ -22,7 +22,8 @@
 //    tile: p * scale relative to the largest scale so far, 2^22 of normal range below the strongest
 //    position. e4m3 weights (as two terms) would need no widening but lose what many far positions add
 //    up to beside one strong one. So the keys are the exact products code * scale.
-//  * Softmax with one thread per key and 16 heads (four warps per lane quarter). The running maximum
+//  * Softmax with one thread per key and 32 heads (two warps per lane quarter; the
+//    four warps of the same heads share running maxima and synchronise among themselves). The running maximum
 //    of a head is raised, and O and the sums rescaled, only when some score exceeds it by 2^20 (FP8:
 //    2^6): p and its sums are floating point, so a stale maximum costs no precision, and the exact path runs
 //    for a segment's first tile and almost never again.
@@ -30,20 +31,20 @@
 //    device): rows (token, group of 64 heads) cost their 128-position tiles plus a constant, and
 //    CTA c takes the c-th of G equal parts of the total. A row cut by a border leaves unnormalised
 //    parts in the workspace, which a second, dependent launch joins in the order of the parts.
-//  * Warp roles: 0-15 softmax, 16 scheduler (walks the CTA's rows, finds the slots of each tile's
-//    positions and prefetches them into L2, up to eight tiles ahead), 17 score products, 18 value
-//    products, 19 query loads, 20-23 row loads, 24-27 FP8: query split and widening. Every wait is
-//    bounded. A warp of such a kernel issues about every sixth cycle whatever its role, so the time
-//    of a tile is the instructions a warp spends on it: hence sixteen softmax warps of 16 heads each,
-//    one job per warp and no polling between jobs. The registers are split anew after the start (a
-//    spill would leave the L1 that the tiles leave over: a tile took 9500 cycles with spills).
+//  * Warp roles: 0-7 softmax, 8 scheduler (walks the CTA's rows and finds the slots of each tile's
+//    positions, up to eight tiles ahead), 9 score products, 10 value products, 11 query loads, 12-15
+//    row loads, 16-19 FP8: query split and widening. Every wait is bounded. What bounds a tile is the
+//    instructions its warps issue, so every job has warps of its own with no polling between jobs, a
+//    softmax warp takes 32 heads (sixteen warps of 16 took the same time with twice the waits), and
+//    the arithmetic is on pairs. The registers are split anew after the start (a spill would leave
+//    the L1 that the tiles leave over: a tile took 9500 cycles with spills).
 //  * bf16 tiles without a masked position come by TMA, in boxes of as many rows as a page and a tile
 //    share; other bf16 tiles and FP8 rows (264 bytes: no tensor map takes that pitch) by cp.async
 //    straight to their swizzled place. Either way every free stage of the ring holds loads in flight
 //    and no register does. FP8: other warps widen the rows into a second ring while the softmax
 //    of their tile runs.
 //  * The mass kernel is the same without the value product: with the lse given, each key's thread
-//    adds the weights of all 64 heads; four groups of four warps take tiles in turn.
+//    adds the weights of all 64 heads; two groups of four warps take tiles in turn.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -61,16 +62,19 @@ constexpr int kD = 256;
 constexpr int kMaxHeads = 128;
 constexpr int kHG = 64;    // heads per row (MMA N)
 constexpr int kBN = 128;   // positions per tile (MMA M)
-constexpr int kSoftmaxWarps = 16;
-constexpr int kWarpSched = 16, kWarpScore = 17, kWarpValue = 18, kWarpQuery = 19, kWarpLoad0 = 20, kWarpWiden0 = 24;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kWarpSched = 8, kWarpScore = 9, kWarpValue = 10, kWarpQuery = 11, kWarpLoad0 = 12, kWarpWiden0 = 16;
 constexpr int kLoadWarps = 4, kWidenWarps = 4;
 constexpr int kLoadRows = kBN / kLoadWarps;
 constexpr int kWarps = kWarpWiden0 + kWidenWarps;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxCtas = 192;      // the join's lists
+constexpr int kMaxCtas = 192;      // the join's lists (its threads look at 256 CTAs)
 constexpr int kSegs = 8;           // segment ring depth
 constexpr int kMaps = 8;           // tiles whose slots are known ahead
-constexpr int kPrefetchPage = 16;  // smallest page prefetched into L2: an eighth of a tile per request
+// Smallest page whose rows the scheduler prefetches into L2 (an eighth of a tile per request), FP8
+// only: 128 x 32768 positions 624 us against 706 without; bf16 tiles come by TMA in any case, and 64
+// ragged requests took 72 us with it, 66 without.
+constexpr int kPrefetchPage = 16;
 constexpr int kRowOverhead = 1;    // a row's start and end, in tiles
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -92,12 +96,6 @@ __device__ __forceinline__ bool try_wait_parked(uint32_t bar, uint32_t parity) {
       : "r"(bar), "r"(parity), "r"(1000000u)
       : "memory");
   return ok != 0;
-}
-// Waits for the phase for about half a microsecond.
-__device__ __forceinline__ void park(uint32_t bar, uint32_t parity) {
-  asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%0], %1, %2;\n}" ::"r"(bar),
-               "r"(parity), "r"(500u)
-               : "memory");
 }
 static __device__ __forceinline__ bool bar_wait_retry(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = globaltimer_ns();
@@ -191,12 +189,12 @@ struct Cfg {
   static constexpr int SQ_OFF = SC_OFF + (F8 ? NV * 1024 : 0); // FP8: [kSegs][64] query scales
   static constexpr int NL_OFF = SQ_OFF + (F8 ? kSegs * 256 : 0);  // mass: [kSegs][64] -lse, exp2 domain
   static constexpr int SL_OFF = NL_OFF + (MASS ? kSegs * 256 : 0);  // slopes [128]
-  // -m [2][64], alpha [64], part [4][64], inverse sums [64], raise of m [64]; FP8: largest scales of
-  // the tile [8][2], reference scales [2][2] and their inverses [2][2]
+  // -m [2][64], alpha [64], part [4][64], inverse sums [64], raise of m [64]; FP8, per head group:
+  // largest scales of the tile [4][2], reference scales [2][2] and their inverses [2][2]
   static constexpr int RED_OFF = SL_OFF + 512;
-  static constexpr int PLAN_OFF = RED_OFF + 9 * 256 + 128;  // block scans: 2 x kWarps int64; start row, its cost
+  static constexpr int PLAN_OFF = RED_OFF + 9 * 256 + 2 * 64;  // block scans: 2 x kWarps int64; start row, its cost
   static constexpr int BAR_OFF = PLAN_OFF + 2 * 8 * kWarps + 64;
-  static constexpr int NBARS = 2 + 2 * NST + 3 * kSegs + NV + 2 * kMaps + 2 * NSB + 2 * 2 + 2 + 2 * NW;
+  static constexpr int NBARS = 2 + 2 * NST + 3 * kSegs + 2 * kMaps + 2 * NSB + 2 * 2 + 2 + 2 * NW;
   static constexpr int MISC_OFF = BAR_OFF + 8 * NBARS;
   static constexpr int SMEM_BYTES = MISC_OFF + 16 + 1024;
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
@@ -306,20 +304,21 @@ __device__ __forceinline__ int block_max(int v, int64_t* buf) {
 }
 static_assert(kWarps <= 32, "one lane per warp in the block scans");
 
-// Barrier of the softmax warps that returns the OR of `v`. All of them take the same path through
-// the tiles: a warp whose wait runs out goes on with what it has, waiting no more, and all leave
-// together between two segments, so none is left behind at a barrier.
-__device__ __forceinline__ bool softmax_any(bool v) {
+// Barrier of the four softmax warps of a head group, which returns the OR of `v`. They take the same
+// path through the tiles: a warp whose wait runs out goes on with what it has, waiting no more, and
+// the four leave together between two segments, so none is left behind at a barrier.
+__device__ __forceinline__ bool group_any(int group, bool v) {
   uint32_t r;
   asm volatile(
-      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.or.pred q, 1, 512, p;\nselp.u32 %0, 1, 0, q;\n}"
+      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %2, 0;\nbarrier.cta.red.or.pred q, %1, 128, p;\nselp.u32 %0, 1, 0, q;\n}"
       : "=r"(r)
-      : "r"((uint32_t)v)
+      : "r"(1 + group), "r"((uint32_t)v)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 512;" ::: "memory"); }
-static_assert(32 * kSoftmaxWarps == 512, "the barriers' thread count");
+__device__ __forceinline__ void group_sync(int group) {
+  asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + group) : "memory");
+}
 
 // Splits query rows h0 .. of a widening warp's share of a row (zero past `heads`) into e4m3 hi and lo terms, lane l
 // columns 8 l .. 8 l + 7, per head scaled by 2^-e so that the largest component lies in
@@ -390,10 +389,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
   auto g_empty = [&](uint32_t s) { return b1 + 8 * (kSegs + s); };
   auto aux_full = [&](uint32_t s) { return b1 + 8 * (2 * kSegs + s); };  // the segment's -lse, query scales
   const uint32_t b2 = b1 + 24 * kSegs;
-  auto v_full = [&](uint32_t s) { return b2 + 8 * s; };                 // FP8: scales of a tile
-  auto map_full = [&](uint32_t s) { return b2 + 8 * (C::NV + s); };     // slots of a tile
-  auto map_empty = [&](uint32_t s) { return b2 + 8 * (C::NV + kMaps + s); };
-  const uint32_t b2s = b2 + 8 * (C::NV + 2 * kMaps);
+  auto map_full = [&](uint32_t s) { return b2 + 8 * s; };               // slots of a tile
+  auto map_empty = [&](uint32_t s) { return b2 + 8 * (kMaps + s); };
+  const uint32_t b2s = b2 + 16 * kMaps;
   auto s_full = [&](uint32_t s) { return b2s + 8 * s; };
   auto s_empty = [&](uint32_t s) { return b2s + 8 * (C::NSB + s); };
   const uint32_t b3 = b2s + 16 * C::NSB;
@@ -408,38 +406,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
   float* s_slopes = reinterpret_cast<float*>(smem + C::SL_OFF);
 
   asm volatile("griddepcontrol.launch_dependents;");
-  if (threadIdx.x == 0) {
-    mbar_init(q_full, F8 ? kWidenWarps : 32);  // bf16: one asynchronous arrival per thread
-    mbar_init(q_empty, 1);
-    for (int s = 0; s < C::NST; ++s) {
-      mbar_init(k_full(s), 32 * kLoadWarps);  // one asynchronous arrival per thread
-      mbar_init(k_empty(s), 1 + (C::WIDEN ? kWidenWarps : 0));  // the last product to read it, the widening
-    }
-    for (int s = 0; s < kSegs; ++s) {
-      mbar_init(g_full(s), 1);
-      // softmax warps, score issuer, value issuer, query warp, FP8: widening warps
-      mbar_init(g_empty(s), kSoftmaxWarps + 1 + (MASS ? 0 : 1) + (C::WIDEN ? 0 : 1) + (F8 ? kWidenWarps : 0));
-      mbar_init(aux_full(s), (MASS ? 1 : 0) + (F8 ? kWidenWarps : 0) + (!MASS && !F8 ? 1 : 0));
-    }
-    for (int s = 0; s < C::NV; ++s) mbar_init(v_full(s), 32 * kLoadWarps);
-    for (int s = 0; s < kMaps; ++s) {
-      mbar_init(map_full(s), 1);
-      mbar_init(map_empty(s), MASS ? 4 : kSoftmaxWarps);
-    }
-    for (int s = 0; s < C::NSB; ++s) {
-      mbar_init(s_full(s), 1);
-      mbar_init(s_empty(s), MASS ? 4 : kSoftmaxWarps);
-    }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(p_full(s), kSoftmaxWarps);
-      mbar_init(pv_done(s), 1);
-      mbar_init(drain(s), 1);
-    }
-    for (int s = 0; s < C::NW; ++s) {
-      mbar_init(w_full(s), kWidenWarps);
-      mbar_init(w_empty(s), 1);
-    }
-    *abort_flag = 0;
+  // a barrier per thread, in the order of their addresses
+  if (threadIdx.x < C::NBARS) {
+    constexpr int B0 = 2, B1 = B0 + C::NST, B2 = B1 + C::NST, B3 = B2 + kSegs, B4 = B3 + kSegs, B5 = B4 + kSegs,
+                  B6 = B5 + kMaps, B7 = B6 + kMaps, B8 = B7 + C::NSB, B9 = B8 + C::NSB, B10 = B9 + 2, B11 = B10 + 4,
+                  B12 = B11 + C::NW;
+    const int i = threadIdx.x;
+    int n = 1;                                                 // pv_done, drain, w_empty, q_empty, g_full, map_full
+    if (i == 0) n = F8 ? kWidenWarps : 32;                     // q_full (bf16: an asynchronous arrival per thread)
+    else if (i >= B0 && i < B1) n = 32 * kLoadWarps;           // k_full: an asynchronous arrival per thread
+    else if (i >= B1 && i < B2) n = 1 + (C::WIDEN ? kWidenWarps : 0);  // k_empty: the last product, the widening
+    else if (i >= B3 && i < B4)                                // g_empty: softmax, issuers, query warp, widening
+      n = kSoftmaxWarps + 1 + (MASS ? 0 : 1) + (C::WIDEN ? 0 : 1) + (F8 ? kWidenWarps : 0);
+    else if (i >= B4 && i < B5) n = (MASS ? 1 : 0) + (F8 ? kWidenWarps : 0) + (!MASS && !F8 ? 1 : 0);  // aux_full
+    else if (i >= B6 && i < B7) n = MASS ? 4 : kSoftmaxWarps;  // map_empty
+    else if (i >= B7 && i < B8) n = 2;                         // s_full: the product, and its issuer
+    else if (i >= B8 && i < B9) n = MASS ? 4 : kSoftmaxWarps;  // s_empty
+    else if (i >= B9 && i < B10) n = kSoftmaxWarps;            // p_full
+    else if (i >= B11 && i < B12) n = kWidenWarps;             // w_full
+    mbar_init(bar0 + 8 * i, n);
+    if (i == 0) *abort_flag = 0;
     fence_mbar_init();
   }
   if (MODS && threadIdx.x < kMaxHeads)
@@ -520,11 +506,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     return false;
   };
 
-  // 896 threads x 72 registers at launch; 512 x 80 + 384 x 56 is within that total. (No function is
-  // called from here on: ptxas allocates past the launch's 72 only without calls.)
-  static_assert(32 * kWarps * 72 >= 512 * 80 + 384 * 56 && 32 * kWarps == 896, "register split");
+  // 640 threads x 96 registers at launch; 256 x 144 + 384 x 64 is the same total. (No function is
+  // called from here on: ptxas allocates past the launch's 96 only without calls.)
+  static_assert(32 * kWarps * 96 == 256 * 144 + 384 * 64, "register split");
   if (warp >= kSoftmaxWarps) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
   if (warp == kWarpSched) {
     // ================================================================== scheduler ====
     uint32_t sc = 0;
@@ -571,8 +557,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         *dst = make_int4(sl[0], sl[1], sl[2], sl[3]);
         const bool full = __all_sync(0xffffffffu, sl[0] >= 0 && sl[1] >= 0 && sl[2] >= 0 && sl[3] >= 0);
         if (lane == 0) reinterpret_cast<int*>(smem + C::FULL_OFF)[g % kMaps] = full;
-        // the tile's rows into L2, one request per page: the copies then wait for L2 only
-        if (bt && p.page_size >= kPrefetchPage) {
+        // the tile's rows into L2, one request per page
+        if (F8 && bt && p.page_size >= kPrefetchPage) {
           const uint32_t lo = max(base, a), hi = min(base + (uint32_t)kBN, b);
           const uint32_t pg = (uint32_t)(((uint64_t)lo * p.pg_mul) >> p.pg_shift) + lane;
           const uint64_t first = (uint64_t)pg * (uint32_t)p.page_size;
@@ -721,6 +707,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
             ok = false;
             break;
           }
+          // the slots' and (with k_full) the scales' writes are this thread's to pass on with s_full
+          if (!wait(map_full(g % kMaps), (g / kMaps) & 1)) {
+            ok = false;
+            break;
+          }
           const uint32_t d0 = tmem + sb * C::S_COLS;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -754,7 +745,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
             }
             if (MASS || F8) mma_commit(k_empty(st));
           }
-          if (ok) mma_commit(s_full(sb));
+          if (ok) {
+            mma_commit(s_full(sb));
+            mbar_arrive(s_full(sb));
+          }
         }
         if (ok) mma_commit(q_empty);
       }
@@ -896,7 +890,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
                                                                             8 * (kLoadRows * lw + lane)),
                        "l"(p.cache + (own >= 0 ? (int64_t)own * C::RB + 256 : 0)), "r"(own >= 0 ? 8 : 0)
                        : "memory");
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(v_full(g % C::NV)) : "memory");
         }
         const uint32_t dst = sbase + C::K_OFF + st * C::HALF_BYTES;
         if (boxes) {
@@ -949,13 +942,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     // ================================================= FP8: query split and widening ====
     // Warp w splits heads 16 w .. of a segment's query, then widens rows 32 w .. 32 w + 31 of its tiles.
     const int ww = warp - kWarpWiden0;
-    const int gl = lane & 15, r0 = 32 * ww + (lane >> 4);
-    uint32_t from[4], to[4];  // offsets of row r0 + 2 i's piece as stored, and of its 16-byte granule widened
+    const int gl = lane & 7, r0 = 32 * ww + (lane >> 3);
+    // Lane = 16-byte granule gl of row r0 + 4 i: 16 codes, two granules widened. A granule's swizzle
+    // repeats every second i.
+    uint32_t from[2], to[2][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = r0 + 2 * i;
-      from[i] = (uint32_t)(r * 128 + (((gl >> 1) ^ (r & 7)) << 4) + 8 * (gl & 1));
-      to[i] = (uint32_t)((gl >> 3) * (kBN * 128) + r * 128 + (((gl & 7) ^ (r & 7)) << 4));
+    for (int i = 0; i < 2; ++i) {
+      const int r = r0 + 4 * i;
+      from[i] = (uint32_t)(r * 128 + ((gl ^ (r & 7)) << 4));
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        to[i][j] = (uint32_t)((gl >> 2) * (kBN * 128) + r * 128 + ((((2 * gl + j) & 7) ^ (r & 7)) << 4));
     }
     uint32_t hs = 0, qn = 0;  // halves widened, queries split
     bool ok = true;
@@ -990,14 +987,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
           uint8_t* wide = smem + C::W_OFF + sw * C::WIDE_BYTES;
 #pragma unroll
           for (int part = 0; part < 2; ++part) {
-            uint2 v[8];
+            uint4 v[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint2*>(raw + from[i & 3] + 1024 * (i >> 2) + 2048 * part);
+            for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4*>(raw + from[i & 1] + 1024 * (i >> 1) + 2048 * part);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<uint4*>(wide + to[i & 3] + 1024 * (i >> 2) + 2048 * part) =
-                  make_uint4(e4m3x2_to_f16x2((uint16_t)v[i].x), e4m3x2_to_f16x2((uint16_t)(v[i].x >> 16)),
-                             e4m3x2_to_f16x2((uint16_t)v[i].y), e4m3x2_to_f16x2((uint16_t)(v[i].y >> 16)));
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t c[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                *reinterpret_cast<uint4*>(wide + to[i & 1][j] + 1024 * (i >> 1) + 2048 * part) = make_uint4(
+                    e4m3x2_to_f16x2((uint16_t)c[2 * j]), e4m3x2_to_f16x2((uint16_t)(c[2 * j] >> 16)),
+                    e4m3x2_to_f16x2((uint16_t)c[2 * j + 1]), e4m3x2_to_f16x2((uint16_t)(c[2 * j + 1] >> 16)));
+            }
           }
           __syncwarp();
           if (lane == 0) {
@@ -1009,9 +1010,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     }
   }
   } else {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
   if constexpr (MASS) {
-    // ================================================= weights of a key, 16 warps ====
+    // ================================================== weights of a key, 8 warps ====
     const int qd = warp & 3, gi = warp >> 2;
     const int tr = 32 * qd + lane;
     const float inv_cap2 = MODS && p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
@@ -1030,7 +1031,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       const float* slopes = s_slopes + s.hg * kHG;
       const int64_t qp = MODS && p.qpos ? p.qpos[s.t] : (int64_t)p.lengths[s.t] - 1;
       for (int k = 0; k < s.ntiles; ++k, ++g) {
-        if ((g & 3) != (uint32_t)gi) continue;
+        if ((g & 1) != (uint32_t)gi) continue;
         const uint32_t sb = g % C::NSB;
         const uint32_t tl = tmem + ((uint32_t)(32 * qd) << 16) + sb * C::S_COLS;
         const uint32_t pos = (uint32_t)(s.a & ~127) + 128u * (uint32_t)(s.tile0 + k) + tr;
@@ -1043,8 +1044,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
             dist = fabsf((float)(qp - kp));
           }
         }
-        if (!wait_warp(map_full(g % kMaps), (g / kMaps) & 1) || !wait_warp(s_full(sb), (g / C::NSB) & 1) ||
-            (F8 && !wait_warp(v_full(g % C::NV), (g / C::NV) & 1))) {
+        if (!wait_warp(s_full(sb), (g / C::NSB) & 1)) {
           ok = false;
           break;
         }
@@ -1093,53 +1093,56 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       if (lane == 0) mbar_arrive(g_empty(slot));
     }
   } else {
-    // ==================================================== softmax and outputs, 16 warps ====
-    // Warp = lane quarter qd (keys 32 qd ..; output columns 32 qd .. of the 128 of half oh), heads
-    // 16 hq .. of the scores, 32 (hq & 1) .. of the output.
+    // ===================================================== softmax and outputs, 8 warps ====
+    // Warp = lane quarter qd (keys 32 qd ..; output columns 32 qd .. of both halves), head group hq: 32
+    // heads from 32 hq, or 16 from 16 hq where a row has at most 32 (both groups then share the work;
+    // 32 heads with cap and bias took 52 us with one of them idle, 38 so)
     const int qd = warp & 3, hq = warp >> 2;
-    const int hb = 16 * hq, oh = hq >> 1, ob = 32 * (hq & 1);
+    const int hw = p.H <= 32 ? 16 : 32;
+    const int hb = hw * hq;
     const int tr = 32 * qd + lane;
-    const int sid = threadIdx.x;  // 0 .. 511
+    const int gid = threadIdx.x & 127;  // thread of the head group
     const uint32_t tl = tmem + ((uint32_t)(32 * qd) << 16);
-    float* red = reinterpret_cast<float*>(smem + C::RED_OFF);  // -m, two buffers
+    float* red = reinterpret_cast<float*>(smem + C::RED_OFF);  // -m [2 buffers][64]
     float* red_alpha = red + 128;
     float* red_part = red + 192;  // [4 quarters][64 heads]
     float* red_inv = red + 448;
     float* red_raise = red + 512;
-    float* red_sc = red + 576;   // FP8: largest |scale| of the tile, [4 quarters][2]
-    float* red_ref = red + 592;  // FP8: [2 buffers][2] reference scales (powers of two)
-    float* red_wf = red + 596;   // FP8: [2 buffers][2] 2^kWeightShift / reference
+    float* red_sc = red + 576 + 16 * hq;  // FP8: largest |scale| of the tile, [4 quarters][2]
+    float* red_ref = red_sc + 8;          // FP8: [2 buffers][2] reference scales (powers of two)
+    float* red_wf = red_sc + 12;          // FP8: [2 buffers][2] 2^kWeightShift / reference
     const float inv_cap2 = MODS && p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
-    const float c_log2 = p.sm_scale * kLog2e;
+    const float f = MODS ? p.sm_scale : p.sm_scale * kLog2e;
     uint32_t g = 0, mb = 0;
-    bool failed = false;  // a wait ran out: go on without waiting, and leave with the others
+    bool failed = false;  // a wait ran out: go on without waiting, and leave with the group
     auto await = [&](uint32_t bar, uint32_t par) {
       if (failed || __all_sync(0xffffffffu, bar_wait(bar, par))) return;
       fail();
       failed = true;
     };
     auto pv_wait = [&](uint32_t last) { await(pv_done(last & 1), (last >> 1) & 1); };
-    const uint32_t o_addr = tl + C::O_COL + 64 * oh + ob;
+    const uint32_t o_addr = tl + C::O_COL + hb;  // O^T half 0 (half 1 64 columns on), the group's heads
     // -m of a segment without a valid key so far is 0
-    if (sid < kHG) red[sid] = 0.0f;
+    if (gid < hw) red[hb + gid] = 0.0f;
     for (uint32_t sc = 0;; ++sc) {
       const uint32_t slot = sc % kSegs;
       await(g_full(slot), (sc / kSegs) & 1);
       if (F8 && !failed && segs[slot].type != 0) await(aux_full(slot), (sc / kSegs) & 1);
-      if (softmax_any(failed)) break;
+      if (group_any(hq, failed)) break;
       const Seg s = segs[slot];
       __syncwarp();
       if (lane == 0) mbar_arrive(g_empty(slot));
       if (s.type == 0) break;
       const int heads = min(kHG, p.H - s.hg * kHG);
-      const bool used = hb < heads;  // (the weights of unused heads meet only unused columns of O^T)
+      // chunks of 16 heads in use: the weights of the others meet only unused columns of O^T
+      const int nch = max(0, min(hw >> 4, (heads - hb + 15) >> 4));
       const float* slopes = s_slopes + s.hg * kHG + hb;
       const float* sq = reinterpret_cast<const float*>(smem + C::SQ_OFF) + kHG * slot + hb;
       int64_t qp = 0;
       if (MODS) qp = p.qpos ? p.qpos[s.t] : (int64_t)p.lengths[s.t] - 1;
-      float2 lsum[8];  // heads 2 i, 2 i + 1 of the warp
+      float2 lsum[16];  // heads 2 i, 2 i + 1 of the warp
 #pragma unroll
-      for (int i = 0; i < 8; ++i) lsum[i] = make_float2(0.0f, 0.0f);
+      for (int i = 0; i < 16; ++i) lsum[i] = make_float2(0.0f, 0.0f);
       bool fresh = true;  // no valid key so far: m counts as 0, no reference scale
       for (int k = 0; k < s.ntiles; ++k, ++g) {
         const uint32_t sb = g % C::NSB;
@@ -1150,60 +1153,61 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
           if (p.kpos && pos >= (uint32_t)s.a && pos < (uint32_t)s.b) kp = p.kpos[s.req * p.kp_stride + pos];
           dist = fabsf((float)(qp - kp));
         }
-        await(map_full(g % kMaps), (g / kMaps) & 1);
-        if (F8) await(v_full(g % C::NV), (g / C::NV) & 1);
+        await(s_full(sb), (g / C::NSB) & 1);
+        tc_fence_after();
         const bool valid = reinterpret_cast<const int*>(smem + C::MAP_OFF + (g % kMaps) * 512)[tr] >= 0;
         float2 scl = make_float2(0.0f, 0.0f);
         if (F8) scl = reinterpret_cast<const float2*>(smem + C::SC_OFF + 1024 * (g % C::NV))[tr];
-        await(s_full(sb), (g / C::NSB) & 1);
-        tc_fence_after();
         // y = score - m, exp2 domain
-        float2 y[8];
+        float2 y[16];
         float top = -INFINITY;
-        if (used) {
-          uint32_t x0[16], x1[16];
-          tmem_ld32_x16(tl + sb * C::S_COLS + hb, x0);
-          if (F8) tmem_ld32_x16(tl + sb * C::S_COLS + 64 + hb, x1);
-          const float f = MODS ? p.sm_scale : c_log2;
-          const float2 s0 = make_float2(scl.x, scl.x), s1 = make_float2(scl.y, scl.y), f2 = make_float2(f, f);
-          const float* m = red + 64 * mb + hb;
-          tc_wait_ld();
+        const float2 s0 = make_float2(scl.x, scl.x), s1 = make_float2(scl.y, scl.y), f2 = make_float2(f, f);
+        const float* m = red + 64 * mb + hb;
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            const float4 n = *reinterpret_cast<const float4*>(m + i);
-            float2 xa = make_float2(u2f(x0[i]), u2f(x0[i + 1])), xb = make_float2(u2f(x0[i + 2]), u2f(x0[i + 3]));
-            float2 qa = f2, qb = f2;
-            if (F8) {
-              xa = __ffma2_rn(make_float2(u2f(x1[i]), u2f(x1[i + 1])), s1, __fmul2_rn(xa, s0));
-              xb = __ffma2_rn(make_float2(u2f(x1[i + 2]), u2f(x1[i + 3])), s1, __fmul2_rn(xb, s0));
-              const float4 q = *reinterpret_cast<const float4*>(sq + i);
-              qa = make_float2(q.x, q.y);
-              qb = make_float2(q.z, q.w);
+        for (int ch = 0; ch < 2; ++ch) {
+          if (ch < nch) {
+            uint32_t x0[16], x1[16];
+            tmem_ld32_x16(tl + sb * C::S_COLS + hb + 16 * ch, x0);
+            if (F8) tmem_ld32_x16(tl + sb * C::S_COLS + 64 + hb + 16 * ch, x1);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              const float4 n = *reinterpret_cast<const float4*>(m + 16 * ch + i);
+              float2 xa = make_float2(u2f(x0[i]), u2f(x0[i + 1])), xb = make_float2(u2f(x0[i + 2]), u2f(x0[i + 3]));
+              float2 qa = f2, qb = f2;
+              if (F8) {
+                xa = __ffma2_rn(make_float2(u2f(x1[i]), u2f(x1[i + 1])), s1, __fmul2_rn(xa, s0));
+                xb = __ffma2_rn(make_float2(u2f(x1[i + 2]), u2f(x1[i + 3])), s1, __fmul2_rn(xb, s0));
+                const float4 q = *reinterpret_cast<const float4*>(sq + 16 * ch + i);
+                qa = make_float2(q.x, q.y);
+                qb = make_float2(q.z, q.w);
+              }
+              if (MODS) {
+                const float* sl = slopes + 16 * ch + i;
+                xa = __fmul2_rn(xa, qa);
+                xb = __fmul2_rn(xb, qb);
+                xa.x = modify(xa.x, p.cap, inv_cap2, sl[0] * dist) + n.x;
+                xa.y = modify(xa.y, p.cap, inv_cap2, sl[1] * dist) + n.y;
+                xb.x = modify(xb.x, p.cap, inv_cap2, sl[2] * dist) + n.z;
+                xb.y = modify(xb.y, p.cap, inv_cap2, sl[3] * dist) + n.w;
+              } else {
+                xa = __ffma2_rn(xa, qa, make_float2(n.x, n.y));
+                xb = __ffma2_rn(xb, qb, make_float2(n.z, n.w));
+              }
+              y[8 * ch + i / 2] = xa;
+              y[8 * ch + i / 2 + 1] = xb;
+              top = fmaxf(fmaxf(fmaxf(top, xa.x), fmaxf(xa.y, xb.x)), xb.y);
             }
-            if (MODS) {
-              xa = __fmul2_rn(xa, qa);
-              xb = __fmul2_rn(xb, qb);
-              xa.x = modify(xa.x, p.cap, inv_cap2, slopes[i] * dist) + n.x;
-              xa.y = modify(xa.y, p.cap, inv_cap2, slopes[i + 1] * dist) + n.y;
-              xb.x = modify(xb.x, p.cap, inv_cap2, slopes[i + 2] * dist) + n.z;
-              xb.y = modify(xb.y, p.cap, inv_cap2, slopes[i + 3] * dist) + n.w;
-            } else {
-              xa = __ffma2_rn(xa, qa, make_float2(n.x, n.y));
-              xb = __ffma2_rn(xb, qb, make_float2(n.z, n.w));
-            }
-            y[i / 2] = xa;
-            y[i / 2 + 1] = xb;
-            top = fmaxf(fmaxf(fmaxf(top, xa.x), fmaxf(xa.y, xb.x)), xb.y);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[8 * ch + i] = make_float2(-INFINITY, -INFINITY);
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = make_float2(-INFINITY, -INFINITY);
         }
         if (__any_sync(0xffffffffu, !valid)) {
           if (!valid) {
             top = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = make_float2(-INFINITY, -INFINITY);
+            for (int i = 0; i < 16; ++i) y[i] = make_float2(-INFINITY, -INFINITY);
           }
         }
         tc_fence_before();
@@ -1216,40 +1220,38 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         if (!exact) {
           bool stale = top > (F8 ? kStaleF8 : kStale);
           if (F8) stale = stale || fabsf(scl.x) > red_ref[2 * mb] || fabsf(scl.y) > red_ref[2 * mb + 1];
-          exact = softmax_any(stale);
+          exact = group_any(hq, stale);
         }
-        float rescale = 1.0f;  // FP8: of this warp's half of O^T, beside the heads' factors
         if (exact) {
           // exact maximum of the tile per head; the running maxima are raised to it
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < 16; ++i) {
             const int m0 = redux_max_s32(f2ord(y[i].x)), m1 = redux_max_s32(f2ord(y[i].y));
-            if (lane == 2 * i) red_part[64 * qd + hb + 2 * i] = ord2f(m0);
-            if (lane == 2 * i + 1) red_part[64 * qd + hb + 2 * i + 1] = ord2f(m1);
+            if (lane == 2 * i && lane < hw) red_part[64 * qd + hb + 2 * i] = ord2f(m0);
+            if (lane == 2 * i + 1 && lane < hw) red_part[64 * qd + hb + 2 * i + 1] = ord2f(m1);
           }
           if (F8) {
             // magnitudes order like their bits
             const uint32_t a0 = __reduce_max_sync(0xffffffffu, f2u(fabsf(scl.x)));
             const uint32_t a1 = __reduce_max_sync(0xffffffffu, f2u(fabsf(scl.y)));
-            if (lane == 0 && hq == 0) {
+            if (lane == 0) {
               red_sc[2 * qd] = u2f(a0);
               red_sc[2 * qd + 1] = u2f(a1);
             }
           }
-          const bool some = softmax_any(valid);
-          if (sid < kHG) {
+          const bool some = group_any(hq, valid);
+          if (gid < hw) {
             // relative to the m that y was taken from; a first maximum may be below it
-            const float up = fmaxf(fmaxf(red_part[sid], red_part[64 + sid]), fmaxf(red_part[128 + sid], red_part[192 + sid]));
-            const float mo = fresh ? 0.0f : -red[64 * mb + sid];
+            const float* pt = red_part + hb + gid;
+            const float up = fmaxf(fmaxf(pt[0], pt[64]), fmaxf(pt[128], pt[192]));
+            const float mo = fresh ? 0.0f : -red[64 * mb + hb + gid];
             const float raise = fresh ? (up > kNoMax ? up : 0.0f) : fmaxf(up, 0.0f);
-            red[64 * (mb ^ 1) + sid] = -(mo + raise);
-            red_raise[sid] = raise;
-            red_alpha[sid] = ex2_approx(-raise);
-          } else if (F8 && sid < kHG + 2) {
-            const int t = sid - kHG;
-            float top_sc = 0.0f;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) top_sc = fmaxf(top_sc, red_sc[2 * w + t]);
+            red[64 * (mb ^ 1) + hb + gid] = -(mo + raise);
+            red_raise[hb + gid] = raise;
+            red_alpha[hb + gid] = ex2_approx(-raise);
+          } else if (F8 && gid >= 32 && gid < 34) {
+            const int t = gid - 32;
+            const float top_sc = fmaxf(fmaxf(red_sc[t], red_sc[2 + t]), fmaxf(red_sc[4 + t], red_sc[6 + t]));
             // the power of two at or above it, 2^-100 at least: its inverse is finite
             uint32_t e = (f2u(top_sc) + 0x7FFFFFu) >> 23;
             e = e < 27u ? 27u : (e > 254u ? 254u : e);
@@ -1258,27 +1260,30 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
             red_ref[2 * (mb ^ 1) + t] = ref;
             red_wf[2 * (mb ^ 1) + t] = (float)(1 << kWeightShift) / ref;
           }
-          softmax_sync();
-          if (F8 && !fresh) rescale = red_ref[2 * mb + oh] / red_ref[2 * (mb ^ 1) + oh];
+          group_sync(hq);
           mb ^= 1;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < 16; ++i) {
             const float2 up = *reinterpret_cast<const float2*>(red_raise + hb + 2 * i);
             y[i] = make_float2(y[i].x - up.x, y[i].y - up.y);
           }
           if (!fresh) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) lsum[i] = __fmul2_rn(lsum[i], *reinterpret_cast<const float2*>(red_alpha + hb + 2 * i));
+            for (int i = 0; i < 16; ++i) lsum[i] = __fmul2_rn(lsum[i], *reinterpret_cast<const float2*>(red_alpha + hb + 2 * i));
             pv_wait(g - 1);
             tc_fence_after();
 #pragma unroll 1
-            for (int ch = 0; ch < 2; ++ch) {
+            for (int ch = 0; ch < 4; ++ch) {  // half ch >> 1, 16 heads
+              if (16 * (ch & 1) >= hw) continue;
+              const uint32_t addr = o_addr + 64 * (ch >> 1) + 16 * (ch & 1);
+              const float* al = red_alpha + hb + 16 * (ch & 1);
+              const float r = F8 ? red_ref[2 * (mb ^ 1) + (ch >> 1)] / red_ref[2 * mb + (ch >> 1)] : 1.0f;
               uint32_t o[16];
-              tmem_ld32_x16(o_addr + 16 * ch, o);
+              tmem_ld32_x16(addr, o);
               tc_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = f2u(u2f(o[i]) * (red_alpha[ob + 16 * ch + i] * rescale));
-              tmem_st32_x16(o_addr + 16 * ch, o);
+              for (int i = 0; i < 16; ++i) o[i] = f2u(u2f(o[i]) * (al[i] * r));
+              tmem_st32_x16(addr, o);
             }
             tc_wait_st();
           }
@@ -1286,105 +1291,114 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         }
         float2 wf = make_float2(1.0f, 1.0f);  // FP8: the key's scales relative to the references
         if (F8) wf = __fmul2_rn(scl, *reinterpret_cast<const float2*>(red_wf + 2 * mb));
-        if (used) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            y[i] = make_float2(ex2_approx(y[i].x), ex2_approx(y[i].y));
-            lsum[i] = __fadd2_rn(lsum[i], y[i]);
+        for (int ch = 0; ch < 2; ++ch) {
+          if (ch < nch) {
+#pragma unroll
+            for (int i = 8 * ch; i < 8 * ch + 8; ++i) {
+              y[i] = make_float2(ex2_approx(y[i].x), ex2_approx(y[i].y));
+              lsum[i] = __fadd2_rn(lsum[i], y[i]);
+            }
           }
         }
         // the weights' buffer is free once the value product that read it is complete
         if (g >= C::PBUF) pv_wait(g - C::PBUF);
         uint8_t* prow = smem + C::P_OFF + (g % C::PBUF) * C::P_BYTES + tr * 128;
         const int sw = tr & 7;
-        if (used) {
 #pragma unroll
-          for (int h = 0; h < C::PN; ++h) {
-            uint32_t w[8];
-            const float wh = h == 0 ? wf.x : wf.y;
+        for (int ch = 0; ch < 2; ++ch) {
+          if (ch < nch) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              if (F8) {
-                const float2 v = __fmul2_rn(y[i], make_float2(wh, wh));
-                w[i] = f32x2_to_f16x2(v.x, v.y);
-              } else {
-                w[i] = f32x2_to_bf16x2(y[i].x, y[i].y);
+            for (int h = 0; h < C::PN; ++h) {
+              uint32_t w[8];
+              const float wh = h == 0 ? wf.x : wf.y;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                if (F8) {
+                  const float2 v = __fmul2_rn(y[8 * ch + i], make_float2(wh, wh));
+                  w[i] = f32x2_to_f16x2(v.x, v.y);
+                } else {
+                  w[i] = f32x2_to_bf16x2(y[8 * ch + i].x, y[8 * ch + i].y);
+                }
               }
+              uint8_t* d = prow + h * (kBN * 128);
+              const int gr = (hb >> 3) + 2 * ch;
+              *reinterpret_cast<uint4*>(d + ((gr ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(d + (((gr + 1) ^ sw) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
             }
-            uint8_t* d = prow + h * (kBN * 128);
-            *reinterpret_cast<uint4*>(d + (((2 * hq) ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4*>(d + (((2 * hq + 1) ^ sw) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
           }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full(g % C::PBUF));
       }
-      // ---- the segment's end: sums over the keys, then this warp's columns of O^T
+      // ---- the segment's end: sums over the keys, then the group's columns of O^T
       {
-        // reduce-scatter over the lanes: lanes 2i and 2i + 1 end with the warp's sum of head i
-        float v[16];
+        // reduce-scatter over the lanes: lane i ends with the warp's sum of head i
+        float v[32];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 16; ++i) {
           v[2 * i] = lsum[i].x;
           v[2 * i + 1] = lsum[i].y;
         }
 #pragma unroll
-        for (int w = 8; w > 0; w >>= 1) {
-          const bool upper = lane & (2 * w);
+        for (int w = 16; w > 0; w >>= 1) {
+          const bool upper = lane & w;
 #pragma unroll
           for (int i = 0; i < w; ++i)
-            v[i] = (upper ? v[i + w] : v[i]) + __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[i + w], 2 * w);
+            v[i] = (upper ? v[i + w] : v[i]) + __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[i + w], w);
         }
-        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
-        if ((lane & 1) == 0) red_part[64 * qd + hb + (lane >> 1)] = v[0];
+        if (lane < hw) red_part[64 * qd + hb + lane] = v[0];
       }
-      softmax_sync();
+      group_sync(hq);
       const int part = 2 * cta + (s.kind == 1 ? 1 : 0);
-      if (sid < kHG) {
-        const float L = (red_part[sid] + red_part[64 + sid]) + (red_part[128 + sid] + red_part[192 + sid]);
-        const float m = -red[64 * mb + sid];
-        red[64 * mb + sid] = 0.0f;  // for the next segment
-        red_inv[sid] = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);
+      if (gid < hw) {
+        const int h = hb + gid;
+        const float L = (red_part[h] + red_part[64 + h]) + (red_part[128 + h] + red_part[192 + h]);
+        const float m = -red[64 * mb + h];
+        red[64 * mb + h] = 0.0f;  // for the next segment
+        red_inv[h] = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);
         if (s.kind != 0) {
-          p.ws_ml[(int64_t)part * 2 * kHG + sid] = L == 0.0f ? kNoMax : m;
-          p.ws_ml[(int64_t)part * 2 * kHG + kHG + sid] = L;
-        } else if (p.lse && sid < heads) {
-          p.lse[s.t * p.lse_st + s.hg * kHG + sid] = L == 0.0f ? -INFINITY : (m + log2f(L)) * kLn2;
+          p.ws_ml[(int64_t)part * 2 * kHG + h] = L == 0.0f ? kNoMax : m;
+          p.ws_ml[(int64_t)part * 2 * kHG + kHG + h] = L;
+        } else if (p.lse && h < heads) {
+          p.lse[s.t * p.lse_st + s.hg * kHG + h] = L == 0.0f ? -INFINITY : (m + log2f(L)) * kLn2;
         }
       }
-      softmax_sync();
+      group_sync(hq);
       if (s.ntiles > 0) pv_wait(g - 1);
       tc_fence_after();
-      // FP8: weights were relative to the half's reference scale
-      const float back = F8 && !fresh ? red_ref[2 * mb + oh] * (1.0f / (1 << kWeightShift)) : 1.0f;
-      const int dv = 128 * oh + tr;
       uint16_t* orow = p.out + (int64_t)s.t * p.out_st + (int64_t)s.hg * kHG * p.out_sh;
-      float* prt = p.ws_o + (int64_t)part * kHG * kD + dv;
 #pragma unroll 1
-      for (int h0 = ob; h0 < min(heads, ob + 32); h0 += 16) {
+      for (int ch = 0; ch < 4; ++ch) {  // half ch >> 1, 16 heads
+        const int h0 = hb + 16 * (ch & 1), half = ch >> 1;
+        if (h0 >= heads || 16 * (ch & 1) >= hw) continue;
         uint32_t o[16];
         if (s.ntiles > 0) {
-          tmem_ld32_x16(o_addr + h0 - ob, o);
+          tmem_ld32_x16(o_addr + 64 * half + 16 * (ch & 1), o);
           tc_wait_ld();
         } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[i] = 0u;
         }
+        // FP8: weights were relative to the half's reference scale
+        const float back = F8 && !fresh ? red_ref[2 * mb + half] * (1.0f / (1 << kWeightShift)) : 1.0f;
+        const int dv = 128 * half + tr;
         if (s.kind != 0) {
+          float* prt = p.ws_o + ((int64_t)part * kHG + h0) * kD + dv;
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (h0 + i < heads) prt[(h0 + i) * kD] = u2f(o[i]) * back;
+            if (h0 + i < heads) prt[i * kD] = u2f(o[i]) * back;
         } else {
           // lanes 2i and 2i + 1 hold neighbouring columns: they swap heads, so that each writes
           // two columns of one head
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const float e = u2f(o[2 * i]) * back * red_inv[h0 + 2 * i];
-            const float f = u2f(o[2 * i + 1]) * back * red_inv[h0 + 2 * i + 1];
+            const float d = u2f(o[2 * i + 1]) * back * red_inv[h0 + 2 * i + 1];
             const bool odd = lane & 1;
-            const float other = __shfl_xor_sync(0xffffffffu, odd ? e : f, 1);
-            const uint32_t w = odd ? f32x2_to_bf16x2(other, f) : f32x2_to_bf16x2(e, other);
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? e : d, 1);
+            const uint32_t w = odd ? f32x2_to_bf16x2(other, d) : f32x2_to_bf16x2(e, other);
             const int h = h0 + 2 * i + (odd ? 1 : 0);
             if (h < heads) *reinterpret_cast<uint32_t*>(orow + h * p.out_sh + (dv & ~1)) = w;
           }
@@ -1402,103 +1416,168 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
 }
 
 // Joins the parts of each split row in the order of the parts. Block (x, y) takes row x (when there
-// are at most G rows; else the row that CTA x starts) and heads y * 64 / gridDim.y ..
-// 256 threads: 64 columns of four times 4 parts at a time, heads one after the other.
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Params p) {
+// are at most G rows; else the row that CTA x starts) and 64 / gridDim.y of its heads: 16 at once when
+// there are at most kFewParts parts, else one after the other. 1024 threads: 64 times four columns, 16 parts at a time, so that a row split over the whole
+// device (152 parts) is ten loads per thread, all in flight at once.
+constexpr int kJoinThreads = 1024;
+constexpr int kFewParts = 8;
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p) {
   __shared__ int s_part[kMaxCtas + 1];
   __shared__ float s_w[kMaxCtas + 1];
-  __shared__ int s_fin[8], s_cnt[8], s_n;
-  __shared__ float4 s_acc[4][64];
-  __shared__ float s_L;
+  __shared__ int s_fin[8], s_cnt[8];
+  __shared__ float s_red[2][8];
+  __shared__ float4 s_acc[kJoinThreads / 64][64];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int tid = threadIdx.x;
   const int64_t nrows = p.T * p.HG;
-  int64_t row;
-  int c;
-  if (nrows <= p.G) {
-    row = blockIdx.x;
+  const bool by_row = nrows <= p.G;
+  // the CTAs after the first that hold a part: every one that continues the row, to the one that
+  // finishes it (thread t < 256 looks at CTA c + 1 + t; the chain's start is read meanwhile)
+  int c = blockIdx.x;
+  int64_t row = blockIdx.x;
+  if (by_row) {
     c = p.ws_first[row];
     if (c < 0) return;
   } else {
-    c = blockIdx.x;
     row = p.ws_tail[c];
     if (row < 0) return;
   }
-  // parts in order: the start, then every CTA that continues the row, to the one that finishes it
-  {
-    const int lane = tid & 31, warp = tid >> 5;
-    const int k = c + 1 + tid;
-    const int h = k < p.G ? p.ws_head[k] : 0;
-    const uint32_t fin = __ballot_sync(0xffffffffu, h == 2);
+  const int k = c + 1 + tid;
+  const int hd = tid < 256 && k < p.G ? p.ws_head[k] : 0;
+  if (warp < 8) {
+    const uint32_t fin = __ballot_sync(0xffffffffu, hd == 2);
     if (lane == 0) s_fin[warp] = fin ? 32 * warp + __ffs(fin) - 1 : 1 << 20;
-    __syncthreads();
-    int last = s_fin[0];
-#pragma unroll
-    for (int w = 1; w < 8; ++w) last = min(last, s_fin[w]);
-    const uint32_t mem = __ballot_sync(0xffffffffu, h != 0 && tid <= last);
-    if (lane == 0) s_cnt[warp] = __popc(mem);
-    __syncthreads();
-    int at = 1, total = 1;
-    for (int w = 0; w < 8; ++w) {
-      if (w < warp) at += s_cnt[w];
-      total += s_cnt[w];
-    }
-    if ((mem >> lane) & 1) s_part[at + __popc(mem & ((1u << lane) - 1u))] = 2 * k;
-    if (tid == 0) {
-      s_part[0] = 2 * c + 1;
-      s_n = total;
-    }
   }
   __syncthreads();
-  const int n = s_n;
+  int last = s_fin[0];
+#pragma unroll
+  for (int w = 1; w < 8; ++w) last = min(last, s_fin[w]);
+  uint32_t mem = 0;
+  if (warp < 8) {
+    mem = __ballot_sync(0xffffffffu, hd != 0 && tid <= last);
+    if (lane == 0) s_cnt[warp] = __popc(mem);
+  }
+  __syncthreads();
+  int at = 1, n = 1;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    if (w < warp) at += s_cnt[w];
+    n += s_cnt[w];
+  }
+  if (warp < 8 && ((mem >> lane) & 1)) s_part[at + __popc(mem & ((1u << lane) - 1u))] = 2 * k;
+  if (tid == 0) s_part[0] = 2 * c + 1;
+  __syncthreads();
   const int64_t t = p.HG == 1 ? row : row >> 1;
   const int hg = p.HG == 1 ? 0 : (int)(row & 1);
   const int heads = min(kHG, p.H - hg * kHG);
   const int per = kHG / gridDim.y;
+  const int col = tid & 63, pg = tid >> 6;
+  if (n <= kFewParts) {
+    // few parts: 16 heads at a time, 64 threads each, which read the parts' maxima and sums themselves
+    for (int h = blockIdx.y * per + pg; h < (int)(blockIdx.y + 1) * per && h < heads; h += kJoinThreads / 64) {
+      float m[kFewParts], l[kFewParts];
+      float4 v[kFewParts];
+      float M = kNoMax;
+#pragma unroll
+      for (int i = 0; i < kFewParts; ++i) {
+        m[i] = kNoMax;
+        l[i] = 0.0f;
+        if (i < n) {
+          const int64_t part = s_part[i];
+          m[i] = p.ws_ml[part * 2 * kHG + h];
+          l[i] = p.ws_ml[part * 2 * kHG + kHG + h];
+          v[i] = *reinterpret_cast<const float4*>(p.ws_o + (part * kHG + h) * kD + 4 * col);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kFewParts; ++i) M = fmaxf(M, m[i]);
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float L = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kFewParts; ++i) {
+        if (i < n) {
+          const float w = ex2_approx(m[i] - M);
+          L = fmaf(w, l[i], L);
+          acc.x = fmaf(w, v[i].x, acc.x);
+          acc.y = fmaf(w, v[i].y, acc.y);
+          acc.z = fmaf(w, v[i].z, acc.z);
+          acc.w = fmaf(w, v[i].w, acc.w);
+        }
+      }
+      const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);
+      *reinterpret_cast<uint2*>(p.out + t * p.out_st + (int64_t)(hg * kHG + h) * p.out_sh + 4 * col) =
+          make_uint2(f32x2_to_bf16x2(acc.x * inv, acc.y * inv), f32x2_to_bf16x2(acc.z * inv, acc.w * inv));
+      if (col == 0 && p.lse) p.lse[t * p.lse_st + hg * kHG + h] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
+    }
+    return;
+  }
+  const int my_part = tid < n ? s_part[tid] : -1;  // n <= kMaxCtas + 1 < 256
   for (int h = blockIdx.y * per; h < (int)(blockIdx.y + 1) * per && h < heads; ++h) {
-    if (tid < 32) {
-      float M = kNoMax, L = 0.0f;
-      for (int i = tid; i < n; i += 32) M = fmaxf(M, p.ws_ml[(int64_t)s_part[i] * 2 * kHG + h]);
+    // the parts' weights 2^(m - M), M their largest maximum, and the sum of the weighted sums
+    float m = kNoMax, l = 0.0f;
+    if (my_part >= 0) {
+      m = p.ws_ml[(int64_t)my_part * 2 * kHG + h];
+      l = p.ws_ml[(int64_t)my_part * 2 * kHG + kHG + h];
+    }
+    // the first loads of the sum do not wait for the weights
+    float4 v[4];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      for (int i = tid; i < n; i += 32) {
-        const float w = ex2_approx(p.ws_ml[(int64_t)s_part[i] * 2 * kHG + h] - M);
-        s_w[i] = w;
-        L += w * p.ws_ml[(int64_t)s_part[i] * 2 * kHG + kHG + h];
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int q = pg + 16 * i;
+      if (q < n) v[i] = *reinterpret_cast<const float4*>(p.ws_o + ((int64_t)s_part[q] * kHG + h) * kD + 4 * col);
+    }
+    if (warp < 8) {
+      float x = m;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-      if (tid == 0) {
-        s_L = L;
-        if (p.lse) p.lse[t * p.lse_st + hg * kHG + h] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
-      }
+      for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+      if (lane == 0) s_red[0][warp] = x;
     }
     __syncthreads();
-    const int col = tid & 63, pg = tid >> 6;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int i = pg; i < n; i += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(p.ws_o + ((int64_t)s_part[i] * kHG + h) * kD + 4 * col);
-      const float w = s_w[i];
-      acc.x = fmaf(w, v.x, acc.x);
-      acc.y = fmaf(w, v.y, acc.y);
-      acc.z = fmaf(w, v.z, acc.z);
-      acc.w = fmaf(w, v.w, acc.w);
+    float M = s_red[0][0];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) M = fmaxf(M, s_red[0][w]);
+    if (warp < 8) {
+      const float w = ex2_approx(m - M);
+      if (my_part >= 0) s_w[tid] = w;
+      float x = w * l;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      if (lane == 0) s_red[1][warp] = x;
     }
-    s_acc[pg][col] = acc;
+    __syncthreads();
+    float L = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) L += s_red[1][w];
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int q0 = pg; q0 < n; q0 += 64) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int q = q0 + 16 * i;
+        if (q < n) {
+          if (q0 != pg) v[i] = *reinterpret_cast<const float4*>(p.ws_o + ((int64_t)s_part[q] * kHG + h) * kD + 4 * col);
+          const float w = s_w[q];
+          acc.x = fmaf(w, v[i].x, acc.x);
+          acc.y = fmaf(w, v[i].y, acc.y);
+          acc.z = fmaf(w, v[i].z, acc.z);
+          acc.w = fmaf(w, v[i].w, acc.w);
+        }
+      }
+    }
+    const int groups = n < 16 ? n : 16;  // part groups that hold anything
+    if (pg < groups) s_acc[pg][col] = acc;
     __syncthreads();
     if (pg == 0) {
-      const float L = s_L, inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);
-#pragma unroll
-      for (int i = 1; i < 4; ++i) {
-        const float4 v = s_acc[i][col];
-        acc.x += v.x;
-        acc.y += v.y;
-        acc.z += v.z;
-        acc.w += v.w;
+      const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);
+      for (int i = 1; i < groups; ++i) {
+        const float4 x = s_acc[i][col];
+        acc.x += x.x;
+        acc.y += x.y;
+        acc.z += x.z;
+        acc.w += x.w;
       }
       *reinterpret_cast<uint2*>(p.out + t * p.out_st + (int64_t)(hg * kHG + h) * p.out_sh + 4 * col) =
           make_uint2(f32x2_to_bf16x2(acc.x * inv, acc.y * inv), f32x2_to_bf16x2(acc.z * inv, acc.w * inv));
+      if (tid == 0 && p.lse) p.lse[t * p.lse_st + hg * kHG + h] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
     }
     __syncthreads();
   }
@@ -1717,14 +1796,15 @@ extern "C" dsa_status_t dsa_paged_attn(const dsa_paged_args_t* a, void* stream) 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if ((st = paged::launch<false>(p, a->kind, s)) != DSA_OK) return st;
   if (p.G == 1) return DSA_OK;  // no border, nothing to join
-  // the join's blocks: a row (or CTA) each, its heads over as many blocks as fill the device
+  // the join's blocks: a row (or CTA) each, its heads over as many blocks as fill the device once (most
+  // blocks of many rows find nothing to join and only cost their launch)
   const int64_t nrows = p.T * p.HG;
   const int x = (int)(nrows <= p.G ? nrows : p.G);
   int y = 64;
-  while (y > 8 && x * y > 16 * dev.sm_count) y >>= 1;
+  while (y > 2 && x * y > 2 * dev.sm_count) y >>= 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)x, (unsigned)y);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(paged::kJoinThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
