@@ -513,117 +513,135 @@ def dsa_proj_gemm(x_codes, x_scales, w_codes, w_scales, *, out=None, workspace=N
 
 
 # ------------------------------------------------------- dense attention over the paged cache --
-def _need_on(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}: every tensor must be on one device")
+# A decode step calls these once per layer, so the checks touch each tensor a few times only.
+def _cuda_index(t, name: str, dtype) -> int:
+    """The tensor's CUDA device index; raises unless it is a CUDA tensor of the dtype."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    return t.get_device()
 
 
-def _need_vector(name, t, n):
-    """A contiguous int32 CUDA tensor of n entries (or None)."""
-    import torch
+def _ptr_on(t, name: str, dtype, index: int):
+    """data_ptr() of a tensor that must be on the device, or None."""
+    if t is None:
+        return None
+    i = _cuda_index(t, name, dtype)
+    if i != index:
+        raise ValueError(f"{name} is on cuda:{i}, not on cuda:{index}: every tensor must be on one device")
+    return t.data_ptr()
 
-    _need_cuda(name, t, torch.int32)
-    if t is not None and (t.dim() != 1 or t.numel() != n or not t.is_contiguous()):
+
+def _vector(t, name: str, n: int, dtype, index: int):
+    """data_ptr() of a contiguous tensor of n entries, or None."""
+    if t is None:
+        return None
+    p = _ptr_on(t, name, dtype, index)
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of {n} entries")
+    return p
 
 
-def _need_rows(name, t, rows=None, cols=None):
-    if t is not None and (t.dim() != 2 or t.stride(1) != 1 or (rows is not None and t.shape[0] != rows) or
-                          (cols is not None and t.shape[1] < cols)):
-        raise ValueError(f"{name} must be [{rows if rows is not None else 'rows'}, "
-                         f"{'>=' + str(cols) if cols is not None else 'columns'}], contiguous along its last dimension")
+def _rows(t, name: str, dtype, index: int, rows=None, cols: int = 0):
+    """(data_ptr(), row stride, rows, columns) of a matrix contiguous along its columns."""
+    p = _ptr_on(t, name, dtype, index)
+    shape = t.shape
+    if len(shape) != 2 or (rows is not None and shape[0] != rows) or shape[1] < cols:
+        raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, {'columns' if cols == 0 else f'>={cols}'}]")
+    st = t.stride()
+    if st[1] != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+    # a single row has no second one to step to: torch may report any stride
+    return p, (st[0] if shape[0] > 1 else shape[1]), shape[0], shape[1]
 
 
-def _cache_rows(cache, kind, d):
-    """The cache as [num_slots, row] rows, checked."""
+def _cache_rows(cache, kind: int, row: int):
+    """(device index, data_ptr(), slots) of a cache of contiguous rows."""
     import torch
 
-    if kind not in (CACHE_BF16, CACHE_FP8_SCALED):
+    if kind == CACHE_FP8_SCALED:
+        index = _cuda_index(cache, "cache", torch.uint8)
+    elif kind == CACHE_BF16:
+        index = _cuda_index(cache, "cache", torch.bfloat16)
+    else:
         raise ValueError("kind must be CACHE_BF16 or CACHE_FP8_SCALED")
-    _need_cuda("cache", cache, torch.uint8 if kind == CACHE_FP8_SCALED else torch.bfloat16)
-    if cache.dim() == 3 and cache.shape[1] == 1:
-        cache = cache.view(cache.shape[0], -1)
-    if cache.dim() != 2 or not cache.is_contiguous() or cache.shape[1] != d:
-        raise ValueError(f"cache must be contiguous [num_slots, {d}]")
-    return cache
+    shape = cache.shape
+    if len(shape) == 3 and shape[1] == 1:
+        shape = (shape[0], shape[2])
+    if len(shape) != 2 or shape[1] != row or not cache.is_contiguous():
+        raise ValueError(f"cache must be contiguous [num_slots, {row}]")
+    return index, cache.data_ptr(), shape[0]
 
 
-def _row_stride(t):
-    # a single row has no second one to step to: any stride is as good, and torch may report 1
-    return t.shape[1] if t.shape[0] <= 1 else t.stride(0)
+class _on_device:
+    """Makes the device current, unless it is already."""
+
+    def __init__(self, index: int):
+        import torch
+
+        self.guard = None if torch.cuda.current_device() == index else torch.cuda.device(index)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+_PAGED_WS = {}
+
+
+def _workspace_for(workspace, nbytes: int, index: int):
+    """(tensor, data_ptr(), bytes): the caller's workspace, or memory of the current stream for this
+    call. The caching allocator orders its reuse with the stream, and inside a graph capture it
+    belongs to the graph, so no two calls that may overlap share one."""
+    import torch
+
+    if workspace is None:
+        workspace = torch.empty(nbytes if nbytes > 0 else 1, dtype=torch.uint8, device=index)
+        return workspace, workspace.data_ptr(), nbytes
+    p = _ptr_on(workspace, "workspace", torch.uint8, index)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace, p, workspace.numel()
 
 
 def _paged_args(q, cache, kind, block_table, lengths, sm_scale, page_size, starts, req_of_token, logit_cap, slopes,
                 q_positions, key_positions, lse, error_word):
+    """(device index, the filled DsaPagedArgs); ``out`` and the workspace are left to the caller."""
     import torch
 
-    _need_cuda("q", q, torch.bfloat16)
-    if q.dim() != 3 or q.shape[2] != 256 or q.stride(2) != 1:
-        raise ValueError("q must be [T, H, 256], contiguous along its last dimension")
-    T, H = q.shape[0], q.shape[1]
-    cache = _cache_rows(cache, kind, 264 if kind == CACHE_FP8_SCALED else 256)
-    _need_vector("lengths", lengths, T)
-    _need_vector("starts", starts, T)
-    _need_vector("req_of_token", req_of_token, T)
-    _need_vector("q_positions", q_positions, T)
-    _need_cuda("block_table", block_table, torch.int32)
-    _need_rows("block_table", block_table)
-    _need_cuda("key_positions", key_positions, torch.int32)
-    _need_rows("key_positions", key_positions, None if block_table is None else block_table.shape[0])
-    _need_cuda("slopes", slopes, torch.float32)
-    if slopes is not None and (slopes.dim() != 1 or slopes.numel() != H or not slopes.is_contiguous()):
-        raise ValueError("slopes must be a contiguous tensor of H entries")
-    _need_cuda("lse", lse, torch.float32)
+    i32 = torch.int32
+    index, cache_ptr, slots = _cache_rows(cache, kind, 264 if kind == CACHE_FP8_SCALED else 256)
+    q_ptr = _ptr_on(q, "q", torch.bfloat16, index)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != 256:
+        raise ValueError("q must be [T, H, 256]")
+    T, H = shape[0], shape[1]
+    st = q.stride()
+    if st[2] != 1:
+        raise ValueError("q must be contiguous along its last dimension")
+    # without a table or key positions every request reads the same slots: no row to run out of
+    bt_ptr, bt_stride, pages, requests = None, 0, 0, 1 << 31
+    if block_table is not None:
+        bt_ptr, bt_stride, requests, pages = _rows(block_table, "block_table", i32, index)
+    kp_ptr, kp_stride, kp_width = None, 0, 0
+    if key_positions is not None:
+        kp_ptr, kp_stride, requests, kp_width = _rows(key_positions, "key_positions", i32, index,
+                                                      None if block_table is None else requests)
     if lse is not None and (tuple(lse.shape) != (T, H) or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous [T, H] tensor")
-    _need_cuda("error_word", error_word, torch.int32)
-    _need_on(q.device, cache=cache, block_table=block_table, lengths=lengths, starts=starts, req_of_token=req_of_token,
-             slopes=slopes, q_positions=q_positions, key_positions=key_positions, lse=lse, error_word=error_word)
-    a = DsaPagedArgs()
-    a.q = q.data_ptr()
-    a.q_stride_t, a.q_stride_h = (q.stride(0) if T > 1 else 0), (q.stride(1) if H > 1 else 0)
-    a.T, a.H = T, H
-    a.cache, a.kind, a.num_slots = cache.data_ptr(), kind, cache.shape[0]
-    a.d_nope, a.d_rope, a.d_v = 256, 0, 256
-    a.lengths = lengths.data_ptr()
-    # without a table or key positions every request reads the same slots: no row to run out of
-    a.num_requests = 1 << 31
-    if block_table is not None:
-        a.block_table, a.bt_stride = block_table.data_ptr(), _row_stride(block_table)
-        a.page_size, a.max_pages = page_size, block_table.shape[1]
-        a.num_requests = block_table.shape[0]
-    if key_positions is not None:
-        a.key_positions, a.kp_stride = key_positions.data_ptr(), _row_stride(key_positions)
-        a.kp_width = key_positions.shape[1]
-        a.num_requests = key_positions.shape[0]
-    if starts is not None:
-        a.starts = starts.data_ptr()
-    if req_of_token is not None:
-        a.req_of_token = req_of_token.data_ptr()
-    if q_positions is not None:
-        a.q_positions = q_positions.data_ptr()
-    a.sm_scale, a.logit_cap = float(sm_scale), float(logit_cap)
-    if slopes is not None:
-        a.slopes = slopes.data_ptr()
-    if lse is not None:
-        a.lse = lse.data_ptr()
-    if error_word is not None:
-        a.error_word = error_word.data_ptr()
-    return a
-
-
-def _give_workspace(a, workspace, nbytes, device):
-    """``workspace``, or memory of the current stream for this call: the caching allocator orders
-    its reuse with the stream, and inside a graph capture it belongs to the graph."""
-    import torch
-
-    _need_cuda("workspace", workspace, torch.uint8)
-    if workspace is None:
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
-    _need_on(device, workspace=workspace)
-    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
-    return workspace
+    a = DsaPagedArgs(
+        q_ptr, st[0] if T > 1 else 0, st[1] if H > 1 else 0, T, H, cache_ptr, kind, slots, 256, 0, 256,
+        bt_ptr, bt_stride, page_size, pages, requests, _vector(req_of_token, "req_of_token", T, i32, index),
+        _vector(starts, "starts", T, i32, index), _vector(lengths, "lengths", T, i32, index),
+        _vector(q_positions, "q_positions", T, i32, index), kp_ptr, kp_stride, kp_width, sm_scale, logit_cap,
+        _vector(slopes, "slopes", H, torch.float32, index), None, 0, 0, _ptr_on(lse, "lse", torch.float32, index), None, 0,
+        _ptr_on(error_word, "error_word", i32, index))
+    return index, a
 
 
 def dsa_paged_attn_workspace_size(T: int, H: int = 64) -> int:
@@ -647,21 +665,26 @@ def dsa_paged_attn(q, cache, kind: int, block_table, lengths, sm_scale: float, *
     [T, H] receives the natural log sum of exp(score)."""
     import torch
 
-    a = _paged_args(q, cache, kind, block_table, lengths, sm_scale, page_size, starts, req_of_token, logit_cap, slopes,
-                    q_positions, key_positions, lse, error_word)
+    index, a = _paged_args(q, cache, kind, block_table, lengths, sm_scale, page_size, starts, req_of_token, logit_cap,
+                           slopes, q_positions, key_positions, lse, error_word)
+    T, H = a.T, a.H
     if out is None:
-        out = torch.empty((a.T, a.H, 256), dtype=torch.bfloat16, device=q.device)
-    _need_cuda("out", out, torch.bfloat16)
-    _need_on(q.device, out=out)
-    if tuple(out.shape) != (a.T, a.H, 256) or out.stride(2) != 1:
-        raise ValueError("out must be [T, H, 256], contiguous along its last dimension")
-    a.out = out.data_ptr()
-    a.out_stride_t = out.stride(0) if a.T > 1 else 256 * a.H
-    a.out_stride_h = out.stride(1) if a.H > 1 else 256
-    with torch.cuda.device(q.device):
-        need = 0 if workspace is not None else dsa_paged_attn_workspace_size(a.T, a.H)
-        workspace = _give_workspace(a, workspace, need, q.device)
-        _check(load_library().dsa_paged_attn(ctypes.byref(a), _stream(q.device)), "dsa_paged_attn")
+        out = torch.empty((T, H, 256), dtype=torch.bfloat16, device=index)
+        a.out, a.out_stride_t, a.out_stride_h = out.data_ptr(), 256 * H, 256
+    else:
+        a.out = _ptr_on(out, "out", torch.bfloat16, index)
+        st = out.stride()
+        if tuple(out.shape) != (T, H, 256) or st[2] != 1:
+            raise ValueError("out must be [T, H, 256], contiguous along its last dimension")
+        a.out_stride_t = st[0] if T > 1 else 256 * H
+        a.out_stride_h = st[1] if H > 1 else 256
+    with _on_device(index):
+        need = _PAGED_WS.get(index)
+        if need is None:  # the same for every call on a device
+            need = _PAGED_WS[index] = dsa_paged_attn_workspace_size(1)
+        workspace, a.workspace, a.workspace_bytes = _workspace_for(workspace, need, index)
+        _check((_LIB or load_library()).dsa_paged_attn(ctypes.byref(a), torch.cuda.current_stream(index).cuda_stream),
+               "dsa_paged_attn")
     return out
 
 
@@ -675,20 +698,20 @@ def dsa_paged_attn_mass(q, cache, kind: int, block_table, lengths, sm_scale: flo
 
     if lse is None:
         raise ValueError("lse is required")
-    a = _paged_args(q, cache, kind, block_table, lengths, sm_scale, page_size, starts, req_of_token, logit_cap, slopes,
-                    q_positions, key_positions, lse, error_word)
+    index, a = _paged_args(q, cache, kind, block_table, lengths, sm_scale, page_size, starts, req_of_token, logit_cap,
+                           slopes, q_positions, key_positions, lse, error_word)
+    m_ptr, m_stride, rows, width = _rows(mass, "mass", torch.float32, index,
+                                         None if block_table is None and key_positions is None else a.num_requests)
     if mass_out is None:
-        mass_out = mass
-    for name, t in (("mass", mass), ("mass_out", mass_out)):
-        _need_cuda(name, t, torch.float32)
-        _need_rows(name, t, None if block_table is None and key_positions is None else a.num_requests)
-    _need_on(q.device, mass=mass, mass_out=mass_out)
-    if mass_out.shape != mass.shape:
-        raise ValueError("mass_out must have mass's shape")
-    a.num_requests = mass.shape[0]
-    with torch.cuda.device(q.device):
-        _check(load_library().dsa_paged_attn_mass(ctypes.byref(a), _ptr(mass), _row_stride(mass), _ptr(mass_out),
-                                                  _row_stride(mass_out), mass.shape[1], _stream(q.device)),
+        mass_out, o_ptr, o_stride = mass, m_ptr, m_stride
+    else:
+        o_ptr, o_stride, _, o_width = _rows(mass_out, "mass_out", torch.float32, index, rows)
+        if o_width != width:
+            raise ValueError("mass_out must have mass's shape")
+    a.num_requests = rows
+    with _on_device(index):
+        _check((_LIB or load_library()).dsa_paged_attn_mass(ctypes.byref(a), m_ptr, m_stride, o_ptr, o_stride, width,
+                                                            torch.cuda.current_stream(index).cuda_stream),
                "dsa_paged_attn_mass")
     return mass_out
 
@@ -712,52 +735,38 @@ def dsa_cache_evict(cache, kind: int, block_table, lengths, mass, budget: int = 
     (lengths_out, mass_out, positions_out)."""
     import torch
 
-    row = dsa_cache_row_bytes(kind, d_nope, d_rope)
-    cache = _cache_rows(cache, kind, row if kind == CACHE_FP8_SCALED else row // 2)
-    _need_cuda("mass", mass, torch.float32)
-    _need_rows("mass", mass)
-    R, S = mass.shape
-    lengths_out = lengths if lengths_out is None else lengths_out
-    mass_out = mass if mass_out is None else mass_out
-    positions_out = positions if positions_out is None else positions_out
-    for name, t in (("lengths", lengths), ("budgets", budgets), ("lengths_out", lengths_out)):
-        _need_vector(name, t, R)
-    _need_cuda("block_table", block_table, torch.int32)
-    _need_rows("block_table", block_table, R)
-    _need_cuda("mass_out", mass_out, torch.float32)
-    for name, t in (("positions", positions), ("positions_out", positions_out)):
-        _need_cuda(name, t, torch.int32)
-    for name, t in (("mass_out", mass_out), ("positions", positions), ("positions_out", positions_out)):
-        _need_rows(name, t, R, S)
-    _need_cuda("error_word", error_word, torch.int32)
-    _need_on(cache.device, block_table=block_table, lengths=lengths, budgets=budgets, mass=mass, positions=positions,
-             mass_out=mass_out, positions_out=positions_out, lengths_out=lengths_out, error_word=error_word)
-    a = DsaEvictArgs()
-    a.cache, a.kind, a.num_slots = cache.data_ptr(), kind, cache.shape[0]
-    a.d_nope, a.d_rope = d_nope, d_rope
-    if block_table is not None:
-        a.block_table, a.bt_stride = block_table.data_ptr(), _row_stride(block_table)
-        a.page_size, a.max_pages = page_size, block_table.shape[1]
-    a.num_requests, a.width = R, S
-    a.lengths, a.lengths_out = lengths.data_ptr(), lengths_out.data_ptr()
-    if budgets is not None:
-        a.budgets = budgets.data_ptr()
-    a.budget, a.sink, a.recent = int(budget), int(sink), int(recent)
-
-    # a single row's stride says nothing; one that is at least the width passes the library's check
-    def stride(t):
-        return S if R == 1 else t.stride(0)
-
-    a.mass, a.mass_stride = mass.data_ptr(), stride(mass)
-    a.mass_out, a.mass_out_stride = mass_out.data_ptr(), stride(mass_out)
+    i32, f32 = torch.int32, torch.float32
+    row = d_nope + d_rope if kind == CACHE_BF16 else dsa_packed_row_bytes(d_nope, d_rope)
+    index, cache_ptr, slots = _cache_rows(cache, kind, row)
+    m_ptr, m_stride, R, S = _rows(mass, "mass", f32, index)
+    len_ptr = _vector(lengths, "lengths", R, i32, index)
+    if lengths_out is None:
+        lengths_out, len_out_ptr = lengths, len_ptr
+    else:
+        len_out_ptr = _vector(lengths_out, "lengths_out", R, i32, index)
+    if mass_out is None:
+        mass_out, mo_ptr, mo_stride = mass, m_ptr, m_stride
+    else:
+        mo_ptr, mo_stride, _, _ = _rows(mass_out, "mass_out", f32, index, R, S)
+    p_ptr, p_stride, po_ptr, po_stride = None, 0, None, 0
     if positions is not None:
-        a.positions, a.positions_stride = positions.data_ptr(), stride(positions)
-    if positions_out is not None:
-        a.positions_out, a.positions_out_stride = positions_out.data_ptr(), stride(positions_out)
-    if error_word is not None:
-        a.error_word = error_word.data_ptr()
-    with torch.cuda.device(cache.device):
+        p_ptr, p_stride, _, _ = _rows(positions, "positions", i32, index, R, S)
+    if positions_out is None:
+        positions_out, po_ptr, po_stride = positions, p_ptr, p_stride
+    else:
+        po_ptr, po_stride, _, _ = _rows(positions_out, "positions_out", i32, index, R, S)
+    if R <= 1:  # a single row's stride says nothing; the width passes the library's checks
+        m_stride = mo_stride = p_stride = po_stride = S
+    bt_ptr, bt_stride, pages = None, 0, 0
+    if block_table is not None:
+        bt_ptr, bt_stride, _, pages = _rows(block_table, "block_table", i32, index, R)
+    a = DsaEvictArgs(cache_ptr, kind, slots, d_nope, d_rope, bt_ptr, bt_stride, page_size, pages, R, len_ptr,
+                     _vector(budgets, "budgets", R, i32, index), budget, sink, recent, S, m_ptr, m_stride, p_ptr, p_stride,
+                     mo_ptr, mo_stride, po_ptr, po_stride, len_out_ptr, None, 0,
+                     _ptr_on(error_word, "error_word", i32, index))
+    with _on_device(index):
         need = 0 if workspace is not None else dsa_cache_evict_workspace_size(R, S)
-        workspace = _give_workspace(a, workspace, need, cache.device)
-        _check(load_library().dsa_cache_evict(ctypes.byref(a), _stream(cache.device)), "dsa_cache_evict")
+        workspace, a.workspace, a.workspace_bytes = _workspace_for(workspace, need, index)
+        _check((_LIB or load_library()).dsa_cache_evict(ctypes.byref(a), torch.cuda.current_stream(index).cuda_stream),
+               "dsa_cache_evict")
     return lengths_out, mass_out, positions_out

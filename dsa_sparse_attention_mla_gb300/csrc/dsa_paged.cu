@@ -1416,10 +1416,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
 }
 
 // Joins the parts of each split row in the order of the parts. Block (x, y) takes row x (when there
-// are at most G rows; else the row that CTA x starts) and 64 / gridDim.y of its heads: 16 at once when
-// there are at most kFewParts parts, else one after the other. 1024 threads: 64 times four columns, 16 parts at a time, so that a row split over the whole
-// device (152 parts) is ten loads per thread, all in flight at once.
-constexpr int kJoinThreads = 1024;
+// are at most G rows; else the row that CTA x starts) and 64 / gridDim.y of its heads: 4 at once when
+// there are at most kFewParts parts, else one after the other with 4 parts at a time, 64 threads for
+// the 256 columns of each.
+constexpr int kJoinThreads = 256;
 constexpr int kFewParts = 8;
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p) {
   __shared__ int s_part[kMaxCtas + 1];
@@ -1473,7 +1473,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const int per = kHG / gridDim.y;
   const int col = tid & 63, pg = tid >> 6;
   if (n <= kFewParts) {
-    // few parts: 16 heads at a time, 64 threads each, which read the parts' maxima and sums themselves
+    // few parts: 4 heads at a time, 64 threads each, which read the parts' maxima and sums themselves
     for (int h = blockIdx.y * per + pg; h < (int)(blockIdx.y + 1) * per && h < heads; h += kJoinThreads / 64) {
       float m[kFewParts], l[kFewParts];
       float4 v[kFewParts];
@@ -1520,10 +1520,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       l = p.ws_ml[(int64_t)my_part * 2 * kHG + kHG + h];
     }
     // the first loads of the sum do not wait for the weights
-    float4 v[4];
+    constexpr int kGroups = kJoinThreads / 64, kAhead = 8;
+    float4 v[kAhead];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int q = pg + 16 * i;
+    for (int i = 0; i < kAhead; ++i) {
+      const int q = pg + kGroups * i;
       if (q < n) v[i] = *reinterpret_cast<const float4*>(p.ws_o + ((int64_t)s_part[q] * kHG + h) * kD + 4 * col);
     }
     if (warp < 8) {
@@ -1549,12 +1550,18 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 #pragma unroll
     for (int w = 0; w < 8; ++w) L += s_red[1][w];
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int q0 = pg; q0 < n; q0 += 64) {
+    for (int q0 = pg; q0 < n; q0 += kGroups * kAhead) {
+      if (q0 != pg) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int q = q0 + 16 * i;
+        for (int i = 0; i < kAhead; ++i) {
+          const int q = q0 + kGroups * i;
+          if (q < n) v[i] = *reinterpret_cast<const float4*>(p.ws_o + ((int64_t)s_part[q] * kHG + h) * kD + 4 * col);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int q = q0 + kGroups * i;
         if (q < n) {
-          if (q0 != pg) v[i] = *reinterpret_cast<const float4*>(p.ws_o + ((int64_t)s_part[q] * kHG + h) * kD + 4 * col);
           const float w = s_w[q];
           acc.x = fmaf(w, v[i].x, acc.x);
           acc.y = fmaf(w, v[i].y, acc.y);
@@ -1563,7 +1570,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         }
       }
     }
-    const int groups = n < 16 ? n : 16;  // part groups that hold anything
+    const int groups = kGroups;
     if (pg < groups) s_acc[pg][col] = acc;
     __syncthreads();
     if (pg == 0) {
@@ -1796,12 +1803,11 @@ extern "C" dsa_status_t dsa_paged_attn(const dsa_paged_args_t* a, void* stream) 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if ((st = paged::launch<false>(p, a->kind, s)) != DSA_OK) return st;
   if (p.G == 1) return DSA_OK;  // no border, nothing to join
-  // the join's blocks: a row (or CTA) each, its heads over as many blocks as fill the device once (most
-  // blocks of many rows find nothing to join and only cost their launch)
+  // the join's blocks: a row (or CTA) each, times a head each where few rows can have many parts, four
+  // heads (one pass over few parts) where there are more rows
   const int64_t nrows = p.T * p.HG;
   const int x = (int)(nrows <= p.G ? nrows : p.G);
-  int y = 64;
-  while (y > 2 && x * y > 2 * dev.sm_count) y >>= 1;
+  const int y = x <= 16 ? 64 : 16;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)x, (unsigned)y);
   cfg.blockDim = dim3(paged::kJoinThreads);
