@@ -8,25 +8,35 @@
 // as of the other, and sources and destinations are disjoint, so rows move in place and at once
 // and no more than the evicted number of them.
 //
-// One CTA per request. The b-th largest key is found by a radix selection, eight bits per pass
-// over the masses, on an integer histogram in shared memory; holes and movers are numbered by
-// block scans in position order (no atomics decide an order); the holes go into the workspace, and
-// warps then copy row by row.
+// Two launches.
+//  * select: one CTA per request. The keys are made once and kept in shared memory (rows past
+//    kKeys positions are made anew in every pass). u* by a radix selection of 11, 11 and 10 bits on
+//    an integer histogram in shared memory: a log-normal mass fills few of 256 leading bytes, and the
+//    atomics on them collide, but some fifty of 2048 leading elevens. Then each warp takes a
+//    contiguous share of the positions, and ballots and a scan over the warps number the ties at u*,
+//    the holes below b and the movers past it in position order (no atomic decides an order); the
+//    lists go to the workspace, and masses and positions follow them.
+//  * move: the rows, over the whole device, four rows in flight per warp.
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <mutex>
 
 #include "dsa_host.h"
 
 namespace dsa {
 namespace evict {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kKeys = 49152;      // keys that shared memory holds (192 KB)
+constexpr int kMoveThreads = 256;
+constexpr int kMoveRows = 4;      // rows in flight per warp
 
 struct Params {
   uint8_t* cache;
   int64_t num_slots;
-  int row_words;  // cache row in 8-byte words
   const int32_t* bt;
   int64_t bt_stride;
   int page_size;
@@ -35,6 +45,7 @@ struct Params {
   const int32_t* budgets;
   int budget, sink, recent;
   int64_t width;
+  int keys;  // keys in shared memory
   const float* mass;
   int64_t mass_st;
   const int32_t* pos;
@@ -44,8 +55,9 @@ struct Params {
   int32_t* pos_out;
   int64_t pos_out_st;
   int32_t* len_out;
-  int32_t* ws;
-  int64_t ws_st;  // workspace entries per request
+  int32_t* moves;   // [R] rows to move
+  int32_t* lists;   // [R][2][list_st]: sources, destinations
+  int64_t list_st;
   int32_t* err;
 };
 
@@ -55,47 +67,42 @@ __device__ __forceinline__ uint32_t mass_key(float m) {
   return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 
-__device__ __forceinline__ int64_t slot_of(const Params& p, int64_t r, int64_t j) {
+__device__ __forceinline__ int64_t slot_of(const Params& p, int64_t r, int j) {
   if (!p.bt) return j;
-  return (int64_t)p.bt[r * p.bt_stride + j / p.page_size] * p.page_size + j % p.page_size;
+  const uint32_t pg = (uint32_t)j / (uint32_t)p.page_size;
+  return (int64_t)p.bt[r * p.bt_stride + pg] * p.page_size + ((uint32_t)j - pg * (uint32_t)p.page_size);
 }
 
-// exclusive sum over the block of v (a count per thread); *total gets the block's sum
-__device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
+// Exclusive sum over the warps of one count per warp (lane 0's `v` counts), and the total.
+__device__ __forceinline__ int warp_scan(int v, int* buf, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
+  __syncthreads();  // earlier readers of buf are done
+  if (lane == 0) buf[warp] = v;
+  __syncthreads();
+  const int x = buf[lane];
+  int s = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const int y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
   }
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  int base = 0, sum = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    const int s = warp_sums[w];
-    if (w < warp) base += s;
-    sum += s;
-  }
-  __syncthreads();
-  *total = sum;
-  return base + x - v;
+  *total = __shfl_sync(0xffffffffu, s, 31);
+  return __shfl_sync(0xffffffffu, s - x, warp);
 }
+static_assert(kWarps == 32, "one lane per warp in the scans");
 
-__global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__ Params p) {
-  __shared__ int hist[256];
-  __shared__ int wsum[kThreads / 32];
-  __shared__ int s_newest;
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_need;
-  const int tid = threadIdx.x;
+__global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ Params p) {
+  extern __shared__ uint32_t s_keys[];
+  __shared__ int hist[kBins];
+  __shared__ int wbuf[kWarps];
+  __shared__ int s_newest, s_digit, s_need;
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t r = blockIdx.x;
   const float* mass = p.mass + r * p.mass_st;
   const int32_t* pos = p.pos ? p.pos + r * p.pos_st : nullptr;
   float* mass_out = p.mass_out + r * p.mass_out_st;
   int32_t* pos_out = p.pos_out ? p.pos_out + r * p.pos_out_st : nullptr;
-  int32_t* holes = p.ws + r * p.ws_st;
   const int64_t len = p.lengths[r];
   const int n = (int)(len < 0 ? 0 : (len < p.width ? len : p.width));
   const int bq = p.budgets ? p.budgets[r] : p.budget;
@@ -114,10 +121,11 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
         bad |= pg < 0 || pg * p.page_size + last >= p.num_slots;
       }
     }
-    if (pos) {
+    if (pos && p.recent > 0) {
       int nw = INT32_MIN;
       for (int j = tid; j < n; j += kThreads) nw = max(nw, pos[j]);
-      atomicMax(&s_newest, nw);
+      nw = __reduce_max_sync(0xffffffffu, nw);
+      if (lane == 0) atomicMax(&s_newest, nw);
     }
   }
   bad = __syncthreads_or(bad);
@@ -127,82 +135,202 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
       for (int j = tid; j < n; j += kThreads) mass_out[j] = mass[j];
     if (pos_out && pos_out != pos)
       for (int j = tid; j < n; j += kThreads) pos_out[j] = pos ? pos[j] : j;
-    if (tid == 0) p.len_out[r] = (int32_t)len;
+    if (tid == 0) {
+      p.len_out[r] = (int32_t)len;
+      p.moves[r] = 0;
+    }
     return;
   }
   const int64_t newest = pos ? s_newest : n - 1;
-  auto key_of = [&](int j) -> uint32_t {
+  auto make_key = [&](int j) -> uint32_t {
     const int64_t k = pos ? pos[j] : j;
-    if (k < p.sink || k > newest - p.recent) return 0xFF800000u;  // the key of +inf
+    if (k < p.sink || (p.recent > 0 && k > newest - p.recent)) return 0xFF800000u;  // the key of +inf
     return mass_key(mass[j]);
   };
+  const bool cached = n <= p.keys;
+  auto key_of = [&](int j) -> uint32_t { return cached ? s_keys[j] : make_key(j); };
 
-  // the b-th largest key
+  // the b-th largest key u*; `need` of the keys equal to it are kept
   uint32_t prefix = 0;
-  int need = b;  // of the keys that share the prefix, how many are kept
-  for (int shift = 24; shift >= 0 && b > 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kThreads) hist[i] = 0;
-    __syncthreads();
-    const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-    for (int j = tid; j < n; j += kThreads) {
-      const uint32_t k = key_of(j);
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
+  int need = b;
+  if (b > 0) {
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
+      for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
+      __syncthreads();
+      if (pass == 0) {
+        for (int j = tid; j < n; j += kThreads) {
+          const uint32_t k = make_key(j);
+          if (cached) s_keys[j] = k;
+          atomicAdd(&hist[k >> 21], 1);
+        }
+      } else {
+        for (int j = tid; j < n; j += kThreads) {
+          const uint32_t k = key_of(j);
+          if (((k ^ prefix) >> (shift + bits)) == 0) atomicAdd(&hist[(k >> shift) & ((1 << bits) - 1)], 1);
+        }
+      }
+      __syncthreads();
+      // the digit at which the counts from the top reach `need`: thread t takes bins 2047 - 2t and
+      // 2046 - 2t, and sums run downwards
+      const int c0 = hist[kBins - 1 - 2 * tid], c1 = hist[kBins - 2 - 2 * tid];
+      int s = c0 + c1;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
+      }
+      int total;
+      const int in_warp = __shfl_sync(0xffffffffu, s, 31);
+      const int above = warp_scan(in_warp, wbuf, &total) + s - c0 - c1;  // keys with a digit above this thread's
+      if (above < need && above + c0 + c1 >= need) {
+        const bool upper = above + c0 >= need;
+        s_digit = kBins - 1 - 2 * tid - (upper ? 0 : 1);
+        s_need = need - above - (upper ? 0 : c0);
+      }
+      __syncthreads();
+      prefix |= (uint32_t)s_digit << shift;
+      need = s_need;
     }
-    __syncthreads();
-    if (tid == 0) {
-      int left = need, d = 255;
-      for (; d > 0 && hist[d] < left; --d) left -= hist[d];
-      s_prefix = prefix | ((uint32_t)d << shift);
-      s_need = left;
-    }
-    __syncthreads();
-    prefix = s_prefix;
-    need = s_need;
-    __syncthreads();
   }
+  if (b == 0) __syncthreads();
 
-  // one pass in position order: number the ties at u*, the holes below b and the movers past it
-  int ties = 0, nholes = 0, nmove = 0;
-  for (int j0 = 0; j0 < n; j0 += kThreads) {
-    const int j = j0 + tid;
-    const uint32_t k = j < n && b > 0 ? key_of(j) : 0u;
-    const bool tie = j < n && b > 0 && k == prefix;
-    int total;
-    const int tr = ties + block_scan(tie ? 1 : 0, wsum, &total);
-    ties += total;
-    const bool keep = j < n && b > 0 && (k > prefix || (tie && tr < need));
-    const bool hole = j < b && !keep, mover = j >= b && keep;
-    const int packed = block_scan((hole ? 1 : 0) | (mover ? 1 << 16 : 0), wsum, &total);
-    if (hole) holes[nholes + (packed & 0xFFFF)] = j;
-    nholes += total & 0xFFFF;
-    // every hole is below every mover, but a chunk may hold both: its holes are written first
-    __syncthreads();
-    if (j < b && keep) {
-      if (mass_out != mass) mass_out[j] = mass[j];
-      if (pos_out && pos_out != pos) pos_out[j] = pos ? pos[j] : j;
+  // a contiguous share of whole strips of 32 positions per warp
+  const int strips = (n + 31) / 32, per = (strips + kWarps - 1) / kWarps;
+  const int j0 = warp * per * 32, j1 = min(n, j0 + per * 32);
+  int ties = 0;
+  if (b > 0)
+    for (int j = j0 + lane; j - lane < j1; j += 32)
+      ties += __popc(__ballot_sync(0xffffffffu, j < j1 && key_of(j) == prefix));
+  int total;
+  const int tie0 = warp_scan(ties, wbuf, &total);
+  // whether position j is kept (all lanes of a strip at once); t counts the ties before the strip
+  auto kept = [&](int j, int& t) -> bool {
+    if (b == 0) return false;
+    const uint32_t k = j < j1 ? key_of(j) : 0u;
+    const bool tie = j < j1 && k == prefix;
+    const uint32_t m = __ballot_sync(0xffffffffu, tie);
+    const int rank = t + __popc(m & ((1u << lane) - 1u));
+    t += __popc(m);
+    return j < j1 && (k > prefix || (tie && rank < need));
+  };
+  int holes = 0, movers = 0;
+  {
+    int t = tie0;
+    for (int j = j0 + lane; j - lane < j1; j += 32) {
+      const bool keep = kept(j, t);
+      holes += __popc(__ballot_sync(0xffffffffu, j < j1 && j < b && !keep));
+      movers += __popc(__ballot_sync(0xffffffffu, j >= b && keep));
     }
-    if (mover) {
-      const int i = nmove + (packed >> 16);
-      const int dst = holes[i];
-      mass_out[dst] = mass[j];
-      if (pos_out) pos_out[dst] = pos ? pos[j] : j;
-      holes[i] = j;
-      // the destination's place is known by rank again when the rows move
-      p.ws[r * p.ws_st + p.ws_st / 2 + i] = dst;
-    }
-    nmove += total >> 16;
   }
-  __syncthreads();
+  int count;
+  int hole0 = warp_scan(holes, wbuf, &total), mover0 = warp_scan(movers, wbuf, &count);
+  int32_t* src = p.lists + r * 2 * p.list_st;
+  int32_t* dst = src + p.list_st;
+  {
+    int t = tie0;
+    const uint32_t below = (1u << lane) - 1u;
+    for (int j = j0 + lane; j - lane < j1; j += 32) {
+      const bool keep = kept(j, t);
+      const bool hole = j < j1 && j < b && !keep, mover = j >= b && keep;
+      const uint32_t hm = __ballot_sync(0xffffffffu, hole), mm = __ballot_sync(0xffffffffu, mover);
+      if (hole) dst[hole0 + __popc(hm & below)] = j;
+      if (mover) src[mover0 + __popc(mm & below)] = j;
+      hole0 += __popc(hm);
+      mover0 += __popc(mm);
+      if (keep && j < b) {
+        if (mass_out != mass) mass_out[j] = mass[j];
+        if (pos_out && pos_out != pos) pos_out[j] = pos ? pos[j] : j;
+      }
+    }
+  }
+  if (tid == 0) {
+    p.moves[r] = count;
+    p.len_out[r] = b;
+  }
+  __syncthreads();  // the lists are complete
+  for (int i = tid; i < count; i += kThreads) {
+    const int s = src[i], d = dst[i];
+    mass_out[d] = mass[s];
+    if (pos_out) pos_out[d] = pos ? pos[s] : s;
+  }
+  __syncthreads();  // in place: the movers' masses are read before they are cleared
   for (int j = b + tid; j < n; j += kThreads) mass_out[j] = 0.0f;
-  if (tid == 0) p.len_out[r] = b;
+}
 
-  const int lane = tid & 31;
-  for (int i = tid >> 5; i < nmove; i += kThreads / 32) {
-    const int64_t src = slot_of(p, r, holes[i]), dst = slot_of(p, r, holes[p.ws_st / 2 + i]);
-    const uint2* s = reinterpret_cast<const uint2*>(p.cache + src * 8 * p.row_words);
-    uint2* d = reinterpret_cast<uint2*>(p.cache + dst * 8 * p.row_words);
-    for (int w = lane; w < p.row_words; w += 32) d[w] = s[w];
+// Rows of 8 * WORDS bytes. Block (x, y) moves rows of request y: four per warp at a time, all read
+// before the first is written (sources and destinations are disjoint anyhow).
+template <int WORDS>
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ Params p) {
+  constexpr int PER = (WORDS + 31) / 32;
+  const int lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t r = blockIdx.y;
+  const int n = p.moves[r];
+  const int32_t* list = p.lists + r * 2 * p.list_st;
+  const int warps = gridDim.x * (kMoveThreads / 32);
+  for (int i0 = (blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5)) * kMoveRows; i0 < n; i0 += warps * kMoveRows) {
+    // lanes 0 - 3: source slots, 4 - 7: destinations
+    int64_t slot = -1;
+    const int i = i0 + (lane & 3);
+    if (lane < 8 && i < n) slot = slot_of(p, r, list[(lane >> 2) * p.list_st + i]);
+    uint2 v[kMoveRows][PER];
+#pragma unroll
+    for (int k = 0; k < kMoveRows; ++k) {
+      const int64_t s = __shfl_sync(0xffffffffu, slot, k);
+#pragma unroll
+      for (int w = 0; w < PER; ++w)
+        if (s >= 0 && 32 * w + lane < WORDS)
+          v[k][w] = reinterpret_cast<const uint2*>(p.cache + s * (8 * WORDS))[32 * w + lane];
+    }
+#pragma unroll
+    for (int k = 0; k < kMoveRows; ++k) {
+      const int64_t d = __shfl_sync(0xffffffffu, slot, 4 + k);
+#pragma unroll
+      for (int w = 0; w < PER; ++w)
+        if (d >= 0 && 32 * w + lane < WORDS) reinterpret_cast<uint2*>(p.cache + d * (8 * WORDS))[32 * w + lane] = v[k][w];
+    }
   }
+}
+
+struct Ws {
+  size_t moves, lists, bytes;
+  int64_t list_st;
+};
+// At most half of a request's positions move: a source and a destination each.
+Ws ws_layout(int64_t requests, int64_t width) {
+  Ws w;
+  w.list_st = (width + 1) / 2;
+  w.lists = 0;
+  w.moves = (size_t)requests * (size_t)w.list_st * 8;
+  w.bytes = w.moves + (size_t)requests * 4;
+  return w;
+}
+
+dsa_status_t prepare(int device) {
+  static std::mutex mu;
+  static bool done[64];
+  std::lock_guard<std::mutex> lock(mu);
+  if (done[device]) return DSA_OK;
+  const cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeys * 4);
+  if (e != cudaSuccess) return cuda_fail(e);
+  done[device] = true;
+  return DSA_OK;
+}
+
+template <int WORDS>
+cudaError_t launch_move(const Params& p, dim3 grid, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, move_kernel<WORDS>, p);
 }
 
 }  // namespace evict
@@ -210,10 +338,9 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
 
 using namespace dsa;
 
-// At most half of a request's positions move: a source and a destination each.
 extern "C" dsa_status_t dsa_cache_evict_workspace_size(int64_t num_requests, int64_t width, size_t* bytes) {
   if (!bytes || num_requests < 0 || width < 1 || width > (1 << 30)) return DSA_ERR_INVALID_ARGUMENT;
-  *bytes = (size_t)num_requests * (size_t)((width + 1) / 2) * 8;
+  *bytes = evict::ws_layout(num_requests, width).bytes;
   return DSA_OK;
 }
 
@@ -223,7 +350,7 @@ extern "C" dsa_status_t dsa_cache_evict(const dsa_evict_args_t* a, void* stream)
   if (!((a->d_nope == 256 && a->d_rope == 0) || (a->d_nope == 512 && a->d_rope == 64))) return DSA_ERR_UNSUPPORTED;
   if (a->num_requests < 0) return DSA_ERR_INVALID_ARGUMENT;
   if (a->num_requests == 0) return DSA_OK;
-  if (a->num_requests > 0x7FFFFFFF) return DSA_ERR_UNSUPPORTED;
+  if (a->num_requests > 65535) return DSA_ERR_UNSUPPORTED;
   if (!a->cache || !aligned(a->cache, 8) || a->num_slots < 0 || !a->lengths || !a->mass || !a->mass_out ||
       !a->lengths_out)
     return DSA_ERR_INVALID_ARGUMENT;
@@ -241,17 +368,15 @@ extern "C" dsa_status_t dsa_cache_evict(const dsa_evict_args_t* a, void* stream)
   if (a->mass_out == a->mass && a->mass_out_stride != a->mass_stride) return DSA_ERR_INVALID_ARGUMENT;
   if (a->positions && a->positions_out == a->positions && a->positions_out_stride != a->positions_stride)
     return DSA_ERR_INVALID_ARGUMENT;
-  size_t need = 0;
-  dsa_status_t st = dsa_cache_evict_workspace_size(a->num_requests, a->width, &need);
-  if (st != DSA_OK) return st;
+  const evict::Ws w = evict::ws_layout(a->num_requests, a->width);
   if (!a->workspace || !aligned(a->workspace, 8)) return DSA_ERR_INVALID_ARGUMENT;
-  if (a->workspace_bytes < need) return DSA_ERR_WORKSPACE_TOO_SMALL;
+  if (a->workspace_bytes < w.bytes) return DSA_ERR_WORKSPACE_TOO_SMALL;
   DeviceInfo dev;
-  if ((st = current_device(&dev)) != DSA_OK) return st;
+  dsa_status_t st = current_device(&dev);
+  if (st != DSA_OK || (st = evict::prepare(dev.device)) != DSA_OK) return st;
   evict::Params p{};
   p.cache = static_cast<uint8_t*>(a->cache);
   p.num_slots = a->num_slots;
-  p.row_words = (int)(dsa_cache_row_bytes(a->kind, a->d_nope, a->d_rope) / 8);
   p.bt = a->block_table;
   p.bt_stride = a->bt_stride;
   p.page_size = a->block_table ? a->page_size : 1;
@@ -262,6 +387,7 @@ extern "C" dsa_status_t dsa_cache_evict(const dsa_evict_args_t* a, void* stream)
   p.sink = a->sink;
   p.recent = a->recent;
   p.width = a->width;
+  p.keys = (int)(a->width < evict::kKeys ? a->width : evict::kKeys);
   p.mass = a->mass;
   p.mass_st = a->mass_stride;
   p.pos = a->positions;
@@ -271,10 +397,26 @@ extern "C" dsa_status_t dsa_cache_evict(const dsa_evict_args_t* a, void* stream)
   p.pos_out = a->positions_out;
   p.pos_out_st = a->positions_out_stride;
   p.len_out = a->lengths_out;
-  p.ws = static_cast<int32_t*>(a->workspace);
-  p.ws_st = (a->width + 1) / 2 * 2;
+  uint8_t* ws = static_cast<uint8_t*>(a->workspace);
+  p.lists = reinterpret_cast<int32_t*>(ws + w.lists);
+  p.moves = reinterpret_cast<int32_t*>(ws + w.moves);
+  p.list_st = w.list_st;
   p.err = a->error_word;
-  evict::evict_kernel<<<(unsigned)a->num_requests, evict::kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  evict::select_kernel<<<(unsigned)a->num_requests, evict::kThreads, (size_t)p.keys * 4, s>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e);
+  // blocks per request: the device eight blocks deep, and no more than the most moves can use
+  const int64_t rows_per_block = evict::kMoveRows * (evict::kMoveThreads / 32);
+  const int64_t most = (w.list_st + rows_per_block - 1) / rows_per_block;
+  int64_t x = (8 * (int64_t)dev.sm_count + a->num_requests - 1) / a->num_requests;
+  if (x > most) x = most;
+  const dim3 grid((unsigned)x, (unsigned)a->num_requests);
+  switch (dsa_cache_row_bytes(a->kind, a->d_nope, a->d_rope)) {
+    case 264: e = evict::launch_move<33>(p, grid, s); break;
+    case 512: e = evict::launch_move<64>(p, grid, s); break;
+    case 656: e = evict::launch_move<82>(p, grid, s); break;
+    default: e = evict::launch_move<144>(p, grid, s); break;
+  }
   return e == cudaSuccess ? DSA_OK : cuda_fail(e);
 }

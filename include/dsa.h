@@ -394,7 +394,7 @@ typedef struct dsa_evict_args {
   const int32_t* block_table;    /* int32 [num_requests, bt_stride] or NULL (direct slots) */
   int64_t bt_stride;
   int page_size, max_pages;
-  int64_t num_requests;          /* 0 = no-op */
+  int64_t num_requests;          /* at most 65535 (0 = no-op) */
   const int32_t* lengths;        /* int32 [num_requests] */
   const int32_t* budgets;        /* int32 [num_requests] or NULL */
   int budget;                    /* used when budgets is NULL: >= 0 */
