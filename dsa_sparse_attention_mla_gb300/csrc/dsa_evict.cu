@@ -27,10 +27,13 @@
 namespace dsa {
 namespace evict {
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kKeys = 49152;      // keys that shared memory holds (192 KB)
+// Threads of a select CTA, by the rows' width: passes over few positions are bound by what every
+// thread does beside them (scans, barriers). 256 requests of 1088 positions: 24 us with 512, 32 with
+// 1024; 48 of 8192: 46 and 42.
+constexpr int kFew = 512, kMany = 1024;
+constexpr int kFewWidth = 4096;
 constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = 4;      // rows in flight per warp
 
@@ -73,13 +76,14 @@ __device__ __forceinline__ int64_t slot_of(const Params& p, int64_t r, int j) {
   return (int64_t)p.bt[r * p.bt_stride + pg] * p.page_size + ((uint32_t)j - pg * (uint32_t)p.page_size);
 }
 
-// Exclusive sum over the warps of one count per warp (lane 0's `v` counts), and the total.
+// Exclusive sum over the NW warps of one count per warp (lane 0's `v` counts), and the total.
+template <int NW>
 __device__ __forceinline__ int warp_scan(int v, int* buf, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __syncthreads();  // earlier readers of buf are done
   if (lane == 0) buf[warp] = v;
   __syncthreads();
-  const int x = buf[lane];
+  const int x = lane < NW ? buf[lane] : 0;
   int s = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -89,9 +93,10 @@ __device__ __forceinline__ int warp_scan(int v, int* buf, int* total) {
   *total = __shfl_sync(0xffffffffu, s, 31);
   return __shfl_sync(0xffffffffu, s - x, warp);
 }
-static_assert(kWarps == 32, "one lane per warp in the scans");
-
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ Params p) {
+  constexpr int kWarps = kThreads / 32, kPer = kBins / kThreads;  // bins per thread
+  static_assert(kWarps <= 32 && kPer * kThreads == kBins, "one lane per warp in the scans");
   extern __shared__ uint32_t s_keys[];
   __shared__ int hist[kBins];
   __shared__ int wbuf[kWarps];
@@ -172,10 +177,15 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
         }
       }
       __syncthreads();
-      // the digit at which the counts from the top reach `need`: thread t takes bins 2047 - 2t and
-      // 2046 - 2t, and sums run downwards
-      const int c0 = hist[kBins - 1 - 2 * tid], c1 = hist[kBins - 2 - 2 * tid];
-      int s = c0 + c1;
+      // the digit at which the counts from the top reach `need`: thread t takes the kPer bins that end
+      // at 2047 - kPer t, and sums run downwards
+      int c[kPer], mine = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        c[i] = hist[kBins - 1 - kPer * tid - i];
+        mine += c[i];
+      }
+      int s = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, s, o);
@@ -183,11 +193,16 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
       }
       int total;
       const int in_warp = __shfl_sync(0xffffffffu, s, 31);
-      const int above = warp_scan(in_warp, wbuf, &total) + s - c0 - c1;  // keys with a digit above this thread's
-      if (above < need && above + c0 + c1 >= need) {
-        const bool upper = above + c0 >= need;
-        s_digit = kBins - 1 - 2 * tid - (upper ? 0 : 1);
-        s_need = need - above - (upper ? 0 : c0);
+      int above = warp_scan<kWarps>(in_warp, wbuf, &total) + s - mine;  // keys with a digit above this thread's
+      if (above < need && above + mine >= need) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          if (above < need && above + c[i] >= need) {
+            s_digit = kBins - 1 - kPer * tid - i;
+            s_need = need - above;
+          }
+          above += c[i];
+        }
       }
       __syncthreads();
       prefix |= (uint32_t)s_digit << shift;
@@ -204,7 +219,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     for (int j = j0 + lane; j - lane < j1; j += 32)
       ties += __popc(__ballot_sync(0xffffffffu, j < j1 && key_of(j) == prefix));
   int total;
-  const int tie0 = warp_scan(ties, wbuf, &total);
+  const int tie0 = warp_scan<kWarps>(ties, wbuf, &total);
   // whether position j is kept (all lanes of a strip at once); t counts the ties before the strip
   auto kept = [&](int j, int& t) -> bool {
     if (b == 0) return false;
@@ -225,7 +240,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     }
   }
   int count;
-  int hole0 = warp_scan(holes, wbuf, &total), mover0 = warp_scan(movers, wbuf, &count);
+  int hole0 = warp_scan<kWarps>(holes, wbuf, &total), mover0 = warp_scan<kWarps>(movers, wbuf, &count);
   int32_t* src = p.lists + r * 2 * p.list_st;
   int32_t* dst = src + p.list_st;
   {
@@ -313,7 +328,9 @@ dsa_status_t prepare(int device) {
   static bool done[64];
   std::lock_guard<std::mutex> lock(mu);
   if (done[device]) return DSA_OK;
-  const cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeys * 4);
+  cudaError_t e = cudaFuncSetAttribute(select_kernel<kFew>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeys * 4);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(select_kernel<kMany>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeys * 4);
   if (e != cudaSuccess) return cuda_fail(e);
   done[device] = true;
   return DSA_OK;
@@ -403,7 +420,10 @@ extern "C" dsa_status_t dsa_cache_evict(const dsa_evict_args_t* a, void* stream)
   p.list_st = w.list_st;
   p.err = a->error_word;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  evict::select_kernel<<<(unsigned)a->num_requests, evict::kThreads, (size_t)p.keys * 4, s>>>(p);
+  if (a->width <= evict::kFewWidth)
+    evict::select_kernel<evict::kFew><<<(unsigned)a->num_requests, evict::kFew, (size_t)p.keys * 4, s>>>(p);
+  else
+    evict::select_kernel<evict::kMany><<<(unsigned)a->num_requests, evict::kMany, (size_t)p.keys * 4, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e);
   // blocks per request: the device eight blocks deep, and no more than the most moves can use
