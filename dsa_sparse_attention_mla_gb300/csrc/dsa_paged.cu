@@ -62,8 +62,10 @@ constexpr int kD = 256;
 constexpr int kMaxHeads = 128;
 constexpr int kHG = 64;    // heads per row (MMA N)
 constexpr int kBN = 128;   // positions per tile (MMA M)
-constexpr int kSoftmaxWarps = 8;
-constexpr int kWarpSched = 8, kWarpScore = 9, kWarpValue = 10, kWarpQuery = 11, kWarpLoad0 = 12, kWarpWiden0 = 16;
+constexpr int kSoftmaxWarps = 16;
+constexpr int kWarpSched = 16, kWarpScore = 17, kWarpValue = 18, kWarpQuery = 19, kWarpLoad0 = 20, kWarpWiden0 = 24;
+constexpr int kGroups = kSoftmaxWarps / 4;   // head groups
+constexpr int kHW = kHG / kGroups;           // heads per group
 constexpr int kLoadWarps = 4, kWidenWarps = 4;
 constexpr int kLoadRows = kBN / kLoadWarps;
 constexpr int kWarps = kWarpWiden0 + kWidenWarps;
@@ -192,7 +194,7 @@ struct Cfg {
   // -m [2][64], alpha [64], part [4][64], inverse sums [64], raise of m [64]; FP8, per head group:
   // largest scales of the tile [4][2], reference scales [2][2] and their inverses [2][2]
   static constexpr int RED_OFF = SL_OFF + 512;
-  static constexpr int PLAN_OFF = RED_OFF + 9 * 256 + 2 * 64;  // block scans: 2 x kWarps int64; start row, its cost
+  static constexpr int PLAN_OFF = RED_OFF + 9 * 256 + 64 * kGroups;  // block scans: 2 x kWarps int64; start row, its cost
   static constexpr int BAR_OFF = PLAN_OFF + 2 * 8 * kWarps + 64;
   static constexpr int NBARS = 2 + 2 * NST + 3 * kSegs + 2 * kMaps + 2 * NSB + 2 * 2 + 2 + 2 * NW;
   static constexpr int MISC_OFF = BAR_OFF + 8 * NBARS;
@@ -506,11 +508,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     return false;
   };
 
-  // 640 threads x 96 registers at launch; 256 x 144 + 384 x 64 is the same total. (No function is
-  // called from here on: ptxas allocates past the launch's 96 only without calls.)
-  static_assert(32 * kWarps * 96 == 256 * 144 + 384 * 64, "register split");
+  // 896 threads x 72 registers at launch; 512 x 80 + 384 x 56 is within that total. (No function is
+  // called from here on: ptxas allocates past the launch's 72 only without calls.)
+  static_assert(32 * kWarps == 896 && 32 * kWarps * 72 >= 512 * 80 + 384 * 56, "register split");
   if (warp >= kSoftmaxWarps) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (warp == kWarpSched) {
     // ================================================================== scheduler ====
     uint32_t sc = 0;
@@ -1010,9 +1012,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     }
   }
   } else {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
   if constexpr (MASS) {
-    // ================================================== weights of a key, 8 warps ====
+    // ================================================== weights of a key, 16 warps ===
     const int qd = warp & 3, gi = warp >> 2;
     const int tr = 32 * qd + lane;
     const float inv_cap2 = MODS && p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
@@ -1031,7 +1033,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       const float* slopes = s_slopes + s.hg * kHG;
       const int64_t qp = MODS && p.qpos ? p.qpos[s.t] : (int64_t)p.lengths[s.t] - 1;
       for (int k = 0; k < s.ntiles; ++k, ++g) {
-        if ((g & 1) != (uint32_t)gi) continue;
+        if (g % kGroups != (uint32_t)gi) continue;
         const uint32_t sb = g % C::NSB;
         const uint32_t tl = tmem + ((uint32_t)(32 * qd) << 16) + sb * C::S_COLS;
         const uint32_t pos = (uint32_t)(s.a & ~127) + 128u * (uint32_t)(s.tile0 + k) + tr;
@@ -1093,13 +1095,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       if (lane == 0) mbar_arrive(g_empty(slot));
     }
   } else {
-    // ===================================================== softmax and outputs, 8 warps ====
-    // Warp = lane quarter qd (keys 32 qd ..; output columns 32 qd .. of both halves), head group hq: 32
-    // heads from 32 hq, or 16 from 16 hq where a row has at most 32 (both groups then share the work;
-    // 32 heads with cap and bias took 52 us with one of them idle, 38 so)
+    // ===================================================== softmax and outputs, 16 warps ===
+    // Warp = lane quarter qd (keys 32 qd ..; output columns 32 qd .. of both halves), head group hq: the
+    // heads from kHW hq on
     const int qd = warp & 3, hq = warp >> 2;
-    const int hw = p.H <= 32 ? 16 : 32;
-    const int hb = hw * hq;
+    constexpr int CH = kHW / 16, NP = kHW / 2;  // chunks of 16 heads, pairs
+    const int hb = kHW * hq;
     const int tr = 32 * qd + lane;
     const int gid = threadIdx.x & 127;  // thread of the head group
     const uint32_t tl = tmem + ((uint32_t)(32 * qd) << 16);
@@ -1123,7 +1124,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     auto pv_wait = [&](uint32_t last) { await(pv_done(last & 1), (last >> 1) & 1); };
     const uint32_t o_addr = tl + C::O_COL + hb;  // O^T half 0 (half 1 64 columns on), the group's heads
     // -m of a segment without a valid key so far is 0
-    if (gid < hw) red[hb + gid] = 0.0f;
+    if (gid < kHW) red[hb + gid] = 0.0f;
     for (uint32_t sc = 0;; ++sc) {
       const uint32_t slot = sc % kSegs;
       await(g_full(slot), (sc / kSegs) & 1);
@@ -1135,14 +1136,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       if (s.type == 0) break;
       const int heads = min(kHG, p.H - s.hg * kHG);
       // chunks of 16 heads in use: the weights of the others meet only unused columns of O^T
-      const int nch = max(0, min(hw >> 4, (heads - hb + 15) >> 4));
+      const int nch = max(0, min(CH, (heads - hb + 15) >> 4));
       const float* slopes = s_slopes + s.hg * kHG + hb;
       const float* sq = reinterpret_cast<const float*>(smem + C::SQ_OFF) + kHG * slot + hb;
       int64_t qp = 0;
       if (MODS) qp = p.qpos ? p.qpos[s.t] : (int64_t)p.lengths[s.t] - 1;
-      float2 lsum[16];  // heads 2 i, 2 i + 1 of the warp
+      float2 lsum[NP];  // heads 2 i, 2 i + 1 of the group
 #pragma unroll
-      for (int i = 0; i < 16; ++i) lsum[i] = make_float2(0.0f, 0.0f);
+      for (int i = 0; i < NP; ++i) lsum[i] = make_float2(0.0f, 0.0f);
       bool fresh = true;  // no valid key so far: m counts as 0, no reference scale
       for (int k = 0; k < s.ntiles; ++k, ++g) {
         const uint32_t sb = g % C::NSB;
@@ -1159,12 +1160,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         float2 scl = make_float2(0.0f, 0.0f);
         if (F8) scl = reinterpret_cast<const float2*>(smem + C::SC_OFF + 1024 * (g % C::NV))[tr];
         // y = score - m, exp2 domain
-        float2 y[16];
+        float2 y[NP];
         float top = -INFINITY;
         const float2 s0 = make_float2(scl.x, scl.x), s1 = make_float2(scl.y, scl.y), f2 = make_float2(f, f);
         const float* m = red + 64 * mb + hb;
 #pragma unroll
-        for (int ch = 0; ch < 2; ++ch) {
+        for (int ch = 0; ch < CH; ++ch) {
           if (ch < nch) {
             uint32_t x0[16], x1[16];
             tmem_ld32_x16(tl + sb * C::S_COLS + hb + 16 * ch, x0);
@@ -1207,7 +1208,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
           if (!valid) {
             top = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = make_float2(-INFINITY, -INFINITY);
+            for (int i = 0; i < NP; ++i) y[i] = make_float2(-INFINITY, -INFINITY);
           }
         }
         tc_fence_before();
@@ -1225,10 +1226,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         if (exact) {
           // exact maximum of the tile per head; the running maxima are raised to it
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < NP; ++i) {
             const int m0 = redux_max_s32(f2ord(y[i].x)), m1 = redux_max_s32(f2ord(y[i].y));
-            if (lane == 2 * i && lane < hw) red_part[64 * qd + hb + 2 * i] = ord2f(m0);
-            if (lane == 2 * i + 1 && lane < hw) red_part[64 * qd + hb + 2 * i + 1] = ord2f(m1);
+            if (lane == 2 * i) red_part[64 * qd + hb + 2 * i] = ord2f(m0);
+            if (lane == 2 * i + 1) red_part[64 * qd + hb + 2 * i + 1] = ord2f(m1);
           }
           if (F8) {
             // magnitudes order like their bits
@@ -1240,7 +1241,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
             }
           }
           const bool some = group_any(hq, valid);
-          if (gid < hw) {
+          if (gid < kHW) {
             // relative to the m that y was taken from; a first maximum may be below it
             const float* pt = red_part + hb + gid;
             const float up = fmaxf(fmaxf(pt[0], pt[64]), fmaxf(pt[128], pt[192]));
@@ -1263,21 +1264,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
           group_sync(hq);
           mb ^= 1;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < NP; ++i) {
             const float2 up = *reinterpret_cast<const float2*>(red_raise + hb + 2 * i);
             y[i] = make_float2(y[i].x - up.x, y[i].y - up.y);
           }
           if (!fresh) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) lsum[i] = __fmul2_rn(lsum[i], *reinterpret_cast<const float2*>(red_alpha + hb + 2 * i));
+            for (int i = 0; i < NP; ++i) lsum[i] = __fmul2_rn(lsum[i], *reinterpret_cast<const float2*>(red_alpha + hb + 2 * i));
             pv_wait(g - 1);
             tc_fence_after();
 #pragma unroll 1
-            for (int ch = 0; ch < 4; ++ch) {  // half ch >> 1, 16 heads
-              if (16 * (ch & 1) >= hw) continue;
-              const uint32_t addr = o_addr + 64 * (ch >> 1) + 16 * (ch & 1);
-              const float* al = red_alpha + hb + 16 * (ch & 1);
-              const float r = F8 ? red_ref[2 * (mb ^ 1) + (ch >> 1)] / red_ref[2 * mb + (ch >> 1)] : 1.0f;
+            for (int c = 0; c < 2 * CH; ++c) {  // half c / CH, 16 heads
+              const int half = c / CH, h16 = 16 * (c % CH);
+              const uint32_t addr = o_addr + 64 * half + h16;
+              const float* al = red_alpha + hb + h16;
+              const float r = F8 ? red_ref[2 * (mb ^ 1) + half] / red_ref[2 * mb + half] : 1.0f;
               uint32_t o[16];
               tmem_ld32_x16(addr, o);
               tc_wait_ld();
@@ -1292,7 +1293,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         float2 wf = make_float2(1.0f, 1.0f);  // FP8: the key's scales relative to the references
         if (F8) wf = __fmul2_rn(scl, *reinterpret_cast<const float2*>(red_wf + 2 * mb));
 #pragma unroll
-        for (int ch = 0; ch < 2; ++ch) {
+        for (int ch = 0; ch < CH; ++ch) {
           if (ch < nch) {
 #pragma unroll
             for (int i = 8 * ch; i < 8 * ch + 8; ++i) {
@@ -1306,7 +1307,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         uint8_t* prow = smem + C::P_OFF + (g % C::PBUF) * C::P_BYTES + tr * 128;
         const int sw = tr & 7;
 #pragma unroll
-        for (int ch = 0; ch < 2; ++ch) {
+        for (int ch = 0; ch < CH; ++ch) {
           if (ch < nch) {
 #pragma unroll
             for (int h = 0; h < C::PN; ++h) {
@@ -1334,25 +1335,28 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       }
       // ---- the segment's end: sums over the keys, then the group's columns of O^T
       {
-        // reduce-scatter over the lanes: lane i ends with the warp's sum of head i
-        float v[32];
+        // reduce-scatter over the lanes: head i of the group ends in lanes i * 32 / kHW ..
+        float v[kHW];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < NP; ++i) {
           v[2 * i] = lsum[i].x;
           v[2 * i + 1] = lsum[i].y;
         }
+        constexpr int R = 32 / kHW;  // lanes per head
 #pragma unroll
-        for (int w = 16; w > 0; w >>= 1) {
-          const bool upper = lane & w;
+        for (int w = kHW / 2; w > 0; w >>= 1) {
+          const bool upper = lane & (w * R);
 #pragma unroll
           for (int i = 0; i < w; ++i)
-            v[i] = (upper ? v[i + w] : v[i]) + __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[i + w], w);
+            v[i] = (upper ? v[i + w] : v[i]) + __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[i + w], w * R);
         }
-        if (lane < hw) red_part[64 * qd + hb + lane] = v[0];
+#pragma unroll
+        for (int o = R / 2; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+        if (lane % R == 0) red_part[64 * qd + hb + lane / R] = v[0];
       }
       group_sync(hq);
       const int part = 2 * cta + (s.kind == 1 ? 1 : 0);
-      if (gid < hw) {
+      if (gid < kHW) {
         const int h = hb + gid;
         const float L = (red_part[h] + red_part[64 + h]) + (red_part[128 + h] + red_part[192 + h]);
         const float m = -red[64 * mb + h];
@@ -1370,12 +1374,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       tc_fence_after();
       uint16_t* orow = p.out + (int64_t)s.t * p.out_st + (int64_t)s.hg * kHG * p.out_sh;
 #pragma unroll 1
-      for (int ch = 0; ch < 4; ++ch) {  // half ch >> 1, 16 heads
-        const int h0 = hb + 16 * (ch & 1), half = ch >> 1;
-        if (h0 >= heads || 16 * (ch & 1) >= hw) continue;
+      for (int c = 0; c < 2 * CH; ++c) {  // half c / CH, 16 heads
+        const int half = c / CH, h16 = 16 * (c % CH), h0 = hb + h16;
+        if (h0 >= heads) continue;
         uint32_t o[16];
         if (s.ntiles > 0) {
-          tmem_ld32_x16(o_addr + 64 * half + 16 * (ch & 1), o);
+          tmem_ld32_x16(o_addr + 64 * half + h16, o);
           tc_wait_ld();
         } else {
 #pragma unroll
