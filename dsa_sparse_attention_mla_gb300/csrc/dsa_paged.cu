@@ -71,6 +71,7 @@ constexpr int kLoadRows = kBN / kLoadWarps;
 constexpr int kWarps = kWarpWiden0 + kWidenWarps;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCtas = 192;      // the join's lists (its threads look at 256 CTAs)
+constexpr int kWarpRows = 256;     // rows whose costs one warp sums up, eight per lane
 constexpr int kSegs = 8;           // segment ring depth
 constexpr int kMaps = 8;           // tiles whose slots are known ahead
 // Smallest page whose rows the scheduler prefetches into L2 (an eighth of a tile per request), FP8
@@ -145,10 +146,16 @@ struct Params {
   float* ws_o;      // [2 G][64 heads][256] unnormalised partial outputs: slot 2c the row CTA c
                     // continues, 2c + 1 the row it starts and does not finish
   float* ws_ml;     // [2 G][2][64] their maxima (exp2 domain) and sums
-  int64_t* ws_tail; // [G] the row CTA c starts and does not finish, or -1
-  int* ws_head;     // [G] 0: continues no row, 1: continues one to its border, 2: finishes one
-  int* ws_first;    // [T * HG], when that is at most G: the CTA that starts a split row, or -1
+  int64_t* ws_split; // [G][3] split rows, entry r for row r when there are at most G rows, else entry c
+                     // for the row that CTA c starts: the row (-1: not split, none), the CTAs that
+                     // start and finish it, and the split's total cost
 };
+
+// First cost of CTA c's share.
+__device__ __forceinline__ int64_t share(int c, int64_t total, int G) {
+  // G is at most kMaxCtas < 2^9: 32-bit divisions below 2^22
+  return total < (1 << 22) ? (int64_t)((uint32_t)c * (uint32_t)total / (uint32_t)G) : c * total / G;
+}
 
 struct Seg {
   int type;  // 0: done, 1: a row's tiles
@@ -211,6 +218,12 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn_major, i
 __device__ __forceinline__ uint32_t f32x2_to_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Warp-wide maximum (NaN ignored).
+__device__ __forceinline__ float redux_max_f32(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
   return r;
 }
 // 2-D tiled tensor load (coordinates innermost first).
@@ -322,21 +335,27 @@ __device__ __forceinline__ void group_sync(int group) {
   asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + group) : "memory");
 }
 
-// Splits query rows h0 .. of a widening warp's share of a row (zero past `heads`) into e4m3 hi and lo terms, lane l
-// columns 8 l .. 8 l + 7, per head scaled by 2^-e so that the largest component lies in
-// [128, 256); sq[h] = f * 2^e.
+// Splits query rows h0 .. h0 + HEADS - 1 of a row (zero past `heads`) into e4m3 hi and lo terms, lane
+// l columns 8 l .. 8 l + 7, per head scaled by 2^-e so that the largest component lies in
+// [128, 256); sq[h] = f * 2^e. Four heads at a time, the next four on their way meanwhile.
+template <int HEADS>
 __device__ __forceinline__ void split_query(const uint16_t* q, int64_t q_sh, int h0, int heads, float f, uint8_t* qbuf,
                                             float* sq) {
   const int lane = threadIdx.x & 31;
   const int gl = lane & 15, tile = lane >> 4;
+  uint4 next[4];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      next[i] = h + i < heads ? *reinterpret_cast<const uint4*>(q + (h + i) * q_sh + 8 * lane) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  load(h0);
 #pragma unroll 1
-  for (int part = 0; part < kHG / kWidenWarps / 4; ++part) {
+  for (int part = 0; part < HEADS / 4; ++part) {
     uint4 v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int h = h0 + 4 * part + i;
-      v[i] = h < heads ? *reinterpret_cast<const uint4*>(q + h * q_sh + 8 * lane) : make_uint4(0u, 0u, 0u, 0u);
-    }
+    for (int i = 0; i < 4; ++i) v[i] = next[i];
+    if (part + 1 < HEADS / 4) load(h0 + 4 * part + 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int h = h0 + 4 * part + i;
@@ -415,12 +434,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
                   B12 = B11 + C::NW;
     const int i = threadIdx.x;
     int n = 1;                                                 // pv_done, drain, w_empty, q_empty, g_full, map_full
-    if (i == 0) n = F8 ? kWidenWarps : 32;                     // q_full (bf16: an asynchronous arrival per thread)
+    if (i == 0) n = F8 ? kSoftmaxWarps : 32;                   // q_full (bf16: an asynchronous arrival per thread)
     else if (i >= B0 && i < B1) n = 32 * kLoadWarps;           // k_full: an asynchronous arrival per thread
     else if (i >= B1 && i < B2) n = 1 + (C::WIDEN ? kWidenWarps : 0);  // k_empty: the last product, the widening
     else if (i >= B3 && i < B4)                                // g_empty: softmax, issuers, query warp, widening
       n = kSoftmaxWarps + 1 + (MASS ? 0 : 1) + (C::WIDEN ? 0 : 1) + (F8 ? kWidenWarps : 0);
-    else if (i >= B4 && i < B5) n = (MASS ? 1 : 0) + (F8 ? kWidenWarps : 0) + (!MASS && !F8 ? 1 : 0);  // aux_full
+    else if (i >= B4 && i < B5) n = (MASS ? 1 : 0) + (F8 ? kSoftmaxWarps : 0) + (!MASS && !F8 ? 1 : 0);  // aux_full
     else if (i >= B6 && i < B7) n = MASS ? 4 : kSoftmaxWarps;  // map_empty
     else if (i >= B7 && i < B8) n = 2;                         // s_full: the product, and its issuer
     else if (i >= B8 && i < B9) n = MASS ? 4 : kSoftmaxWarps;  // s_empty
@@ -437,12 +456,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     tmem_relinquish();
   }
 
-  // ---- the split: total cost of the rows, and the row in which this CTA's share begins
+  // ---- the split: the total cost of the rows, and the row in which this CTA's share begins. Up to
+  // kWarpRows rows the scheduler alone finds them (no block barrier waits for the lengths), else all.
   int64_t* plan = reinterpret_cast<int64_t*>(smem + C::PLAN_OFF);
   int64_t* plan_start = plan + 2 * kWarps;  // row, its cost offset, running maximum of the requests
   const int64_t nrows = p.T * p.HG;
-  int64_t c0, c1;
-  {
+  int64_t total = 0, row = 0, cost = 0;  // the scheduler's: where its walk begins
+  int run = INT32_MIN;
+  auto cost_of = [&](const Row& r, int& run) -> int64_t {
+    bool ok = true;
+    if (MASS && p.req) {
+      ok = r.req > run;
+      run = max(run, r.req);
+    }
+    return (ok ? r.n : 0) + kRowOverhead;
+  };
+  if (nrows > kWarpRows) {
     const int64_t per = (nrows + kThreads - 1) / kThreads;
     const int64_t i0 = threadIdx.x * per, i1 = i0 + per < nrows ? i0 + per : nrows;
     int mx = INT32_MIN;
@@ -451,33 +480,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       for (int64_t i = i0; i < i1; ++i) m = max(m, p.req[i]);
       mx = block_max(m, plan);
     }
-    auto cost_of = [&](int64_t i, int& run) -> int64_t {
-      const Row r = row_of(p, i);
-      bool ok = true;
-      if (MASS && p.req) {
-        ok = r.req > run;
-        run = max(run, r.req);
-      }
-      return (ok ? r.n : 0) + kRowOverhead;
-    };
     int64_t sum = 0;
-    int run = mx;
-    for (int64_t i = i0; i < i1; ++i) sum += cost_of(i, run);
-    int64_t total;
+    run = mx;
+    for (int64_t i = i0; i < i1; ++i) sum += cost_of(row_of(p, i), run);
     const int64_t pre = block_sum(sum, plan + kWarps, &total);
-    if (total < (1 << 22)) {  // G is at most kMaxCtas < 2^9: 32-bit divisions
-      c0 = (uint32_t)cta * (uint32_t)total / (uint32_t)p.G;
-      c1 = (uint32_t)(cta + 1) * (uint32_t)total / (uint32_t)p.G;
-    } else {
-      c0 = cta * total / p.G;
-      c1 = (cta + 1) * total / p.G;
-    }
-    if (c0 < c1 && pre <= c0 && c0 < pre + sum) {
+    const int64_t c0 = share(cta, total, p.G);
+    if (pre <= c0 && c0 < pre + sum) {
       int64_t at = pre, i = i0;
       run = mx;
       for (;; ++i) {
         int next = run;
-        const int64_t c = cost_of(i, next);
+        const int64_t c = cost_of(row_of(p, i), next);
         if (c0 < at + c) break;
         at += c;
         run = next;
@@ -486,6 +499,46 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       plan_start[1] = at;
       plan_start[2] = run;
     }
+  } else if (warp == kWarpSched) {
+    constexpr int PER = kWarpRows / 32;
+    const int per = ((int)nrows + 31) / 32, i0 = lane * per;
+    Row r[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+      if (k < per && i0 + k < nrows) r[k] = row_of(p, i0 + k);
+    int mx = INT32_MIN;
+    if (MASS && p.req) {
+      int m = INT32_MIN;
+#pragma unroll
+      for (int k = 0; k < PER; ++k)
+        if (k < per && i0 + k < nrows) m = max(m, r[k].req);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, m, o);
+        if (lane >= o) m = max(m, y);
+      }
+      mx = __shfl_up_sync(0xffffffffu, m, 1);
+      if (lane == 0) mx = INT32_MIN;
+    }
+    int64_t mine = 0;
+    int rn = mx;
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+      if (k < per && i0 + k < nrows) mine += cost_of(r[k], rn);
+    int64_t cum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, cum, o);
+      if (lane >= o) cum += y;
+    }
+    total = __shfl_sync(0xffffffffu, cum, 31);
+    // the last 32 rows at most are walked from the lane whose rows hold the start
+    const int64_t c0 = share(cta, total, p.G), pre = cum - mine;
+    const uint32_t in = __ballot_sync(0xffffffffu, pre <= c0 && c0 < cum);
+    const int src = __ffs(in) - 1;  // some lane: c0 < total
+    row = (int64_t)src * per;
+    cost = __shfl_sync(0xffffffffu, pre, src);
+    run = __shfl_sync(0xffffffffu, mx, src);
   }
   tc_fence_before();
   __syncthreads();
@@ -502,6 +555,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     return false;
   };
   // the whole warp waits, and agrees on the outcome
+  // FP8: the first segment's query, by the softmax warps
+  auto split_first = [&](const Seg& s, uint32_t slot) {
+    constexpr int HEADS = kHG / kSoftmaxWarps;
+    split_query<HEADS>(p.q + (int64_t)s.t * p.q_st + (int64_t)s.hg * kHG * p.q_sh, p.q_sh, HEADS * warp,
+                       min(kHG, p.H - s.hg * kHG), MODS ? p.sm_scale : p.sm_scale * kLog2e, smem + C::Q_OFF,
+                       reinterpret_cast<float*>(smem + C::SQ_OFF) + kHG * slot);
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(q_full);
+      mbar_arrive(aux_full(slot));
+    }
+  };
   auto wait_warp = [&](uint32_t bar, uint32_t par) -> bool {
     if (__all_sync(0xffffffffu, bar_wait(bar, par))) return true;
     fail();
@@ -517,8 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     // ================================================================== scheduler ====
     uint32_t sc = 0;
     uint32_t g = 0;  // tiles mapped
-    int64_t tail = -1;
-    int head = 0;
+    int64_t split_row = -1, split_last = 0;  // the row this CTA starts and does not finish
     bool ok = true;
     auto map_slot = [&](bool& good) -> int4* {
       const uint32_t m = g % kMaps;
@@ -539,20 +603,41 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         if (!good) return false;
         int sl[4];
         bool bad = false;
+        const uint32_t pos0 = base + 4 * lane;
+        uint32_t pg = 0, off = pos0;
+        if (bt) {
+          pg = (uint32_t)(((uint64_t)pos0 * p.pg_mul) >> p.pg_shift);
+          off = pos0 - pg * (uint32_t)p.page_size;
+        }
+        if (pos0 >= a && pos0 + 4 <= b && (!bt || off + 4 <= (uint32_t)p.page_size)) {
+          // four rows of one page
+          int64_t s0 = off;
+          if (bt) {
+            const int64_t page = bt[pg];
+            s0 = page < 0 ? p.num_slots : page * p.page_size + off;
+          }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t pos = base + 4 * lane + i;
-          sl[i] = -1;
-          if (pos >= a && pos < b) {
-            if (bt) {
-              const uint32_t pg = (uint32_t)(((uint64_t)pos * p.pg_mul) >> p.pg_shift);
-              const int64_t page = bt[pg];
-              const int64_t slot = page * p.page_size + (pos - pg * (uint32_t)p.page_size);
-              if (page < 0 || slot >= p.num_slots) bad = true;
-              else sl[i] = (int)slot;
-            } else {
-              sl[i] = (int)pos;
+          for (int i = 0; i < 4; ++i) sl[i] = s0 + i < p.num_slots ? (int)s0 + i : -1;
+          bad = sl[3] < 0;
+        } else {
+#pragma unroll 1
+          for (int i = 3; i >= 0; --i) {
+            const uint32_t pos = pos0 + i;
+            int v = -1;
+            if (pos >= a && pos < b) {
+              int64_t slot = pos;
+              if (bt) {
+                pg = (uint32_t)(((uint64_t)pos * p.pg_mul) >> p.pg_shift);
+                const int64_t page = bt[pg];
+                slot = page < 0 ? p.num_slots : page * p.page_size + (pos - pg * (uint32_t)p.page_size);
+              }
+              if (slot < p.num_slots) v = (int)slot;
+              else bad = true;
             }
+            sl[3] = sl[2];
+            sl[2] = sl[1];
+            sl[1] = sl[0];
+            sl[0] = v;
           }
         }
         if (bad) set_err(p.err, DSA_DEVERR_INDEX_OUT_OF_RANGE);
@@ -580,9 +665,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       }
       return true;
     };
+    if (nrows > kWarpRows) {
+      row = plan_start[0];
+      cost = plan_start[1];
+      run = (int)plan_start[2];
+    }
+    const int64_t c0 = share(cta, total, p.G), c1 = share(cta + 1, total, p.G);
     if (c0 < c1) {
-      int64_t row = plan_start[0], cost = plan_start[1];
-      int run = (int)plan_start[2];
       while (ok && cost < c1 && row < nrows) {
         const int64_t i = row + lane;
         Row r{};
@@ -622,13 +711,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         if (owner && !order && r.a < r.b) set_err(p.err, DSA_DEVERR_REQUEST_ORDER);
         const bool has = c && (n > 0 ? lo < hi : owner && !MASS);
         const int kind = lo > 0 ? 2 : (hi < n ? 1 : 0);
-        if (!MASS && nrows <= p.G && has && kind != 2) p.ws_first[i] = kind == 1 ? cta : -1;
+        // the CTA of a split row's last tile: the largest whose share starts at or before it
+        int64_t last = 0;
+        if (kind == 1) {
+          const int64_t end = (at + kRowOverhead + n) * p.G - 1;
+          last = total < (1 << 22) ? (int64_t)((uint32_t)end / (uint32_t)total) : end / total;
+        }
+        if (!MASS && nrows <= p.G && has && kind != 2) {
+          int64_t* w = p.ws_split + 3 * i;
+          w[0] = kind == 1 ? i : -1;
+          w[1] = (int64_t)cta | (last << 32);
+          w[2] = total;
+        }
         uint32_t todo = __ballot_sync(0xffffffffu, has);
         if (!MASS) {
           const uint32_t st = __ballot_sync(0xffffffffu, has && kind == 1);
-          if (st) tail = row + (31 - __clz(st));
-          const uint32_t co = __ballot_sync(0xffffffffu, has && kind == 2 && n > 0);
-          if (co) head = __shfl_sync(0xffffffffu, hi < n ? 1 : 2, 31 - __clz(co));
+          if (st) {  // at most one, the CTA's last
+            split_row = row + (31 - __clz(st));
+            split_last = __shfl_sync(0xffffffffu, last, 31 - __clz(st));
+          }
         }
         while (todo) {
           const int src = __ffs(todo) - 1;
@@ -666,9 +767,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         cost += __shfl_sync(0xffffffffu, cum, 31);
       }
     }
-    if (!MASS && lane == 0) {
-      p.ws_tail[cta] = tail;
-      p.ws_head[cta] = head;
+    if (!MASS && nrows > p.G && lane == 0) {
+      int64_t* w = p.ws_split + 3 * cta;
+      w[0] = split_row;
+      w[1] = (int64_t)cta | (split_last << 32);
+      w[2] = total;
     }
     if (ok) {
       bool good;
@@ -942,7 +1045,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if constexpr (F8) {
     // ================================================= FP8: query split and widening ====
-    // Warp w splits heads 16 w .. of a segment's query, then widens rows 32 w .. 32 w + 31 of its tiles.
+    // Warp w splits heads 16 w .. of a segment's query (the CTA's first is split by the softmax warps,
+    // which have nothing else to do yet), then widens rows 32 w .. 32 w + 31 of its tiles.
     const int ww = warp - kWarpWiden0;
     const int gl = lane & 7, r0 = 32 * ww + (lane >> 3);
     // Lane = 16-byte granule gl of row r0 + 4 i: 16 codes, two granules widened. A granule's swizzle
@@ -963,19 +1067,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       if (!wait_warp(g_full(slot), (sc / kSegs) & 1)) break;
       const Seg s = segs[slot];
       if (s.type == 0) break;
-      if (s.ntiles > 0) {
-        if (qn > 0 && !wait_warp(q_empty, (qn - 1) & 1)) break;
-        ++qn;
-        split_query(p.q + (int64_t)s.t * p.q_st + (int64_t)s.hg * kHG * p.q_sh, p.q_sh, kHG / kWidenWarps * ww,
-                    min(kHG, p.H - s.hg * kHG), MODS ? p.sm_scale : p.sm_scale * kLog2e, smem + C::Q_OFF,
-                    reinterpret_cast<float*>(smem + C::SQ_OFF) + kHG * slot);
+      const bool split = s.ntiles > 0 && qn > 0;
+      if (split) {
+        if (!wait_warp(q_empty, (qn - 1) & 1)) break;
+        split_query<kHG / kWidenWarps>(p.q + (int64_t)s.t * p.q_st + (int64_t)s.hg * kHG * p.q_sh, p.q_sh,
+                                       kHG / kWidenWarps * ww, min(kHG, p.H - s.hg * kHG),
+                                       MODS ? p.sm_scale : p.sm_scale * kLog2e, smem + C::Q_OFF,
+                                       reinterpret_cast<float*>(smem + C::SQ_OFF) + kHG * slot);
       }
       __syncwarp();
-      if (lane == 0) {
-        if (s.ntiles > 0) mbar_arrive(q_full);
-        mbar_arrive(aux_full(slot));
-        mbar_arrive(g_empty(slot));
+      // (an arrival for each of the softmax warps, who arrive at the first segment's)
+      if (lane < kSoftmaxWarps / kWidenWarps) {
+        if (split) mbar_arrive(q_full);
+        if (split || s.ntiles == 0) mbar_arrive(aux_full(slot));
       }
+      if (lane == 0) mbar_arrive(g_empty(slot));
+      qn += s.ntiles > 0;
       if constexpr (C::WIDEN) {
         const uint32_t end = hs + 2 * (uint32_t)s.ntiles;
         for (; hs < end; ++hs) {
@@ -1026,6 +1133,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       if (!wait_warp(g_full(slot), (sc / kSegs) & 1)) break;
       const Seg s = segs[slot];
       if (s.type == 0) break;
+      if (F8 && sc == 0) split_first(s, slot);  // (a mass segment has tiles)
       if (!wait_warp(aux_full(slot), (sc / kSegs) & 1)) break;
       const float* sq = reinterpret_cast<const float*>(smem + C::SQ_OFF) + kHG * slot;
       const int heads = min(kHG, p.H - s.hg * kHG);
@@ -1115,6 +1223,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     const float inv_cap2 = MODS && p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
     const float f = MODS ? p.sm_scale : p.sm_scale * kLog2e;
     uint32_t g = 0, mb = 0;
+    bool first_query = true;
     bool failed = false;  // a wait ran out: go on without waiting, and leave with the group
     auto await = [&](uint32_t bar, uint32_t par) {
       if (failed || __all_sync(0xffffffffu, bar_wait(bar, par))) return;
@@ -1128,7 +1237,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     for (uint32_t sc = 0;; ++sc) {
       const uint32_t slot = sc % kSegs;
       await(g_full(slot), (sc / kSegs) & 1);
-      if (F8 && !failed && segs[slot].type != 0) await(aux_full(slot), (sc / kSegs) & 1);
+      if (F8 && !failed && segs[slot].type != 0) {
+        if (first_query && segs[slot].ntiles > 0) {
+          split_first(segs[slot], slot);
+          first_query = false;
+        }
+        await(aux_full(slot), (sc / kSegs) & 1);
+      }
       if (group_any(hq, failed)) break;
       const Seg s = segs[slot];
       __syncwarp();
@@ -1225,12 +1340,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         }
         if (exact) {
           // exact maximum of the tile per head; the running maxima are raised to it
+          float mine = -INFINITY;  // lane i ends with head i's
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
-            const int m0 = redux_max_s32(f2ord(y[i].x)), m1 = redux_max_s32(f2ord(y[i].y));
-            if (lane == 2 * i) red_part[64 * qd + hb + 2 * i] = ord2f(m0);
-            if (lane == 2 * i + 1) red_part[64 * qd + hb + 2 * i + 1] = ord2f(m1);
+            const float m0 = redux_max_f32(y[i].x), m1 = redux_max_f32(y[i].y);
+            mine = lane == 2 * i ? m0 : (lane == 2 * i + 1 ? m1 : mine);
           }
+          if (lane < kHW) red_part[64 * qd + hb + lane] = mine;
           if (F8) {
             // magnitudes order like their bits
             const uint32_t a0 = __reduce_max_sync(0xffffffffu, f2u(fabsf(scl.x)));
@@ -1428,39 +1544,20 @@ constexpr int kFewParts = 8;
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p) {
   __shared__ int s_part[kMaxCtas + 1];
   __shared__ float s_w[kMaxCtas + 1];
-  __shared__ int s_fin[8], s_cnt[8];
+  __shared__ int s_cnt[8];
   __shared__ float s_red[2][8];
   __shared__ float4 s_acc[kJoinThreads / 64][64];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t nrows = p.T * p.HG;
-  const bool by_row = nrows <= p.G;
-  // the CTAs after the first that hold a part: every one that continues the row, to the one that
-  // finishes it (thread t < 256 looks at CTA c + 1 + t; the chain's start is read meanwhile)
-  int c = blockIdx.x;
-  int64_t row = blockIdx.x;
-  if (by_row) {
-    c = p.ws_first[row];
-    if (c < 0) return;
-  } else {
-    row = p.ws_tail[c];
-    if (row < 0) return;
-  }
-  const int k = c + 1 + tid;
-  const int hd = tid < 256 && k < p.G ? p.ws_head[k] : 0;
-  if (warp < 8) {
-    const uint32_t fin = __ballot_sync(0xffffffffu, hd == 2);
-    if (lane == 0) s_fin[warp] = fin ? 32 * warp + __ffs(fin) - 1 : 1 << 20;
-  }
-  __syncthreads();
-  int last = s_fin[0];
-#pragma unroll
-  for (int w = 1; w < 8; ++w) last = min(last, s_fin[w]);
-  uint32_t mem = 0;
-  if (warp < 8) {
-    mem = __ballot_sync(0xffffffffu, hd != 0 && tid <= last);
-    if (lane == 0) s_cnt[warp] = __popc(mem);
-  }
+  const int64_t* rec = p.ws_split + 3 * (int64_t)blockIdx.x;
+  const int64_t row = rec[0], ends = rec[1], total = rec[2];
+  if (row < 0) return;
+  // the parts: of the CTA that starts the row, and of those after it to the one that finishes it whose
+  // share is not empty (there are more CTAs than tiles then)
+  const int c = (int)ends, last = (int)(ends >> 32);
+  const int k = c + 1 + tid;  // G is below the block's threads
+  const uint32_t mem = __ballot_sync(0xffffffffu, k <= last && share(k, total, p.G) < share(k + 1, total, p.G));
+  if (lane == 0) s_cnt[warp] = __popc(mem);
   __syncthreads();
   int at = 1, n = 1;
 #pragma unroll
@@ -1468,7 +1565,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     if (w < warp) at += s_cnt[w];
     n += s_cnt[w];
   }
-  if (warp < 8 && ((mem >> lane) & 1)) s_part[at + __popc(mem & ((1u << lane) - 1u))] = 2 * k;
+  if ((mem >> lane) & 1) s_part[at + __popc(mem & ((1u << lane) - 1u))] = 2 * k;
   if (tid == 0) s_part[0] = 2 * c + 1;
   __syncthreads();
   const int64_t t = p.HG == 1 ? row : row >> 1;
@@ -1666,16 +1763,14 @@ Params make_params(const dsa_paged_args_t* a) {
 
 // Workspace: partial outputs, their maxima and sums, then the split's records.
 struct Ws {
-  size_t o, ml, tail, head, first, bytes;
+  size_t o, ml, split, bytes;
 };
 Ws ws_layout(int G) {
   Ws w;
   w.o = 0;
   w.ml = w.o + (size_t)2 * G * kHG * kD * 4;
-  w.tail = w.ml + (size_t)2 * G * 2 * kHG * 4;
-  w.head = w.tail + (size_t)G * 8;
-  w.first = w.head + (size_t)G * 4;
-  w.bytes = w.first + (size_t)G * 4;
+  w.split = w.ml + (size_t)2 * G * 2 * kHG * 4;
+  w.bytes = w.split + (size_t)G * 24;
   return w;
 }
 
@@ -1800,9 +1895,7 @@ extern "C" dsa_status_t dsa_paged_attn(const dsa_paged_args_t* a, void* stream) 
   uint8_t* ws = static_cast<uint8_t*>(a->workspace);
   p.ws_o = reinterpret_cast<float*>(ws + w.o);
   p.ws_ml = reinterpret_cast<float*>(ws + w.ml);
-  p.ws_tail = reinterpret_cast<int64_t*>(ws + w.tail);
-  p.ws_head = reinterpret_cast<int*>(ws + w.head);
-  p.ws_first = reinterpret_cast<int*>(ws + w.first);
+  p.ws_split = reinterpret_cast<int64_t*>(ws + w.split);
   if ((st = paged::prepare_kernels(dev.device)) != DSA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if ((st = paged::launch<false>(p, a->kind, s)) != DSA_OK) return st;
