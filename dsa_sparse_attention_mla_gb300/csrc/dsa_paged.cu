@@ -146,15 +146,15 @@ struct Params {
   float* ws_o;      // [2 G][64 heads][256] unnormalised partial outputs: slot 2c the row CTA c
                     // continues, 2c + 1 the row it starts and does not finish
   float* ws_ml;     // [2 G][2][64] their maxima (exp2 domain) and sums
-  int64_t* ws_split; // [G][3] split rows, entry r for row r when there are at most G rows, else entry c
-                     // for the row that CTA c starts: the row (-1: not split, none), the CTAs that
-                     // start and finish it, and the split's total cost
+  int4* ws_split;   // [G] split rows, entry r for row r when there are at most G rows, else entry c for the
+                    // row that CTA c starts: the row (-1: not split, none), the CTAs that start and
+                    // finish it, and the split's total cost
 };
 
-// First cost of CTA c's share.
-__device__ __forceinline__ int64_t share(int c, int64_t total, int G) {
-  // G is at most kMaxCtas < 2^9: 32-bit divisions below 2^22
-  return total < (1 << 22) ? (int64_t)((uint32_t)c * (uint32_t)total / (uint32_t)G) : c * total / G;
+// First cost of CTA c's share, floor(c * total / G): G is at most kMaxCtas < 2^8.
+__device__ __forceinline__ int share(int c, int total, int G) {
+  const uint32_t q = (uint32_t)total / (uint32_t)G, r = (uint32_t)total - q * (uint32_t)G;
+  return (int)((uint32_t)c * q + (uint32_t)c * r / (uint32_t)G);
 }
 
 struct Seg {
@@ -245,9 +245,9 @@ struct Row {
   bool bad;          // something of it is not addressable
 };
 // Range of row `row` clipped to the addressable positions, and its tiles (0: nothing to read).
-__device__ __forceinline__ Row row_of(const Params& p, int64_t row) {
-  const int64_t t = p.HG == 1 ? row : row >> 1;
-  const int req = p.req ? p.req[t] : (int)t;
+__device__ __forceinline__ Row row_of(const Params& p, int row) {
+  const int t = p.HG == 1 ? row : row >> 1;
+  const int req = p.req ? p.req[t] : t;
   const int s = p.starts ? p.starts[t] : 0;
   Row r;
   r.req = req;
@@ -279,28 +279,28 @@ __device__ __forceinline__ float modify(float u, float cap, float inv_cap2, floa
 }
 
 // Exclusive sum over the block, and its total; `buf` holds kWarps values.
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* buf, int64_t* total) {
+__device__ __forceinline__ int block_sum(int v, int* buf, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t x = v;
+  int x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   if (lane == 31) buf[warp] = x;
   __syncthreads();
-  int64_t w = lane < kWarps ? buf[lane] : 0;  // every warp sums up the warps
+  int w = lane < kWarps ? buf[lane] : 0;  // every warp sums up the warps
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
+    const int y = __shfl_up_sync(0xffffffffu, w, o);
     if (lane >= o) w += y;
   }
   *total = __shfl_sync(0xffffffffu, w, 31);
-  const int64_t before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+  const int before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
   return (warp > 0 ? before : 0) + x - v;
 }
 // Exclusive running maximum over the block.
-__device__ __forceinline__ int block_max(int v, int64_t* buf) {
+__device__ __forceinline__ int block_max(int v, int* buf) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = v;
 #pragma unroll
@@ -312,7 +312,7 @@ __device__ __forceinline__ int block_max(int v, int64_t* buf) {
   int ex = __shfl_up_sync(0xffffffffu, x, 1);
   if (lane == 0) ex = INT32_MIN;
   __syncthreads();
-  int w = lane < warp ? (int)buf[lane] : INT32_MIN;
+  int w = lane < warp ? buf[lane] : INT32_MIN;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) w = max(w, __shfl_xor_sync(0xffffffffu, w, o));
   return max(ex, w);
@@ -337,57 +337,53 @@ __device__ __forceinline__ void group_sync(int group) {
 
 // Splits query rows h0 .. h0 + HEADS - 1 of a row (zero past `heads`) into e4m3 hi and lo terms, lane
 // l columns 8 l .. 8 l + 7, per head scaled by 2^-e so that the largest component lies in
-// [128, 256); sq[h] = f * 2^e. Four heads at a time, the next four on their way meanwhile.
+// [128, 256); sq[h] = f * 2^e. One head per round of a short loop, the next one on its way meanwhile
+// (the first call meets a cold instruction cache, and an unrolled body cost it 4 us).
 template <int HEADS>
 __device__ __forceinline__ void split_query(const uint16_t* q, int64_t q_sh, int h0, int heads, float f, uint8_t* qbuf,
                                             float* sq) {
   const int lane = threadIdx.x & 31;
   const int gl = lane & 15, tile = lane >> 4;
-  uint4 next[4];
   auto load = [&](int h) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      next[i] = h + i < heads ? *reinterpret_cast<const uint4*>(q + (h + i) * q_sh + 8 * lane) : make_uint4(0u, 0u, 0u, 0u);
+    return h < heads ? *reinterpret_cast<const uint4*>(q + h * q_sh + 8 * lane) : make_uint4(0u, 0u, 0u, 0u);
   };
-  load(h0);
+  // two lanes and two 128-byte lines each per head
+  if (HEADS > 1 && lane < 2 * HEADS && h0 + (lane >> 1) < heads) {
+    const uint16_t* a = q + (h0 + (lane >> 1)) * q_sh + 128 * (lane & 1);
+    asm volatile("prefetch.global.L2 [%0];\nprefetch.global.L2 [%1];" ::"l"(a), "l"(a + 64));
+  }
+  uint4 next = load(h0);
 #pragma unroll 1
-  for (int part = 0; part < HEADS / 4; ++part) {
-    uint4 v[4];
+  for (int h = h0; h < h0 + HEADS; ++h) {
+    const uint32_t w[4] = {next.x, next.y, next.z, next.w};
+    if (h + 1 < h0 + HEADS) next = load(h + 1);
+    uint32_t a = 0u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = next[i];
-    if (part + 1 < HEADS / 4) load(h0 + 4 * part + 4);
+    for (int j = 0; j < 4; ++j) a = max(a, max((w[j] << 16) & 0x7FFFFFFFu, w[j] & 0x7FFF0000u));
+    a = __reduce_max_sync(0xffffffffu, a);
+    int e = (int)(a >> 23) - 127 - 7;
+    e = a == 0u ? 0 : (e < -126 ? -126 : e);
+    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+    uint32_t hi[2], lo[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int h = h0 + 4 * part + i;
-      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-      uint32_t a = 0u;
+    for (int j = 0; j < 2; ++j) {
+      float x[4], r[4];
+      x[0] = __uint_as_float(w[2 * j] << 16) * inv;
+      x[1] = __uint_as_float(w[2 * j] & 0xFFFF0000u) * inv;
+      x[2] = __uint_as_float(w[2 * j + 1] << 16) * inv;
+      x[3] = __uint_as_float(w[2 * j + 1] & 0xFFFF0000u) * inv;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) a = max(a, max((w[j] << 16) & 0x7FFFFFFFu, w[j] & 0x7FFF0000u));
-      a = __reduce_max_sync(0xffffffffu, a);
-      int e = (int)(a >> 23) - 127 - 7;
-      e = a == 0u ? 0 : (e < -126 ? -126 : e);
-      const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-      uint32_t hi[2], lo[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float x[4], r[4];
-        x[0] = __uint_as_float(w[2 * j] << 16) * inv;
-        x[1] = __uint_as_float(w[2 * j] & 0xFFFF0000u) * inv;
-        x[2] = __uint_as_float(w[2 * j + 1] << 16) * inv;
-        x[3] = __uint_as_float(w[2 * j + 1] & 0xFFFF0000u) * inv;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) r[c] = __uint_as_float(__float_as_uint(x[c]) & 0xFFF00000u);  // four significant bits
-        hi[j] = (uint32_t)f32x2_to_e4m3x2(r[0], r[1]) | ((uint32_t)f32x2_to_e4m3x2(r[2], r[3]) << 16);
-        lo[j] = (uint32_t)f32x2_to_e4m3x2(x[0] - r[0], x[1] - r[1]) |
-                ((uint32_t)f32x2_to_e4m3x2(x[2] - r[2], x[3] - r[3]) << 16);
-      }
-      uint8_t* d = qbuf + tile * (kHG * 128) + h * 128 + (((gl >> 1) ^ (h & 7)) << 4) + 8 * (gl & 1);
-      *reinterpret_cast<uint2*>(d) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(d + 2 * kHG * 128) = make_uint2(lo[0], lo[1]);
-      // an infinite or NaN component makes the head's scores NaN
-      if (lane == 0)
-        sq[h] = a >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : f * __uint_as_float((uint32_t)(127 + e) << 23);
+      for (int c = 0; c < 4; ++c) r[c] = __uint_as_float(__float_as_uint(x[c]) & 0xFFF00000u);  // four significant bits
+      hi[j] = (uint32_t)f32x2_to_e4m3x2(r[0], r[1]) | ((uint32_t)f32x2_to_e4m3x2(r[2], r[3]) << 16);
+      lo[j] = (uint32_t)f32x2_to_e4m3x2(x[0] - r[0], x[1] - r[1]) |
+              ((uint32_t)f32x2_to_e4m3x2(x[2] - r[2], x[3] - r[3]) << 16);
     }
+    uint8_t* d = qbuf + tile * (kHG * 128) + h * 128 + (((gl >> 1) ^ (h & 7)) << 4) + 8 * (gl & 1);
+    *reinterpret_cast<uint2*>(d) = make_uint2(hi[0], hi[1]);
+    *reinterpret_cast<uint2*>(d + 2 * kHG * 128) = make_uint2(lo[0], lo[1]);
+    // an infinite or NaN component makes the head's scores NaN
+    if (lane == 0)
+      sq[h] = a >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : f * __uint_as_float((uint32_t)(127 + e) << 23);
   }
 }
 
@@ -458,12 +454,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
 
   // ---- the split: the total cost of the rows, and the row in which this CTA's share begins. Up to
   // kWarpRows rows the scheduler alone finds them (no block barrier waits for the lengths), else all.
-  int64_t* plan = reinterpret_cast<int64_t*>(smem + C::PLAN_OFF);
-  int64_t* plan_start = plan + 2 * kWarps;  // row, its cost offset, running maximum of the requests
-  const int64_t nrows = p.T * p.HG;
-  int64_t total = 0, row = 0, cost = 0;  // the scheduler's: where its walk begins
+  int* plan = reinterpret_cast<int*>(smem + C::PLAN_OFF);
+  int* plan_start = plan + 2 * kWarps;  // row, its cost offset, running maximum of the requests
+  const int nrows = (int)(p.T * p.HG);
+  int total = 0, row = 0, cost = 0;  // the scheduler's: where its walk begins
   int run = INT32_MIN;
-  auto cost_of = [&](const Row& r, int& run) -> int64_t {
+  auto cost_of = [&](const Row& r, int& run) -> int {
     bool ok = true;
     if (MASS && p.req) {
       ok = r.req > run;
@@ -472,25 +468,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     return (ok ? r.n : 0) + kRowOverhead;
   };
   if (nrows > kWarpRows) {
-    const int64_t per = (nrows + kThreads - 1) / kThreads;
-    const int64_t i0 = threadIdx.x * per, i1 = i0 + per < nrows ? i0 + per : nrows;
+    const int per = (nrows + kThreads - 1) / kThreads;
+    const int i0 = min((int)threadIdx.x * per, nrows), i1 = min(i0 + per, nrows);
     int mx = INT32_MIN;
     if (MASS && p.req) {
       int m = INT32_MIN;
-      for (int64_t i = i0; i < i1; ++i) m = max(m, p.req[i]);
+      for (int i = i0; i < i1; ++i) m = max(m, p.req[i]);
       mx = block_max(m, plan);
     }
-    int64_t sum = 0;
+    int sum = 0;
     run = mx;
-    for (int64_t i = i0; i < i1; ++i) sum += cost_of(row_of(p, i), run);
-    const int64_t pre = block_sum(sum, plan + kWarps, &total);
-    const int64_t c0 = share(cta, total, p.G);
+    for (int i = i0; i < i1; ++i) sum += cost_of(row_of(p, i), run);
+    const int pre = block_sum(sum, plan + kWarps, &total);
+    const int c0 = share(cta, total, p.G);
     if (pre <= c0 && c0 < pre + sum) {
-      int64_t at = pre, i = i0;
+      int at = pre, i = i0;
       run = mx;
       for (;; ++i) {
         int next = run;
-        const int64_t c = cost_of(row_of(p, i), next);
+        const int c = cost_of(row_of(p, i), next);
         if (c0 < at + c) break;
         at += c;
         run = next;
@@ -501,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     }
   } else if (warp == kWarpSched) {
     constexpr int PER = kWarpRows / 32;
-    const int per = ((int)nrows + 31) / 32, i0 = lane * per;
+    const int per = (nrows + 31) / 32, i0 = lane * per;
     Row r[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k)
@@ -520,23 +516,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       mx = __shfl_up_sync(0xffffffffu, m, 1);
       if (lane == 0) mx = INT32_MIN;
     }
-    int64_t mine = 0;
+    int mine = 0;
     int rn = mx;
 #pragma unroll
     for (int k = 0; k < PER; ++k)
       if (k < per && i0 + k < nrows) mine += cost_of(r[k], rn);
-    int64_t cum = mine;
+    int cum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, cum, o);
+      const int y = __shfl_up_sync(0xffffffffu, cum, o);
       if (lane >= o) cum += y;
     }
     total = __shfl_sync(0xffffffffu, cum, 31);
     // the last 32 rows at most are walked from the lane whose rows hold the start
-    const int64_t c0 = share(cta, total, p.G), pre = cum - mine;
+    const int c0 = share(cta, total, p.G), pre = cum - mine;
     const uint32_t in = __ballot_sync(0xffffffffu, pre <= c0 && c0 < cum);
     const int src = __ffs(in) - 1;  // some lane: c0 < total
-    row = (int64_t)src * per;
+    row = src * per;
     cost = __shfl_sync(0xffffffffu, pre, src);
     run = __shfl_sync(0xffffffffu, mx, src);
   }
@@ -582,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     // ================================================================== scheduler ====
     uint32_t sc = 0;
     uint32_t g = 0;  // tiles mapped
-    int64_t split_row = -1, split_last = 0;  // the row this CTA starts and does not finish
+    int split_row = -1, split_last = 0;  // the row this CTA starts and does not finish
     bool ok = true;
     auto map_slot = [&](bool& good) -> int4* {
       const uint32_t m = g % kMaps;
@@ -668,12 +664,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     if (nrows > kWarpRows) {
       row = plan_start[0];
       cost = plan_start[1];
-      run = (int)plan_start[2];
+      run = plan_start[2];
     }
-    const int64_t c0 = share(cta, total, p.G), c1 = share(cta + 1, total, p.G);
+    const int c0 = share(cta, total, p.G), c1 = share(cta + 1, total, p.G);
     if (c0 < c1) {
       while (ok && cost < c1 && row < nrows) {
-        const int64_t i = row + lane;
+        const int i = row + lane;
         Row r{};
         int c = 0;
         bool order = true;
@@ -695,15 +691,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
           order = r.req > before;
         }
         const int n = order ? r.n : 0;
-        int64_t cum = c ? (int64_t)n + kRowOverhead : 0;
-        const int64_t mine = cum;
+        int cum = c ? n + kRowOverhead : 0;
+        const int mine = cum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const int64_t y = __shfl_up_sync(0xffffffffu, cum, o);
+          const int y = __shfl_up_sync(0xffffffffu, cum, o);
           if (lane >= o) cum += y;
         }
-        const int64_t at = cost + cum - mine;  // this row's cost offset
-        int64_t lo = c0 - at - kRowOverhead, hi = c1 - at - kRowOverhead;
+        const int at = cost + cum - mine;  // this row's cost offset
+        int lo = c0 - at - kRowOverhead, hi = c1 - at - kRowOverhead;
         lo = lo < 0 ? 0 : lo;
         hi = hi > n ? n : hi;
         const bool owner = c && at >= c0 && at < c1;
@@ -712,16 +708,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         const bool has = c && (n > 0 ? lo < hi : owner && !MASS);
         const int kind = lo > 0 ? 2 : (hi < n ? 1 : 0);
         // the CTA of a split row's last tile: the largest whose share starts at or before it
-        int64_t last = 0;
+        int last = 0;
         if (kind == 1) {
-          const int64_t end = (at + kRowOverhead + n) * p.G - 1;
-          last = total < (1 << 22) ? (int64_t)((uint32_t)end / (uint32_t)total) : end / total;
+          // from the quotient's estimate: shares are total / G long, give or take one
+          last = min(p.G - 1, (int)((float)(at + kRowOverhead + n) * ((float)p.G / (float)total)));
+          while (last > 0 && share(last, total, p.G) >= at + kRowOverhead + n) --last;
+          while (last + 1 < p.G && share(last + 1, total, p.G) < at + kRowOverhead + n) ++last;
         }
         if (!MASS && nrows <= p.G && has && kind != 2) {
-          int64_t* w = p.ws_split + 3 * i;
-          w[0] = kind == 1 ? i : -1;
-          w[1] = (int64_t)cta | (last << 32);
-          w[2] = total;
+          p.ws_split[i] = make_int4(kind == 1 ? i : -1, cta, last, total);
         }
         uint32_t todo = __ballot_sync(0xffffffffu, has);
         if (!MASS) {
@@ -742,21 +737,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
           if (lane == src) {
             Seg* s = segs + slot;
             s->type = 1;
-            s->t = (int)(p.HG == 1 ? i : i >> 1);
-            s->hg = p.HG == 1 ? 0 : (int)(i & 1);
+            s->t = p.HG == 1 ? i : i >> 1;
+            s->hg = p.HG == 1 ? 0 : i & 1;
             s->req = r.req;
             s->a = r.a;
             s->b = r.b;
-            s->tile0 = (int)lo;
-            s->ntiles = n > 0 ? (int)(hi - lo) : 0;
+            s->tile0 = lo;
+            s->ntiles = n > 0 ? hi - lo : 0;
             s->kind = kind;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(g_full(slot));
           ++sc;
           const int a = __shfl_sync(0xffffffffu, r.a, src), b = __shfl_sync(0xffffffffu, r.b, src);
-          const int t0 = __shfl_sync(0xffffffffu, (int)lo, src);
-          const int nt = __shfl_sync(0xffffffffu, n > 0 ? (int)(hi - lo) : 0, src);
+          const int t0 = __shfl_sync(0xffffffffu, lo, src);
+          const int nt = __shfl_sync(0xffffffffu, n > 0 ? hi - lo : 0, src);
           const int req = __shfl_sync(0xffffffffu, r.req, src);
           if (!map_tiles(req, (uint32_t)a, (uint32_t)b, (uint32_t)(a & ~127) + 128u * (uint32_t)t0, nt)) {
             ok = false;
@@ -767,12 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         cost += __shfl_sync(0xffffffffu, cum, 31);
       }
     }
-    if (!MASS && nrows > p.G && lane == 0) {
-      int64_t* w = p.ws_split + 3 * cta;
-      w[0] = split_row;
-      w[1] = (int64_t)cta | (split_last << 32);
-      w[2] = total;
-    }
+    if (!MASS && nrows > p.G && lane == 0) p.ws_split[cta] = make_int4(split_row, cta, split_last, total);
     if (ok) {
       bool good;
       int4* dst = map_slot(good);
@@ -1549,12 +1539,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   __shared__ float4 s_acc[kJoinThreads / 64][64];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t* rec = p.ws_split + 3 * (int64_t)blockIdx.x;
-  const int64_t row = rec[0], ends = rec[1], total = rec[2];
+  const int4 rec = p.ws_split[blockIdx.x];
+  const int row = rec.x, c = rec.y, last = rec.z, total = rec.w;
   if (row < 0) return;
   // the parts: of the CTA that starts the row, and of those after it to the one that finishes it whose
   // share is not empty (there are more CTAs than tiles then)
-  const int c = (int)ends, last = (int)(ends >> 32);
   const int k = c + 1 + tid;  // G is below the block's threads
   const uint32_t mem = __ballot_sync(0xffffffffu, k <= last && share(k, total, p.G) < share(k + 1, total, p.G));
   if (lane == 0) s_cnt[warp] = __popc(mem);
@@ -1569,7 +1558,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   if (tid == 0) s_part[0] = 2 * c + 1;
   __syncthreads();
   const int64_t t = p.HG == 1 ? row : row >> 1;
-  const int hg = p.HG == 1 ? 0 : (int)(row & 1);
+  const int hg = p.HG == 1 ? 0 : row & 1;
   const int heads = min(kHG, p.H - hg * kHG);
   const int per = kHG / gridDim.y;
   const int col = tid & 63, pg = tid >> 6;
@@ -1770,15 +1759,18 @@ Ws ws_layout(int G) {
   w.o = 0;
   w.ml = w.o + (size_t)2 * G * kHG * kD * 4;
   w.split = w.ml + (size_t)2 * G * 2 * kHG * 4;
-  w.bytes = w.split + (size_t)G * 24;
+  w.bytes = w.split + (size_t)G * sizeof(int4);
   return w;
 }
 
+int64_t most_tiles(const Params& p) { return (p.pos_limit < 0x7FFFFFFF ? p.pos_limit : 0x7FFFFFFF) / kBN + 1; }
+// The rows' costs must add up within 31 bits.
+bool splittable(const Params& p) { return p.T * p.HG * (most_tiles(p) + kRowOverhead) <= 0x7FFFFFFF; }
+
 // One CTA per SM, and no more than there can be tiles.
 int grid_of(const Params& p, const DeviceInfo& dev) {
-  const int64_t tiles = (p.pos_limit < 0x7FFFFFFF ? p.pos_limit : 0x7FFFFFFF) / kBN + 1;
   const int sms = dev.sm_count < kMaxCtas ? dev.sm_count : kMaxCtas;
-  const int64_t most = p.T * p.HG * tiles;
+  const int64_t most = p.T * p.HG * most_tiles(p);
   return (int)(most < sms ? most : sms);
 }
 
@@ -1885,9 +1877,10 @@ extern "C" dsa_status_t dsa_paged_attn_workspace_size(const dsa_paged_args_t* a,
 extern "C" dsa_status_t dsa_paged_attn(const dsa_paged_args_t* a, void* stream) {
   dsa_status_t st = paged::check(a, false);
   if (st != DSA_OK || a->T == 0) return st;
+  paged::Params p = paged::make_params(a);
+  if (!paged::splittable(p)) return DSA_ERR_UNSUPPORTED;
   DeviceInfo dev;
   if ((st = current_device(&dev)) != DSA_OK) return st;
-  paged::Params p = paged::make_params(a);
   p.G = paged::grid_of(p, dev);
   const paged::Ws w = paged::ws_layout(p.G);
   if (!a->workspace || !aligned(a->workspace, 256)) return DSA_ERR_INVALID_ARGUMENT;
@@ -1895,7 +1888,7 @@ extern "C" dsa_status_t dsa_paged_attn(const dsa_paged_args_t* a, void* stream) 
   uint8_t* ws = static_cast<uint8_t*>(a->workspace);
   p.ws_o = reinterpret_cast<float*>(ws + w.o);
   p.ws_ml = reinterpret_cast<float*>(ws + w.ml);
-  p.ws_split = reinterpret_cast<int64_t*>(ws + w.split);
+  p.ws_split = reinterpret_cast<int4*>(ws + w.split);
   if ((st = paged::prepare_kernels(dev.device)) != DSA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if ((st = paged::launch<false>(p, a->kind, s)) != DSA_OK) return st;
@@ -1926,10 +1919,11 @@ extern "C" dsa_status_t dsa_paged_attn_mass(const dsa_paged_args_t* a, const flo
   if (!mass || !mass_out || mass_width < 0 || mass_stride < mass_width || mass_out_stride < mass_width)
     return DSA_ERR_INVALID_ARGUMENT;
   if (mass_out == mass && mass_out_stride != mass_stride) return DSA_ERR_INVALID_ARGUMENT;  // in place: the same rows
-  DeviceInfo dev;
-  if ((st = current_device(&dev)) != DSA_OK) return st;
   paged::Params p = paged::make_params(a);
   if (mass_width < p.pos_limit) p.pos_limit = mass_width;
+  if (!paged::splittable(p)) return DSA_ERR_UNSUPPORTED;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != DSA_OK) return st;
   p.mass = mass;
   p.mass_st = mass_stride;
   p.mass_out = mass_out;

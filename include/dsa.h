@@ -308,7 +308,8 @@ DSA_API dsa_status_t dsa_proj_gemm(const void* x_codes, const void* x_scales, co
 typedef struct dsa_paged_args {
   const void* q;                 /* bf16 [T, H, 256], 16-byte aligned, strides multiples of 8 */
   int64_t q_stride_t, q_stride_h;
-  int64_t T;                     /* query tokens, at most 2^24 (0 = no-op) */
+  int64_t T;                     /* query tokens, at most 2^24 (0 = no-op); T * ceil(H / 64) *
+                                    (addressable positions / 128 + 2) below 2^31 */
   int H;                         /* heads: 1 .. 128 */
   const void* cache;
   dsa_cache_kind_t kind;

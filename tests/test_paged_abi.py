@@ -84,6 +84,15 @@ def test_paged_more_refusals(dsa_lib):
     assert L.dsa_paged_attn_mass(ctypes.byref(a), PTR, 640, PTR, 640, -1, None) == INVALID
     # in place means the same rows
     assert L.dsa_paged_attn_mass(ctypes.byref(a), PTR, 640, PTR, 648, 640, None) == INVALID
+    # rows' costs that do not fit 31 bits; the mass's rows bound them too
+    b = _paged()
+    b.T = b.num_requests = 1 << 24
+    b.bt_stride = b.max_pages = 1000
+    b.lse = PTR
+    assert L.dsa_paged_attn(ctypes.byref(b), None) == UNSUPPORTED
+    assert L.dsa_paged_attn_mass(ctypes.byref(b), PTR, 64000, PTR, 64000, 64000, None) == UNSUPPORTED
+    b.num_slots = 1 << 31
+    assert L.dsa_paged_attn(ctypes.byref(b), None) == UNSUPPORTED
     a.T = 0
     assert L.dsa_paged_attn(ctypes.byref(a), None) == OK
     n = ctypes.c_size_t(0)
@@ -109,7 +118,8 @@ def _evict():
     ("max_pages", 11, INVALID), ("block_table", 0, INVALID), ("sink", -1, INVALID), ("recent", -1, INVALID),
     ("budget", -1, INVALID), ("width", 0, INVALID), ("width", (1 << 30) + 1, INVALID), ("mass_stride", 639, INVALID),
     ("mass_out_stride", 639, INVALID), ("mass_out_stride", 648, INVALID), ("workspace", 0, INVALID),
-    ("workspace", PTR + 4, INVALID), ("workspace_bytes", 100, SMALL), ("num_requests", 0, OK)])
+    ("workspace", PTR + 4, INVALID), ("workspace_bytes", 100, SMALL), ("num_requests", 0, OK),
+    ("num_requests", 65536, UNSUPPORTED)])
 def test_evict_refusals(dsa_lib, field, value, want):
     a = _evict()
     setattr(a, field, value)
