@@ -1038,18 +1038,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     // Warp w splits heads 16 w .. of a segment's query (the CTA's first is split by the softmax warps,
     // which have nothing else to do yet), then widens rows 32 w .. 32 w + 31 of its tiles.
     const int ww = warp - kWarpWiden0;
-    const int gl = lane & 7, r0 = 32 * ww + (lane >> 3);
-    // Lane = 16-byte granule gl of row r0 + 4 i: 16 codes, two granules widened. A granule's swizzle
-    // repeats every second i.
-    uint32_t from[2], to[2][2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = r0 + 4 * i;
-      from[i] = (uint32_t)(r * 128 + ((gl ^ (r & 7)) << 4));
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        to[i][j] = (uint32_t)((gl >> 2) * (kBN * 128) + r * 128 + ((((2 * gl + j) & 7) ^ (r & 7)) << 4));
-    }
+    // In round t a lane takes a 16-byte granule (4 t + lane % 4) of a row and writes two. Eight lanes
+    // that access memory together take rows k and k ^ 5 of a group of eight, whose swizzles keep the
+    // four granules read, and the four written, of one row off the other's banks.
+    const int g4 = lane & 3, r7 = (lane >> 3) ^ (lane & 4 ? 5 : 0);
+    const uint32_t row = (uint32_t)(32 * ww + r7) * 128;
+    const uint32_t from[2] = {row + ((g4 ^ r7) << 4), row + (((4 + g4) ^ r7) << 4)};
+    const uint32_t to[2] = {row + (((2 * g4) ^ r7) << 4), row + (((2 * g4 + 1) ^ r7) << 4)};
     uint32_t hs = 0, qn = 0;  // halves widened, queries split
     bool ok = true;
     for (uint32_t sc = 0; ok; ++sc) {
@@ -1086,15 +1081,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
           uint8_t* wide = smem + C::W_OFF + sw * C::WIDE_BYTES;
 #pragma unroll
           for (int part = 0; part < 2; ++part) {
-            uint4 v[4];
+            uint4 v[4];  // row groups 2 part, 2 part + 1, both rounds
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4*>(raw + from[i & 1] + 1024 * (i >> 1) + 2048 * part);
+            for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4*>(raw + from[i & 1] + 1024 * (2 * part + (i >> 1)));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const uint32_t c[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
               for (int j = 0; j < 2; ++j)
-                *reinterpret_cast<uint4*>(wide + to[i & 1][j] + 1024 * (i >> 1) + 2048 * part) = make_uint4(
+                *reinterpret_cast<uint4*>(wide + to[j] + (i & 1) * (kBN * 128) + 1024 * (2 * part + (i >> 1))) = make_uint4(
                     e4m3x2_to_f16x2((uint16_t)c[2 * j]), e4m3x2_to_f16x2((uint16_t)(c[2 * j] >> 16)),
                     e4m3x2_to_f16x2((uint16_t)c[2 * j + 1]), e4m3x2_to_f16x2((uint16_t)(c[2 * j + 1] >> 16)));
             }
