@@ -407,3 +407,107 @@ def test_slots_past_32_bits_of_bytes(gpu):
     got = dsa.dsa_paged_attn(q, cache, k, bt2, lens, s, page_size=64)
     torch.cuda.synchronize()
     assert torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("kind", [BF16, FP8])
+@pytest.mark.parametrize("n,H,top", [(257, 1, 3), (300, 8, 400), (300, 65, 300), (1500, 2, 140)])
+def test_many_tokens(gpu, kind, n, H, top):
+    """More rows than one warp plans, far more than CTAs, empty ones among them."""
+    lens = np.random.default_rng(n + H).integers(0, top + 1, n)
+    lens[lens % 5 == 0] = 0
+    c = Case(gpu, kind, lens, H, 16, seed=n)
+    out, lse, opts = run_and_check(c)
+    check_mass(c, lse, opts)
+
+
+@pytest.mark.parametrize("kind", [BF16, FP8])
+def test_many_tokens_of_one_request(gpu, kind):
+    """A prompt's last tokens, each attending to all before it."""
+    c = Case(gpu, kind, np.arange(1, 301), 4, 64, seed=43, req=[0] * 300)
+    run_and_check(c)
+
+
+@pytest.mark.parametrize("kind", [BF16, FP8])
+def test_mass_order_among_many_tokens(gpu, kind):
+    """Requests out of order and repeated, in a batch that the whole block plans: the mass holds what
+    the tokens in order give, the others add nothing."""
+    n, H = 400, 8
+    rng = np.random.default_rng(47)
+    req = np.arange(n)
+    back = np.sort(rng.choice(np.arange(1, n), 60, replace=False))
+    req[back] = [rng.integers(0, i) for i in back]
+    c = Case(gpu, kind, rng.integers(1, 300, n), H, 16, seed=53, req=req)
+    q, cache, k, bt, lens, s = c.args()
+    opts = c.opts()
+    lse = torch.zeros((n, H), device=gpu)
+    dsa.dsa_paged_attn(*c.args(), lse=lse, **opts)
+    good = np.zeros(n, dtype=bool)
+    top = -1
+    for i in range(n):
+        good[i] = req[i] > top
+        top = max(top, req[i])
+    assert not good[back].any() and good.sum() == n - 60
+    err = torch.zeros(1, dtype=torch.int32, device=gpu)
+    mass = torch.zeros((c.bt.shape[0], 310), device=gpu)
+    dsa.dsa_paged_attn_mass(*c.args(), lse, mass, error_word=err, **opts)
+    torch.cuda.synchronize()
+    assert err.item() == dsa.DEVERR_REQUEST_ORDER
+    got = mass.cpu().numpy().astype(np.float64)
+    gl = lse.cpu().numpy().astype(np.float64)
+    ref, tol = np.zeros(got.shape), np.zeros(got.shape)
+    for t in np.flatnonzero(good):
+        u, _, pos, d = c.reference(t)
+        w = np.exp(u - gl[t][:, None])
+        ref[req[t], pos] = w.sum(axis=0)
+        tol[req[t], pos] = (w * (d[:, None] + 2.0 ** -20)).sum(axis=0)
+    tol += (H + 2) * 2.0 ** -24 * np.abs(ref)
+    assert (np.abs(got - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("page", [33, 65, 129, 255])
+@pytest.mark.parametrize("start", [0, 1, 97])
+def test_fp8_rows_from_odd_slots(gpu, page, start):
+    """Pages of an odd number of rows: runs of rows begin at odd and at even slots, where an FP8 row
+    (264 bytes) starts on 8 and on 16 bytes."""
+    c = Case(gpu, FP8, [700, 333, 2000], 16, page, seed=page + start)
+    # pages that follow one another from an odd and from an even one: whole tiles of adjacent rows
+    c.bt[2, :6] = np.arange(3, 9)
+    c.bt[1, :2] = [2, 3]
+    starts = np.array([start, start, start], dtype=np.int32)
+    out, lse, opts = run_and_check(c, starts=starts)
+    check_mass(c, lse, opts, starts=starts)
+
+
+@pytest.mark.parametrize("kind", [BF16, FP8])
+def test_mass_streams_and_graphs(gpu, kind):
+    """Two streams at once, and two captured graphs replayed in turn."""
+    c = Case(gpu, kind, [3000, 45], 64, seed=59)
+    d = Case(gpu, kind, [129, 2500], 33, seed=61)
+    calls = []
+    for x in (c, d):
+        lse = torch.zeros((2, x.H), device=gpu)
+        a = x.args()
+        dsa.dsa_paged_attn(*a, lse=lse, page_size=64)
+        mass = torch.rand((2, 3010), device=gpu)
+        to = torch.zeros_like(mass)
+        calls.append((a, lse, mass, to))
+    def go(i):
+        a, lse, mass, to = calls[i]
+        dsa.dsa_paged_attn_mass(*a, lse, mass, mass_out=to, page_size=64)
+    go(0), go(1)
+    torch.cuda.synchronize()
+    ref = [calls[0][3].clone(), calls[1][3].clone()]
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    for i in range(2):
+        with torch.cuda.graph(graphs[i]):
+            go(i)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for call in (go, lambda i: graphs[i].replay()):
+        for _ in range(3):
+            calls[0][3].zero_(), calls[1][3].zero_()
+            torch.cuda.synchronize()
+            for i in range(2):
+                with torch.cuda.stream(streams[i]):
+                    call(i)
+            torch.cuda.synchronize()
+            assert torch.equal(calls[0][3], ref[0]) and torch.equal(calls[1][3], ref[1])
