@@ -6,8 +6,13 @@
 //   out_h = sum_j softmax_j(u_h) k_j,  lse_h = log sum_j exp(u_hj)
 //   mass_out[r, j] = mass[r, j] + sum_h exp(u_hj - lse_h)
 // The latent row k_j is key and value of every head: a position costs 264 (FP8) or 512 (bf16) bytes
-// and 4 * 256 operations per head, so with 64 heads a bf16 cache is bound by HBM and an FP8 one
-// about equally by HBM and the tensor core.
+// and 4 * 256 operations per head, so with 64 heads a bf16 cache is bound by HBM and an FP8 one by
+// HBM and the tensor core about equally. What an FP8 tile meets first is shared memory: its operands,
+// copies, widened values and weights are some 2800 cycles at 128 bytes each, against 1470 of HBM, and of
+// what was tried only less work on shared memory made it faster (128 tokens x 32768 positions: widening
+// without bank conflicts 575 -> 549 us, 16-byte copies 549 -> 489; deeper rings, or weights handed over
+// by halves, did not). Measured: 128 x 32768 FP8 positions 484 us (2.3 TB/s; 167 at HBM's rate), 64
+// ragged bf16 requests, 144 MB of rows, 51 us (2.8 TB/s; 21).
 //
 // Shape of the computation
 //  * Transposed products: S^T[key, head] = K Q^T with M = 128 keys, N = 64 heads, then
@@ -22,29 +27,28 @@
 //    tile: p * scale relative to the largest scale so far, 2^22 of normal range below the strongest
 //    position. e4m3 weights (as two terms) would need no widening but lose what many far positions add
 //    up to beside one strong one. So the keys are the exact products code * scale.
-//  * Softmax with one thread per key and 32 heads (two warps per lane quarter; the
-//    four warps of the same heads share running maxima and synchronise among themselves). The running maximum
-//    of a head is raised, and O and the sums rescaled, only when some score exceeds it by 2^20 (FP8:
-//    2^6): p and its sums are floating point, so a stale maximum costs no precision, and the exact path runs
-//    for a segment's first tile and almost never again.
+//  * Softmax with one thread per key and 16 heads: four groups of four warps, a warp per lane quarter of
+//    tensor memory in each. The warps of a group share running maxima and synchronise among themselves. The
+//    running maximum of a head is raised, and O and the sums rescaled, only when some score exceeds it by
+//    2^20 (FP8: 2^6): p and its sums are floating point, so a stale maximum costs no precision, and the
+//    exact path runs for a segment's first tile and almost never again.
 //  * Persistent CTAs, one per SM. Each computes the same split from the lengths (they live on the
 //    device): rows (token, group of 64 heads) cost their 128-position tiles plus a constant, and
 //    CTA c takes the c-th of G equal parts of the total. A row cut by a border leaves unnormalised
 //    parts in the workspace, which a second, dependent launch joins in the order of the parts.
-//  * Warp roles: 0-7 softmax, 8 scheduler (walks the CTA's rows and finds the slots of each tile's
-//    positions, up to eight tiles ahead), 9 score products, 10 value products, 11 query loads, 12-15
-//    row loads, 16-19 FP8: query split and widening. Every wait is bounded. What bounds a tile is the
-//    instructions its warps issue, so every job has warps of its own with no polling between jobs, a
-//    softmax warp takes 32 heads (sixteen warps of 16 took the same time with twice the waits), and
-//    the arithmetic is on pairs. The registers are split anew after the start (a spill would leave
-//    the L1 that the tiles leave over: a tile took 9500 cycles with spills).
+//  * Warp roles: 0-15 softmax, 16 scheduler (walks the CTA's rows and finds the slots of each tile's
+//    positions, up to eight tiles ahead), 17 score products, 18 value products, 19 query loads, 20-23
+//    row loads, 24-27 FP8: query split and widening. Every wait is bounded. Every job has warps of its
+//    own with no polling between jobs, and the arithmetic is on pairs. The registers are split anew after
+//    the start (a spill in the loop would leave the L1 that the tiles leave over: a tile took 9500 cycles
+//    with spills).
 //  * bf16 tiles without a masked position come by TMA, in boxes of as many rows as a page and a tile
 //    share; other bf16 tiles and FP8 rows (264 bytes: no tensor map takes that pitch) by cp.async
 //    straight to their swizzled place. Either way every free stage of the ring holds loads in flight
 //    and no register does. FP8: other warps widen the rows into a second ring while the softmax
 //    of their tile runs.
 //  * The mass kernel is the same without the value product: with the lse given, each key's thread
-//    adds the weights of all 64 heads; two groups of four warps take tiles in turn.
+//    adds the weights of all 64 heads; four groups of four warps take tiles in turn.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -75,8 +79,9 @@ constexpr int kWarpRows = 256;     // rows whose costs one warp sums up, eight p
 constexpr int kSegs = 8;           // segment ring depth
 constexpr int kMaps = 8;           // tiles whose slots are known ahead
 // Smallest page whose rows the scheduler prefetches into L2 (an eighth of a tile per request), FP8
-// only: 128 x 32768 positions 624 us against 706 without; bf16 tiles come by TMA in any case, and 64
-// ragged requests took 72 us with it, 66 without.
+// only. It shortens the start of short shares: 8 heads with a distance bias 45 us with it, 48 without;
+// 128 x 32768 positions take the same (488 and 487). bf16 tiles come by TMA in any case, and 64 ragged
+// requests took 72 us with it, 66 without, when it was tried.
 constexpr int kPrefetchPage = 16;
 constexpr int kRowOverhead = 1;    // a row's start and end, in tiles
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -908,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
   } else if (warp == kWarpQuery) {
     // ================================================================ query loads ====
     // 64 heads x 256 columns in four 128-byte-swizzled chunks; heads past the row's are zero.
-    // FP8: the load warps split the query, and for the attention nothing is left to do here.
+    // FP8: the softmax and the widening warps split the query, and for the attention nothing is left to do here.
     uint32_t qc = 0;
     for (uint32_t sc = 0; !C::WIDEN; ++sc) {
       const uint32_t slot = sc % kSegs;
@@ -1679,12 +1684,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         }
       }
     }
-    const int groups = kGroups;
-    if (pg < groups) s_acc[pg][col] = acc;
+    s_acc[pg][col] = acc;
     __syncthreads();
     if (pg == 0) {
       const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);
-      for (int i = 1; i < groups; ++i) {
+      for (int i = 1; i < kGroups; ++i) {
         const float4 x = s_acc[i][col];
         acc.x += x.x;
         acc.y += x.y;

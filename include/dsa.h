@@ -382,8 +382,9 @@ DSA_API dsa_status_t dsa_paged_attn_mass(const dsa_paged_args_t* args, const flo
  * A request whose n exceeds `width` or the addressable positions, or with a page among its n
  * positions that addresses no slot, keeps all as well and sets DSA_DEVERR_INDEX_OUT_OF_RANGE
  * (only its first min(n, width) entries are copied).
- * The pages of a request that is shrunk must be its own: a page that another request also names
- * would change under it (give such a request a budget of at least its length).
+ * The pages of a request that is shrunk must be its own, each named once among its n positions: a
+ * page that another request also names would change under it, and rows of a page named twice would
+ * move over one another (give such a request a budget of at least its length).
  * Cache rows of both kinds and both geometries (256+0, 512+64). Direct mode (block_table NULL)
  * takes one request. Bit-identical across repeated calls.
  */

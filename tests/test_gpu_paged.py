@@ -511,3 +511,36 @@ def test_mass_streams_and_graphs(gpu, kind):
                     call(i)
             torch.cuda.synchronize()
             assert torch.equal(calls[0][3], ref[0]) and torch.equal(calls[1][3], ref[1])
+
+
+@pytest.mark.parametrize("kind", [BF16, FP8])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_mass_of_bad_pages(gpu, kind, cap):
+    """Positions of bad pages, a whole request of them (its lse is -inf) among them: they add nothing
+    and are copied."""
+    lens = [300, 200, 64]
+    c = Case(gpu, kind, lens, 32, seed=67)
+    c.bt[0, 1] = -7
+    c.bt[1, :] = -1
+    c.bt[2, 0] = c.cache.shape[0]
+    lse = torch.zeros((3, 32), device=gpu)
+    dsa.dsa_paged_attn(*c.args(), lse=lse, logit_cap=cap, **c.opts())
+    m0 = np.random.default_rng(71).random((3, 310)).astype(np.float32)
+    mass = torch.from_numpy(m0).to(gpu)
+    to = torch.full_like(mass, -5.0)
+    err = torch.zeros(1, dtype=torch.int32, device=gpu)
+    dsa.dsa_paged_attn_mass(*c.args(), lse, mass, mass_out=to, error_word=err, logit_cap=cap, **c.opts())
+    torch.cuda.synchronize()
+    assert err.item() == dsa.DEVERR_INDEX_OUT_OF_RANGE
+    got, gl = to.cpu().numpy(), lse.cpu().numpy().astype(np.float64)
+    assert np.isfinite(gl[0]).all() and np.isneginf(gl[1:]).all()
+    assert (got[0, 64:128] == m0[0, 64:128]).all()
+    assert (got[1, :200] == m0[1, :200]).all() and (got[2, :64] == m0[2, :64]).all()
+    assert (got[0, 300:] == -5).all() and (got[1, 200:] == -5).all() and (got[2, 64:] == -5).all()
+    u, _, pos, d = c.reference(0, cap=cap)
+    w = np.exp(u - gl[0][:, None])
+    ref = m0[0].astype(np.float64)
+    ref[pos] += w.sum(axis=0)
+    tol = (c.H + 2) * 2.0 ** -24 * np.abs(ref)
+    tol[pos] += (w * (d[:, None] + 2.0 ** -20)).sum(axis=0)
+    assert (np.abs(got[0] - ref) <= tol)[:300].all()
