@@ -397,7 +397,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
   using C = Cfg<KIND, MASS>;
   constexpr bool F8 = C::F8;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // an offset, not a rounded address: the compiler keeps knowing that this is shared memory
+  uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x;
