@@ -1260,29 +1260,28 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         await(aux_full(slot), (sc / kSegs) & 1);
       }
       if (group_any(hq, failed)) break;
-      const Seg s = segs[slot];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(g_empty(slot));
+      const Seg& s = segs[slot];  // read where it is needed: registers are short in the loop over the tiles
       if (s.type == 0) break;
       const int heads = min(kHG, p.H - s.hg * kHG);
       // chunks of 16 heads in use: the weights of the others meet only unused columns of O^T
       const int nch = max(0, min(CH, (heads - hb + 15) >> 4));
       const float* slopes = s_slopes + s.hg * kHG + hb;
       const float* sq = reinterpret_cast<const float*>(smem + C::SQ_OFF) + kHG * slot + hb;
-      int64_t qp = 0;
-      if (MODS) qp = p.qpos ? p.qpos[s.t] : (int64_t)p.lengths[s.t] - 1;
+      int qp = 0;
+      if (MODS) qp = p.qpos ? p.qpos[s.t] : (int)((uint32_t)p.lengths[s.t] - 1u);  // (used where there are tiles: a length above 0)
       float2 lsum[NP];  // heads 2 i, 2 i + 1 of the group
 #pragma unroll
       for (int i = 0; i < NP; ++i) lsum[i] = make_float2(0.0f, 0.0f);
       bool fresh = true;  // no valid key so far: m counts as 0, no reference scale
-      for (int k = 0; k < s.ntiles; ++k, ++g) {
+      const int ntiles = s.ntiles;
+      for (int k = 0; k < ntiles; ++k, ++g) {
         const uint32_t sb = g % C::NSB;
         float dist = 0.0f;
         if (MODS && p.slopes) {
           const uint32_t pos = (uint32_t)(s.a & ~127) + 128u * (uint32_t)(s.tile0 + k) + tr;
-          int64_t kp = pos;
+          int kp = (int)pos;
           if (p.kpos && pos >= (uint32_t)s.a && pos < (uint32_t)s.b) kp = p.kpos[s.req * p.kp_stride + pos];
-          dist = fabsf((float)(qp - kp));
+          dist = fabsf((float)((int64_t)qp - kp));
         }
         await(s_full(sb), (g / C::NSB) & 1);
         tc_fence_after();
@@ -1541,6 +1540,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       }
       // (the barrier at the next segment's start keeps it from rewriting sums still being read)
       tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(g_empty(slot));
     }
   }
   }
