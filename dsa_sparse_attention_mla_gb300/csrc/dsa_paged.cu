@@ -7,12 +7,13 @@
 //   mass_out[r, j] = mass[r, j] + sum_h exp(u_hj - lse_h)
 // The latent row k_j is key and value of every head: a position costs 264 (FP8) or 512 (bf16) bytes
 // and 4 * 256 operations per head, so with 64 heads a bf16 cache is bound by HBM and an FP8 one by
-// HBM and the tensor core about equally. What an FP8 tile meets first is shared memory: its operands,
-// copies, widened values and weights are some 2800 cycles at 128 bytes each, against 1470 of HBM, and of
-// what was tried only less work on shared memory made it faster (128 tokens x 32768 positions: widening
-// without bank conflicts 575 -> 549 us, 16-byte copies 549 -> 489; deeper rings, or weights handed over
-// by halves, did not). Measured: 128 x 32768 FP8 positions 484 us (2.3 TB/s; 167 at HBM's rate), 64
-// ragged bf16 requests, 144 MB of rows, 51 us (2.8 TB/s; 21).
+// HBM and the tensor core about equally. What a tile takes is set by its chains of hand-offs: 128 tokens x
+// 32768 FP8 positions take 453 us (2.5 TB/s; 167 at HBM's rate), some 4200 cycles a tile, and with parts of
+// the work left out 372 (no softmax arithmetic), 390 (next to no products), 343 (no copies and no widening),
+// 271 (none of the three: the hand-offs between the warps alone). No unit is full, shared memory is the
+// busiest: a product step of N = 64 reads 6 KB, all that its 48 cycles can carry, and with copies, widening
+// and weights a tile moves some 2800 cycles' worth. 64 ragged bf16 requests, 144 MB of rows, take 50 us
+// (2.9 TB/s; 21 at HBM's rate).
 //
 // Shape of the computation
 //  * Transposed products: S^T[key, head] = K Q^T with M = 128 keys, N = 64 heads, then
@@ -79,9 +80,9 @@ constexpr int kWarpRows = 256;     // rows whose costs one warp sums up, eight p
 constexpr int kSegs = 8;           // segment ring depth
 constexpr int kMaps = 8;           // tiles whose slots are known ahead
 // Smallest page whose rows the scheduler prefetches into L2 (an eighth of a tile per request), FP8
-// only. It shortens the start of short shares: 8 heads with a distance bias 45 us with it, 48 without;
-// 128 x 32768 positions take the same (488 and 487). bf16 tiles come by TMA in any case, and 64 ragged
-// requests took 72 us with it, 66 without, when it was tried.
+// only. It shortens the start of short shares: 8 heads with a distance bias 45 us with it and 48 without
+// when it was tried; 128 x 32768 positions took the same (488 and 487). bf16 tiles come by TMA in any
+// case, and 64 ragged requests took 72 us with it, 66 without.
 constexpr int kPrefetchPage = 16;
 constexpr int kRowOverhead = 1;    // a row's start and end, in tiles
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -176,7 +177,8 @@ template <int KIND, bool MASS>
 struct Cfg {
   static constexpr bool F8 = KIND == DSA_CACHE_FP8_SCALED;
   static constexpr int RB = F8 ? 264 : 512;
-  static constexpr int NSB = MASS ? 4 : 2;            // score buffers
+  static constexpr int NSB = MASS ? 4 : 2;            // score buffers (3: 128 x 32768 FP8 454 us for 458, but
+                                                      // one token over 131071 positions 44 for 42)
   static constexpr int S_COLS = F8 ? 128 : 64;        // columns of one (FP8: one 64 per scale tile)
   static constexpr int O_COL = NSB * S_COLS;          // O^T halves at O_COL and O_COL + 64
   static constexpr int TMEM_USED = O_COL + (MASS ? 0 : 128);
@@ -397,7 +399,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
   using C = Cfg<KIND, MASS>;
   constexpr bool F8 = C::F8;
   extern __shared__ uint8_t smem_raw[];
-  // an offset, not a rounded address: the compiler keeps knowing that this is shared memory
+  // an offset, not a rounded address: the compiler keeps knowing that this is shared memory (8 heads with
+  // a distance bias 39 us; 46 with the rounded address, whose accesses are generic)
   uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -972,7 +975,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     constexpr int PIECE = F8 ? 8 : 16, HALF_ROW = F8 ? 128 : 256;
     // FP8 rows that follow one another from an even slot (a slot is 264 bytes, the base is 16-byte aligned):
     // even rows start on 16 bytes and go in 16-byte pieces, four rows per instruction, odd ones in 8-byte
-    // pieces, two rows per instruction (128 tokens x 32768 keys: 489 us; 549 with 8-byte pieces alone)
+    // pieces, two rows per instruction (128 tokens x 32768 keys when it was tried: 489 us; 549 with 8-byte
+    // pieces alone)
     const int er = 2 * (lane >> 3);  // even row 8 i + er, granule lane % 8
     const uint32_t even = (uint32_t)((kLoadRows * lw + er) * 128 + (((lane & 7) ^ er) << 4));
     uint32_t odd[2];                 // odd row 4 i + 2 hi16 + 1, which is 4 (i % 2) + 2 hi16 + 1 of eight
