@@ -574,6 +574,13 @@ def _cache_rows(cache, kind: int, row: int):
     return index, cache.data_ptr(), shape[0]
 
 
+def _c_int(name: str, v) -> int:
+    """An argument of a C int: a wider one would wrap silently on its way (2**32 to 0)."""
+    if not -(1 << 31) <= v < 1 << 31:
+        raise ValueError(f"{name} must fit 32 bits, got {v}")
+    return v
+
+
 class _on_device:
     """Makes the device current, unless it is already."""
 
@@ -615,6 +622,7 @@ def _paged_args(q, cache, kind, block_table, lengths, sm_scale, page_size, start
     import torch
 
     i32 = torch.int32
+    _c_int("page_size", page_size)
     index, cache_ptr, slots = _cache_rows(cache, kind, 264 if kind == CACHE_FP8_SCALED else 256)
     q_ptr = _ptr_on(q, "q", torch.bfloat16, index)
     shape = q.shape
@@ -736,6 +744,8 @@ def dsa_cache_evict(cache, kind: int, block_table, lengths, mass, budget: int = 
     import torch
 
     i32, f32 = torch.int32, torch.float32
+    for name, v in (("budget", budget), ("page_size", page_size), ("sink", sink), ("recent", recent)):
+        _c_int(name, v)
     row = d_nope + d_rope if kind == CACHE_BF16 else dsa_packed_row_bytes(d_nope, d_rope)
     index, cache_ptr, slots = _cache_rows(cache, kind, row)
     m_ptr, m_stride, R, S = _rows(mass, "mass", f32, index)

@@ -154,3 +154,19 @@ def test_binding_refusals():
     with pytest.raises(ValueError, match="CUDA"):
         dsa.dsa_cache_evict(torch.zeros((64, 264), dtype=torch.uint8), dsa.CACHE_FP8_SCALED, None,
                             torch.zeros(1, dtype=torch.int32), torch.zeros((1, 64)), 8)
+
+
+@pytest.mark.parametrize("value", [1 << 31, 1 << 32, -(1 << 31) - 1])
+@pytest.mark.parametrize("name", ["budget", "sink", "recent", "page_size"])
+def test_binding_refuses_integers_that_would_wrap(name, value):
+    """2**32 as a budget would arrive as 0 and evict everything."""
+    import torch
+
+    args = (torch.zeros((64, 264), dtype=torch.uint8), dsa.CACHE_FP8_SCALED, None, torch.zeros(1, dtype=torch.int32),
+            torch.zeros((1, 64)))
+    with pytest.raises(ValueError, match=f"{name} must fit 32 bits"):
+        dsa.dsa_cache_evict(*args, **{name: value})
+    if name == "page_size":
+        q = torch.zeros((2, 4, 256), dtype=torch.bfloat16)
+        with pytest.raises(ValueError, match="page_size must fit 32 bits"):
+            dsa.dsa_paged_attn(q, q[0], dsa.CACHE_BF16, None, torch.zeros(2, dtype=torch.int32), 1.0, page_size=value)
