@@ -635,11 +635,12 @@ def _paged_args(q, cache, kind, block_table, lengths, sm_scale, page_size, start
     # without a table or key positions every request reads the same slots: no row to run out of
     bt_ptr, bt_stride, pages, requests = None, 0, 0, 1 << 31
     if block_table is not None:
-        bt_ptr, bt_stride, requests, pages = _rows(block_table, "block_table", i32, index)
+        # (an empty tensor has no address, and the library would read direct slots)
+        bt_ptr, bt_stride, requests, pages = _rows(block_table, "block_table", i32, index, cols=1 if T else 0)
     kp_ptr, kp_stride, kp_width = None, 0, 0
     if key_positions is not None:
         kp_ptr, kp_stride, requests, kp_width = _rows(key_positions, "key_positions", i32, index,
-                                                      None if block_table is None else requests)
+                                                      None if block_table is None else requests, 1 if T else 0)
     if lse is not None and (tuple(lse.shape) != (T, H) or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous [T, H] tensor")
     a = DsaPagedArgs(
@@ -769,7 +770,7 @@ def dsa_cache_evict(cache, kind: int, block_table, lengths, mass, budget: int = 
         m_stride = mo_stride = p_stride = po_stride = S
     bt_ptr, bt_stride, pages = None, 0, 0
     if block_table is not None:
-        bt_ptr, bt_stride, _, pages = _rows(block_table, "block_table", i32, index, R)
+        bt_ptr, bt_stride, _, pages = _rows(block_table, "block_table", i32, index, R, 1 if R else 0)
     a = DsaEvictArgs(cache_ptr, kind, slots, d_nope, d_rope, bt_ptr, bt_stride, page_size, pages, R, len_ptr,
                      _vector(budgets, "budgets", R, i32, index), budget, sink, recent, S, m_ptr, m_stride, p_ptr, p_stride,
                      mo_ptr, mo_stride, po_ptr, po_stride, len_out_ptr, None, 0,

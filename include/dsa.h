@@ -311,7 +311,7 @@ typedef struct dsa_paged_args {
   int64_t T;                     /* query tokens, at most 2^24 (0 = no-op); T * ceil(H / 64) *
                                     (addressable positions / 128 + 2) below 2^31 */
   int H;                         /* heads: 1 .. 128 */
-  const void* cache;
+  const void* cache;             /* contiguous rows, 16-byte aligned */
   dsa_cache_kind_t kind;
   int64_t num_slots;
   int d_nope, d_rope, d_v;       /* (256, 0, 256) */
@@ -389,7 +389,7 @@ DSA_API dsa_status_t dsa_paged_attn_mass(const dsa_paged_args_t* args, const flo
  * takes one request. Bit-identical across repeated calls.
  */
 typedef struct dsa_evict_args {
-  void* cache;
+  void* cache;                   /* contiguous rows, 8-byte aligned */
   dsa_cache_kind_t kind;
   int64_t num_slots;
   int d_nope, d_rope;

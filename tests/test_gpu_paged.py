@@ -544,3 +544,23 @@ def test_mass_of_bad_pages(gpu, kind, cap):
     tol = (c.H + 2) * 2.0 ** -24 * np.abs(ref)
     tol[pos] += (w * (d[:, None] + 2.0 ** -20)).sum(axis=0)
     assert (np.abs(got[0] - ref) <= tol)[:300].all()
+
+
+def test_tables_without_columns_are_refused(gpu):
+    """An empty tensor has no address: it must not pass for no table, which means direct slots."""
+    c = Case(gpu, BF16, [40, 50], 8, seed=73)
+    q, cache, kind, bt, lens, s = c.args()
+    none = torch.empty((2, 0), dtype=torch.int32, device=gpu)
+    lse = torch.zeros((2, 8), device=gpu)
+    mass = torch.zeros((2, 64), device=gpu)
+    with pytest.raises(ValueError, match="block_table"):
+        dsa.dsa_paged_attn(q, cache, kind, none, lens, s, page_size=64)
+    with pytest.raises(ValueError, match="block_table"):
+        dsa.dsa_paged_attn_mass(q, cache, kind, none, lens, s, lse, mass, page_size=64)
+    with pytest.raises(ValueError, match="key_positions"):
+        dsa.dsa_paged_attn(q, cache, kind, bt, lens, s, page_size=64, slopes=torch.ones(8, device=gpu),
+                           key_positions=none)
+    with pytest.raises(ValueError, match="block_table"):
+        dsa.dsa_cache_evict(cache, kind, none, lens, mass, 8, page_size=64)
+    # a batch without tokens may bring one
+    assert dsa.dsa_paged_attn(q[:0], cache, kind, none[:0], lens[:0], s, page_size=64).shape[0] == 0
