@@ -256,3 +256,46 @@ def test_decode_loop_with_eviction(gpu, kind):
             assert lengths.cpu().tolist() == host_len
             evictions += 1
     assert evictions >= 3
+
+
+def test_two_evictions_at_once(gpu):
+    """On two streams, then from two captured graphs on two streams: each keeps its own lists."""
+    rng = np.random.default_rng(12)
+    states = []
+    for lens, S, b in (([5000, 4100, 9], 5000, 1500), ([900] * 40, 1000, 333)):  # both select variants
+        raw, bt, mass, pos = build(rng, lens, S, 64, 264)
+        start = [torch.from_numpy(raw).to(gpu), torch.from_numpy(mass).to(gpu), torch.from_numpy(pos).to(gpu),
+                 torch.tensor(lens, dtype=torch.int32, device=gpu)]
+        states.append({"table": torch.from_numpy(bt).to(gpu), "start": start, "b": b, "now": [x.clone() for x in start]})
+
+    def call(s):
+        c, m, p, ln = s["now"]
+        dsa.dsa_cache_evict(c, FP8, s["table"], ln, m, s["b"], page_size=64, sink=2, recent=16, positions=p)
+
+    def reset():
+        for s in states:
+            for x, x0 in zip(s["now"], s["start"]):
+                x.copy_(x0)
+        torch.cuda.synchronize()
+
+    for s in states:
+        call(s)
+    torch.cuda.synchronize()
+    want = [[x.clone() for x in s["now"]] for s in states]
+    assert [w[3].max().item() for w in want] == [1500, 333]
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    for g, s in zip(graphs, states):
+        reset()
+        with torch.cuda.graph(g):
+            call(s)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for go in (lambda i: call(states[i]), lambda i: graphs[i].replay()):
+        for _ in range(4):
+            reset()
+            for i in range(2):
+                with torch.cuda.stream(streams[i]):
+                    go(i)
+            torch.cuda.synchronize()
+            for s, w in zip(states, want):
+                for x, y in zip(s["now"], w):
+                    assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
