@@ -275,12 +275,28 @@ __device__ __forceinline__ Row row_of(const Params& p, int row) {
   return r;
 }
 
+// 2 log2(e) / cap: the cap's exponential is exp2(-|u| times this). Held finite (a cap below 2^-127 gives
+// infinity, and a score of 0 would turn NaN).
+__device__ __forceinline__ float cap_factor(float cap) { return cap > 0.0f ? fminf(2.0f * kLog2e / cap, 3.402823466e38f) : 0.0f; }
+
 // One score in natural units -> exp2 domain, with cap and distance bias.
 __device__ __forceinline__ float modify(float u, float cap, float inv_cap2, float bias) {
   if (cap > 0.0f) {
-    // cap * tanh(u / cap) = cap * (1 - e) / (1 + e), e = exp(-2 |u| / cap), with u's sign
-    const float e = ex2_approx(-fabsf(u) * inv_cap2);
-    u = copysignf(__fdividef(cap * (1.0f - e), 1.0f + e), u);
+    // cap * tanh(z), z = u / cap. From |z| = 1/4 on cap * (1 - e) / (1 + e), e = exp(-2 |z|), with u's sign:
+    // e's relative error (2^-22, and |z| 2^-22 of its argument) comes to 2.4 * 2^-22 of the result there
+    // and falls from there on. Below, 1 - e would cancel (an error of cap * 2^-24, whatever u is), and
+    // tanh's Taylor series as u * (1 - z^2 / 3 + 2 z^4 / 15 - 17 z^6 / 315 + 62 z^8 / 2835) is off by the next
+    // term at most, 1382 / 155925 z^10 < 2^-26.
+    const float w = fabsf(u) * inv_cap2;  // 2 log2(e) |z|
+    constexpr float kZ = 0.5f * kLn2;     // z = kZ w
+    constexpr float c1 = -kZ * kZ / 3.0f, c2 = kZ * kZ * kZ * kZ * (2.0f / 15.0f),
+                    c3 = -kZ * kZ * kZ * kZ * kZ * kZ * (17.0f / 315.0f),
+                    c4 = kZ * kZ * kZ * kZ * kZ * kZ * kZ * kZ * (62.0f / 2835.0f);
+    const float w2 = w * w;
+    const float series = fmaf(u, w2 * fmaf(w2, fmaf(w2, fmaf(w2, c4, c3), c2), c1), u);
+    const float e = ex2_approx(-w);
+    const float far = copysignf(__fdividef(cap * (1.0f - e), 1.0f + e), u);
+    u = w < 0.25f / kZ ? series : far;
   }
   return (u - bias) * kLog2e;
 }
@@ -1143,7 +1159,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     // ================================================== weights of a key, 16 warps ===
     const int qd = warp & 3, gi = warp >> 2;
     const int tr = 32 * qd + lane;
-    const float inv_cap2 = MODS && p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
+    const float inv_cap2 = MODS ? cap_factor(p.cap) : 0.0f;
     const float c_log2 = p.sm_scale * kLog2e;
     uint32_t g = 0;
     bool ok = true;
@@ -1239,7 +1255,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     float* red_sc = red + 576 + 16 * hq;  // FP8: largest |scale| of the tile, [4 quarters][2]
     float* red_ref = red_sc + 8;          // FP8: [2 buffers][2] reference scales (powers of two)
     float* red_wf = red_sc + 12;          // FP8: [2 buffers][2] 2^kWeightShift / reference
-    const float inv_cap2 = MODS && p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
+    const float inv_cap2 = MODS ? cap_factor(p.cap) : 0.0f;
     const float f = MODS ? p.sm_scale : p.sm_scale * kLog2e;
     uint32_t g = 0, mb = 0;
     bool first_query = true;

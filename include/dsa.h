@@ -327,7 +327,8 @@ typedef struct dsa_paged_args {
   int64_t kp_stride;
   int64_t kp_width;              /* entries of a key_positions row */
   float sm_scale;                /* any finite value */
-  float logit_cap;               /* 0: none; else positive and finite */
+  float logit_cap;               /* 0: none; else positive and finite; the capped score errs by less than
+                                    2^-20 of itself, whatever the cap's size */
   const float* slopes;           /* fp32 [H] or NULL */
   void* out;                     /* bf16 [T, H, 256], 16-byte aligned, strides multiples of 8 */
   int64_t out_stride_t, out_stride_h;

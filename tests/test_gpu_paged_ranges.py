@@ -1,0 +1,84 @@
+"""Dense paged attention and its mass where a score, a scale or a component is far from the others,
+against the fp64 definitions (oracle/paged.py).
+
+Tolerances, per element (u = 2^-24 fp32, 2^-8 bf16 half steps):
+  score    d = 256 * 2^-23 * B + 2^-19 |u|, B = max_j |sm_scale| sum |q k| (an fp32 sum of 256 exact
+           products in any order, one step of slack for truncation; then cap, bias and the change to
+           base 2: below 2^-19 of the score's parts, the exponential of the cap's long branch
+           amplified by 1 / sinh(2 |u| / cap) < 2); with an FP8 cache
+           + 2^-17 |sm_scale| max |q| max_j sum |k| over the columns in which q is not zero (half of the
+           query's smallest second step)
+  lse, out, mass: as in test_gpu_paged.py, from this d
+"""
+import numpy as np
+import pytest
+import torch
+
+import dsa_sparse_attention_mla_gb300 as dsa
+from oracle import paged as R
+from oracle import projection as P
+
+from _helpers import f32_of
+from test_gpu_paged import Case, dev_t
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP8 = dsa.CACHE_BF16, dsa.CACHE_FP8_SCALED
+
+
+def score_error(c, t, u, k, bias):
+    """[H] bound of the scores' error."""
+    if u.shape[1] == 0:
+        return np.zeros(c.H)
+    q = P.bf16_to_f64(c.q[t])
+    d = 256 * 2.0 ** -23 * (np.abs(q) @ np.abs(k).T).max(axis=1) * abs(c.sm_scale)
+    d = d + 2.0 ** -19 * (np.abs(u).max(axis=1) + bias)
+    if c.kind == FP8:
+        d = d + 2.0 ** -17 * abs(c.sm_scale) * np.abs(q).max(axis=1) * ((q != 0) @ np.abs(k).T).max(axis=1)
+    return d
+
+
+def run_and_check(c, cap=0.0, slopes=None, qpos=None, mass=True):
+    dev, T = c.dev, len(c.lens)
+    opts = c.opts(logit_cap=cap, slopes=dev_t(slopes, dev), q_positions=dev_t(qpos, dev))
+    lse = torch.full((T, c.H), float("nan"), device=dev)
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+    out = dsa.dsa_paged_attn(*c.args(), lse=lse, error_word=err, **opts)
+    m0 = np.random.default_rng(5).random((T, int(c.lens.max()) + 3)).astype(np.float32)
+    weights = torch.from_numpy(m0).to(dev)
+    if mass:
+        dsa.dsa_paged_attn_mass(*c.args(), lse, weights, error_word=err, **opts)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    got, gl = f32_of(out).astype(np.float64), lse.cpu().numpy().astype(np.float64)
+    got_m = weights.cpu().numpy().astype(np.float64)
+    for t in range(T):
+        b = int(c.lens[t])
+        qp = b - 1 if qpos is None else int(qpos[t])
+        u, k, pos, _ = R.scores(P.bf16_to_f64(c.q[t]), c.cache, c.bt, c.page, t, 0, b, c.sm_scale,
+                                float(np.float32(cap)), slopes, qp)
+        n = len(pos)
+        bias = 0.0 if slopes is None else np.abs(slopes).max() * np.abs(qp - pos).max()
+        d = score_error(c, t, u, k, bias)
+        ref, rl, absum, l2 = R.softmax_output(u, k)
+        e = np.abs(gl[t] - rl)
+        assert (e <= d + n * 2.0 ** -23 + 2.0 ** -20 + 2.0 ** -22 * np.abs(rl)).all(), (t, e.max(), d.max())
+        tol = 2.0 ** -8 * np.abs(ref) + 5 * 2.0 ** -8 * l2 + (2 * d[:, None] + n * 2.0 ** -22 + 2.0 ** -20) * absum
+        e = np.abs(got[t] - ref)
+        assert (e <= tol).all(), (t, np.unravel_index(np.argmax(e - tol), e.shape), (e / np.maximum(tol, 1e-300)).max())
+        if mass:
+            w = np.exp(u - gl[t][:, None])
+            tol = (w * (d[:, None] + 2.0 ** -20)).sum(axis=0) + (c.H + 2) * 2.0 ** -24 * np.abs(m0[t, pos] + w.sum(axis=0))
+            e = np.abs(got_m[t, pos] - (m0[t, pos] + w.sum(axis=0)))
+            assert (e <= tol).all(), (t, (e / tol).max())
+    return out, lse
+
+
+@pytest.mark.parametrize("kind", [BF16, FP8])
+@pytest.mark.parametrize("cap", [1e-40, 1e-3, 2.0, 1e3, 1e6, 1e9, 1e30, 3e38])
+def test_caps_of_every_size(gpu, kind, cap):
+    """A cap far above the scores leaves them as they are, whatever its size; one far below them
+    makes them all equal in magnitude. Scores of exactly zero among them."""
+    c = Case(gpu, kind, [1, 700], 16, seed=83)
+    c.q[:, 3] = 0
+    run_and_check(c, cap=cap)
