@@ -25,14 +25,20 @@
 //    within 2^9 of the head's largest. S keeps one accumulator per scale tile and the fp32 scales
 //    multiply there. The value product takes the codes widened to f16, which is exact and one
 //    conversion per two codes (to bf16 it is four instructions), and one f16 weight matrix per scale
-//    tile: p * scale relative to the largest scale so far, 2^22 of normal range below the strongest
-//    position. e4m3 weights (as two terms) would need no widening but lose what many far positions add
-//    up to beside one strong one. So the keys are the exact products code * scale.
+//    tile: p * scale relative to a reference, the head's largest p * scale so far, 2^22 of normal range
+//    below it. (The largest scale would not do: a row of large scale that a head ignores would take the
+//    range from those it reads.) The first tile's reference is taken off the scores with the running
+//    maximum, and the second's differs from it by about the same factor in all heads of a group, so a
+//    weight is one product, p times a factor of the key. Where the heads differ by more, theirs come in
+//    between the two tiles (128 x 32768 positions: 430 us; 530 with a factor per head for every weight).
+//    The references cost a row's first tile some 2 us: 8 x 2112 positions take 27.8 us for 25.7 with
+//    the largest scale as the reference. e4m3 weights (as two terms) would need no widening but lose what
+//    many far positions add up to beside one strong one. So the keys are the exact products code * scale.
 //  * Softmax with one thread per key and 16 heads: four groups of four warps, a warp per lane quarter of
 //    tensor memory in each. The warps of a group share running maxima and synchronise among themselves. The
 //    running maximum of a head is raised, and O and the sums rescaled, only when some score exceeds it by
-//    2^20 (FP8: 2^6): p and its sums are floating point, so a stale maximum costs no precision, and the
-//    exact path runs for a segment's first tile and almost never again.
+//    2^20 (FP8: when some weight may leave the range of f16): p and its sums are floating point, so a stale
+//    maximum costs no precision, and the exact path runs for a segment's first tile and almost never again.
 //  * Persistent CTAs, one per SM. Each computes the same split from the lengths (they live on the
 //    device): rows (token, group of 64 heads) cost their 128-position tiles plus a constant, and
 //    CTA c takes the c-th of G equal parts of the total. A row cut by a border leaves unnormalised
@@ -89,10 +95,21 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -1e30f;   // running maximum before the first valid score
-// A score may exceed the running maximum by 2^20; FP8: by 2^6, so that an f16 weight is at most
-// 2^(6 + kWeightShift) < 65504.
-constexpr float kStale = 20.0f, kStaleF8 = 6.0f;
-constexpr int kWeightShift = 8;
+// bf16: a score may exceed the running maximum by 2^20. FP8: by what the sums hold (2^55 and 2^64 of kOwn
+// are finite together), and a weight p * scale the head's reference by what f16 holds, kMostWeight =
+// 2^kWeightShift * 2^6 or so.
+constexpr float kStale = 20.0f, kStaleF8 = 55.0f, kMostWeight = 65000.0f;
+constexpr int kWeightShift = 10;
+// FP8: the heads of a group share the second tile's factor while theirs lie within 2^kSpread of one another:
+// the smallest of them leaves 2^(14 + kWeightShift - kSpread) = 2^22 of normal range below each reference.
+// Else a head's own is at most 2^kOwn of the smallest.
+constexpr int kSpread = 2, kOwn = 64;
+// References are powers of two between these. What of the first tile's is taken off the scores goes kFoldLow
+// down from the group's largest, and no factor falls below 2^-126.
+constexpr int kRefLow = -80, kRefHigh = 127, kFoldLow = -40;
+__device__ __forceinline__ float fold_of(float ref0, float ref1, float base) {
+  return fmaxf(ref0 - base, fmaxf((float)kFoldLow, ref1 - (float)(126 + kWeightShift)));
+}
 
 // Bounded wait for the phase of the given parity. The hint lets the hardware park the warp for up to
 // a millisecond: some twenty warps wait at any time, and polling took a third of the issue slots.
@@ -205,10 +222,12 @@ struct Cfg {
   static constexpr int SQ_OFF = SC_OFF + (F8 ? NV * 1024 : 0); // FP8: [kSegs][64] query scales
   static constexpr int NL_OFF = SQ_OFF + (F8 ? kSegs * 256 : 0);  // mass: [kSegs][64] -lse, exp2 domain
   static constexpr int SL_OFF = NL_OFF + (MASS ? kSegs * 256 : 0);  // slopes [128]
-  // -m [2][64], alpha [64], part [4][64], inverse sums [64], raise of m [64]; FP8, per head group:
-  // largest scales of the tile [4][2], reference scales [2][2] and their inverses [2][2]
+  // -m [2][64], alpha [64], part [4][64], inverse sums [64], raise of m [64]; FP8: largest weights of the
+  // tile [4][2][64], then the accumulators' factors [2][64]; the weights' factors [2][64]; references
+  // [2][64], log2; the heads' own factors [64]; per group both tiles' factors [2], the largest first
+  // reference, and the second tile's largest factor
   static constexpr int RED_OFF = SL_OFF + 512;
-  static constexpr int PLAN_OFF = RED_OFF + 9 * 256 + 64 * kGroups;  // block scans: 2 x kWarps int64; start row, its cost
+  static constexpr int PLAN_OFF = RED_OFF + 9 * 256 + (WIDEN ? 13 * 256 + 64 : 0);  // block scans: 2 x kWarps int64; start row, its cost
   static constexpr int BAR_OFF = PLAN_OFF + 2 * 8 * kWarps + 64;
   static constexpr int NBARS = 2 + 2 * NST + 3 * kSegs + 2 * kMaps + 2 * NSB + 2 * 2 + 2 + 2 * NW;
   static constexpr int MISC_OFF = BAR_OFF + 8 * NBARS;
@@ -1252,9 +1271,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     float* red_part = red + 192;  // [4 quarters][64 heads]
     float* red_inv = red + 448;
     float* red_raise = red + 512;
-    float* red_sc = red + 576 + 16 * hq;  // FP8: largest |scale| of the tile, [4 quarters][2]
-    float* red_ref = red_sc + 8;          // FP8: [2 buffers][2] reference scales (powers of two)
-    float* red_wf = red_sc + 12;          // FP8: [2 buffers][2] 2^kWeightShift / reference
+    float* red_top = red + 576;    // FP8: log2 of the tile's largest p * |scale|, [4 quarters][2 tiles][64], then
+                                   // [2][64] what the accumulators take when m and the factors change
+    float* red_wf = red + 1088;    // FP8: [2][64] weight = p * scale * this, a power of two
+    float* red_ref = red + 1216;   // FP8: [2][64] log2 of the reference, relative to m
+    float* red_own = red + 1344;   // FP8: [64] red_wf of the second tile over the group's factor
+    float* red_grp = red + 1408 + 4 * hq;  // FP8: the group's factors of both tiles [2], its largest reference
+                                           // of the first tile, its largest red_wf of the second
     const float inv_cap2 = MODS ? cap_factor(p.cap) : 0.0f;
     const float f = MODS ? p.sm_scale : p.sm_scale * kLog2e;
     uint32_t g = 0, mb = 0;
@@ -1369,11 +1392,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         bool exact = fresh;
         if (!exact) {
           bool stale = top > (F8 ? kStaleF8 : kStale);
-          if (F8) stale = stale || fabsf(scl.x) > red_ref[2 * mb] || fabsf(scl.y) > red_ref[2 * mb + 1];
+          // (the most that any of the group's heads can make of this key: one that none of them reads passes,
+          // whatever its scales; heads with factors far apart may take the exact path more often than they must)
+          if (F8) stale = stale || ex2_approx(top) * fmaxf(fabsf(scl.x) * red_grp[0], fabsf(scl.y) * red_grp[3]) > kMostWeight;
           exact = group_any(hq, stale);
         }
         if (exact) {
-          // exact maximum of the tile per head; the running maxima are raised to it
+          // exact maximum of the tile per head; the running maxima are raised to it. FP8: the largest weights
+          // as well (unrolled: in a loop over the three the compiler spills, 128 x 32768 positions 488 us, not 430)
           float mine = -INFINITY;  // lane i ends with head i's
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
@@ -1382,34 +1408,61 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
           }
           if (lane < kHW) red_part[64 * qd + hb + lane] = mine;
           if (F8) {
-            // magnitudes order like their bits
-            const uint32_t a0 = __reduce_max_sync(0xffffffffu, f2u(fabsf(scl.x)));
-            const uint32_t a1 = __reduce_max_sync(0xffffffffu, f2u(fabsf(scl.y)));
-            if (lane == 0) {
-              red_sc[2 * qd] = u2f(a0);
-              red_sc[2 * qd + 1] = u2f(a1);
+#pragma unroll 2
+            for (int t = 0; t < 2; ++t) {
+              const float ls = __log2f(fabsf(t == 0 ? scl.x : scl.y));
+#pragma unroll
+              for (int i = 0; i < NP; ++i) {
+                const float m0 = redux_max_f32(y[i].x + ls), m1 = redux_max_f32(y[i].y + ls);
+                mine = lane == 2 * i ? m0 : (lane == 2 * i + 1 ? m1 : mine);
+              }
+              if (lane < kHW) red_top[64 * (2 * qd + t) + hb + lane] = mine;
             }
           }
           const bool some = group_any(hq, valid);
-          if (gid < kHW) {
-            // relative to the m that y was taken from; a first maximum may be below it
-            const float* pt = red_part + hb + gid;
+          static_assert(2 * kHW == 32, "a lane of one warp per tile and head");
+          if (gid < (F8 ? 2 * kHW : kHW)) {
+            const int h = hb + (gid & (kHW - 1)), t = gid / kHW;
+            // relative to what y was taken from; a first maximum may be below it. FP8: that is m plus the fold,
+            // what of the first tile's reference is taken off as well
+            const float* pt = red_part + h;
             const float up = fmaxf(fmaxf(pt[0], pt[64]), fmaxf(pt[128], pt[192]));
-            const float mo = fresh ? 0.0f : -red[64 * mb + hb + gid];
-            const float raise = fresh ? (up > kNoMax ? up : 0.0f) : fmaxf(up, 0.0f);
-            red[64 * (mb ^ 1) + hb + gid] = -(mo + raise);
-            red_raise[hb + gid] = raise;
-            red_alpha[hb + gid] = ex2_approx(-raise);
-          } else if (F8 && gid >= 32 && gid < 34) {
-            const int t = gid - 32;
-            const float top_sc = fmaxf(fmaxf(red_sc[t], red_sc[2 + t]), fmaxf(red_sc[4 + t], red_sc[6 + t]));
-            // the power of two at or above it, 2^-100 at least: its inverse is finite
-            uint32_t e = (f2u(top_sc) + 0x7FFFFFu) >> 23;
-            e = e < 27u ? 27u : (e > 254u ? 254u : e);
-            const float old = fresh ? 0.0f : red_ref[2 * mb + t];
-            const float ref = fmaxf(old, u2f(e << 23));
-            red_ref[2 * (mb ^ 1) + t] = ref;
-            red_wf[2 * (mb ^ 1) + t] = (float)(1 << kWeightShift) / ref;
+            const float mo = fresh ? 0.0f : -red[64 * mb + h];
+            float fold = F8 && !fresh ? fold_of(red_ref[h], red_ref[64 + h], red_grp[2]) : 0.0f;
+            float raise = fresh ? (up > kNoMax ? up : 0.0f) : fmaxf(up, -fold);
+            if (F8) {
+              // the power of two at or above the largest p * |scale| so far, p relative to the new m
+              const int at = 64 * t + h;
+              const float* tt = red_top + at;
+              const float old = fresh ? -INFINITY : red_ref[at] - fold;
+              const float seen = fmaxf(fmaxf(fmaxf(tt[0], tt[128]), fmaxf(tt[256], tt[384])), old) - raise;
+              const float ref = fminf(fmaxf(ceilf(seen), (float)kRefLow), (float)kRefHigh);
+              const float other = __shfl_xor_sync(0xffffffffu, ref, kHW);
+              const float ref0 = t == 0 ? ref : other, ref1 = t == 0 ? other : ref;
+              const int base = __reduce_max_sync(0xffffffffu, (int)ref0);
+              fold = fold_of(ref0, ref1, (float)base);
+              raise += fold;
+              // the factors' exponents, biased; the first tile's are one another's but for folds at their limit
+              const int w1 = 127 + kWeightShift - (int)ref1 + (int)fold;
+              const int lo = __reduce_min_sync(0xffffffffu, w1), spread = __reduce_max_sync(0xffffffffu, w1) - lo;
+              const int own = spread > kSpread ? min(w1 - lo, kOwn) : 0;
+              const int e = t == 0 ? 127 + kWeightShift - base : lo + own;
+              red_top[at] = ex2_approx((float)(e - (int)(f2u(red_wf[at]) >> 23)) - raise);
+              red_wf[at] = u2f((uint32_t)e << 23);
+              red_ref[at] = ref;
+              if (t == 0) red_own[h] = u2f((uint32_t)(127 + own) << 23);
+              if (gid == 0) {
+                red_grp[0] = u2f((uint32_t)e << 23);
+                red_grp[1] = u2f((uint32_t)lo << 23);
+                red_grp[2] = (float)base;
+                red_grp[3] = u2f((uint32_t)(lo + (spread > kSpread ? min(spread, kOwn) : 0)) << 23);
+              }
+            }
+            if (t == 0) {
+              red[64 * (mb ^ 1) + h] = -(mo + raise);
+              red_raise[h] = raise;
+              red_alpha[h] = ex2_approx(-raise);
+            }
           }
           group_sync(hq);
           mb ^= 1;
@@ -1427,21 +1480,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
             for (int c = 0; c < 2 * CH; ++c) {  // half c / CH, 16 heads
               const int half = c / CH, h16 = 16 * (c % CH);
               const uint32_t addr = o_addr + 64 * half + h16;
-              const float* al = red_alpha + hb + h16;
-              const float r = F8 ? red_ref[2 * (mb ^ 1) + half] / red_ref[2 * mb + half] : 1.0f;
+              const float* al = (F8 ? red_top + 64 * half : red_alpha) + hb + h16;
               uint32_t o[16];
               tmem_ld32_x16(addr, o);
               tc_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = f2u(u2f(o[i]) * (al[i] * r));
+              for (int i = 0; i < 16; ++i) o[i] = f2u(u2f(o[i]) * al[i]);
               tmem_st32_x16(addr, o);
             }
             tc_wait_st();
           }
           fresh = fresh && !some;
         }
-        float2 wf = make_float2(1.0f, 1.0f);  // FP8: the key's scales relative to the references
-        if (F8) wf = __fmul2_rn(scl, *reinterpret_cast<const float2*>(red_wf + 2 * mb));
 #pragma unroll
         for (int ch = 0; ch < CH; ++ch) {
           if (ch < nch) {
@@ -1457,16 +1507,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         uint8_t* prow = smem + C::P_OFF + (g % C::PBUF) * C::P_BYTES + tr * 128;
         const int sw = tr & 7;
 #pragma unroll
-        for (int ch = 0; ch < CH; ++ch) {
-          if (ch < nch) {
+        for (int h = 0; h < C::PN; ++h) {
+          float wf = 1.0f;
+          if (F8) {
+            // the key's factor, held finite (a weight of 0 stays 0)
+            wf = fminf(fmaxf((h == 0 ? scl.x : scl.y) * red_grp[h], -3.402823466e38f), 3.402823466e38f);
+            if (h == 1 && red_grp[1] != red_grp[3]) {  // the heads' own factors
 #pragma unroll
-            for (int h = 0; h < C::PN; ++h) {
+              for (int i = 0; i < NP; ++i) y[i] = __fmul2_rn(y[i], *reinterpret_cast<const float2*>(red_own + hb + 2 * i));
+            }
+          }
+#pragma unroll
+          for (int ch = 0; ch < CH; ++ch) {
+            if (ch < nch) {
               uint32_t w[8];
-              const float wh = h == 0 ? wf.x : wf.y;
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 if (F8) {
-                  const float2 v = __fmul2_rn(y[8 * ch + i], make_float2(wh, wh));
+                  const float2 v = __fmul2_rn(y[8 * ch + i], make_float2(wf, wf));
                   w[i] = f32x2_to_f16x2(v.x, v.y);
                 } else {
                   w[i] = f32x2_to_bf16x2(y[8 * ch + i].x, y[8 * ch + i].y);
@@ -1535,21 +1593,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[i] = 0u;
         }
-        // FP8: weights were relative to the half's reference scale
-        const float back = F8 && !fresh ? red_ref[2 * mb + half] * (1.0f / (1 << kWeightShift)) : 1.0f;
+        // FP8: the inverse of the weights' factor, a power of two, by its bits
+        auto back = [&](int h) -> float { return F8 && !fresh ? u2f(0x7F000000u - f2u(red_wf[64 * half + h])) : 1.0f; };
         const int dv = 128 * half + tr;
         if (s.kind != 0) {
           float* prt = p.ws_o + ((int64_t)part * kHG + h0) * kD + dv;
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (h0 + i < heads) prt[i * kD] = u2f(o[i]) * back;
+            if (h0 + i < heads) prt[i * kD] = u2f(o[i]) * back(h0 + i);
         } else {
           // lanes 2i and 2i + 1 hold neighbouring columns: they swap heads, so that each writes
           // two columns of one head
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float e = u2f(o[2 * i]) * back * red_inv[h0 + 2 * i];
-            const float d = u2f(o[2 * i + 1]) * back * red_inv[h0 + 2 * i + 1];
+            const float e = u2f(o[2 * i]) * back(h0 + 2 * i) * red_inv[h0 + 2 * i];
+            const float d = u2f(o[2 * i + 1]) * back(h0 + 2 * i + 1) * red_inv[h0 + 2 * i + 1];
             const bool odd = lane & 1;
             const float other = __shfl_xor_sync(0xffffffffu, odd ? e : d, 1);
             const uint32_t w = odd ? f32x2_to_bf16x2(other, d) : f32x2_to_bf16x2(e, other);

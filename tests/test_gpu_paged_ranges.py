@@ -82,3 +82,65 @@ def test_caps_of_every_size(gpu, kind, cap):
     c = Case(gpu, kind, [1, 700], 16, seed=83)
     c.q[:, 3] = 0
     run_and_check(c, cap=cap)
+
+
+def _far_scales(dev, n, at, exponent, both, H=16):
+    """n FP8 keys whose first tile has scale 2^-exponent, except the key at position `at`: scale 1 and a
+    score near -60 (odd heads, if `both`: 60). Scores come from the second tile alone."""
+    c = Case(dev, FP8, [n], H, seed=exponent + at)
+    rng = np.random.default_rng(at)
+    c.cache[:, :256] &= 0x7F
+    c.cache[:, :256] = np.minimum(c.cache[:, :256], 0x7E) | (rng.integers(0, 2, (len(c.cache), 256)) << 7).astype(np.uint8)
+    scale = np.tile(np.array([2.0 ** -exponent, 1.0 / 448], dtype=np.float32), (len(c.cache), 1))
+    q = np.zeros((1, H, 256))
+    q[:, :, 128:] = rng.choice([-1.0, 1.0], 128) + 0.1 * rng.standard_normal((1, H, 128))
+    if both:
+        q[:, 1::2] *= -1
+    c.q = P.f64_to_bf16(q)
+    c.sm_scale = 0.5
+    slot = R.slots_of(c.bt, c.page, len(c.cache), 0, np.arange(n))
+    scale[slot[at], 0] = 1.0
+    # all of the key's second tile against the query's signs: 0.5 * 128 * 0.9375 = 60
+    scale[slot[at], 1] = 1.0
+    one = np.where(q[0, 0, 128:] > 0, 0xB7, 0x37).astype(np.uint8)  # -+0.9375
+    c.cache[slot[at], 128:256] = one
+    c.cache[:, 256:] = scale.view(np.uint8).reshape(-1, 8)
+    return c
+
+
+@pytest.mark.parametrize("both", [False, True])
+@pytest.mark.parametrize("exponent", [8, 20, 24, 28, 33, 40])
+@pytest.mark.parametrize("n,at", [(400, 5), (400, 399), (3000, 1500)])
+def test_a_large_scale_of_no_weight(gpu, n, at, exponent, both):
+    """The output keeps its precision beside a key of large scale that the softmax ignores, before and
+    behind the others, and whether or not other heads attend to that key."""
+    run_and_check(_far_scales(gpu, n, at, exponent, both))
+
+
+def test_scales_that_grow_along_the_range(gpu):
+    """Scales rise and fall by 2^60 over the range, in both tiles, under a flat and a sharp softmax."""
+    for sm in (1e-4, 1.0):
+        c = Case(gpu, FP8, [50, 3000], 16, seed=89)
+        for r in range(2):
+            slot = R.slots_of(c.bt, c.page, len(c.cache), r, np.arange(c.lens[r]))
+            x = np.abs(np.linspace(-1, 1, len(slot)))
+            c.cache[slot, 256:] = np.exp2(-60 * np.stack([x, 1 - x], axis=1)).astype(np.float32).view(np.uint8).reshape(-1, 8)
+        c.sm_scale = sm
+        run_and_check(c)
+
+
+@pytest.mark.parametrize("exponent", [-100, -60, 100])
+def test_scales_of_every_size(gpu, exponent):
+    """All scales far from 1, where references meet their limits, and a first tile without any."""
+    c = Case(gpu, FP8, [50, 1500], 16, seed=103)
+    scale = np.exp2(exponent + np.random.default_rng(3).uniform(-1, 1, (len(c.cache), 2))).astype(np.float32)
+    slot = R.slots_of(c.bt, c.page, len(c.cache), 1, np.arange(256))
+    scale[slot] = 0.0
+    if exponent == -100:  # (below 2^-80 precision may fall: what is left has to be finite and small)
+        c.cache[:, 256:] = scale.view(np.uint8).reshape(-1, 8)
+        out = dsa.dsa_paged_attn(*c.args(), **c.opts())
+        assert (f32_of(out)[1] == 0).sum() < out[1].numel() and np.abs(f32_of(out)).max() < 2.0 ** -90
+        return
+    c.cache[:, 256:] = scale.view(np.uint8).reshape(-1, 8)
+    c.sm_scale = 2.0 ** -exponent / 4000
+    run_and_check(c)
