@@ -22,7 +22,8 @@
 //    token has at most 64 heads per pass: heads as M would leave half of the tensor core idle.
 //  * FP8 rows: scores run on the e4m3 codes as they are (kind::f8f6f4), the bf16 query split into two
 //    e4m3 terms per head, scaled by a power of two: hi + lo is the bf16 component for every component
-//    within 2^9 of the head's largest. S keeps one accumulator per scale tile and the fp32 scales
+//    within 2^9 of the head's largest, and off by at most 2^-17 of the largest otherwise. S keeps one
+//    accumulator per scale tile and the fp32 scales
 //    multiply there. The value product takes the codes widened to f16, which is exact and one
 //    conversion per two codes (to bf16 it is four instructions), and one f16 weight matrix per scale
 //    tile: p * scale relative to a reference, the head's largest p * scale so far, 2^22 of normal range
@@ -415,7 +416,11 @@ __device__ __forceinline__ void split_query(const uint16_t* q, int64_t q_sh, int
       x[2] = __uint_as_float(w[2 * j + 1] << 16) * inv;
       x[3] = __uint_as_float(w[2 * j + 1] & 0xFFFF0000u) * inv;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) r[c] = __uint_as_float(__float_as_uint(x[c]) & 0xFFF00000u);  // four significant bits
+      for (int c = 0; c < 4; ++c) {
+        // four significant bits; none below e4m3's normal range (2^-6), where hi would round as well as lo
+        const uint32_t bits = __float_as_uint(x[c]);
+        r[c] = __uint_as_float(bits & ((bits & 0x7F800000u) < 0x3C800000u ? 0u : 0xFFF00000u));
+      }
       hi[j] = (uint32_t)f32x2_to_e4m3x2(r[0], r[1]) | ((uint32_t)f32x2_to_e4m3x2(r[2], r[3]) << 16);
       lo[j] = (uint32_t)f32x2_to_e4m3x2(x[0] - r[0], x[1] - r[1]) |
               ((uint32_t)f32x2_to_e4m3x2(x[2] - r[2], x[3] - r[3]) << 16);

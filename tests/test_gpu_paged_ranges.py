@@ -144,3 +144,20 @@ def test_scales_of_every_size(gpu, exponent):
     c.cache[:, 256:] = scale.view(np.uint8).reshape(-1, 8)
     c.sm_scale = 2.0 ** -exponent / 4000
     run_and_check(c)
+
+
+@pytest.mark.parametrize("H", [1, 64])
+def test_query_components_far_below_the_largest(gpu, H):
+    """Components below 2^-9 of the head's largest err by at most 2^-17 of it: keys that read these
+    components alone add up their errors. Half the heads hold the component that a split of both terms
+    at the same step errs by 1.94 times as much on."""
+    c = Case(gpu, FP8, [1, 1, 130], H, seed=97)
+    c.cache[:, :256] = 0x38
+    c.cache[:, 0] = 0
+    c.cache[:, 256:] = np.ones((len(c.cache), 2), dtype=np.float32).view(np.uint8)
+    q = np.full((3, H, 256), 0.00970458984375 / 128)
+    q[:, 1::2] = np.exp(np.random.default_rng(1).uniform(-14, -5, q[:, 1::2].shape))
+    q[:, :, 0] = 1.0
+    c.q = P.f64_to_bf16(q)
+    c.sm_scale = 1.0
+    run_and_check(c)
