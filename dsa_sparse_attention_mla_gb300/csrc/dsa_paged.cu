@@ -95,7 +95,7 @@ constexpr int kRowOverhead = 1;    // a row's start and end, in tiles
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNoMax = -1e30f;   // running maximum before the first valid score
+constexpr float kNoMax = -3.402823466e38f;  // maximum of no score: below every finite one
 // bf16: a score may exceed the running maximum by 2^20. FP8: by what the sums hold (2^55 and 2^64 of kOwn
 // are finite together), and a weight p * scale the head's reference by what f16 holds, kMostWeight =
 // 2^kWeightShift * 2^6 or so.

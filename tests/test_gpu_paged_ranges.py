@@ -161,3 +161,16 @@ def test_query_components_far_below_the_largest(gpu, H):
     c.q = P.f64_to_bf16(q)
     c.sm_scale = 1.0
     run_and_check(c)
+
+
+@pytest.mark.parametrize("kind", [BF16, FP8])
+@pytest.mark.parametrize("lens", [[1, 7], [130, 5000]])
+def test_scores_far_below_zero(gpu, kind, lens):
+    """All scores of a head below -1e30: the largest still takes all of the weight, in one part or
+    joined from many."""
+    c = Case(gpu, kind, lens, 3, seed=101)
+    slopes = np.array([2e31, 0.0, 3e33], dtype=np.float32)
+    out, lse = run_and_check(c, slopes=slopes, qpos=np.array([9000, 9001], dtype=np.int32), mass=False)
+    for t, n in enumerate(lens):
+        k = R.latent_rows(c.cache, R.slots_of(c.bt, c.page, len(c.cache), t, [n - 1]))[0]
+        assert (np.abs(f32_of(out)[t, [0, 2]] - k) <= 2.0 ** -8 * np.abs(k)).all()
