@@ -733,11 +733,11 @@ def dsa_cache_evict_workspace_size(num_requests: int, width: int) -> int:
     return int(n.value)
 
 
-def dsa_cache_evict(cache, kind: int, block_table, lengths, mass, budget: int = 0, *, page_size: int = 0, sink: int = 0,
+def dsa_cache_evict(cache, kind: int, block_table, lengths, mass, budget=None, *, page_size: int = 0, sink: int = 0,
                     recent: int = 0, budgets=None, positions=None, mass_out=None, positions_out=None, lengths_out=None,
                     d_nope: int = 256, d_rope: int = 0, workspace=None, error_word=None):
-    """Shrinks request r from lengths[r] to at most budgets[r] (``budget`` without them) positions,
-    in place in the paged cache: the positions of largest ``mass`` fp32 [R, S] stay, the first
+    """Shrinks request r from lengths[r] to at most ``budget`` positions, or budgets[r] (one of the two is
+    given), in place in the paged cache: the positions of largest ``mass`` fp32 [R, S] stay, the first
     ``sink`` and ``recent`` newest token positions always. Kept rows past the budget move into the
     evicted places below it; ``mass``, ``positions`` int32 [R, S] (each entry's token position; its
     index without them) and ``lengths`` follow, in place or into the ``_out`` tensors. Returns
@@ -745,8 +745,14 @@ def dsa_cache_evict(cache, kind: int, block_table, lengths, mass, budget: int = 
     import torch
 
     i32, f32 = torch.int32, torch.float32
-    for name, v in (("budget", budget), ("page_size", page_size), ("sink", sink), ("recent", recent)):
+    for name, v in (("budget", 0 if budget is None else budget), ("page_size", page_size), ("sink", sink),
+                    ("recent", recent)):
         _c_int(name, v)
+    # left out, a budget of 0 would evict everything; beside budgets it would go unused
+    if (budget is None) == (budgets is None):
+        raise ValueError("one of budget and budgets is required")
+    if budget is None:
+        budget = 0
     row = d_nope + d_rope if kind == CACHE_BF16 else dsa_packed_row_bytes(d_nope, d_rope)
     index, cache_ptr, slots = _cache_rows(cache, kind, row)
     m_ptr, m_stride, R, S = _rows(mass, "mass", f32, index)

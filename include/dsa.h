@@ -401,7 +401,7 @@ typedef struct dsa_evict_args {
   int64_t num_requests;          /* at most 65535 (0 = no-op) */
   const int32_t* lengths;        /* int32 [num_requests] */
   const int32_t* budgets;        /* int32 [num_requests] or NULL */
-  int budget;                    /* used when budgets is NULL: >= 0 */
+  int budget;                    /* used when budgets is NULL: >= 0 (0 evicts every position) */
   int sink, recent;              /* >= 0 */
   int64_t width;                 /* entries of a row of mass and positions: 1 .. 2^30 */
   const float* mass;             /* fp32 [num_requests, width] */

@@ -170,3 +170,19 @@ def test_binding_refuses_integers_that_would_wrap(name, value):
         q = torch.zeros((2, 4, 256), dtype=torch.bfloat16)
         with pytest.raises(ValueError, match="page_size must fit 32 bits"):
             dsa.dsa_paged_attn(q, q[0], dsa.CACHE_BF16, None, torch.zeros(2, dtype=torch.int32), 1.0, page_size=value)
+
+
+def test_evict_needs_one_budget():
+    """Without a budget nothing says what may go (0 would evict every position); with both, which holds?"""
+    import torch
+
+    args = (torch.zeros((64, 264), dtype=torch.uint8), dsa.CACHE_FP8_SCALED, None, torch.zeros(1, dtype=torch.int32),
+            torch.zeros((1, 64)))
+    budgets = torch.zeros(1, dtype=torch.int32)
+    for kw in ({}, {"budget": None}, {"budget": 8, "budgets": budgets}, {"budget": 0, "budgets": budgets}):
+        with pytest.raises(ValueError, match="one of budget and budgets"):
+            dsa.dsa_cache_evict(*args, **kw)
+    # either alone gets as far as the device check
+    for kw in ({"budget": 0}, {"budgets": budgets}):
+        with pytest.raises(ValueError, match="CUDA"):
+            dsa.dsa_cache_evict(*args, **kw)
