@@ -65,6 +65,7 @@
 #include <mutex>
 
 #include "dsa_host.h"
+#include "dsa_paged_split.h"
 #include "dsa_ptx.cuh"
 
 namespace dsa {
@@ -82,7 +83,6 @@ constexpr int kLoadWarps = 4, kWidenWarps = 4;
 constexpr int kLoadRows = kBN / kLoadWarps;
 constexpr int kWarps = kWarpWiden0 + kWidenWarps;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxCtas = 192;      // the join's lists (its threads look at 256 CTAs)
 constexpr int kWarpRows = 256;     // rows whose costs one warp sums up, eight per lane
 constexpr int kSegs = 8;           // segment ring depth
 constexpr int kMaps = 8;           // tiles whose slots are known ahead
@@ -174,12 +174,6 @@ struct Params {
                     // row that CTA c starts: the row (-1: not split, none), the CTAs that start and
                     // finish it, and the split's total cost
 };
-
-// First cost of CTA c's share, floor(c * total / G): G is at most kMaxCtas < 2^8.
-__device__ __forceinline__ int share(int c, int total, int G) {
-  const uint32_t q = (uint32_t)total / (uint32_t)G, r = (uint32_t)total - q * (uint32_t)G;
-  return (int)((uint32_t)c * q + (uint32_t)c * r / (uint32_t)G);
-}
 
 struct Seg {
   int type;  // 0: done, 1: a row's tiles
@@ -1650,7 +1644,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 rec = p.ws_split[blockIdx.x];
   const int row = rec.x, c = rec.y, last = rec.z, total = rec.w;
-  if (row < 0) return;
+  if (!record_valid(row, c, last, total, p.T * p.HG, p.G, (int)blockIdx.x)) return;  // (-1: a row that is not split)
   // the parts: of the CTA that starts the row, and of those after it to the one that finishes it whose
   // share is not empty (there are more CTAs than tiles then)
   const int k = c + 1 + tid;  // G is below the block's threads
