@@ -66,6 +66,7 @@
 
 #include "dsa_host.h"
 #include "dsa_paged_split.h"
+#include "dsa_paged_wait.cuh"
 #include "dsa_ptx.cuh"
 
 namespace dsa {
@@ -92,7 +93,6 @@ constexpr int kMaps = 8;           // tiles whose slots are known ahead
 // case, and 64 ragged requests took 72 us with it, 66 without.
 constexpr int kPrefetchPage = 16;
 constexpr int kRowOverhead = 1;    // a row's start and end, in tiles
-constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -3.402823466e38f;  // maximum of no score: below every finite one
@@ -110,28 +110,6 @@ constexpr int kSpread = 2, kOwn = 64;
 constexpr int kRefLow = -80, kRefHigh = 127, kFoldLow = -40;
 __device__ __forceinline__ float fold_of(float ref0, float ref1, float base) {
   return fmaxf(ref0 - base, fmaxf((float)kFoldLow, ref1 - (float)(126 + kWeightShift)));
-}
-
-// Bounded wait for the phase of the given parity. The hint lets the hardware park the warp for up to
-// a millisecond: some twenty warps wait at any time, and polling took a third of the issue slots.
-__device__ __forceinline__ bool try_wait_parked(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n"
-      "selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(1000000u)
-      : "memory");
-  return ok != 0;
-}
-static __device__ __forceinline__ bool bar_wait_retry(uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer_ns();
-  while (!try_wait_parked(bar, parity))
-    if (globaltimer_ns() - t0 > kWaitNs) return false;
-  return true;
-}
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
-  return try_wait_parked(bar, parity) || bar_wait_retry(bar, parity);
 }
 
 struct Params {
@@ -589,11 +567,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     *abort_flag = 1;
   };
   auto wait = [&](uint32_t bar, uint32_t par) -> bool {
-    if (bar_wait(bar, par)) return true;
+    if (bar_wait(bar, par, abort_flag)) return true;
     fail();
     return false;
   };
-  // the whole warp waits, and agrees on the outcome
   // FP8: the first segment's query, by the softmax warps
   auto split_first = [&](const Seg& s, uint32_t slot) {
     constexpr int HEADS = kHG / kSoftmaxWarps;
@@ -606,8 +583,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       mbar_arrive(aux_full(slot));
     }
   };
+  // the whole warp waits, and agrees on the outcome
   auto wait_warp = [&](uint32_t bar, uint32_t par) -> bool {
-    if (__all_sync(0xffffffffu, bar_wait(bar, par))) return true;
+    if (__all_sync(0xffffffffu, bar_wait(bar, par, abort_flag))) return true;
     fail();
     return false;
   };
@@ -891,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         if (ok) mma_commit(q_empty);
       }
       mma_commit(drain(0));
-      bar_wait(drain(0), 0);
+      bar_wait(drain(0), 0, nullptr);  // (products in flight end before the block does)
     }
     __syncwarp();
   } else if (warp == kWarpValue) {
@@ -945,7 +923,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         }
       }
       mma_commit(drain(1));
-      bar_wait(drain(1), 0);
+      bar_wait(drain(1), 0, nullptr);
     }
     __syncwarp();
   } else if (warp == kWarpQuery) {
@@ -1019,6 +997,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       const int r = 4 * i + 2 * hi16 + 1;
       odd[i] = (uint32_t)((kLoadRows * lw + r) * 128 + (((gl >> 1) ^ r) << 4) + 8 * (gl & 1));
     }
+    uint32_t issued = 0;  // halves
     for (uint32_t g = 0;; ++g) {
       if (!wait_warp(map_full(g % kMaps), (g / kMaps) & 1)) break;
       const int own = reinterpret_cast<const int*>(smem + C::MAP_OFF + (g % kMaps) * 512)[kLoadRows * lw + lane];
@@ -1041,6 +1020,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
                        "l"(p.cache + (own >= 0 ? (int64_t)own * C::RB + 256 : 0)), "r"(own >= 0 ? 8 : 0)
                        : "memory");
         }
+        issued = hs + 1;
         const uint32_t dst = sbase + C::K_OFF + st * C::HALF_BYTES;
         if (boxes) {
           // boxes of 64 columns x box_rows rows, a box by the warp its first row belongs to
@@ -1101,6 +1081,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       if (stop) break;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    if constexpr (!F8) {
+      // boxes in flight land before the block ends (after a wait that ran out a load warp may lack another's
+      // arrivals: the first wait then takes its whole limit, which is the time they had)
+      for (uint32_t hs = issued; hs > 0 && issued - hs < (uint32_t)C::NST; --hs)
+        if (!bar_wait(k_full((hs - 1) % C::NST), ((hs - 1) / C::NST) & 1, nullptr)) break;
+    }
   } else if constexpr (F8) {
     // ================================================= FP8: query split and widening ====
     // Warp w splits heads 16 w .. of a segment's query (the CTA's first is split by the softmax warps,
@@ -1283,7 +1269,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     bool first_query = true;
     bool failed = false;  // a wait ran out: go on without waiting, and leave with the group
     auto await = [&](uint32_t bar, uint32_t par) {
-      if (failed || __all_sync(0xffffffffu, bar_wait(bar, par))) return;
+      if (failed || __all_sync(0xffffffffu, bar_wait(bar, par, abort_flag))) return;
       fail();
       failed = true;
     };
