@@ -440,6 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
   auto w_empty = [&](uint32_t s) { return b3 + 48 + 8 * (C::NW + s); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
+  volatile int* progress = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 8);  // tiles mapped
   Seg* segs = reinterpret_cast<Seg*>(smem + C::SEG_OFF);
   float* s_slopes = reinterpret_cast<float*>(smem + C::SL_OFF);
 
@@ -463,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     else if (i >= B9 && i < B10) n = kSoftmaxWarps;            // p_full
     else if (i >= B11 && i < B12) n = kWidenWarps;             // w_full
     mbar_init(bar0 + 8 * i, n);
-    if (i == 0) *abort_flag = 0;
+    if (i == 0) *abort_flag = *progress = 0;
     fence_mbar_init();
   }
   if (MODS && threadIdx.x < kMaxHeads)
@@ -590,6 +591,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     return false;
   };
 
+  // for warps that have nothing to do between two rows' starts
+  auto wait_row = [&](uint32_t bar, uint32_t par) -> bool {
+    if (__all_sync(0xffffffffu, bar_wait_row(bar, par, abort_flag, progress))) return true;
+    fail();
+    return false;
+  };
+
   // 896 threads x 72 registers at launch; 512 x 80 + 384 x 56 is within that total. (No function is
   // called from here on: ptxas allocates past the launch's 72 only without calls.)
   static_assert(32 * kWarps == 896 && 32 * kWarps * 72 >= 512 * 80 + 384 * 56, "register split");
@@ -610,6 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       __syncwarp();
       if (lane == 0) mbar_arrive(map_full(g % kMaps));
       ++g;
+      if (lane == 0) *progress = (int)g;
     };
     // the slots of `n` tiles from position `base` of the range [a, b): lane l rows 4 l .. 4 l + 3
     auto map_tiles = [&](int req, uint32_t a, uint32_t b, uint32_t base, int n) -> bool {
@@ -933,7 +942,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     uint32_t qc = 0;
     for (uint32_t sc = 0; !C::WIDEN; ++sc) {
       const uint32_t slot = sc % kSegs;
-      if (!wait_warp(g_full(slot), (sc / kSegs) & 1)) break;
+      if (!wait_row(g_full(slot), (sc / kSegs) & 1)) break;
       const Seg s = segs[slot];
       if (s.type == 0) {
         __syncwarp();
@@ -1103,7 +1112,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     bool ok = true;
     for (uint32_t sc = 0; ok; ++sc) {
       const uint32_t slot = sc % kSegs;
-      if (!wait_warp(g_full(slot), (sc / kSegs) & 1)) break;
+      if (!(C::WIDEN ? wait_warp(g_full(slot), (sc / kSegs) & 1) : wait_row(g_full(slot), (sc / kSegs) & 1))) break;
       const Seg s = segs[slot];
       if (s.type == 0) break;
       const bool split = s.ntiles > 0 && qn > 0;

@@ -33,5 +33,16 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const vo
   return true;
 }
 
+// The same for a wait that may last a row, whose tiles can take longer than any limit for a hand-off: the limit
+// starts anew whenever *progress (in shared memory) has changed.
+__device__ __forceinline__ bool bar_wait_row(uint32_t bar, uint32_t parity, const volatile int* abort,
+                                             const volatile int* progress, uint64_t limit = kWaitNs) {
+  for (;;) {
+    const int seen = *progress;
+    if (bar_wait(bar, parity, abort, limit)) return true;
+    if (*abort || *progress == seen) return false;
+  }
+}
+
 }  // namespace paged
 }  // namespace dsa
