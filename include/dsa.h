@@ -302,8 +302,9 @@ DSA_API dsa_status_t dsa_proj_gemm(const void* x_codes, const void* x_scales, co
  * enters as two e4m3 terms per head (a power-of-two scale each; exact for every component within 2^9
  * of the head's largest, and within 2^-17 of the largest otherwise); scores, softmax statistics and
  * sums in fp32; the probabilities enter the value product as bf16 (FP8: times the key's tile scale,
- * as f16: 11 bits down to 2^-22 of the largest such weight of the head and tile so far, or of 2^-80
- * where all are smaller). Results are
+ * as f16: 11 bits down to 2^-22 of the largest such weight of the head and tile so far; largest weights
+ * below 2^-80, or 2^40 below that of another of the same 16 heads, count as that). The value products'
+ * fp32 sums truncate: within n * 2^-22 of sum p |k| for n positions. Results are
  * bit-identical across repeated calls with the same inputs on one device.
  */
 typedef struct dsa_paged_args {
