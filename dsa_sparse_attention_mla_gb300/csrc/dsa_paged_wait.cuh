@@ -28,9 +28,12 @@ __device__ __forceinline__ bool try_wait_parked(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const volatile int* abort, uint64_t limit = kWaitNs) {
   if (try_wait_parked(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
-  while (!try_wait_parked(bar, parity))
-    if ((abort && *abort) || globaltimer_ns() - t0 > limit) return false;
-  return true;
+  for (;;) {
+    // (the time before an attempt, not after it: a block that the GPU has not run for a while tries again)
+    const bool late = globaltimer_ns() - t0 > limit;
+    if (try_wait_parked(bar, parity)) return true;
+    if ((abort && *abort) || late) return false;
+  }
 }
 
 // The same for a wait that may last a row, whose tiles can take longer than any limit for a hand-off: the limit
