@@ -30,9 +30,10 @@ namespace evict {
 constexpr int kBins = 2048;
 constexpr int kKeys = 49152;      // keys that shared memory holds (192 KB)
 // Threads of a select CTA, by the rows' width: passes over few positions are bound by what every
-// thread does beside them (scans, barriers). Both launches on the device, 256 requests of 1088 positions:
-// 24 us with 512, 32 with 1024; 48 of 8192: 46 and 42. (Calls from the host, one after another, take
-// 26 - 31 us for the former with either: the host's own time.)
+// thread does beside them (scans, barriers). Both launches from a captured graph behind an L2 flush, of
+// which an empty replay takes 7 us: 256 requests of 1088 positions 24 us with 512, 32 with 1024; 48 of
+// 8192 46 and 42 when it was tried (40 now). Calls from the host, one after another: 26 - 32 us for the
+// former with either (the host's own time), 36.9 for the latter.
 constexpr int kFew = 512, kMany = 1024;
 constexpr int kFewWidth = 4096;
 constexpr int kMoveThreads = 256;

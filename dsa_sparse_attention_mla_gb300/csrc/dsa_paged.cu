@@ -8,12 +8,12 @@
 // The latent row k_j is key and value of every head: a position costs 264 (FP8) or 512 (bf16) bytes
 // and 4 * 256 operations per head, so with 64 heads a bf16 cache is bound by HBM and an FP8 one by
 // HBM and the tensor core about equally. What a tile takes is set by its chains of hand-offs: 128 tokens x
-// 32768 FP8 positions take 453 us (2.5 TB/s; 167 at HBM's rate), some 4200 cycles a tile, and with parts of
-// the work left out 372 (no softmax arithmetic), 390 (next to no products), 343 (no copies and no widening),
-// 271 (none of the three: the hand-offs between the warps alone). No unit is full, shared memory is the
-// busiest: a product step of N = 64 reads 6 KB, all that its 48 cycles can carry, and with copies, widening
-// and weights a tile moves some 2800 cycles' worth. 64 ragged bf16 requests, 144 MB of rows, take 50 us
-// (2.9 TB/s; 21 at HBM's rate).
+// 32768 FP8 positions take 444 us (2.5 TB/s; 167 at HBM's rate), some 4100 cycles a tile. With parts of
+// the work left out, when the whole took 453: 372 (no softmax arithmetic), 390 (next to no products), 343 (no
+// copies and no widening), 271 (none of the three: the hand-offs between the warps alone). No unit is full,
+// shared memory is the busiest: a product step of N = 64 reads 6 KB, all that its 48 cycles can carry, and
+// with copies, widening and weights a tile moves some 2800 cycles' worth. 64 ragged bf16 requests, 144 MB of
+// rows, take 50 us (2.9 TB/s; 21 at HBM's rate).
 //
 // Shape of the computation
 //  * Transposed products: S^T[key, head] = K Q^T with M = 128 keys, N = 64 heads, then
@@ -23,17 +23,16 @@
 //  * FP8 rows: scores run on the e4m3 codes as they are (kind::f8f6f4), the bf16 query split into two
 //    e4m3 terms per head, scaled by a power of two: hi + lo is the bf16 component for every component
 //    within 2^9 of the head's largest, and off by at most 2^-17 of the largest otherwise. S keeps one
-//    accumulator per scale tile and the fp32 scales
-//    multiply there. The value product takes the codes widened to f16, which is exact and one
-//    conversion per two codes (to bf16 it is four instructions), and one f16 weight matrix per scale
-//    tile: p * scale relative to a reference, the head's largest p * scale so far, 2^22 of normal range
+//    accumulator per scale tile and the fp32 scales multiply there. The value product takes the codes
+//    widened to f16, which is exact and one conversion per two codes (to bf16 it is four instructions), and
+//    one f16 weight matrix per scale tile: p * scale relative to a reference, the head's largest p * scale so far, 2^22 of normal range
 //    below it. (The largest scale would not do: a row of large scale that a head ignores would take the
 //    range from those it reads.) The first tile's reference is taken off the scores with the running
 //    maximum, and the second's differs from it by about the same factor in all heads of a group, so a
 //    weight is one product, p times a factor of the key. Where the heads differ by more, theirs come in
-//    between the two tiles (128 x 32768 positions: 430 us; 530 with a factor per head for every weight).
-//    The references cost a row's first tile some 2 us: 8 x 2112 positions take 27.8 us for 25.7 with
-//    the largest scale as the reference. e4m3 weights (as two terms) would need no widening but lose what
+//    between the two tiles (128 x 32768 positions when it was tried: 430 us; 530 with a factor per head for
+//    every weight). The references cost a row's first tile up to 2 us: 8 x 2112 positions take 27.8 us from
+//    a graph, 25.7 with the largest scale as the reference. e4m3 weights (as two terms) would need no widening but lose what
 //    many far positions add up to beside one strong one. So the keys are the exact products code * scale.
 //  * Softmax with one thread per key and 16 heads: four groups of four warps, a warp per lane quarter of
 //    tensor memory in each. The warps of a group share running maxima and synchronise among themselves. The
@@ -1393,7 +1392,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         }
         if (exact) {
           // exact maximum of the tile per head; the running maxima are raised to it. FP8: the largest weights
-          // as well (unrolled: in a loop over the three the compiler spills, 128 x 32768 positions 488 us, not 430)
+          // as well (unrolled: in a loop over the three the compiler spills, 488 us for 430 at 128 x 32768)
           float mine = -INFINITY;  // lane i ends with head i's
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
