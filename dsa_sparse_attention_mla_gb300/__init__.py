@@ -25,6 +25,8 @@ __all__ = [
     "dsa_sparse_attn_workspace_size", "dsa_sparse_attn", "dsa_sparse_attn_static_ws", "dsa_topk_select", "DsaAttnArgs",
     "DEVERR_REQUEST_ORDER", "DsaPagedArgs", "DsaEvictArgs", "dsa_paged_attn_workspace_size", "dsa_paged_attn",
     "dsa_paged_attn_mass", "dsa_cache_evict_workspace_size", "dsa_cache_evict",
+    "DEVERR_OUT_OF_PAGES", "DEVERR_TOKEN_CAPACITY", "DsaPlanArgs", "DsaQkArgs", "dsa_batch_plan", "dsa_qk_norm_rope",
+    "dsa_block_pool", "dsa_block_scores", "dsa_block_select",
 ]
 
 CACHE_BF16 = 0
@@ -33,6 +35,8 @@ DEVERR_INDEX_OUT_OF_RANGE = 0x1
 DEVERR_TIMEOUT = 0x2
 DEVERR_SLOT_OUT_OF_RANGE = 0x4
 DEVERR_REQUEST_ORDER = 0x8
+DEVERR_OUT_OF_PAGES = 0x10
+DEVERR_TOKEN_CAPACITY = 0x20
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lock = threading.Lock()
@@ -106,6 +110,37 @@ class DsaEvictArgs(ctypes.Structure):
     ]
 
 
+class DsaPlanArgs(ctypes.Structure):
+    """ctypes mirror of ``dsa_plan_args_t``."""
+
+    _fields_ = [
+        ("num_requests", ctypes.c_int64), ("lengths", ctypes.c_void_p), ("new_tokens", ctypes.c_void_p),
+        ("held", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("bt_stride", ctypes.c_int64),
+        ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int),
+        ("free_pages", ctypes.c_void_p), ("free_capacity", ctypes.c_int64), ("num_free", ctypes.c_void_p),
+        ("lengths_out", ctypes.c_void_p), ("held_out", ctypes.c_void_p), ("num_free_out", ctypes.c_void_p),
+        ("T", ctypes.c_int64), ("cu_tokens", ctypes.c_void_p), ("req_of_token", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p), ("token_lengths", ctypes.c_void_p), ("out_loc", ctypes.c_void_p),
+        ("error_word", ctypes.c_void_p),
+    ]
+
+
+class DsaQkArgs(ctypes.Structure):
+    """ctypes mirror of ``dsa_qk_args_t``."""
+
+    _fields_ = [
+        ("T", ctypes.c_int64), ("d_nope", ctypes.c_int), ("d_rope", ctypes.c_int),
+        ("q", ctypes.c_void_p), ("q_stride_t", ctypes.c_int64), ("q_stride_h", ctypes.c_int64), ("H", ctypes.c_int),
+        ("q_out", ctypes.c_void_p), ("q_out_stride_t", ctypes.c_int64), ("q_out_stride_h", ctypes.c_int64),
+        ("q_norm", ctypes.c_int), ("q_weight", ctypes.c_void_p),
+        ("k", ctypes.c_void_p), ("k_stride_t", ctypes.c_int64), ("k_norm", ctypes.c_int), ("k_weight", ctypes.c_void_p),
+        ("cache", ctypes.c_void_p), ("kind", ctypes.c_int), ("num_slots", ctypes.c_int64), ("out_loc", ctypes.c_void_p),
+        ("eps", ctypes.c_float), ("positions", ctypes.c_void_p), ("cos_sin", ctypes.c_void_p),
+        ("cs_stride", ctypes.c_int64), ("num_positions", ctypes.c_int64), ("interleaved", ctypes.c_int),
+        ("error_word", ctypes.c_void_p),
+    ]
+
+
 def load_library():
     """Load libdsa_gb300.so (built in-tree by ``__graft_entry__.build()``)."""
     global _LIB
@@ -155,6 +190,18 @@ def load_library():
         lib.dsa_cache_evict_workspace_size.restype = i32
         lib.dsa_cache_evict.argtypes = [ctypes.POINTER(DsaEvictArgs), P]
         lib.dsa_cache_evict.restype = i32
+        lib.dsa_batch_plan.argtypes = [ctypes.POINTER(DsaPlanArgs), P]
+        lib.dsa_batch_plan.restype = i32
+        lib.dsa_qk_norm_rope.argtypes = [ctypes.POINTER(DsaQkArgs), P]
+        lib.dsa_qk_norm_rope.restype = i32
+        lib.dsa_block_pool.argtypes = [P, i32, i64, P, i64, i32, i32, i64, P, P, i64, P, P, i64, P, P]
+        lib.dsa_block_pool.restype = i32
+        lib.dsa_block_scores.argtypes = [P, i64, i64, i64, i32, P, i64, P, i64, i32, i32, i64, P, P, ctypes.c_float, P, P,
+                                         i64, i64, P, P]
+        lib.dsa_block_scores.restype = i32
+        lib.dsa_block_select.argtypes = [P, i64, i64, i64, P, i64, i32, i32, i64, P, P, i32, i32, i32, P, i64, P, i64, P,
+                                         P, P]
+        lib.dsa_block_select.restype = i32
         _LIB = lib
         return lib
 
@@ -787,3 +834,216 @@ def dsa_cache_evict(cache, kind: int, block_table, lengths, mass, budget=None, *
         _check((_LIB or load_library()).dsa_cache_evict(ctypes.byref(a), torch.cuda.current_stream(index).cuda_stream),
                "dsa_cache_evict")
     return lengths_out, mass_out, positions_out
+
+
+# --------------------------------------------------------- a serving step around the paged cache --
+def dsa_batch_plan(lengths, new_tokens, held, block_table, free_pages, num_free, tokens: int, *, page_size: int,
+                   lengths_out=None, held_out=None, num_free_out=None, cu_tokens=None, req_of_token=None, positions=None,
+                   token_lengths=None, out_loc=None, error_word=None):
+    """Brings block tables int32 [R, pages] to the requests' lengths and builds the step's slot maps.
+
+    Request r of ``lengths`` int32 [R] adds ``new_tokens[r]`` positions, or ends when that is negative;
+    it holds the first ``held[r]`` pages of its table row. Pages come from, and go back to, the stack
+    ``free_pages`` int32 [N] with ``num_free`` int32 [1] entries. ``tokens`` is the room for new tokens
+    (a captured step keeps it fixed; entries behind the last token read as padding). ``lengths``,
+    ``held`` and ``num_free`` change in place, unless their ``_out`` tensors are given. Returns
+    (cu_tokens int32 [R + 1], req_of_token, positions, token_lengths int32 [tokens], out_loc int64
+    [tokens])."""
+    import torch
+
+    i32 = torch.int32
+    _c_int("page_size", page_size)
+    index = _cuda_index(lengths, "lengths", i32)
+    R, T = lengths.shape[0], tokens
+    if T < 0:
+        raise ValueError("tokens must not be negative")
+    bt_ptr, bt_stride, _, pages = _rows(block_table, "block_table", i32, index, R)
+    free_ptr = _ptr_on(free_pages, "free_pages", i32, index)
+    if free_pages.dim() != 1 or not free_pages.is_contiguous():
+        raise ValueError("free_pages must be a contiguous vector")
+    if new_tokens is None or held is None or num_free is None:
+        raise ValueError("new_tokens, held and num_free are required")
+    len_ptr, held_ptr = _vector(lengths, "lengths", R, i32, index), _vector(held, "held", R, i32, index)
+    free_n = _vector(num_free, "num_free", 1, i32, index)
+    # the outputs that the caller does not bring lie in two buffers
+    if cu_tokens is None or req_of_token is None or positions is None or token_lengths is None:
+        buf = torch.empty(3 * T + R + 1, dtype=i32, device=index)
+        if req_of_token is None:
+            req_of_token = buf[:T]
+        if positions is None:
+            positions = buf[T:2 * T]
+        if token_lengths is None:
+            token_lengths = buf[2 * T:3 * T]
+        if cu_tokens is None:
+            cu_tokens = buf[3 * T:]
+    if out_loc is None:
+        out_loc = torch.empty(T, dtype=torch.int64, device=index)
+    a = DsaPlanArgs(
+        R, len_ptr, _vector(new_tokens, "new_tokens", R, i32, index), held_ptr, bt_ptr, bt_stride, page_size, pages,
+        free_ptr, free_pages.shape[0], free_n,
+        len_ptr if lengths_out is None else _vector(lengths_out, "lengths_out", R, i32, index),
+        held_ptr if held_out is None else _vector(held_out, "held_out", R, i32, index),
+        free_n if num_free_out is None else _vector(num_free_out, "num_free_out", 1, i32, index),
+        T, _vector(cu_tokens, "cu_tokens", R + 1, i32, index), _vector(req_of_token, "req_of_token", T, i32, index),
+        _vector(positions, "positions", T, i32, index), _vector(token_lengths, "token_lengths", T, i32, index),
+        _vector(out_loc, "out_loc", T, torch.int64, index), _ptr_on(error_word, "error_word", i32, index))
+    with _on_device(index):
+        _check((_LIB or load_library()).dsa_batch_plan(ctypes.byref(a), torch.cuda.current_stream(index).cuda_stream),
+               "dsa_batch_plan")
+    return cu_tokens, req_of_token, positions, token_lengths, out_loc
+
+
+def dsa_qk_norm_rope(q=None, k=None, positions=None, cos_sin=None, eps: float = 1e-6, cache=None, kind: int = None,
+                     out_loc=None, *, d_nope: int = 256, d_rope: int = 0, q_norm: int = 0, k_norm: int = 0,
+                     q_weight=None, k_weight=None, interleaved: bool = False, q_out=None, error_word=None):
+    """Norm of every query head and of the latent key, rotation of their RoPE columns, and the key's
+    cache row, in one pass. Returns q_out (a new tensor by default; q itself for in place), None without q.
+
+    q bf16 [T, H, d_nope + d_rope] and k bf16 [T, d_nope + d_rope], either may be None. The norm covers
+    the first ``q_norm`` (``k_norm``) columns: 0 (none), d_nope or d_nope + d_rope, with weights bf16 of
+    that size. ``cos_sin`` fp32 [positions, d_rope]: cosines, then sines, of each position's angles; None
+    for no rotation. k's row goes to slot ``out_loc[t]`` (t when None) of ``cache``. A token with a
+    negative position is padding and left alone."""
+    import torch
+
+    bf16, i32 = torch.bfloat16, torch.int32
+    lead = q if q is not None else k
+    if lead is None:
+        raise ValueError("q or k is required")
+    index = _cuda_index(lead, "q" if q is not None else "k", bf16)
+    T, D = lead.shape[0], d_nope + d_rope
+    a = DsaQkArgs()
+    a.T, a.d_nope, a.d_rope, a.eps, a.interleaved = T, d_nope, d_rope, eps, bool(interleaved)
+    if q is not None:
+        st = q.stride()
+        if q.dim() != 3 or q.shape[2] != D or st[2] != 1:
+            raise ValueError("q must be [T, H, d_nope + d_rope], contiguous along its last dimension")
+        H = q.shape[1]
+        a.H, a.q, a.q_stride_t, a.q_stride_h = H, q.data_ptr(), st[0] if T > 1 else 0, st[1] if H > 1 else 0
+        if q_out is None:
+            q_out = torch.empty((T, H, D), dtype=bf16, device=index)
+        a.q_out = _ptr_on(q_out, "q_out", bf16, index)
+        st = q_out.stride()
+        if q_out.shape != q.shape or st[2] != 1:
+            raise ValueError("q_out must have q's shape, contiguous along its last dimension")
+        a.q_out_stride_t, a.q_out_stride_h = st[0] if T > 1 else 0, st[1] if H > 1 else 0
+        a.q_norm = _c_int("q_norm", q_norm)
+        a.q_weight = _vector(q_weight, "q_weight", q_norm, bf16, index)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if k is not None:
+        if cache is None or kind is None:
+            raise ValueError("k needs cache and kind")
+        k_index = _cuda_index(k, "k", bf16)
+        if k_index != index:
+            raise ValueError(f"k is on cuda:{k_index}, not on cuda:{index}: every tensor must be on one device")
+        a.k, a.k_stride_t, _, width = _rows(k, "k", bf16, index, T)
+        if width != D:
+            raise ValueError("k must be [T, d_nope + d_rope]")
+        if T <= 1:
+            a.k_stride_t = 0
+        c_index, a.cache, a.num_slots = _cache_rows(cache, kind, D if kind == CACHE_BF16 else dsa_packed_row_bytes(d_nope, d_rope))
+        if c_index != index:
+            raise ValueError(f"cache is on cuda:{c_index}, not on cuda:{index}: every tensor must be on one device")
+        a.kind = kind
+        a.k_norm = _c_int("k_norm", k_norm)
+        a.k_weight = _vector(k_weight, "k_weight", k_norm, bf16, index)
+        a.out_loc = _vector(out_loc, "out_loc", T, torch.int64, index)
+    a.positions = _vector(positions, "positions", T, i32, index)
+    if cos_sin is not None:
+        a.cos_sin, a.cs_stride, a.num_positions, _ = _rows(cos_sin, "cos_sin", torch.float32, index, None, d_rope)
+    a.error_word = _ptr_on(error_word, "error_word", i32, index)
+    with _on_device(index):
+        _check((_LIB or load_library()).dsa_qk_norm_rope(ctypes.byref(a), torch.cuda.current_stream(index).cuda_stream),
+               "dsa_qk_norm_rope")
+    return q_out
+
+
+def dsa_block_pool(cache, kind: int, block_table, positions, lengths, summary, *, page_size: int, req_of_token=None,
+                   error_word=None):
+    """Writes the mean row of every block (page) that a token of this step lies in to ``summary`` bf16
+    [pages, 256]: token t is position positions[t] of request req_of_token[t] (t without it), whose cache
+    holds lengths[r] positions. Returns summary."""
+    import torch
+
+    i32 = torch.int32
+    _c_int("page_size", page_size)
+    index, cache_ptr, slots = _cache_rows(cache, kind, 264 if kind == CACHE_FP8_SCALED else 256)
+    T = positions.shape[0]
+    bt_ptr, bt_stride, R, pages = _rows(block_table, "block_table", i32, index, None, 1 if T else 0)
+    s_ptr = _ptr_on(summary, "summary", torch.bfloat16, index)
+    if summary.dim() != 2 or summary.shape[1] != 256 or not summary.is_contiguous():
+        raise ValueError("summary must be contiguous [pages, 256]")
+    with _on_device(index):
+        _check((_LIB or load_library()).dsa_block_pool(
+            cache_ptr, kind, slots, bt_ptr, bt_stride, page_size, pages, R, _vector(positions, "positions", T, i32, index),
+            _vector(req_of_token, "req_of_token", T, i32, index), T, _vector(lengths, "lengths", R, i32, index), s_ptr,
+            summary.shape[0], _ptr_on(error_word, "error_word", i32, index),
+            torch.cuda.current_stream(index).cuda_stream), "dsa_block_pool")
+    return summary
+
+
+def dsa_block_scores(q, summary, block_table, lengths, sm_scale: float, *, page_size: int, req_of_token=None, weights=None,
+                     out=None, error_word=None):
+    """fp32 [T, pages]: for token t and each block b of its first lengths[t] positions, the sum over
+    heads of weights[t, h] * max(0, sm_scale * q[t, h] . summary[page of b]) (weight 1 without
+    ``weights`` fp32 [T, H]). Entries past the token's blocks are left as they are (-inf in a new result)."""
+    import torch
+
+    i32, f32 = torch.int32, torch.float32
+    _c_int("page_size", page_size)
+    index = _cuda_index(q, "q", torch.bfloat16)
+    st = q.stride()
+    if q.dim() != 3 or q.shape[2] != 256 or st[2] != 1:
+        raise ValueError("q must be [T, H, 256], contiguous along its last dimension")
+    T, H = q.shape[0], q.shape[1]
+    bt_ptr, bt_stride, R, pages = _rows(block_table, "block_table", i32, index, None, 1 if T else 0)
+    s_ptr = _ptr_on(summary, "summary", torch.bfloat16, index)
+    if summary.dim() != 2 or summary.shape[1] != 256 or not summary.is_contiguous():
+        raise ValueError("summary must be contiguous [pages, 256]")
+    if out is None:
+        out = torch.full((T, pages), -float("inf"), dtype=f32, device=index)
+    o_ptr, o_stride, _, width = _rows(out, "out", f32, index, T, 1)
+    if weights is not None and (tuple(weights.shape) != (T, H) or not weights.is_contiguous()):
+        raise ValueError("weights must be a contiguous [T, H] tensor")
+    with _on_device(index):
+        _check((_LIB or load_library()).dsa_block_scores(
+            q.data_ptr(), st[0] if T > 1 else 0, st[1] if H > 1 else 0, T, H, s_ptr, summary.shape[0], bt_ptr, bt_stride,
+            page_size, pages, R, _vector(req_of_token, "req_of_token", T, i32, index),
+            _vector(lengths, "lengths", T, i32, index), sm_scale, _ptr_on(weights, "weights", f32, index), o_ptr, o_stride,
+            width, _ptr_on(error_word, "error_word", i32, index), torch.cuda.current_stream(index).cuda_stream),
+            "dsa_block_scores")
+    return out
+
+
+def dsa_block_select(scores, block_table, lengths, K: int, *, page_size: int, req_of_token=None, sink: int = 0,
+                     recent: int = 1, blocks=None, table=None, lengths_out=None, error_word=None):
+    """The K best blocks of each token by ``scores`` fp32 [T, S], its first ``sink`` and last ``recent``
+    always: (blocks int32 [T, K] in ascending order, then -1; table int32 [T, K], their pages;
+    lengths_out int32 [T], their positions). dsa_paged_attn(q, cache, kind, table, lengths_out, ...)
+    attends to exactly these blocks."""
+    import torch
+
+    i32 = torch.int32
+    for name, v in (("page_size", page_size), ("K", K), ("sink", sink), ("recent", recent)):
+        _c_int(name, v)
+    index = _cuda_index(scores, "scores", torch.float32)
+    s_ptr, s_stride, T, width = _rows(scores, "scores", torch.float32, index, None, 1)
+    bt_ptr, bt_stride, R, pages = _rows(block_table, "block_table", i32, index, None, 1 if T else 0)
+    if blocks is None and table is None and K > 0:
+        buf = torch.empty((2, T, K), dtype=i32, device=index)
+        blocks, table = buf[0], buf[1]
+    elif blocks is None or table is None:
+        raise ValueError("blocks and table come together, and K is positive")
+    if lengths_out is None:
+        lengths_out = torch.empty(T, dtype=i32, device=index)
+    b_ptr, b_stride, _, b_width = _rows(blocks, "blocks", i32, index, T, K)
+    t_ptr, t_stride, _, t_width = _rows(table, "table", i32, index, T, K)
+    with _on_device(index):
+        _check((_LIB or load_library()).dsa_block_select(
+            s_ptr, s_stride, width, T, bt_ptr, bt_stride, page_size, pages, R,
+            _vector(req_of_token, "req_of_token", T, i32, index), _vector(lengths, "lengths", T, i32, index), K, sink, recent,
+            b_ptr, b_stride, t_ptr, t_stride, _vector(lengths_out, "lengths_out", T, i32, index),
+            _ptr_on(error_word, "error_word", i32, index), torch.cuda.current_stream(index).cuda_stream),
+            "dsa_block_select")
+    return blocks, table, lengths_out

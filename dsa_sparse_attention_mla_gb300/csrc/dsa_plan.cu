@@ -1,0 +1,264 @@
+// dsa_plan.cu - the batch plan of a serving step: block tables brought to the requests' lengths
+// through a stack of free pages, and the slot maps of the tokens that the step adds.
+//
+// Three prefix sums over the requests carry it: pages given back, then pages wanted and tokens
+// wanted (whose inclusive sums decide what is refused), then both again over what is granted. Every
+// page moved finds its request by a binary search in the sums of its chunk of requests, so a step
+// with one long prompt and one with many short ones cost the same per page.
+//
+// One block does the requests: the sums need all of them, and a decode step has a few hundred. What
+// bounds it is the chain of dependent loads (state, table, stack, table again), not bytes.
+#include <cuda_runtime.h>
+
+#include <climits>
+
+#include "dsa_host.h"
+
+namespace dsa {
+namespace plan {
+
+constexpr int kThreads = 1024;     // requests of a chunk, one per thread
+constexpr int kFillThreads = 256;
+constexpr int64_t kMaxFill = 4096;  // tokens that the plan's own block writes
+
+struct Params {
+  int64_t R;
+  const int32_t *lengths, *add, *held;
+  int32_t* bt;
+  int64_t bt_st;
+  int page, max_pages;
+  int32_t* stack;
+  int64_t cap;
+  const int32_t* num_free;
+  int32_t *len_out, *held_out, *num_free_out;
+  int64_t T;
+  int32_t *cu, *req, *pos, *tlen;
+  int64_t* loc;
+  int32_t* err;
+};
+
+// Inclusive sums over the block of two values per thread; *total receives the sums over all threads.
+__device__ __forceinline__ longlong2 block_scan(longlong2 v, longlong2 (&s_warp)[32], longlong2* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, v.x, o), y = __shfl_up_sync(0xffffffffu, v.y, o);
+    if (lane >= o) {
+      v.x += x;
+      v.y += y;
+    }
+  }
+  __syncthreads();
+  if (lane == 31) s_warp[warp] = v;
+  __syncthreads();
+  longlong2 w = s_warp[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, w.x, o), y = __shfl_up_sync(0xffffffffu, w.y, o);
+    if (lane >= o) {
+      w.x += x;
+      w.y += y;
+    }
+  }
+  total->x = __shfl_sync(0xffffffffu, w.x, 31);
+  total->y = __shfl_sync(0xffffffffu, w.y, 31);
+  if (warp > 0) {
+    v.x += __shfl_sync(0xffffffffu, w.x, warp - 1);
+    v.y += __shfl_sync(0xffffffffu, w.y, warp - 1);
+  }
+  return v;
+}
+
+// The first of n ascending entries that exceeds i.
+template <class V>
+__device__ __forceinline__ int64_t first_above(const V* a, int64_t n, int64_t i) {
+  int64_t lo = 0, hi = n;
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (a[mid] > i)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  return lo;
+}
+
+// The entries of token slot i. cu and the requests' new lengths were written by this block, or by an
+// earlier kernel.
+__device__ __forceinline__ void fill(const Params& p, int64_t i, int64_t total) {
+  if (i >= total) {
+    p.req[i] = 0;
+    p.pos[i] = -1;
+    p.tlen[i] = 0;
+    p.loc[i] = -1;
+    return;
+  }
+  const int64_t r = first_above(p.cu + 1, p.R, i);
+  const int pos = p.len_out[r] - p.cu[r + 1] + (int)i;
+  const int page = p.bt[r * p.bt_st + pos / p.page];
+  p.req[i] = (int)r;
+  p.pos[i] = pos;
+  p.tlen[i] = pos + 1;
+  p.loc[i] = page < 0 ? -1 : (int64_t)page * p.page + pos % p.page;
+}
+
+struct Want {
+  int64_t after, need;  // the request's length and pages if it is granted
+  int l, h;
+  bool fits;
+  long long back, take, tokens;
+};
+
+__device__ __forceinline__ Want want_of(const Params& p, int64_t r) {
+  Want w;
+  w.l = max(p.lengths[r], 0);
+  w.h = min(max(p.held[r], 0), p.max_pages);
+  const int n = p.add[r];
+  w.after = n < 0 ? 0 : (int64_t)w.l + n;
+  w.need = (w.after + p.page - 1) / p.page;
+  w.fits = w.need <= p.max_pages && w.after <= INT_MAX;
+  w.back = w.need < w.h ? w.h - w.need : 0;
+  w.take = w.fits && w.need > w.h ? w.need - w.h : 0;
+  w.tokens = w.fits && n > 0 ? n : 0;
+  return w;
+}
+
+__global__ void __launch_bounds__(kThreads) plan_kernel(const Params p, const int fill_here) {
+  __shared__ longlong2 s_warp[32];
+  __shared__ long long s_sum[kThreads];  // inclusive page sums of the chunk
+  __shared__ int s_first[kThreads];      // first table entry that a request gives back or takes
+  const int tid = threadIdx.x;
+  const int64_t nf = min((int64_t)max(*p.num_free, 0), p.cap);
+  int bad = 0;
+  longlong2 total;
+  // pages given back go onto the stack
+  int64_t have = nf;
+  for (int64_t r0 = 0; r0 < p.R; r0 += kThreads) {
+    const int64_t r = r0 + tid;
+    Want w{};
+    if (r < p.R) w = want_of(p, r);
+    const longlong2 sum = block_scan(make_longlong2(w.back, 0), s_warp, &total);
+    s_sum[tid] = sum.x;
+    s_first[tid] = (int)w.need;
+    __syncthreads();
+    for (int64_t i = tid; i < total.x; i += kThreads) {
+      const int64_t k = first_above(s_sum, kThreads, i);
+      const int64_t j = s_first[k] + i - (k ? s_sum[k - 1] : 0);
+      if (have + i < p.cap)
+        p.stack[have + i] = p.bt[(r0 + k) * p.bt_st + j];
+      else
+        bad = DSA_DEVERR_SLOT_OUT_OF_RANGE;
+    }
+    have += total.x;
+    __syncthreads();
+  }
+  if (have > p.cap) have = p.cap;
+  // what is wanted, what of it is granted, and the pages taken from the top
+  longlong2 wanted = make_longlong2(0, 0), granted = make_longlong2(0, 0);
+  for (int64_t r0 = 0; r0 < p.R; r0 += kThreads) {
+    const int64_t r = r0 + tid;
+    Want w{};
+    if (r < p.R) w = want_of(p, r);
+    longlong2 sum = block_scan(make_longlong2(w.take, w.tokens), s_warp, &total);
+    const bool no_page = w.take > 0 && wanted.x + sum.x > have;
+    const bool no_room = w.tokens > 0 && wanted.y + sum.y > p.T;
+    wanted.x += total.x;
+    wanted.y += total.y;
+    const bool ok = w.fits && !no_page && !no_room;
+    if (r < p.R) {
+      if (!w.fits) bad |= DSA_DEVERR_INDEX_OUT_OF_RANGE;
+      if (no_page) bad |= DSA_DEVERR_OUT_OF_PAGES;
+      if (no_room) bad |= DSA_DEVERR_TOKEN_CAPACITY;
+    }
+    if (!ok) w.take = w.tokens = 0;
+    sum = block_scan(make_longlong2(w.take, w.tokens), s_warp, &total);
+    s_sum[tid] = sum.x;
+    s_first[tid] = w.h;
+    if (r < p.R) {
+      p.len_out[r] = ok ? (int)w.after : w.l;
+      p.held_out[r] = w.take > 0 || w.need < w.h ? (int)w.need : w.h;
+      p.cu[r + 1] = (int)(granted.y + sum.y);
+    }
+    __syncthreads();
+    for (int64_t i = tid; i < total.x; i += kThreads) {
+      const int64_t k = first_above(s_sum, kThreads, i);
+      const int64_t j = s_first[k] + i - (k ? s_sum[k - 1] : 0);
+      p.bt[(r0 + k) * p.bt_st + j] = p.stack[have - 1 - granted.x - i];
+    }
+    granted.x += total.x;
+    granted.y += total.y;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    p.cu[0] = 0;
+    *p.num_free_out = (int)(have - granted.x);
+  }
+  if (bad && p.err) atomicOr(p.err, bad);
+  if (!fill_here) return;
+  __syncthreads();
+  for (int64_t i = tid; i < p.T; i += kThreads) fill(p, i, granted.y);
+}
+
+__global__ void __launch_bounds__(kFillThreads) fill_kernel(const Params p) {
+  const int64_t i = (int64_t)blockIdx.x * kFillThreads + threadIdx.x;
+  if (i < p.T) fill(p, i, p.cu[p.R]);
+}
+
+}  // namespace plan
+}  // namespace dsa
+
+using namespace dsa;
+
+extern "C" dsa_status_t dsa_batch_plan(const dsa_plan_args_t* a, void* stream) {
+  if (!a || a->num_requests < 0 || a->T < 0 || a->free_capacity < 0) return DSA_ERR_INVALID_ARGUMENT;
+  if (a->num_requests > (1 << 20) || a->T > (1 << 30) || a->free_capacity > INT_MAX) return DSA_ERR_UNSUPPORTED;
+  if (a->page_size < 1 || a->max_pages < 0 || a->bt_stride < a->max_pages) return DSA_ERR_INVALID_ARGUMENT;
+  if (!a->num_free || !a->num_free_out || !a->cu_tokens || (a->free_capacity > 0 && !a->free_pages))
+    return DSA_ERR_INVALID_ARGUMENT;
+  if (a->num_requests > 0 && (!a->lengths || !a->new_tokens || !a->held || !a->lengths_out || !a->held_out ||
+                              (a->max_pages > 0 && !a->block_table)))
+    return DSA_ERR_INVALID_ARGUMENT;
+  if (a->T > 0 && (!a->req_of_token || !a->positions || !a->token_lengths || !a->out_loc)) return DSA_ERR_INVALID_ARGUMENT;
+  if (!aligned(a->out_loc, 8)) return DSA_ERR_INVALID_ARGUMENT;
+  for (const void* q : {(const void*)a->lengths, (const void*)a->new_tokens, (const void*)a->held, (const void*)a->block_table,
+                        (const void*)a->free_pages, (const void*)a->num_free, (const void*)a->lengths_out,
+                        (const void*)a->held_out, (const void*)a->num_free_out, (const void*)a->cu_tokens,
+                        (const void*)a->req_of_token, (const void*)a->positions, (const void*)a->token_lengths,
+                        (const void*)a->error_word})
+    if (!aligned(q, 4)) return DSA_ERR_INVALID_ARGUMENT;
+  DeviceInfo dev;
+  const dsa_status_t st = current_device(&dev);
+  if (st != DSA_OK) return st;
+  plan::Params p{};
+  p.R = a->num_requests;
+  p.lengths = a->lengths;
+  p.add = a->new_tokens;
+  p.held = a->held;
+  p.bt = a->block_table;
+  p.bt_st = a->bt_stride;
+  p.page = a->page_size;
+  p.max_pages = a->max_pages;
+  p.stack = a->free_pages;
+  p.cap = a->free_capacity;
+  p.num_free = a->num_free;
+  p.len_out = a->lengths_out;
+  p.held_out = a->held_out;
+  p.num_free_out = a->num_free_out;
+  p.T = a->T;
+  p.cu = a->cu_tokens;
+  p.req = a->req_of_token;
+  p.pos = a->positions;
+  p.tlen = a->token_lengths;
+  p.loc = a->out_loc;
+  p.err = a->error_word;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool here = p.T <= plan::kMaxFill;
+  plan::plan_kernel<<<1, plan::kThreads, 0, s>>>(p, here);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (!here) {
+    plan::fill_kernel<<<(unsigned)((p.T + plan::kFillThreads - 1) / plan::kFillThreads), plan::kFillThreads, 0, s>>>(p);
+    e = cudaGetLastError();
+  }
+  return e == cudaSuccess ? DSA_OK : cuda_fail(e);
+}

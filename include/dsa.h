@@ -55,6 +55,8 @@ typedef enum {
 #define DSA_DEVERR_TIMEOUT 0x2             /* a bounded device-side wait gave up */
 #define DSA_DEVERR_SLOT_OUT_OF_RANGE 0x4   /* quant_k_cache: out_loc outside [0, num_slots): row skipped */
 #define DSA_DEVERR_REQUEST_ORDER 0x8       /* paged_attn_mass: a request named twice or out of order: token skipped */
+#define DSA_DEVERR_OUT_OF_PAGES 0x10       /* batch_plan: the free pages do not suffice: request refused */
+#define DSA_DEVERR_TOKEN_CAPACITY 0x20     /* batch_plan: more new tokens than room for them: request refused */
 
 typedef enum {
   DSA_CACHE_BF16 = 0,        /* bf16 latent rows [num_slots, d_nope + d_rope] */
@@ -422,6 +424,184 @@ typedef struct dsa_evict_args {
 
 DSA_API dsa_status_t dsa_cache_evict_workspace_size(int64_t num_requests, int64_t width, size_t* bytes);
 DSA_API dsa_status_t dsa_cache_evict(const dsa_evict_args_t* args, void* stream);
+
+/*
+ * A serving step around the paged cache: the batch plan that brings block tables to the requests'
+ * lengths, the norms and the rotation of queries and keys with the cache write, and the selection
+ * of the blocks (a block = a page of positions) that each token attends to. In turn: dsa_batch_plan
+ * -> dsa_qk_norm_rope -> dsa_block_pool -> dsa_block_scores -> dsa_block_select -> dsa_paged_attn
+ * over the selected table; dsa_cache_evict shrinks lengths, and the next plan takes its pages back.
+ * Results are bit-identical across repeated calls with the same inputs on one device.
+ */
+
+/*
+ * dsa_batch_plan - block tables and slot maps of a step, from request lengths on the device. For
+ * request r with l = lengths[r] cached positions, h = held[r] pages in its table row and
+ * n = new_tokens[r]:
+ *   n < 0       the request ends: its length becomes 0
+ *   n >= 0      its length becomes l + n
+ *   need        ceil(new length / page_size) pages
+ *   need < h    pages block_table[r, need .. h) go onto the free stack (the entries stay as they are)
+ *   need > h    block_table[r, h .. need) are taken from the top of the free stack
+ * The free stack is free_pages[0 .. *num_free), its last entry the top. Pages given back are put on
+ * it first, requests in order and pages in order, so this call may take them; then pages are taken,
+ * requests in order and pages in order. A request is refused when need > max_pages or l + n exceeds
+ * 2^31 - 1 (DSA_DEVERR_INDEX_OUT_OF_RANGE); or, of the requests not refused by that, when it takes
+ * pages and it and those before it want more pages than there are (DSA_DEVERR_OUT_OF_PAGES), or
+ * when it adds tokens and it and those before it add more than T (DSA_DEVERR_TOKEN_CAPACITY). A
+ * refused request adds no token and takes no page; its length stays l, and pages past need still
+ * go back. Negative lengths and held count as 0, held past max_pages as max_pages, *num_free as
+ * clamped to [0, free_capacity]. Pages that find no room on the stack are dropped and set
+ * DSA_DEVERR_SLOT_OUT_OF_RANGE.
+ * The tokens that requests add are numbered in order of requests and positions, i = 0, 1, ...:
+ *   cu_tokens     [R + 1]: the first token of each request, and the number of all
+ *   req_of_token  [T], positions [T] (the token's position), token_lengths [T] (position + 1: what
+ *                 the token attends to), out_loc int64 [T] (the cache slot of its position; -1 for a
+ *                 page < 0). Entries behind the last token: request 0, position -1, length 0, slot
+ *                 -1, which every operator skips.
+ * Each of lengths_out, held_out and num_free_out may be its input (in place) or disjoint; the block
+ * table and the free stack change in place.
+ */
+typedef struct dsa_plan_args {
+  int64_t num_requests;          /* at most 2^20 */
+  const int32_t* lengths;        /* int32 [num_requests] */
+  const int32_t* new_tokens;     /* int32 [num_requests] */
+  const int32_t* held;           /* int32 [num_requests] */
+  int32_t* block_table;          /* int32 [num_requests, bt_stride] */
+  int64_t bt_stride;
+  int page_size, max_pages;
+  int32_t* free_pages;           /* int32 [free_capacity] */
+  int64_t free_capacity;         /* at most 2^31 - 1 */
+  const int32_t* num_free;       /* int32 [1] */
+  int32_t* lengths_out;          /* int32 [num_requests] */
+  int32_t* held_out;             /* int32 [num_requests] */
+  int32_t* num_free_out;         /* int32 [1] */
+  int64_t T;                     /* room for tokens: at most 2^30 */
+  int32_t* cu_tokens;            /* int32 [num_requests + 1] */
+  int32_t* req_of_token;         /* int32 [T] */
+  int32_t* positions;            /* int32 [T] */
+  int32_t* token_lengths;        /* int32 [T] */
+  int64_t* out_loc;              /* int64 [T] */
+  int32_t* error_word;
+} dsa_plan_args_t;
+
+DSA_API dsa_status_t dsa_batch_plan(const dsa_plan_args_t* args, void* stream);
+
+/*
+ * dsa_qk_norm_rope - the norm of every query head and of the latent key, the rotation of their
+ * RoPE columns and the key's cache row, in one pass. A row x of d_nope + d_rope columns becomes
+ *   y_d = x_d * rsqrt(mean_{d < n} x_d^2 + eps) * weight_d      for the first n columns
+ * (n = q_norm for queries, k_norm for keys: 0 leaves them as they are, d_nope, or all; weight 1
+ * when NULL), then, when cos_sin is given, the last d_rope columns turn by the token's angles:
+ *   (a, b) -> (a cos - b sin, b cos + a sin) for the pairs (i, i + d_rope / 2), or (2 i, 2 i + 1) when interleaved,
+ * with cos = cos_sin[positions[t], i] and sin = cos_sin[positions[t], d_rope / 2 + i]. Everything is
+ * in fp32 and rounded once: queries to bf16, the key's row as the cache holds it (bf16, or packed as
+ * dsa_quant_k_cache packs, from the unrounded row). Sums of squares must stay below the fp32 range.
+ * A token with a negative position is padding: nothing of it is read or written. A position at or
+ * past num_positions skips the token and sets DSA_DEVERR_INDEX_OUT_OF_RANGE. A key whose out_loc is
+ * negative is not written; one at or past num_slots is not either and sets
+ * DSA_DEVERR_SLOT_OUT_OF_RANGE. Slots of one call must differ.
+ * Geometries 256+0 and 512+64. q_out may be q (in place, equal strides) or disjoint.
+ */
+typedef struct dsa_qk_args {
+  int64_t T;                     /* tokens, at most 2^24 (0 = no-op) */
+  int d_nope, d_rope;
+  const void* q;                 /* bf16 [T, H, d_nope + d_rope], 16-byte aligned, strides multiples
+                                    of 8; NULL: keys only */
+  int64_t q_stride_t, q_stride_h;
+  int H;                         /* 1 .. 128 (unused without q) */
+  void* q_out;                   /* bf16, the shape of q */
+  int64_t q_out_stride_t, q_out_stride_h;
+  int q_norm;
+  const void* q_weight;          /* bf16 [q_norm], 16-byte aligned, or NULL */
+  const void* k;                 /* bf16 [T, d_nope + d_rope], 16-byte aligned, stride a multiple of
+                                    8; NULL: queries only */
+  int64_t k_stride_t;
+  int k_norm;
+  const void* k_weight;          /* bf16 [k_norm], 16-byte aligned, or NULL */
+  void* cache;                   /* contiguous rows, 16-byte aligned (unused without k) */
+  dsa_cache_kind_t kind;
+  int64_t num_slots;
+  const int64_t* out_loc;        /* int64 [T], or NULL: token t's key goes to slot t */
+  float eps;                     /* positive and finite */
+  const int32_t* positions;      /* int32 [T], or NULL (not with cos_sin): no padding */
+  const float* cos_sin;          /* fp32 [num_positions, cs_stride], or NULL: no rotation */
+  int64_t cs_stride;             /* >= d_rope */
+  int64_t num_positions;
+  int interleaved;
+  int32_t* error_word;
+} dsa_qk_args_t;
+
+DSA_API dsa_status_t dsa_qk_norm_rope(const dsa_qk_args_t* args, void* stream);
+
+/*
+ * dsa_block_pool - the mean row of each block that tokens of this step lie in (geometry 256+0):
+ *   summary[page] = bf16(mean of the cached rows of the block's positions below lengths[r])
+ * for the block positions[t] / page_size of request r = req_of_token[t] (request t when NULL) of
+ * every token t, page = block_table[r, block]. Rows in fp32 (FP8: code * tile scale), summed in a
+ * fixed order. Negative positions are skipped. A request or page that does not exist, a position
+ * at or past max_pages * page_size, a block without a position below lengths[r] or with rows past
+ * num_slots sets DSA_DEVERR_INDEX_OUT_OF_RANGE and is skipped.
+ *   cache         contiguous rows, 16-byte aligned; num_slots below 2^31
+ *   lengths       int32 [num_requests], with this step's tokens
+ *   summary       bf16 [num_pages, 256], 16-byte aligned; the summaries of other pages stay as they are
+ */
+DSA_API dsa_status_t dsa_block_pool(const void* cache, dsa_cache_kind_t kind, int64_t num_slots,
+                                    const int32_t* block_table, int64_t bt_stride, int page_size, int max_pages,
+                                    int64_t num_requests, const int32_t* positions, const int32_t* req_of_token,
+                                    int64_t T, const int32_t* lengths, void* summary, int64_t num_pages,
+                                    int32_t* error_word, void* stream);
+
+/*
+ * dsa_block_scores - a cheap score of each block for each token:
+ *   scores[t, b] = sum_h w[t,h] * max(0, sm_scale * dot(q[t,h,:], summary[block_table[r, b]]))
+ * for the blocks b < ceil(lengths[t] / page_size) of the token's request r; other entries of scores
+ * are left as they are. w = weights, or 1 when NULL. bf16 products (exact) accumulated in fp32 on
+ * the tensor cores, the sum over heads in fp32. NaN passes through the maximum. A block whose page does not
+ * exist scores -inf and sets DSA_DEVERR_INDEX_OUT_OF_RANGE, as do blocks at or past max_pages or
+ * width (not scored) and a request that does not exist (its token is skipped).
+ * Causality: a token's own block, and with several tokens of a request in one call the blocks after
+ * it, hold rows the token must not see. Blocks after it are not scored (lengths[t]); its own block
+ * has to be selected whatever its score (recent >= 1 below).
+ *   q             bf16 [T, H, 256], 16-byte aligned, strides multiples of 8; H 1 .. 128, T <= 2^24
+ *   summary       bf16 [num_pages, 256], 16-byte aligned
+ *   req_of_token  int32 [T], or NULL: token t belongs to request t. Neighbouring tokens of one
+ *                 request share the reads of its summaries.
+ *   lengths       int32 [T]: the positions each token attends to
+ *   sm_scale      positive and finite
+ *   weights       fp32 [T, H] or NULL
+ *   scores        fp32 [T, width], row stride score_stride >= width; width 1 .. 2^24
+ */
+DSA_API dsa_status_t dsa_block_scores(const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_t T, int H,
+                                      const void* summary, int64_t num_pages, const int32_t* block_table,
+                                      int64_t bt_stride, int page_size, int max_pages, int64_t num_requests,
+                                      const int32_t* req_of_token, const int32_t* lengths, float sm_scale,
+                                      const float* weights, float* scores, int64_t score_stride, int64_t width,
+                                      int32_t* error_word, void* stream);
+
+/*
+ * dsa_block_select - the K best blocks of each token, as a block table of the token's own. Of the
+ * n = ceil(lengths[t] / page_size) blocks of token t, m = min(K, n) are chosen: the first `sink`,
+ * the last `recent`, and of the others those of the largest score (ties to the lower block; -0.0
+ * equals +0.0; NaN is outside the contract, but m are chosen).
+ *   blocks        int32 [T, K]: the chosen blocks in ascending order, then -1 (NULL: not wanted)
+ *   table         int32 [T, K]: their pages, block_table[r, block], then -1
+ *   lengths_out   int32 [T]: the positions of the chosen blocks, where the token's last block counts
+ *                 those below lengths[t] only: it comes last, so dsa_paged_attn(q, cache, table,
+ *                 lengths_out) with one table row per token attends to exactly these positions. (Its
+ *                 distance bias wants key_positions of the same order.)
+ * A request that does not exist chooses nothing; it and a token with more blocks than max_pages or
+ * width (the excess is left out, its last block then counting as full) set
+ * DSA_DEVERR_INDEX_OUT_OF_RANGE.
+ *   scores        fp32 [T, width], row stride score_stride >= width; width 1 .. 2^24
+ *   K             1 .. 16384; sink, recent >= 0 with sink + recent <= K
+ *   T             at most 2^24 (0 = no-op)
+ */
+DSA_API dsa_status_t dsa_block_select(const float* scores, int64_t score_stride, int64_t width, int64_t T,
+                                      const int32_t* block_table, int64_t bt_stride, int page_size, int max_pages,
+                                      int64_t num_requests, const int32_t* req_of_token, const int32_t* lengths, int K,
+                                      int sink, int recent, int32_t* blocks, int64_t blocks_stride, int32_t* table,
+                                      int64_t table_stride, int32_t* lengths_out, int32_t* error_word, void* stream);
 
 #ifdef __cplusplus
 }
