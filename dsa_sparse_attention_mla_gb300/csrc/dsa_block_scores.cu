@@ -1,91 +1,461 @@
 // dsa_block_scores.cu - a cheap score of each block (page) for each token:
 //   scores[t, b] = sum_h w[t,h] * max(0, sm_scale * q[t,h] . summary[page of b]).
 //
-// A warp per block of a token: its lanes hold the summary row, eight columns each, and go through the
-// heads.
+// Transposed products: S^T[block, head] = P Q^T with M = 128 blocks and, as N, the heads of up to
+// 256 / H neighbouring tokens (tcgen05 kind::f16, fp32 accumulators in tensor memory). A block is then a
+// lane of tensor memory, so the sum over heads stays within a thread: no shuffle, and what a
+// block's row holds (NaN, infinities, nothing) reaches its own scores only. Tokens of one request share the tile
+// of summaries; where a group of tokens has several requests, each run of equal ones is a product of
+// its own over its part of the query rows.
+//
+// Long prefills are bound by the tensor core, decode by HBM (a summary is read once per request).
+//
+// One CTA per SM walks units (group of tokens, part of its block tiles). Warps 0-3 sum up and store, 4-7 load
+// summaries (cp.async, row by row: pages are scattered) in quarters of a tile's columns through a ring of
+// six, 8 issues the products, 9-10 load queries, up to four groups ahead where they are small. Two accumulators
+// let the products of a tile run while the one before it is summed up. Every wait is bounded.
 #include <cuda_runtime.h>
 
 #include <climits>
 #include <cmath>
+#include <mutex>
 
 #include "dsa_host.h"
+#include "dsa_paged_wait.cuh"
 #include "dsa_ptx.cuh"
 
 namespace dsa {
 namespace scores {
 
+using paged::bar_wait;
+
 constexpr int kD = 256;
 constexpr int kMaxHeads = 128;
-constexpr int kThreads = 256;
+constexpr int kBM = 128;     // blocks per tile (MMA M)
+constexpr int kMaxN = 256;   // query rows per group (MMA N)
+constexpr int kChunks = kD / 64;
+constexpr int kStages = 6;
+constexpr int kWarpLoad0 = 4, kLoadWarps = 4, kWarpMma = 8, kWarpQuery0 = 9, kQueryWarps = 2;
+constexpr int kWarps = kWarpQuery0 + kQueryWarps;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxSlots = 4;  // query groups in shared memory
+constexpr uint32_t kChunkBytes = kBM * 128;
+constexpr uint32_t kQueryBytes = kMaxN * kD * 2;
+constexpr uint32_t kRingOff = kQueryBytes;
+constexpr uint32_t kMiscOff = kRingOff + kStages * kChunkBytes;
+constexpr uint32_t kSmemBytes = kMiscOff + 256 + 1024;  // and room to align
 
 struct Params {
   const uint16_t* q;
   int64_t q_st, q_sh;
   int64_t T;
-  int H;
+  int H, HP;  // heads, rounded up to a multiple of 16
+  int G;      // tokens per group
+  int slots;  // groups of query rows that fit
+  int parts;  // units per group
+  int units;
   const uint16_t* summary;
   int64_t num_pages;
   const int32_t* bt;
   int64_t bt_st;
-  int page, max_pages;
+  int page;
+  int most;   // blocks that the table and the scores hold
   int64_t num_requests;
   const int32_t *req, *lengths;
   float scale;
   const float* w;
   float* out;
-  int64_t out_st, width;
+  int64_t out_st;
   int32_t* err;
 };
 
-__device__ __forceinline__ void widen(const uint4 v, float (&x)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
 // max(x, 0) that passes NaN on
 __device__ __forceinline__ float relu(float x) {
   float r;
   asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(x));
   return r;
 }
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// Waits for tensor-memory loads; the registers pass through, so that no use of them moves before it.
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void set_err(int32_t* err, int bit) {
+  if (err) atomicOr(err, bit);
+}
 
-__global__ void __launch_bounds__(kThreads) scores_kernel(const Params p) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t t = blockIdx.x;
-  const int64_t r = p.req ? p.req[t] : t;
-  const int64_t most = p.width < p.max_pages ? p.width : p.max_pages;
-  int64_t n = ((int64_t)max(p.lengths[t], 0) + p.page - 1) / p.page;
-  bool bad = n > most;
-  if (bad) n = most;
-  if (r < 0 || r >= p.num_requests) {
-    bad = true;
-    n = 0;
+// The tiles of this CTA's units in order; every warp walks them for itself. Lane i holds token i of the
+// unit's group, and the next unit's lengths and requests are loaded while this one is worked on.
+struct Walk {
+  int u, t0;             // unit, first token of its group (both below 2^25)
+  int req, nb;           // lane: request, blocks
+  int count;             // tokens of the group
+  int a, b;              // the run: tokens a .. b - 1 share a request
+  int m, m_end;          // tile, end of the run's tiles in this part
+  int next_req, next_len;
+
+  __device__ __forceinline__ void fetch(const Params& p, int unit) {
+    const int lane = threadIdx.x & 31;
+    next_req = 0;
+    next_len = 0;
+    if (unit >= p.units) return;
+    const int t = unit / p.parts * p.G + lane;
+    if (lane < p.G && t < p.T) {
+      next_req = p.req ? p.req[t] : t;
+      next_len = p.lengths[t];
+    }
   }
-  if (bad && threadIdx.x == 0 && blockIdx.y == 0 && p.err) atomicOr(p.err, DSA_DEVERR_INDEX_OUT_OF_RANGE);
-  for (int64_t b = (int64_t)blockIdx.y * (kThreads / 32) + warp; b < n; b += (int64_t)gridDim.y * (kThreads / 32)) {
-    const int64_t page = p.bt[r * p.bt_st + b];
-    float total = -INFINITY;
-    if (page < 0 || page >= p.num_pages) {
-      if (lane == 0 && p.err) atomicOr(p.err, DSA_DEVERR_INDEX_OUT_OF_RANGE);
-    } else {
-      float k[8];
-      widen(*reinterpret_cast<const uint4*>(p.summary + page * kD + 8 * lane), k);
-      total = 0.0f;
-      for (int h = 0; h < p.H; ++h) {
-        float x[8], dot = 0.0f;
-        widen(*reinterpret_cast<const uint4*>(p.q + t * p.q_st + h * p.q_sh + 8 * lane), x);
+  __device__ __forceinline__ void start(const Params& p) {
+    u = (int)blockIdx.x - (int)gridDim.x;
+    a = b = count = m = m_end = 0;
+    fetch(p, blockIdx.x);
+  }
+  // The next tile; false at the end. `report`: whether this warp tells of tokens that cannot be scored.
+  __device__ __forceinline__ bool next(const Params& p, bool report = false) {
+    if (++m < m_end) return true;
+    const int lane = threadIdx.x & 31;
+    for (;;) {
+      if (b >= count) {  // the next unit
+        u += gridDim.x;
+        if (u >= p.units) return false;
+        t0 = u / p.parts * p.G;
+        count = (int)(p.T - t0 < p.G ? p.T - t0 : p.G);
+        req = next_req;
+        const int64_t n = ((int64_t)max(next_len, 0) + p.page - 1) / p.page;
+        nb = (int)(n < p.most ? n : p.most);
+        bool bad = n > p.most;
+        if (req < 0 || req >= p.num_requests) {
+          bad = true;
+          nb = 0;
+        }
+        if (lane >= count) nb = 0;
+        if (report && bad && lane < count && u % p.parts == 0) set_err(p.err, DSA_DEVERR_INDEX_OUT_OF_RANGE);
+        b = 0;
+        fetch(p, u + (int)gridDim.x);
+      }
+      a = b;
+      const int r = __shfl_sync(0xffffffffu, req, a);
+      const uint32_t other = __ballot_sync(0xffffffffu, lane > a && (lane >= count || req != r));
+      b = other ? __ffs(other) - 1 : 32;
+      const int most = __reduce_max_sync(0xffffffffu, lane >= a && lane < b ? nb : 0);
+      const int tiles = (most + kBM - 1) / kBM;
+      const int part = u % p.parts;
+      m = (int)((int64_t)tiles * part / p.parts);
+      m_end = (int)((int64_t)tiles * (part + 1) / p.parts);
+      if (m < m_end) return true;
+    }
+  }
+  __device__ __forceinline__ int64_t run_req() const { return __shfl_sync(0xffffffffu, req, a); }
+  __device__ __forceinline__ int run_blocks() const {
+    const int lane = threadIdx.x & 31;
+    return __reduce_max_sync(0xffffffffu, lane >= a && lane < b ? nb : 0);
+  }
+};
+
+template <bool WEIGHTS>
+__global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t bars = base + kMiscOff;
+  auto full = [&](int s) { return bars + 8 * s; };
+  auto empty = [&](int s) { return bars + 8 * (kStages + s); };
+  auto q_full = [&](int s) { return bars + 8 * (2 * kStages + s); };
+  auto q_empty = [&](int s) { return bars + 8 * (2 * kStages + kMaxSlots + s); };
+  auto acc_full = [&](int s) { return bars + 8 * (2 * kStages + 2 * kMaxSlots + s); };
+  auto acc_empty = [&](int s) { return bars + 8 * (2 * kStages + 2 * kMaxSlots + 2 + s); };
+  const uint32_t drained = bars + 8 * (2 * kStages + 2 * kMaxSlots + 4);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + kMiscOff + 8 * (2 * kStages + 2 * kMaxSlots + 5));
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMiscOff + 8 * (2 * kStages + 2 * kMaxSlots + 5) + 4);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full(s), 32 * kLoadWarps);
+      mbar_init(empty(s), 1);
+    }
+    for (int s = 0; s < kMaxSlots; ++s) {
+      mbar_init(q_full(s), 32 * kQueryWarps);
+      mbar_init(q_empty(s), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(acc_full(s), 1);
+      mbar_init(acc_empty(s), 4);
+    }
+    mbar_init(drained, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto give_up = [&]() {
+    *abort = 1;
+    if (lane == 0) set_err(p.err, DSA_DEVERR_TIMEOUT);
+  };
+  const uint32_t row_bytes_q = (uint32_t)(p.G * p.HP) * 128;  // one column quarter of a group's rows
+  Walk k;
+  k.start(p);
+
+  if (warp >= kWarpLoad0 && warp < kWarpLoad0 + kLoadWarps) {
+    // ---- summaries: this warp's 32 rows of each tile, four rows of a column quarter per instruction
+    const int w = warp - kWarpLoad0;
+    const uint32_t sub = lane >> 3, piece = lane & 7;
+    uint32_t dst[2];  // rows 4 i + sub alternate between two places in the swizzle
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dot = fmaf(x[i], k[i], dot);
+    for (uint32_t i = 0; i < 2; ++i) dst[i] = (32 * w + 4 * i + sub) * 128 + ((piece ^ ((4 * i + sub) & 7)) << 4);
+    auto page_of = [&]() {  // lane's row of the current tile
+      const int64_t r = k.run_req();
+      const int row = k.m * kBM + 32 * w + lane;
+      if (row >= k.run_blocks()) return -1;
+      int page = p.bt[r * p.bt_st + row];
+      if (page < 0 || page >= p.num_pages) {
+        set_err(p.err, DSA_DEVERR_INDEX_OUT_OF_RANGE);
+        page = -1;
+      }
+      return page;
+    };
+    int stage = 0;
+    uint32_t phase = 0;
+    bool more = k.next(p, w == 0);
+    int page = more ? page_of() : -1;
+    while (more) {
+      const int now = page;
+      more = k.next(p, w == 0);
+      page = more ? page_of() : -1;
+      // rows without a summary keep what the stage holds: their lanes are not read
+      const uint8_t* src[8];
+      bool have[8];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        total = fmaf(p.w ? p.w[t * p.H + h] : 1.0f, relu(dot * p.scale), total);
+      for (int i = 0; i < 8; ++i) {
+        const int pg = __shfl_sync(0xffffffffu, now, 4 * i + sub);
+        have[i] = pg >= 0;
+        src[i] = reinterpret_cast<const uint8_t*>(p.summary) + (int64_t)max(pg, 0) * (2 * kD) + 16 * piece;
+      }
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        if (!bar_wait(empty(stage), phase ^ 1, abort)) {
+          give_up();
+          more = false;
+          break;
+        }
+        const uint32_t to = base + kRingOff + stage * kChunkBytes;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (have[i]) cp16(to + dst[i & 1] + 1024 * (i >> 1), src[i] + 128 * c);
+        cp_arrive(full(stage));
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
       }
     }
-    if (lane == 0) p.out[t * p.out_st + b] = total;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp >= kWarpQuery0) {
+    // ---- queries: a group's rows once per unit
+    const int w = warp - kWarpQuery0;
+    int slot = 0;
+    uint32_t phase = 0;
+    int last = -1;
+    while (k.next(p)) {
+      if (k.u == last) continue;
+      last = k.u;
+      if (!bar_wait(q_empty(slot), phase ^ 1, abort)) {
+        give_up();
+        break;
+      }
+      const uint32_t to = base + (uint32_t)slot * kChunks * row_bytes_q;
+      const uint32_t c = lane >> 3, piece = lane & 7;
+      for (int n = w; n < k.count * p.HP; n += kQueryWarps) {
+        const int i = n / p.HP, h = n - i * p.HP;
+        if (h >= p.H) continue;  // columns that are not read
+        cp16(to + c * row_bytes_q + n * 128 + ((piece ^ (n & 7)) << 4),
+             p.q + (int64_t)(k.t0 + i) * p.q_st + h * p.q_sh + 8 * lane);
+      }
+      cp_arrive(q_full(slot));
+      if (++slot == p.slots) {
+        slot = 0;
+        phase ^= 1;
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == kWarpMma) {
+    // ---- products
+    const uint64_t d0 = sw128_desc(0, 16, 1024);
+    const uint32_t d_hi = (uint32_t)(d0 >> 32), d_lo = (uint32_t)d0;
+    int stage = 0, slot = -1, buf = 0;
+    uint32_t phase = 0, q_phase = 0, acc_phase = 0;
+    int last = -1;
+    bool ok = true;
+    while (ok && k.next(p)) {
+      if (k.u != last) {
+        if (slot >= 0 && lane == 0) mma_commit(q_empty(slot));
+        __syncwarp();
+        if (++slot == p.slots) {
+          slot = 0;
+          q_phase ^= 1;
+        }
+        last = k.u;
+        if (!bar_wait(q_full(slot), q_phase, abort)) {
+          give_up();
+          break;
+        }
+      }
+      if (!bar_wait(acc_empty(buf), acc_phase ^ 1, abort)) {
+        give_up();
+        break;
+      }
+      tc_fence_after();
+      const int n = (k.b - k.a) * p.HP;
+      const uint32_t idesc = idesc_bf16(kBM, n, 0, 0);
+      const uint32_t acc = tmem + buf * kMaxN;
+      const uint32_t q0 = base + (uint32_t)slot * kChunks * row_bytes_q + (uint32_t)(k.a * p.HP) * 128;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        if (!bar_wait(full(stage), phase, abort)) {
+          give_up();
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          fence_proxy_async_smem();
+          const uint32_t a_lo = d_lo | ((base + kRingOff + stage * kChunkBytes) >> 4);
+          const uint32_t b_lo = d_lo | ((q0 + c * row_bytes_q) >> 4);
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            if (c == 0 && s == 0)
+              mma_bf16_lohi<0>(acc, a_lo, d_hi, b_lo, d_hi, idesc);
+            else
+              mma_bf16_lohi<1>(acc, a_lo + 2 * s, d_hi, b_lo + 2 * s, d_hi, idesc);
+          }
+          mma_commit(empty(stage));
+        }
+        __syncwarp();
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (!ok) break;
+      if (lane == 0) mma_commit(acc_full(buf));
+      __syncwarp();
+      buf ^= 1;
+      acc_phase ^= buf == 0;
+    }
+    // every product ends before tensor memory is given back
+    if (lane == 0) mma_commit(drained);
+    __syncwarp();
+    bar_wait(drained, 0, nullptr);
+  } else {
+    // ---- sums over heads: a block per lane
+    int buf = 0;
+    uint32_t acc_phase = 0;
+    const uint64_t scale2 = pack2(p.scale, p.scale);
+    while (k.next(p)) {
+      const int row = k.m * kBM + 32 * warp + lane;
+      const int64_t r = k.run_req();
+      int page = -1;
+      if (row < k.run_blocks()) page = p.bt[r * p.bt_st + row];
+      if (!bar_wait(acc_full(buf), acc_phase, abort)) {
+        give_up();
+        break;
+      }
+      tc_fence_after();
+      const uint32_t acc0 = tmem + buf * kMaxN + ((uint32_t)(32 * warp) << 16);
+      for (int i = k.a; i < k.b; ++i) {
+        const uint32_t col = acc0 + (i - k.a) * p.HP;
+        const float* w = WEIGHTS ? p.w + (int64_t)(k.t0 + i) * p.H : nullptr;
+        uint64_t sum[2] = {0, 0};  // even and odd heads, in two chains
+        for (int h0 = 0; h0 < p.H; h0 += 16) {
+          uint32_t x[16];
+          tmem_ld32_x16(col + h0, x);
+          wait_ld(x);
+          const int left = p.H - h0;
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            float u = relu(__uint_as_float(x[j])), v = relu(__uint_as_float(x[j + 1]));
+            float wu = 1.0f, wv = 1.0f;
+            if (left < 16) {  // heads that are not there
+              if (j >= left) u = 0.0f;
+              if (j + 1 >= left) v = 0.0f;
+            }
+            if (WEIGHTS) {
+              wu = j < left ? w[h0 + j] : 0.0f;
+              wv = j + 1 < left ? w[h0 + j + 1] : 0.0f;
+              sum[(j >> 1) & 1] = fma2(mul2(pack2(u, v), scale2), pack2(wu, wv), sum[(j >> 1) & 1]);
+            } else {
+              sum[(j >> 1) & 1] = fma2(pack2(u, v), scale2, sum[(j >> 1) & 1]);
+            }
+          }
+        }
+        const float2 s0 = unpack2(sum[0]), s1 = unpack2(sum[1]);
+        const int nb = __shfl_sync(0xffffffffu, k.nb, i);
+        if (row < nb)
+          p.out[(int64_t)(k.t0 + i) * p.out_st + row] =
+              page < 0 || page >= p.num_pages ? -INFINITY : (s0.x + s0.y) + (s1.x + s1.y);
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty(buf));
+      buf ^= 1;
+      acc_phase ^= buf == 0;
+    }
   }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// The kernels' shared-memory limits, once per device.
+dsa_status_t prepare(int device) {
+  static std::mutex mu;
+  static bool done[64];
+  std::lock_guard<std::mutex> lock(mu);
+  if (done[device]) return DSA_OK;
+  cudaError_t e = cudaFuncSetAttribute(scores_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(scores_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return cuda_fail(e);
+  done[device] = true;
+  return DSA_OK;
 }
 
 }  // namespace scores
@@ -112,7 +482,7 @@ extern "C" dsa_status_t dsa_block_scores(const void* q, int64_t q_stride_t, int6
                         (const void*)scores_out, (const void*)error_word})
     if (!aligned(x, 4)) return DSA_ERR_INVALID_ARGUMENT;
   DeviceInfo dev;
-  const dsa_status_t st = current_device(&dev);
+  dsa_status_t st = current_device(&dev);
   if (st != DSA_OK) return st;
   scores::Params p{};
   p.q = static_cast<const uint16_t*>(q);
@@ -125,7 +495,6 @@ extern "C" dsa_status_t dsa_block_scores(const void* q, int64_t q_stride_t, int6
   p.bt = block_table;
   p.bt_st = bt_stride;
   p.page = page_size;
-  p.max_pages = max_pages;
   p.num_requests = num_requests;
   p.req = req_of_token;
   p.lengths = lengths;
@@ -133,12 +502,28 @@ extern "C" dsa_status_t dsa_block_scores(const void* q, int64_t q_stride_t, int6
   p.w = weights;
   p.out = scores_out;
   p.out_st = score_stride;
-  p.width = width;
   p.err = error_word;
-  const int64_t most = width < max_pages ? width : max_pages;
-  const int64_t y = (most + 31) / 32;
-  scores::scores_kernel<<<dim3((unsigned)T, (unsigned)(y < 1 ? 1 : y > 1024 ? 1024 : y)), scores::kThreads, 0,
-                          static_cast<cudaStream_t>(stream)>>>(p);
+  p.most = (int)(width < max_pages ? width : max_pages);
+  const int64_t tiles = p.most > 0 ? (p.most + scores::kBM - 1) / scores::kBM : 1;
+  const int sms = dev.sm_count;
+  // As many tokens in a group as an MMA takes, while there are units enough for every SM; tokens that do not
+  // name their requests have one each.
+  p.HP = (H + 15) / 16 * 16;
+  p.G = req_of_token ? scores::kMaxN / p.HP : 1;
+  while (p.G > 1 && (T + p.G - 1) / p.G * tiles < 4 * sms) p.G >>= 1;
+  const int64_t groups = (T + p.G - 1) / p.G;
+  int64_t parts = (4 * sms + groups - 1) / groups;
+  p.parts = (int)(parts < tiles ? parts : tiles);
+  p.units = (int)(groups * p.parts);
+  p.slots = (int)(scores::kQueryBytes / ((uint32_t)(p.G * p.HP) * scores::kD * 2));
+  if (p.slots > scores::kMaxSlots) p.slots = scores::kMaxSlots;
+  if ((st = scores::prepare(dev.device)) != DSA_OK) return st;
+  const unsigned grid = (unsigned)(p.units < sms ? p.units : sms);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (weights)
+    scores::scores_kernel<true><<<grid, scores::kThreads, scores::kSmemBytes, s>>>(p);
+  else
+    scores::scores_kernel<false><<<grid, scores::kThreads, scores::kSmemBytes, s>>>(p);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? DSA_OK : cuda_fail(e);
 }
