@@ -10,9 +10,9 @@
 //
 // Long prefills are bound by the tensor core, decode by HBM (a summary is read once per request).
 //
-// One CTA per SM walks units (group of tokens, part of its block tiles). Warps 0-3 sum up and store, 4-7 load
+// One CTA per SM walks units (group of tokens, part of its block tiles). Warps 0-7 sum up and store, 8-11 load
 // summaries (cp.async, row by row: pages are scattered) in quarters of a tile's columns through a ring of
-// six, 8 issues the products, 9-10 load queries, up to four groups ahead where they are small. Two accumulators
+// six, 12 issues the products, 13-15 load queries, up to four groups ahead where they are small. Two accumulators
 // let the products of a tile run while the one before it is summed up. Every wait is bounded.
 #include <cuda_runtime.h>
 
@@ -35,7 +35,7 @@ constexpr int kBM = 128;     // blocks per tile (MMA M)
 constexpr int kMaxN = 256;   // query rows per group (MMA N)
 constexpr int kChunks = kD / 64;
 constexpr int kStages = 6;
-constexpr int kWarpLoad0 = 4, kLoadWarps = 4, kWarpMma = 8, kWarpQuery0 = 9, kQueryWarps = 2;
+constexpr int kWarpLoad0 = 8, kLoadWarps = 4, kWarpMma = 12, kWarpQuery0 = 13, kQueryWarps = 3;
 constexpr int kWarps = kWarpQuery0 + kQueryWarps;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxSlots = 4;  // query groups in shared memory
@@ -181,7 +181,8 @@ struct Walk {
   }
 };
 
-template <bool WEIGHTS>
+// WHOLE: the heads fill groups of 16, and rows of weights are 16-byte aligned.
+template <bool WEIGHTS, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -238,25 +239,26 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     uint32_t dst[2];  // rows 4 i + sub alternate between two places in the swizzle
 #pragma unroll
     for (uint32_t i = 0; i < 2; ++i) dst[i] = (32 * w + 4 * i + sub) * 128 + ((piece ^ ((4 * i + sub) & 7)) << 4);
-    auto page_of = [&]() {  // lane's row of the current tile
+    int page = -1;
+    bool in = false;
+    auto load_page = [&]() {  // of the lane's row of the current tile; looked at a tile later
       const int64_t r = k.run_req();
       const int row = k.m * kBM + 32 * w + lane;
-      if (row >= k.run_blocks()) return -1;
-      int page = p.bt[r * p.bt_st + row];
-      if (page < 0 || page >= p.num_pages) {
-        set_err(p.err, DSA_DEVERR_INDEX_OUT_OF_RANGE);
-        page = -1;
-      }
-      return page;
+      in = row < k.run_blocks();
+      page = in ? p.bt[r * p.bt_st + row] : -1;
     };
     int stage = 0;
     uint32_t phase = 0;
     bool more = k.next(p, w == 0);
-    int page = more ? page_of() : -1;
+    if (more) load_page();
     while (more) {
-      const int now = page;
+      int now = page;
+      if (now < 0 || now >= p.num_pages) {
+        if (in) set_err(p.err, DSA_DEVERR_INDEX_OUT_OF_RANGE);
+        now = -1;
+      }
       more = k.next(p, w == 0);
-      page = more ? page_of() : -1;
+      if (more) load_page();
       // rows without a summary keep what the stage holds: their lanes are not read
       const uint8_t* src[8];
       bool have[8];
@@ -381,44 +383,65 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     __syncwarp();
     bar_wait(drained, 0, nullptr);
   } else {
-    // ---- sums over heads: a block per lane
-    int buf = 0;
-    uint32_t acc_phase = 0;
+    // ---- sums over heads: a block per lane, tiles in turn between the warps of either accumulator
+    const int buf = warp >> 2, quarter = warp & 3;
+    uint32_t phase = 0;
+    bool mine = buf != 0;
     const uint64_t scale2 = pack2(p.scale, p.scale);
+    const uint32_t acc0 = tmem + buf * kMaxN + ((uint32_t)(32 * quarter) << 16);
     while (k.next(p)) {
-      const int row = k.m * kBM + 32 * warp + lane;
+      mine = !mine;
+      if (!mine) continue;
+      const int row = k.m * kBM + 32 * quarter + lane;
       const int64_t r = k.run_req();
       int page = -1;
       if (row < k.run_blocks()) page = p.bt[r * p.bt_st + row];
-      if (!bar_wait(acc_full(buf), acc_phase, abort)) {
+      if (!bar_wait(acc_full(buf), phase, abort)) {
         give_up();
         break;
       }
+      phase ^= 1;
       tc_fence_after();
-      const uint32_t acc0 = tmem + buf * kMaxN + ((uint32_t)(32 * warp) << 16);
+      uint32_t col = acc0;
+      uint32_t x[16];
+      tmem_ld32_x16(col, x);
       for (int i = k.a; i < k.b; ++i) {
-        const uint32_t col = acc0 + (i - k.a) * p.HP;
         const float* w = WEIGHTS ? p.w + (int64_t)(k.t0 + i) * p.H : nullptr;
-        uint64_t sum[2] = {0, 0};  // even and odd heads, in two chains
-        for (int h0 = 0; h0 < p.H; h0 += 16) {
-          uint32_t x[16];
-          tmem_ld32_x16(col + h0, x);
-          wait_ld(x);
-          const int left = p.H - h0;
+        uint64_t sum[2] = {0, 0};  // two chains of pairs of heads
+        for (int h0 = 0; h0 < p.HP; h0 += 16) {
+          float4 wt[4];
+          if (WEIGHTS && WHOLE) {
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            float u = relu(__uint_as_float(x[j])), v = relu(__uint_as_float(x[j + 1]));
-            float wu = 1.0f, wv = 1.0f;
-            if (left < 16) {  // heads that are not there
-              if (j >= left) u = 0.0f;
-              if (j + 1 >= left) v = 0.0f;
+            for (int j = 0; j < 4; ++j) wt[j] = *reinterpret_cast<const float4*>(w + h0 + 4 * j);
+          } else if (WEIGHTS) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int h = h0 + 4 * j;
+              wt[j] = make_float4(h < p.H ? w[h] : 0.0f, h + 1 < p.H ? w[h + 1] : 0.0f, h + 2 < p.H ? w[h + 2] : 0.0f,
+                                  h + 3 < p.H ? w[h + 3] : 0.0f);
             }
+          }
+          wait_ld(x);
+          float u[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) u[j] = relu(__uint_as_float(x[j]));
+          // the next columns come while these are summed up
+          col += 16;
+          if (h0 + 16 < p.HP || i + 1 < k.b) tmem_ld32_x16(col, x);
+          if (!WHOLE && h0 + 16 > p.H) {  // heads that are not there
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (h0 + j >= p.H) u[j] = 0.0f;
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint64_t v = pack2(u[2 * j], u[2 * j + 1]);
             if (WEIGHTS) {
-              wu = j < left ? w[h0 + j] : 0.0f;
-              wv = j + 1 < left ? w[h0 + j + 1] : 0.0f;
-              sum[(j >> 1) & 1] = fma2(mul2(pack2(u, v), scale2), pack2(wu, wv), sum[(j >> 1) & 1]);
+              const float4 f = wt[j >> 1];
+              v = mul2(v, scale2);
+              sum[j & 1] = fma2(v, j & 1 ? pack2(f.z, f.w) : pack2(f.x, f.y), sum[j & 1]);
             } else {
-              sum[(j >> 1) & 1] = fma2(pack2(u, v), scale2, sum[(j >> 1) & 1]);
+              sum[j & 1] = fma2(v, scale2, sum[j & 1]);
             }
           }
         }
@@ -432,8 +455,6 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(acc_empty(buf));
-      buf ^= 1;
-      acc_phase ^= buf == 0;
     }
   }
   tc_fence_before();
@@ -450,9 +471,10 @@ dsa_status_t prepare(int device) {
   static bool done[64];
   std::lock_guard<std::mutex> lock(mu);
   if (done[device]) return DSA_OK;
-  cudaError_t e = cudaFuncSetAttribute(scores_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(scores_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  cudaError_t e = cudaSuccess;
+  for (const void* f : {(const void*)scores_kernel<false, false>, (const void*)scores_kernel<false, true>,
+                        (const void*)scores_kernel<true, false>, (const void*)scores_kernel<true, true>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return cuda_fail(e);
   done[device] = true;
   return DSA_OK;
@@ -520,10 +542,10 @@ extern "C" dsa_status_t dsa_block_scores(const void* q, int64_t q_stride_t, int6
   if ((st = scores::prepare(dev.device)) != DSA_OK) return st;
   const unsigned grid = (unsigned)(p.units < sms ? p.units : sms);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (weights)
-    scores::scores_kernel<true><<<grid, scores::kThreads, scores::kSmemBytes, s>>>(p);
-  else
-    scores::scores_kernel<false><<<grid, scores::kThreads, scores::kSmemBytes, s>>>(p);
+  const bool whole = H % 16 == 0 && aligned(weights, 16);
+  auto kernel = weights ? (whole ? scores::scores_kernel<true, true> : scores::scores_kernel<true, false>)
+                        : (whole ? scores::scores_kernel<false, true> : scores::scores_kernel<false, false>);
+  kernel<<<grid, scores::kThreads, scores::kSmemBytes, s>>>(p);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? DSA_OK : cuda_fail(e);
 }
