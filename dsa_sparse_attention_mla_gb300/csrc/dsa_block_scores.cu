@@ -38,6 +38,8 @@ constexpr int kStages = 6;
 constexpr int kWarpLoad0 = 8, kLoadWarps = 4, kWarpMma = 12, kWarpQuery0 = 13, kQueryWarps = 3;
 constexpr int kWarps = kWarpQuery0 + kQueryWarps;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kPagesAhead = 3;
+constexpr int kInFlight = 3;  // quarters of a tile on their way per loading warp, besides the newest
 constexpr int kMaxSlots = 4;  // query groups in shared memory
 constexpr uint32_t kChunkBytes = kBM * 128;
 constexpr uint32_t kQueryBytes = kMaxN * kD * 2;
@@ -90,9 +92,9 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 // Waits for tensor-memory loads; the registers pass through, so that no use of them moves before it.
@@ -103,86 +105,126 @@ __device__ __forceinline__ void wait_ld(uint32_t (&r)[16]) {
                :
                : "memory");
 }
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld32_x16(taddr, r); }
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void set_err(int32_t* err, int bit) {
   if (err) atomicOr(err, bit);
 }
 
 // The tiles of this CTA's units in order; every warp walks them for itself. Lane i holds token i of the
-// unit's group, and the next unit's lengths and requests are loaded while this one is worked on.
+// unit's group; the requests and lengths of the next two units are on their way meanwhile (units may be
+// one tile long, shorter than a load).
 struct Walk {
-  int u, t0;             // unit, first token of its group (both below 2^25)
+  int u;                 // unit
+  int t0, part;          // first token of its group, its part of the tiles
+  int step_t, step_part; // from one unit of this CTA to the next, before the carry
   int req, nb;           // lane: request, blocks
   int count;             // tokens of the group
   int a, b;              // the run: tokens a .. b - 1 share a request
+  int blocks;            // most blocks of a token of the run
   int m, m_end;          // tile, end of the run's tiles in this part
-  int next_req, next_len;
+  int ahead_t, ahead_part;
+  int req1, len1, req2, len2;
 
-  __device__ __forceinline__ void fetch(const Params& p, int unit) {
+  __device__ __forceinline__ void advance(const Params& p, int& t, int& part_) const {
+    t += step_t;
+    part_ += step_part;
+    if (part_ >= p.parts) {
+      part_ -= p.parts;
+      t += p.G;
+    }
+  }
+  __device__ __forceinline__ void fetch(const Params& p, int unit, int first, int& r, int& len) const {
     const int lane = threadIdx.x & 31;
-    next_req = 0;
-    next_len = 0;
-    if (unit >= p.units) return;
-    const int t = unit / p.parts * p.G + lane;
-    if (lane < p.G && t < p.T) {
-      next_req = p.req ? p.req[t] : t;
-      next_len = p.lengths[t];
+    r = len = 0;
+    if (unit < p.units && lane < p.G && first + lane < p.T) {
+      r = p.req ? p.req[first + lane] : first + lane;
+      len = p.lengths[first + lane];
     }
   }
   __device__ __forceinline__ void start(const Params& p) {
-    u = (int)blockIdx.x - (int)gridDim.x;
-    a = b = count = m = m_end = 0;
-    fetch(p, blockIdx.x);
+    const int grid = (int)gridDim.x;
+    step_t = grid / p.parts * p.G;
+    step_part = grid % p.parts;
+    u = (int)blockIdx.x - grid;
+    ahead_t = (int)blockIdx.x / p.parts * p.G;
+    ahead_part = (int)blockIdx.x % p.parts;
+    a = b = count = m = m_end = t0 = part = 0;
+    fetch(p, u + grid, ahead_t, req1, len1);
+    int t = ahead_t, q = ahead_part;
+    advance(p, t, q);
+    fetch(p, u + 2 * grid, t, req2, len2);
   }
   // The next tile; false at the end. `report`: whether this warp tells of tokens that cannot be scored.
   __device__ __forceinline__ bool next(const Params& p, bool report = false) {
     if (++m < m_end) return true;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, grid = (int)gridDim.x;
     for (;;) {
       if (b >= count) {  // the next unit
-        u += gridDim.x;
+        u += grid;
         if (u >= p.units) return false;
-        t0 = u / p.parts * p.G;
-        count = (int)(p.T - t0 < p.G ? p.T - t0 : p.G);
-        req = next_req;
-        const int64_t n = ((int64_t)max(next_len, 0) + p.page - 1) / p.page;
-        nb = (int)(n < p.most ? n : p.most);
+        t0 = ahead_t;
+        part = ahead_part;
+        advance(p, ahead_t, ahead_part);
+        count = p.T - t0 < p.G ? (int)(p.T - t0) : p.G;
+        req = req1;
+        const int n = len1 > 0 ? (int)((uint32_t)(len1 - 1) / (uint32_t)p.page) + 1 : 0;
+        req1 = req2;
+        len1 = len2;
+        nb = n < p.most ? n : p.most;
         bool bad = n > p.most;
         if (req < 0 || req >= p.num_requests) {
           bad = true;
           nb = 0;
         }
         if (lane >= count) nb = 0;
-        if (report && bad && lane < count && u % p.parts == 0) set_err(p.err, DSA_DEVERR_INDEX_OUT_OF_RANGE);
+        if (report && bad && lane < count && part == 0) set_err(p.err, DSA_DEVERR_INDEX_OUT_OF_RANGE);
         b = 0;
-        fetch(p, u + (int)gridDim.x);
+        int t = ahead_t, q = ahead_part;
+        advance(p, t, q);
+        fetch(p, u + 2 * grid, t, req2, len2);
       }
       a = b;
       const int r = __shfl_sync(0xffffffffu, req, a);
       const uint32_t other = __ballot_sync(0xffffffffu, lane > a && (lane >= count || req != r));
       b = other ? __ffs(other) - 1 : 32;
-      const int most = __reduce_max_sync(0xffffffffu, lane >= a && lane < b ? nb : 0);
-      const int tiles = (most + kBM - 1) / kBM;
-      const int part = u % p.parts;
-      m = (int)((int64_t)tiles * part / p.parts);
-      m_end = (int)((int64_t)tiles * (part + 1) / p.parts);
+      blocks = __reduce_max_sync(0xffffffffu, lane >= a && lane < b ? nb : 0);
+      const int tiles = (blocks + kBM - 1) / kBM;
+      m = 0;
+      m_end = tiles;
+      if (p.parts > 1) {
+        m = tiles * part / p.parts;
+        m_end = tiles * (part + 1) / p.parts;
+      }
       if (m < m_end) return true;
     }
   }
   __device__ __forceinline__ int64_t run_req() const { return __shfl_sync(0xffffffffu, req, a); }
-  __device__ __forceinline__ int run_blocks() const {
-    const int lane = threadIdx.x & 31;
-    return __reduce_max_sync(0xffffffffu, lane >= a && lane < b ? nb : 0);
-  }
 };
 
-// WHOLE: the heads fill groups of 16, and rows of weights are 16-byte aligned.
-template <bool WEIGHTS, bool WHOLE>
+// N: heads summed up per step, 16 or 32. WHOLE: they fill steps, and rows of weights are 16-byte aligned.
+template <bool WEIGHTS, bool WHOLE, int N>
 __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -201,11 +243,11 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMiscOff + 8 * (2 * kStages + 2 * kMaxSlots + 5) + 4);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(full(s), 32 * kLoadWarps);
+      mbar_init(full(s), kLoadWarps);
       mbar_init(empty(s), 1);
     }
     for (int s = 0; s < kMaxSlots; ++s) {
-      mbar_init(q_full(s), 32 * kQueryWarps);
+      mbar_init(q_full(s), kQueryWarps);
       mbar_init(q_empty(s), 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -239,26 +281,48 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     uint32_t dst[2];  // rows 4 i + sub alternate between two places in the swizzle
 #pragma unroll
     for (uint32_t i = 0; i < 2; ++i) dst[i] = (32 * w + 4 * i + sub) * 128 + ((piece ^ ((4 * i + sub) & 7)) << 4);
-    int page = -1;
-    bool in = false;
-    auto load_page = [&]() {  // of the lane's row of the current tile; looked at a tile later
+    // the pages of the next tiles are loaded ahead, and looked at when their tile's turn has come
+    int page[kPagesAhead];
+    bool in[kPagesAhead], more[kPagesAhead];
+    bool any = true;
+    // A quarter is handed over when kInFlight later ones are on their way. The writer's fence makes it visible
+    // to the tensor core: one at the reader would hold up the products (720 cycles a quarter with it).
+    int issued = 0, landed = 0;
+    auto hand_over = [&]() {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kInFlight) : "memory");
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full(landed));
+      if (++landed == kStages) landed = 0;
+    };
+    auto load_page = [&](int& pg, bool& is, bool& tile) {
+      any = any && k.next(p, w == 0);
+      tile = any;
+      pg = -1;
+      is = false;
+      if (!any) return;
       const int64_t r = k.run_req();
       const int row = k.m * kBM + 32 * w + lane;
-      in = row < k.run_blocks();
-      page = in ? p.bt[r * p.bt_st + row] : -1;
+      is = row < k.blocks;
+      if (is) pg = p.bt[r * p.bt_st + row];
     };
     int stage = 0;
     uint32_t phase = 0;
-    bool more = k.next(p, w == 0);
-    if (more) load_page();
-    while (more) {
-      int now = page;
+#pragma unroll
+    for (int i = 0; i < kPagesAhead; ++i) load_page(page[i], in[i], more[i]);
+    while (more[0]) {
+      int now = page[0];
       if (now < 0 || now >= p.num_pages) {
-        if (in) set_err(p.err, DSA_DEVERR_INDEX_OUT_OF_RANGE);
+        if (in[0]) set_err(p.err, DSA_DEVERR_INDEX_OUT_OF_RANGE);
         now = -1;
       }
-      more = k.next(p, w == 0);
-      if (more) load_page();
+#pragma unroll
+      for (int i = 0; i + 1 < kPagesAhead; ++i) {
+        page[i] = page[i + 1];
+        in[i] = in[i + 1];
+        more[i] = more[i + 1];
+      }
+      load_page(page[kPagesAhead - 1], in[kPagesAhead - 1], more[kPagesAhead - 1]);
       // rows without a summary keep what the stage holds: their lanes are not read
       const uint8_t* src[8];
       bool have[8];
@@ -272,14 +336,16 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
       for (int c = 0; c < kChunks; ++c) {
         if (!bar_wait(empty(stage), phase ^ 1, abort)) {
           give_up();
-          more = false;
+          more[0] = false;
           break;
         }
         const uint32_t to = base + kRingOff + stage * kChunkBytes;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (have[i]) cp16(to + dst[i & 1] + 1024 * (i >> 1), src[i] + 128 * c);
-        cp_arrive(full(stage));
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (issued >= kInFlight) hand_over();
+        ++issued;
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1;
@@ -287,6 +353,12 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    fence_proxy_async_smem();
+    __syncwarp();
+    for (int n = issued < kInFlight ? issued : kInFlight; n > 0 && lane == 0; --n) {
+      mbar_arrive(full(landed));
+      if (++landed == kStages) landed = 0;
+    }
   } else if (warp >= kWarpQuery0) {
     // ---- queries: a group's rows once per unit
     const int w = warp - kWarpQuery0;
@@ -300,21 +372,26 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
         give_up();
         break;
       }
-      const uint32_t to = base + (uint32_t)slot * kChunks * row_bytes_q;
+      // a row per instruction: lane l brings columns 8 l .. 8 l + 7. Rows past H stay as they are: what
+      // they give is not read.
       const uint32_t c = lane >> 3, piece = lane & 7;
-      for (int n = w; n < k.count * p.HP; n += kQueryWarps) {
-        const int i = n / p.HP, h = n - i * p.HP;
-        if (h >= p.H) continue;  // columns that are not read
-        cp16(to + c * row_bytes_q + n * 128 + ((piece ^ (n & 7)) << 4),
-             p.q + (int64_t)(k.t0 + i) * p.q_st + h * p.q_sh + 8 * lane);
+      const uint32_t to = base + (uint32_t)slot * kChunks * row_bytes_q + c * row_bytes_q;
+      for (int i = 0; i < k.count; ++i) {
+        const uint16_t* src = p.q + (int64_t)(k.t0 + i) * p.q_st + 8 * lane;
+        const int n0 = i * p.HP;
+#pragma unroll 8
+        for (int h = w; h < p.H; h += kQueryWarps)
+          cp16(to + (n0 + h) * 128 + ((piece ^ (h & 7)) << 4), src + h * p.q_sh);
       }
-      cp_arrive(q_full(slot));
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full(slot));
       if (++slot == p.slots) {
         slot = 0;
         phase ^= 1;
       }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == kWarpMma) {
     // ---- products
     const uint64_t d0 = sw128_desc(0, 16, 1024);
@@ -354,7 +431,6 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
           break;
         }
         if (lane == 0) {
-          fence_proxy_async_smem();
           const uint32_t a_lo = d_lo | ((base + kRingOff + stage * kChunkBytes) >> 4);
           const uint32_t b_lo = d_lo | ((q0 + c * row_bytes_q) >> 4);
 #pragma unroll
@@ -387,7 +463,6 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     const int buf = warp >> 2, quarter = warp & 3;
     uint32_t phase = 0;
     bool mine = buf != 0;
-    const uint64_t scale2 = pack2(p.scale, p.scale);
     const uint32_t acc0 = tmem + buf * kMaxN + ((uint32_t)(32 * quarter) << 16);
     while (k.next(p)) {
       mine = !mine;
@@ -395,61 +470,69 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
       const int row = k.m * kBM + 32 * quarter + lane;
       const int64_t r = k.run_req();
       int page = -1;
-      if (row < k.run_blocks()) page = p.bt[r * p.bt_st + row];
+      if (row < k.blocks) page = p.bt[r * p.bt_st + row];
       if (!bar_wait(acc_full(buf), phase, abort)) {
         give_up();
         break;
       }
       phase ^= 1;
       tc_fence_after();
+      // N heads at a time; the next products and weights come while these are summed up
       uint32_t col = acc0;
-      uint32_t x[16];
-      tmem_ld32_x16(col, x);
+      uint32_t x[N];
+      float4 wt[N / 4];
+      const float* w = WEIGHTS ? p.w + (int64_t)(k.t0 + k.a) * p.H : nullptr;
+      auto load_weights = [&](const float* from, int h0) {
+#pragma unroll
+        for (int j = 0; j < N / 4; ++j) {
+          const int h = h0 + 4 * j;
+          if (WHOLE)
+            wt[j] = *reinterpret_cast<const float4*>(from + h);
+          else
+            wt[j] = make_float4(h < p.H ? from[h] : 0.0f, h + 1 < p.H ? from[h + 1] : 0.0f, h + 2 < p.H ? from[h + 2] : 0.0f,
+                                h + 3 < p.H ? from[h + 3] : 0.0f);
+        }
+      };
+      if (WEIGHTS) load_weights(w, 0);
+      tmem_ld32(col, x);
       for (int i = k.a; i < k.b; ++i) {
-        const float* w = WEIGHTS ? p.w + (int64_t)(k.t0 + i) * p.H : nullptr;
-        uint64_t sum[2] = {0, 0};  // two chains of pairs of heads
-        for (int h0 = 0; h0 < p.HP; h0 += 16) {
-          float4 wt[4];
-          if (WEIGHTS && WHOLE) {
+        uint64_t sum[4] = {0, 0, 0, 0};  // chains of pairs of heads
+        for (int h0 = 0; h0 < p.HP; h0 += N) {
+          wait_ld(x);
+          float u[N];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) wt[j] = *reinterpret_cast<const float4*>(w + h0 + 4 * j);
-          } else if (WEIGHTS) {
+          for (int j = 0; j < N; ++j) u[j] = relu(__uint_as_float(x[j]));
+          uint64_t f[N / 2];
+          if (WEIGHTS) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int h = h0 + 4 * j;
-              wt[j] = make_float4(h < p.H ? w[h] : 0.0f, h + 1 < p.H ? w[h + 1] : 0.0f, h + 2 < p.H ? w[h + 2] : 0.0f,
-                                  h + 3 < p.H ? w[h + 3] : 0.0f);
+            for (int j = 0; j < N / 4; ++j) {
+              f[2 * j] = pack2(wt[j].x, wt[j].y);
+              f[2 * j + 1] = pack2(wt[j].z, wt[j].w);
             }
           }
-          wait_ld(x);
-          float u[16];
+          col += N;
+          const bool same = h0 + N < p.HP;
+          if (same || i + 1 < k.b) {
+            tmem_ld32(col, x);
+            if (WEIGHTS) load_weights(same ? w : w + p.H, same ? h0 + N : 0);
+          }
+          if (!WHOLE && h0 + N > p.H) {  // heads that are not there
 #pragma unroll
-          for (int j = 0; j < 16; ++j) u[j] = relu(__uint_as_float(x[j]));
-          // the next columns come while these are summed up
-          col += 16;
-          if (h0 + 16 < p.HP || i + 1 < k.b) tmem_ld32_x16(col, x);
-          if (!WHOLE && h0 + 16 > p.H) {  // heads that are not there
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
+            for (int j = 0; j < N; ++j)
               if (h0 + j >= p.H) u[j] = 0.0f;
           }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint64_t v = pack2(u[2 * j], u[2 * j + 1]);
-            if (WEIGHTS) {
-              const float4 f = wt[j >> 1];
-              v = mul2(v, scale2);
-              sum[j & 1] = fma2(v, j & 1 ? pack2(f.z, f.w) : pack2(f.x, f.y), sum[j & 1]);
-            } else {
-              sum[j & 1] = fma2(v, scale2, sum[j & 1]);
-            }
+          for (int j = 0; j < N / 2; ++j) {
+            const uint64_t v = pack2(u[2 * j], u[2 * j + 1]);
+            sum[j & 3] = WEIGHTS ? fma2(v, f[j], sum[j & 3]) : add2(v, sum[j & 3]);
           }
         }
-        const float2 s0 = unpack2(sum[0]), s1 = unpack2(sum[1]);
+        if (WEIGHTS) w += p.H;
+        const float2 s0 = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
         const int nb = __shfl_sync(0xffffffffu, k.nb, i);
         if (row < nb)
           p.out[(int64_t)(k.t0 + i) * p.out_st + row] =
-              page < 0 || page >= p.num_pages ? -INFINITY : (s0.x + s0.y) + (s1.x + s1.y);
+              page < 0 || page >= p.num_pages ? -INFINITY : (s0.x + s0.y) * p.scale;
         __syncwarp();
       }
       tc_fence_before();
@@ -472,8 +555,8 @@ dsa_status_t prepare(int device) {
   std::lock_guard<std::mutex> lock(mu);
   if (done[device]) return DSA_OK;
   cudaError_t e = cudaSuccess;
-  for (const void* f : {(const void*)scores_kernel<false, false>, (const void*)scores_kernel<false, true>,
-                        (const void*)scores_kernel<true, false>, (const void*)scores_kernel<true, true>})
+  for (const void* f : {(const void*)scores_kernel<false, false, 16>, (const void*)scores_kernel<true, false, 16>,
+                        (const void*)scores_kernel<false, true, 32>, (const void*)scores_kernel<true, true, 16>})
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return cuda_fail(e);
   done[device] = true;
@@ -542,9 +625,9 @@ extern "C" dsa_status_t dsa_block_scores(const void* q, int64_t q_stride_t, int6
   if ((st = scores::prepare(dev.device)) != DSA_OK) return st;
   const unsigned grid = (unsigned)(p.units < sms ? p.units : sms);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool whole = H % 16 == 0 && aligned(weights, 16);
-  auto kernel = weights ? (whole ? scores::scores_kernel<true, true> : scores::scores_kernel<true, false>)
-                        : (whole ? scores::scores_kernel<false, true> : scores::scores_kernel<false, false>);
+  const bool whole = H % (weights ? 16 : 32) == 0 && aligned(weights, 16);
+  auto kernel = weights ? (whole ? scores::scores_kernel<true, true, 16> : scores::scores_kernel<true, false, 16>)
+                        : (whole ? scores::scores_kernel<false, true, 32> : scores::scores_kernel<false, false, 16>);
   kernel<<<grid, scores::kThreads, scores::kSmemBytes, s>>>(p);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? DSA_OK : cuda_fail(e);

@@ -557,7 +557,8 @@ DSA_API dsa_status_t dsa_block_pool(const void* cache, dsa_cache_kind_t kind, in
  *   scores[t, b] = sum_h w[t,h] * max(0, sm_scale * dot(q[t,h,:], summary[block_table[r, b]]))
  * for the blocks b < ceil(lengths[t] / page_size) of the token's request r; other entries of scores
  * are left as they are. w = weights, or 1 when NULL. bf16 products (exact) accumulated in fp32 on
- * the tensor cores, the sum over heads in fp32. NaN passes through the maximum. A block whose page does not
+ * the tensor cores, the sum over heads in fp32 and scaled at its end (before the scale it must stay
+ * within the fp32 range). NaN passes through the maximum. A block whose page does not
  * exist scores -inf and sets DSA_DEVERR_INDEX_OUT_OF_RANGE, as do blocks at or past max_pages or
  * width (not scored) and a request that does not exist (its token is skipped).
  * Causality: a token's own block, and with several tokens of a request in one call the blocks after
