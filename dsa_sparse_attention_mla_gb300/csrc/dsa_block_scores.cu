@@ -10,9 +10,9 @@
 //
 // Long prefills are bound by the tensor core, decode by HBM (a summary is read once per request).
 //
-// One CTA per SM walks units (group of tokens, part of its block tiles). Warps 0-7 sum up and store, 8-11 load
+// One CTA per SM walks units (group of tokens, part of its block tiles). Warps 0-15 sum up and store, 16-19 load
 // summaries (cp.async, row by row: pages are scattered) in quarters of a tile's columns through a ring of
-// six, 12 issues the products, 13-15 load queries, up to four groups ahead where they are small. Two accumulators
+// six, 20 issues the products, 21-23 load queries, up to four groups ahead where they are small. Two accumulators
 // let the products of a tile run while the one before it is summed up. Every wait is bounded.
 #include <cuda_runtime.h>
 
@@ -35,7 +35,9 @@ constexpr int kBM = 128;     // blocks per tile (MMA M)
 constexpr int kMaxN = 256;   // query rows per group (MMA N)
 constexpr int kChunks = kD / 64;
 constexpr int kStages = 6;
-constexpr int kWarpLoad0 = 8, kLoadWarps = 4, kWarpMma = 12, kWarpQuery0 = 13, kQueryWarps = 3;
+constexpr int kSumWarps = 16;  // per accumulator two for each lane quarter, which take its tokens in turn
+constexpr int kWarpLoad0 = kSumWarps, kLoadWarps = 4, kWarpMma = kWarpLoad0 + kLoadWarps, kWarpQuery0 = kWarpMma + 1,
+              kQueryWarps = 3;
 constexpr int kWarps = kWarpQuery0 + kQueryWarps;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kPagesAhead = 3;
@@ -252,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(acc_full(s), 1);
-      mbar_init(acc_empty(s), 4);
+      mbar_init(acc_empty(s), kSumWarps / 2);
     }
     mbar_init(drained, 1);
     *abort = 0;
@@ -324,14 +326,9 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
       }
       load_page(page[kPagesAhead - 1], in[kPagesAhead - 1], more[kPagesAhead - 1]);
       // rows without a summary keep what the stage holds: their lanes are not read
-      const uint8_t* src[8];
-      bool have[8];
+      int row_page[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int pg = __shfl_sync(0xffffffffu, now, 4 * i + sub);
-        have[i] = pg >= 0;
-        src[i] = reinterpret_cast<const uint8_t*>(p.summary) + (int64_t)max(pg, 0) * (2 * kD) + 16 * piece;
-      }
+      for (int i = 0; i < 8; ++i) row_page[i] = __shfl_sync(0xffffffffu, now, 4 * i + sub);
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         if (!bar_wait(empty(stage), phase ^ 1, abort)) {
@@ -342,7 +339,8 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
         const uint32_t to = base + kRingOff + stage * kChunkBytes;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (have[i]) cp16(to + dst[i & 1] + 1024 * (i >> 1), src[i] + 128 * c);
+          if (row_page[i] >= 0)
+            cp16(to + dst[i & 1] + 1024 * (i >> 1), p.summary + (int64_t)row_page[i] * kD + 64 * c + 8 * piece);
         asm volatile("cp.async.commit_group;" ::: "memory");
         if (issued >= kInFlight) hand_over();
         ++issued;
@@ -387,6 +385,16 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full(slot));
+      // with one group in shared memory the next one's rows come in between two units: from L2 then
+      if (p.slots == 1 && k.u + (int)gridDim.x < p.units) {
+        const int n = (int)(p.T - k.ahead_t < p.G ? p.T - k.ahead_t : p.G) * p.H;
+        for (int i = w * 32 + lane; i < n; i += 32 * kQueryWarps)
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                           p.q + (int64_t)(k.ahead_t + i / p.H) * p.q_st + (int64_t)(i % p.H) * p.q_sh),
+                       "r"(2 * kD)
+                       : "memory");
+        __syncwarp();
+      }
       if (++slot == p.slots) {
         slot = 0;
         phase ^= 1;
@@ -460,12 +468,21 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     bar_wait(drained, 0, nullptr);
   } else {
     // ---- sums over heads: a block per lane, tiles in turn between the warps of either accumulator
-    const int buf = warp >> 2, quarter = warp & 3;
+    const int buf = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
     uint32_t phase = 0;
+    int last = -1;
     bool mine = buf != 0;
     const uint32_t acc0 = tmem + buf * kMaxN + ((uint32_t)(32 * quarter) << 16);
     while (k.next(p)) {
       mine = !mine;
+      if (WEIGHTS && k.u != last) {
+        // the next unit's weights into L1, a line per lane: met one by one in its first tile they took 8000 cycles
+        last = k.u;
+        const int64_t f = (int64_t)k.ahead_t * p.H + 32 * lane;
+        const int64_t end = (int64_t)min((int64_t)(k.ahead_t + p.G), p.T) * p.H;
+        float unused;
+        if (f < end) asm volatile("ld.global.f32 %0, [%1];" : "=f"(unused) : "l"(p.w + f));
+      }
       if (!mine) continue;
       const int row = k.m * kBM + 32 * quarter + lane;
       const int64_t r = k.run_req();
@@ -477,57 +494,43 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
       }
       phase ^= 1;
       tc_fence_after();
-      // N heads at a time; the next products and weights come while these are summed up
-      uint32_t col = acc0;
-      uint32_t x[N];
-      float4 wt[N / 4];
-      const float* w = WEIGHTS ? p.w + (int64_t)(k.t0 + k.a) * p.H : nullptr;
-      auto load_weights = [&](const float* from, int h0) {
-#pragma unroll
-        for (int j = 0; j < N / 4; ++j) {
-          const int h = h0 + 4 * j;
-          if (WHOLE)
-            wt[j] = *reinterpret_cast<const float4*>(from + h);
-          else
-            wt[j] = make_float4(h < p.H ? from[h] : 0.0f, h + 1 < p.H ? from[h + 1] : 0.0f, h + 2 < p.H ? from[h + 2] : 0.0f,
-                                h + 3 < p.H ? from[h + 3] : 0.0f);
-        }
-      };
-      if (WEIGHTS) load_weights(w, 0);
-      tmem_ld32(col, x);
-      for (int i = k.a; i < k.b; ++i) {
+      // N heads at a time; while one warp waits for its products and weights, the three others of its
+      // scheduler sum up theirs
+      for (int i = k.a + half; i < k.b; i += 2) {
+        const uint32_t col = acc0 + (i - k.a) * p.HP;
+        const float* w = WEIGHTS ? p.w + (int64_t)(k.t0 + i) * p.H : nullptr;
         uint64_t sum[4] = {0, 0, 0, 0};  // chains of pairs of heads
         for (int h0 = 0; h0 < p.HP; h0 += N) {
-          wait_ld(x);
-          float u[N];
-#pragma unroll
-          for (int j = 0; j < N; ++j) u[j] = relu(__uint_as_float(x[j]));
-          uint64_t f[N / 2];
+          uint32_t x[N];
+          tmem_ld32(col + h0, x);
+          float4 wt[N / 4];
           if (WEIGHTS) {
 #pragma unroll
             for (int j = 0; j < N / 4; ++j) {
-              f[2 * j] = pack2(wt[j].x, wt[j].y);
-              f[2 * j + 1] = pack2(wt[j].z, wt[j].w);
+              const int h = h0 + 4 * j;
+              if (WHOLE)
+                wt[j] = *reinterpret_cast<const float4*>(w + h);
+              else
+                wt[j] = make_float4(h < p.H ? w[h] : 0.0f, h + 1 < p.H ? w[h + 1] : 0.0f, h + 2 < p.H ? w[h + 2] : 0.0f,
+                                    h + 3 < p.H ? w[h + 3] : 0.0f);
             }
           }
-          col += N;
-          const bool same = h0 + N < p.HP;
-          if (same || i + 1 < k.b) {
-            tmem_ld32(col, x);
-            if (WEIGHTS) load_weights(same ? w : w + p.H, same ? h0 + N : 0);
-          }
-          if (!WHOLE && h0 + N > p.H) {  // heads that are not there
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-              if (h0 + j >= p.H) u[j] = 0.0f;
-          }
+          wait_ld(x);
 #pragma unroll
           for (int j = 0; j < N / 2; ++j) {
-            const uint64_t v = pack2(u[2 * j], u[2 * j + 1]);
-            sum[j & 3] = WEIGHTS ? fma2(v, f[j], sum[j & 3]) : add2(v, sum[j & 3]);
+            float u = relu(__uint_as_float(x[2 * j])), v = relu(__uint_as_float(x[2 * j + 1]));
+            if (!WHOLE) {  // heads that are not there
+              if (h0 + 2 * j >= p.H) u = 0.0f;
+              if (h0 + 2 * j + 1 >= p.H) v = 0.0f;
+            }
+            if (WEIGHTS) {
+              const float4 f = wt[j >> 1];
+              sum[j & 3] = fma2(pack2(u, v), j & 1 ? pack2(f.z, f.w) : pack2(f.x, f.y), sum[j & 3]);
+            } else {
+              sum[j & 3] = add2(pack2(u, v), sum[j & 3]);
+            }
           }
         }
-        if (WEIGHTS) w += p.H;
         const float2 s0 = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
         const int nb = __shfl_sync(0xffffffffu, k.nb, i);
         if (row < nb)
