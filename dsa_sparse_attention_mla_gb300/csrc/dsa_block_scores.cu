@@ -3,17 +3,18 @@
 //
 // Transposed products: S^T[block, head] = P Q^T with M = 128 blocks and, as N, the heads of up to
 // 256 / H neighbouring tokens (tcgen05 kind::f16, fp32 accumulators in tensor memory). A block is then a
-// lane of tensor memory, so the sum over heads stays within a thread: no shuffle, and what a
+// lane of tensor memory, so the sum over heads stays within four threads, and what a
 // block's row holds (NaN, infinities, nothing) reaches its own scores only. Tokens of one request share the tile
 // of summaries; where a group of tokens has several requests, each run of equal ones is a product of
 // its own over its part of the query rows.
 //
 // Long prefills are bound by the tensor core, decode by HBM (a summary is read once per request).
 //
-// One CTA per SM walks units (group of tokens, part of its block tiles). Warps 0-15 sum up and store, 16-19 load
+// One CTA per SM walks units (group of tokens, part of its block tiles). Warps 0-7 sum up and store, 8-11 load
 // summaries (cp.async, row by row: pages are scattered) in quarters of a tile's columns through a ring of
-// six, 20 issues the products, 21-23 load queries, up to four groups ahead where they are small. Two accumulators
+// five, 12 issues the products, 13 has queries copied (TMA), up to four groups ahead where they are small, 14 loads weights. Two accumulators
 // let the products of a tile run while the one before it is summed up. Every wait is bounded.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -35,19 +36,19 @@ constexpr int kBM = 128;     // blocks per tile (MMA M)
 constexpr int kMaxN = 256;   // query rows per group (MMA N)
 constexpr int kChunks = kD / 64;
 constexpr int kStages = 6;
-constexpr int kSumWarps = 16;  // per accumulator two for each lane quarter, which take its tokens in turn
-constexpr int kWarpLoad0 = kSumWarps, kLoadWarps = 4, kWarpMma = kWarpLoad0 + kLoadWarps, kWarpQuery0 = kWarpMma + 1,
-              kQueryWarps = 3;
-constexpr int kWarps = kWarpQuery0 + kQueryWarps;
+constexpr int kTurns = 1;  // warps per accumulator and lane quarter: they take its tokens in turn
+constexpr int kSumWarps = 8 * kTurns;
+constexpr int kWarpLoad0 = kSumWarps, kLoadWarps = 4, kWarpMma = kWarpLoad0 + kLoadWarps, kWarpQuery = kWarpMma + 1,
+              kQueryWarps = 2, kWarpWeights = kWarpQuery + kQueryWarps;
+constexpr int kWarps = kWarpWeights + 1;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kPagesAhead = 3;
-constexpr int kInFlight = 3;  // quarters of a tile on their way per loading warp, besides the newest
-constexpr int kMaxSlots = 4;  // query groups in shared memory
+constexpr int kMaxSlots = 4;  // query groups in shared memory, where they are small
 constexpr uint32_t kChunkBytes = kBM * 128;
 constexpr uint32_t kQueryBytes = kMaxN * kD * 2;
 constexpr uint32_t kRingOff = kQueryBytes;
-constexpr uint32_t kMiscOff = kRingOff + kStages * kChunkBytes;
-constexpr uint32_t kSmemBytes = kMiscOff + 256 + 1024;  // and room to align
+constexpr uint32_t kWeightOff = kRingOff + kStages * kChunkBytes;
+constexpr uint32_t kMiscOff = kWeightOff + kMaxN * 4;
+constexpr uint32_t kSmemBytes = kMiscOff + 512 + 1024;  // and room to align
 
 struct Params {
   const uint16_t* q;
@@ -55,6 +56,7 @@ struct Params {
   int64_t T;
   int H, HP;  // heads, rounded up to a multiple of 16
   int G;      // tokens per group
+  int box_tokens;  // tokens per query copy: the group's where its rows lie without gaps, else one
   int slots;  // groups of query rows that fit
   int parts;  // units per group
   int units;
@@ -94,38 +96,41 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
+// 32 lanes x N columns of tensor memory: a lane per thread, a column per register.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                 "=r"(r[15])
+               : "r"(taddr));
 }
-// Waits for tensor-memory loads; the registers pass through, so that no use of them moves before it.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                 "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+                 "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+                 "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+               : "r"(taddr));
+}
+// Waits for them; the registers pass through, so that no use of them moves before it.
 __device__ __forceinline__ void wait_ld(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15])
                :
                : "memory");
 }
 __device__ __forceinline__ void wait_ld(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
-                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
-                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
                :
                : "memory");
-}
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld32_x16(taddr, r); }
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
-      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
 }
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -225,9 +230,9 @@ struct Walk {
   __device__ __forceinline__ int64_t run_req() const { return __shfl_sync(0xffffffffu, req, a); }
 };
 
-// N: heads summed up per step, 16 or 32. WHOLE: they fill steps, and rows of weights are 16-byte aligned.
+// N: heads summed up per step, 16 or 32. WHOLE: they fill steps.
 template <bool WEIGHTS, bool WHOLE, int N>
-__global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p, const __grid_constant__ CUtensorMap tmap_q) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023) & ~1023u;
@@ -236,26 +241,35 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
   const uint32_t bars = base + kMiscOff;
   auto full = [&](int s) { return bars + 8 * s; };
   auto empty = [&](int s) { return bars + 8 * (kStages + s); };
-  auto q_full = [&](int s) { return bars + 8 * (2 * kStages + s); };
-  auto q_empty = [&](int s) { return bars + 8 * (2 * kStages + kMaxSlots + s); };
-  auto acc_full = [&](int s) { return bars + 8 * (2 * kStages + 2 * kMaxSlots + s); };
-  auto acc_empty = [&](int s) { return bars + 8 * (2 * kStages + 2 * kMaxSlots + 2 + s); };
-  const uint32_t drained = bars + 8 * (2 * kStages + 2 * kMaxSlots + 4);
-  volatile int* abort = reinterpret_cast<volatile int*>(smem + kMiscOff + 8 * (2 * kStages + 2 * kMaxSlots + 5));
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMiscOff + 8 * (2 * kStages + 2 * kMaxSlots + 5) + 4);
+  constexpr int kQBar = 2 * kStages, kAccBar = kQBar + 2 * kMaxSlots * kChunks, kWBar = kAccBar + 4;
+  auto q_full = [&](int s, int c) { return bars + 8 * (kQBar + kChunks * s + c); };
+  auto q_empty = [&](int s, int c) { return bars + 8 * (kQBar + kChunks * (kMaxSlots + s) + c); };
+  auto acc_full = [&](int s) { return bars + 8 * (kAccBar + s); };
+  auto acc_empty = [&](int s) { return bars + 8 * (kAccBar + 2 + s); };
+  const uint32_t w_full = bars + 8 * kWBar, w_empty = w_full + 8;
+  constexpr int kBars = kWBar + 3;
+  static_assert(8 * kBars + 8 <= 512, "barriers");
+  const uint32_t drained = bars + 8 * (kBars - 1);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + kMiscOff + 8 * kBars);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMiscOff + 8 * kBars + 4);
+  float* weights = reinterpret_cast<float*>(smem + kWeightOff);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(full(s), kLoadWarps);
+      mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
     for (int s = 0; s < kMaxSlots; ++s) {
-      mbar_init(q_full(s), kQueryWarps);
-      mbar_init(q_empty(s), 1);
+      for (int c = 0; c < kChunks; ++c) {
+        mbar_init(q_full(s, c), kQueryWarps);
+        mbar_init(q_empty(s, c), 1);
+      }
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(acc_full(s), 1);
       mbar_init(acc_empty(s), kSumWarps / 2);
     }
+    mbar_init(w_full, 1);
+    mbar_init(w_empty, kSumWarps);
     mbar_init(drained, 1);
     *abort = 0;
     fence_mbar_init();
@@ -277,101 +291,73 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
   k.start(p);
 
   if (warp >= kWarpLoad0 && warp < kWarpLoad0 + kLoadWarps) {
-    // ---- summaries: this warp's 32 rows of each tile, four rows of a column quarter per instruction
+    // ---- summaries: warp w brings column quarter w of every tile, four rows per instruction. (All four on each
+    // quarter, 32 rows each, took a hand-over per warp and quarter: 512 cycles, a quarter's products, did not do.)
     const int w = warp - kWarpLoad0;
     const uint32_t sub = lane >> 3, piece = lane & 7;
     uint32_t dst[2];  // rows 4 i + sub alternate between two places in the swizzle
 #pragma unroll
-    for (uint32_t i = 0; i < 2; ++i) dst[i] = (32 * w + 4 * i + sub) * 128 + ((piece ^ ((4 * i + sub) & 7)) << 4);
-    // the pages of the next tiles are loaded ahead, and looked at when their tile's turn has come
-    int page[kPagesAhead];
-    bool in[kPagesAhead], more[kPagesAhead];
-    bool any = true;
-    // A quarter is handed over when kInFlight later ones are on their way. The writer's fence makes it visible
-    // to the tensor core: one at the reader would hold up the products (720 cycles a quarter with it).
-    int issued = 0, landed = 0;
-    auto hand_over = [&]() {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kInFlight) : "memory");
+    for (uint32_t i = 0; i < 2; ++i) dst[i] = (4 * i + sub) * 128 + ((piece ^ (4 * i + sub)) << 4);
+    // the next tile's pages (rows 32 i + lane) are loaded ahead, and looked at when its turn has come
+    int page[4], blocks = 0;
+    bool more;
+    auto load_pages = [&]() {
+      more = k.next(p, w == 0);
+      if (!more) return;
+      const int32_t* from = p.bt + k.run_req() * p.bt_st + k.m * kBM + lane;
+      blocks = k.blocks - k.m * kBM;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) page[i] = 32 * i + lane < blocks ? from[32 * i] : -1;
+    };
+    int stage = w;
+    uint32_t phase = 0;
+    load_pages();
+    while (more) {
+      int now[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        now[i] = page[i];
+        if (now[i] >= p.num_pages) now[i] = -1;
+        if (w == 0 && now[i] < 0 && 32 * i + lane < blocks) set_err(p.err, DSA_DEVERR_INDEX_OUT_OF_RANGE);
+      }
+      load_pages();
+      if (!bar_wait(empty(stage), phase ^ 1, abort)) {
+        give_up();
+        break;
+      }
+      // rows without a summary keep what the stage holds: their lanes are not read
+      const uint32_t to = base + kRingOff + stage * kChunkBytes;
+      const uint16_t* from = p.summary + 64 * w + 8 * piece;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const int pg = __shfl_sync(0xffffffffu, now[i >> 3], 4 * (i & 7) + sub);
+        if (pg >= 0) cp16(to + dst[i & 1] + 1024 * (i >> 1), from + (int64_t)pg * kD);
+      }
+      // the writer's fence makes the copies visible to the tensor core: one at the reader would hold up the products
+      asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(full(landed));
-      if (++landed == kStages) landed = 0;
-    };
-    auto load_page = [&](int& pg, bool& is, bool& tile) {
-      any = any && k.next(p, w == 0);
-      tile = any;
-      pg = -1;
-      is = false;
-      if (!any) return;
-      const int64_t r = k.run_req();
-      const int row = k.m * kBM + 32 * w + lane;
-      is = row < k.blocks;
-      if (is) pg = p.bt[r * p.bt_st + row];
-    };
-    int stage = 0;
-    uint32_t phase = 0;
-#pragma unroll
-    for (int i = 0; i < kPagesAhead; ++i) load_page(page[i], in[i], more[i]);
-    while (more[0]) {
-      int now = page[0];
-      if (now < 0 || now >= p.num_pages) {
-        if (in[0]) set_err(p.err, DSA_DEVERR_INDEX_OUT_OF_RANGE);
-        now = -1;
-      }
-#pragma unroll
-      for (int i = 0; i + 1 < kPagesAhead; ++i) {
-        page[i] = page[i + 1];
-        in[i] = in[i + 1];
-        more[i] = more[i + 1];
-      }
-      load_page(page[kPagesAhead - 1], in[kPagesAhead - 1], more[kPagesAhead - 1]);
-      // rows without a summary keep what the stage holds: their lanes are not read
-      int row_page[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) row_page[i] = __shfl_sync(0xffffffffu, now, 4 * i + sub);
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        if (!bar_wait(empty(stage), phase ^ 1, abort)) {
-          give_up();
-          more[0] = false;
-          break;
-        }
-        const uint32_t to = base + kRingOff + stage * kChunkBytes;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (row_page[i] >= 0)
-            cp16(to + dst[i & 1] + 1024 * (i >> 1), p.summary + (int64_t)row_page[i] * kD + 64 * c + 8 * piece);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (issued >= kInFlight) hand_over();
-        ++issued;
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1;
-        }
+      if (lane == 0) mbar_arrive(full(stage));
+      stage += kChunks;
+      if (stage >= kStages) {
+        stage -= kStages;
+        phase ^= 1;
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    fence_proxy_async_smem();
-    __syncwarp();
-    for (int n = issued < kInFlight ? issued : kInFlight; n > 0 && lane == 0; --n) {
-      mbar_arrive(full(landed));
-      if (++landed == kStages) landed = 0;
-    }
-  } else if (warp >= kWarpQuery0) {
+  } else if (warp >= kWarpQuery && warp < kWarpQuery + kQueryWarps) {
     // ---- queries: a group's rows once per unit
-    const int w = warp - kWarpQuery0;
+    const int w = warp - kWarpQuery;
     int slot = 0;
     uint32_t phase = 0;
     int last = -1;
     while (k.next(p)) {
       if (k.u == last) continue;
       last = k.u;
-      if (!bar_wait(q_empty(slot), phase ^ 1, abort)) {
+      if (!bar_wait(q_empty(slot, 0), phase ^ 1, abort)) {
         give_up();
         break;
       }
-      // a row per instruction: lane l brings columns 8 l .. 8 l + 7. Rows past H stay as they are: what
-      // they give is not read.
       const uint32_t c = lane >> 3, piece = lane & 7;
       const uint32_t to = base + (uint32_t)slot * kChunks * row_bytes_q + c * row_bytes_q;
       for (int i = 0; i < k.count; ++i) {
@@ -384,8 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
       asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_full(slot));
-      // with one group in shared memory the next one's rows come in between two units: from L2 then
+      if (lane == 0) mbar_arrive(q_full(slot, 0));
       if (p.slots == 1 && k.u + (int)gridDim.x < p.units) {
         const int n = (int)(p.T - k.ahead_t < p.G ? p.T - k.ahead_t : p.G) * p.H;
         for (int i = w * 32 + lane; i < n; i += 32 * kQueryWarps)
@@ -400,6 +385,30 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
         phase ^= 1;
       }
     }
+  } else if (warp == kWarpWeights) {
+    // ---- weights: w * sm_scale, a group's once per unit, the next one's in registers by the time their place is free
+    uint32_t phase = 0;
+    int last = -1;
+    while (WEIGHTS && k.next(p)) {
+      if (k.u == last) continue;
+      last = k.u;
+      float v[kMaxN / 32];
+      const float* from = p.w + (int64_t)k.t0 * p.H;
+#pragma unroll
+      for (int z = 0; z < kMaxN / 32; ++z) {
+        const int n = 32 * z + lane, i = n / p.HP, h = n - i * p.HP;
+        v[z] = i < k.count && h < p.H ? from[i * p.H + h] : 0.0f;
+      }
+      if (!bar_wait(w_empty, phase ^ 1, abort)) {
+        give_up();
+        break;
+      }
+#pragma unroll
+      for (int z = 0; z < kMaxN / 32; ++z) weights[32 * z + lane] = v[z] * p.scale;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(w_full);
+      phase ^= 1;
+    }
   } else if (warp == kWarpMma) {
     // ---- products
     const uint64_t d0 = sw128_desc(0, 16, 1024);
@@ -407,30 +416,32 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     int stage = 0, slot = -1, buf = 0;
     uint32_t phase = 0, q_phase = 0, acc_phase = 0;
     int last = -1;
-    bool ok = true;
+    bool ok = true, fresh = false, released = true;
     while (ok && k.next(p)) {
       if (k.u != last) {
-        if (slot >= 0 && lane == 0) mma_commit(q_empty(slot));
+        if (!released && lane == 0)
+          mma_commit(q_empty(slot, 0));
         __syncwarp();
         if (++slot == p.slots) {
           slot = 0;
           q_phase ^= 1;
         }
         last = k.u;
-        if (!bar_wait(q_full(slot), q_phase, abort)) {
-          give_up();
-          break;
-        }
+        fresh = true;
+        released = false;
       }
+      // a unit's last tile gives up its query rows quarter by quarter
+      const bool ends = k.m + 1 >= k.m_end && !__any_sync(0xffffffffu, lane >= k.b && k.nb > 0);
+      released |= ends;
       if (!bar_wait(acc_empty(buf), acc_phase ^ 1, abort)) {
         give_up();
         break;
       }
       tc_fence_after();
-      const int n = (k.b - k.a) * p.HP;
-      const uint32_t idesc = idesc_bf16(kBM, n, 0, 0);
+      const uint32_t idesc = idesc_bf16(kBM, (k.b - k.a) * p.HP, 0, 0);
       const uint32_t acc = tmem + buf * kMaxN;
       const uint32_t q0 = base + (uint32_t)slot * kChunks * row_bytes_q + (uint32_t)(k.a * p.HP) * 128;
+      if (fresh && !bar_wait(q_full(slot, 0), q_phase, abort)) { give_up(); break; }
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         if (!bar_wait(full(stage), phase, abort)) {
@@ -449,6 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
               mma_bf16_lohi<1>(acc, a_lo + 2 * s, d_hi, b_lo + 2 * s, d_hi, idesc);
           }
           mma_commit(empty(stage));
+          if (ends && c == kChunks - 1) mma_commit(q_empty(slot, 0));
         }
         __syncwarp();
         if (++stage == kStages) {
@@ -457,6 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
         }
       }
       if (!ok) break;
+      fresh = false;
       if (lane == 0) mma_commit(acc_full(buf));
       __syncwarp();
       buf ^= 1;
@@ -468,23 +481,28 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     bar_wait(drained, 0, nullptr);
   } else {
     // ---- sums over heads: a block per lane, tiles in turn between the warps of either accumulator
-    const int buf = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
-    uint32_t phase = 0;
+    const int buf = warp / (4 * kTurns), first = (warp >> 2) % kTurns, quarter = warp & 3;
+    uint32_t phase = 0, w_phase = 0;
     int last = -1;
     bool mine = buf != 0;
+    const uint64_t scale2 = pack2(p.scale, p.scale);
     const uint32_t acc0 = tmem + buf * kMaxN + ((uint32_t)(32 * quarter) << 16);
     while (k.next(p)) {
       mine = !mine;
       if (WEIGHTS && k.u != last) {
-        // the next unit's weights into L1, a line per lane: met one by one in its first tile they took 8000 cycles
+        if (last >= 0) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(w_empty);
+        }
         last = k.u;
-        const int64_t f = (int64_t)k.ahead_t * p.H + 32 * lane;
-        const int64_t end = (int64_t)min((int64_t)(k.ahead_t + p.G), p.T) * p.H;
-        float unused;
-        if (f < end) asm volatile("ld.global.f32 %0, [%1];" : "=f"(unused) : "l"(p.w + f));
+        if (!bar_wait(w_full, w_phase, abort)) {
+          give_up();
+          break;
+        }
+        w_phase ^= 1;
       }
       if (!mine) continue;
-      const int row = k.m * kBM + 32 * quarter + lane;
+      const int row = k.m * kBM + 32 * quarter + lane;  // the thread's block
       const int64_t r = k.run_req();
       int page = -1;
       if (row < k.blocks) page = p.bt[r * p.bt_st + row];
@@ -494,48 +512,38 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
       }
       phase ^= 1;
       tc_fence_after();
-      // N heads at a time; while one warp waits for its products and weights, the three others of its
-      // scheduler sum up theirs
-      for (int i = k.a + half; i < k.b; i += 2) {
+      // N heads at a time; while one warp waits for its products, the others of its scheduler sum up theirs
+      for (int i = k.a + first; i < k.b; i += kTurns) {
         const uint32_t col = acc0 + (i - k.a) * p.HP;
-        const float* w = WEIGHTS ? p.w + (int64_t)(k.t0 + i) * p.H : nullptr;
+        const float4* w = reinterpret_cast<const float4*>(weights + i * p.HP);
         uint64_t sum[4] = {0, 0, 0, 0};  // chains of pairs of heads
         for (int h0 = 0; h0 < p.HP; h0 += N) {
           uint32_t x[N];
           tmem_ld32(col + h0, x);
-          float4 wt[N / 4];
-          if (WEIGHTS) {
-#pragma unroll
-            for (int j = 0; j < N / 4; ++j) {
-              const int h = h0 + 4 * j;
-              if (WHOLE)
-                wt[j] = *reinterpret_cast<const float4*>(w + h);
-              else
-                wt[j] = make_float4(h < p.H ? w[h] : 0.0f, h + 1 < p.H ? w[h + 1] : 0.0f, h + 2 < p.H ? w[h + 2] : 0.0f,
-                                    h + 3 < p.H ? w[h + 3] : 0.0f);
-            }
-          }
           wait_ld(x);
 #pragma unroll
-          for (int j = 0; j < N / 2; ++j) {
-            float u = relu(__uint_as_float(x[2 * j])), v = relu(__uint_as_float(x[2 * j + 1]));
-            if (!WHOLE) {  // heads that are not there
-              if (h0 + 2 * j >= p.H) u = 0.0f;
-              if (h0 + 2 * j + 1 >= p.H) v = 0.0f;
+          for (int j = 0; j < N / 4; ++j) {
+            float u[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              u[z] = relu(__uint_as_float(x[4 * j + z]));
+              if (!WHOLE && h0 + 4 * j + z >= p.H) u[z] = 0.0f;  // heads that are not there
             }
             if (WEIGHTS) {
-              const float4 f = wt[j >> 1];
-              sum[j & 3] = fma2(pack2(u, v), j & 1 ? pack2(f.z, f.w) : pack2(f.x, f.y), sum[j & 3]);
+              const float4 f = w[h0 / 4 + j];
+              sum[2 * (j & 1)] = fma2(pack2(u[0], u[1]), pack2(f.x, f.y), sum[2 * (j & 1)]);
+              sum[2 * (j & 1) + 1] = fma2(pack2(u[2], u[3]), pack2(f.z, f.w), sum[2 * (j & 1) + 1]);
             } else {
-              sum[j & 3] = add2(pack2(u, v), sum[j & 3]);
+              sum[2 * (j & 1)] = fma2(pack2(u[0], u[1]), scale2, sum[2 * (j & 1)]);
+              sum[2 * (j & 1) + 1] = fma2(pack2(u[2], u[3]), scale2, sum[2 * (j & 1) + 1]);
             }
           }
         }
-        const float2 s0 = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+        const float2 s0 = unpack2(sum[0]), s1 = unpack2(sum[1]), s2 = unpack2(sum[2]), s3 = unpack2(sum[3]);
+        const float total = ((s0.x + s0.y) + (s1.x + s1.y)) + ((s2.x + s2.y) + (s3.x + s3.y));
         const int nb = __shfl_sync(0xffffffffu, k.nb, i);
         if (row < nb)
-          p.out[(int64_t)(k.t0 + i) * p.out_st + row] =
-              page < 0 || page >= p.num_pages ? -INFINITY : (s0.x + s0.y) * p.scale;
+          p.out[(int64_t)(k.t0 + i) * p.out_st + row] = page < 0 || page >= p.num_pages ? -INFINITY : total;
         __syncwarp();
       }
       tc_fence_before();
@@ -559,11 +567,43 @@ dsa_status_t prepare(int device) {
   if (done[device]) return DSA_OK;
   cudaError_t e = cudaSuccess;
   for (const void* f : {(const void*)scores_kernel<false, false, 16>, (const void*)scores_kernel<true, false, 16>,
-                        (const void*)scores_kernel<false, true, 32>, (const void*)scores_kernel<true, true, 16>})
+                        (const void*)scores_kernel<false, true, 32>, (const void*)scores_kernel<true, true, 32>})
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return cuda_fail(e);
   done[device] = true;
   return DSA_OK;
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// 3-D map over the queries, box 64 columns x H heads x p.box_tokens, 128-byte swizzle: the K-major layout the
+// products read.
+dsa_status_t encode_queries(const Params& p, CUtensorMap* map) {
+  static std::mutex mu;
+  static EncodeFn fn = nullptr;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!fn) {
+      void* f = nullptr;
+      cudaDriverEntryPointQueryResult qres;
+      const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &qres);
+      if (e != cudaSuccess) return cuda_fail(e);
+      if (!f || qres != cudaDriverEntryPointSuccess) return cuda_fail(cudaErrorSymbolNotFound);
+      fn = reinterpret_cast<EncodeFn>(f);
+    }
+  }
+  // a dimension of one entry has no stride of its own
+  const int64_t sh = p.H > 1 ? p.q_sh : kD, st = p.T > 1 ? p.q_st : kD * (int64_t)p.H;
+  const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)p.H, (cuuint64_t)p.T};
+  const cuuint64_t strides[2] = {(cuuint64_t)sh * 2, (cuuint64_t)st * 2};
+  const cuuint32_t boxes[3] = {64, (cuuint32_t)p.H, (cuuint32_t)p.box_tokens};
+  const cuuint32_t es[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(p.q), dims, strides, boxes, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? DSA_OK : cuda_fail(cudaErrorInvalidValue);
 }
 
 }  // namespace scores
@@ -584,8 +624,10 @@ extern "C" dsa_status_t dsa_block_scores(const void* q, int64_t q_stride_t, int6
   if (T == 0) return DSA_OK;
   if (!q || !summary || !block_table || !lengths || !scores_out || num_requests < 1 || (!req_of_token && T > num_requests))
     return DSA_ERR_INVALID_ARGUMENT;
-  if (!aligned(q, 16) || q_stride_t < 0 || q_stride_h < 0 || q_stride_t % 8 || q_stride_h % 8 || !aligned(summary, 16))
+  if (!aligned(q, 16) || q_stride_t < 0 || q_stride_h < 0 || q_stride_t % 8 || q_stride_h % 8 || !aligned(summary, 16) ||
+      (T > 1 && q_stride_t < scores::kD) || (H > 1 && q_stride_h < scores::kD))
     return DSA_ERR_INVALID_ARGUMENT;
+  if (q_stride_t >= (int64_t)1 << 39 || q_stride_h >= (int64_t)1 << 39) return DSA_ERR_UNSUPPORTED;
   for (const void* x : {(const void*)block_table, (const void*)req_of_token, (const void*)lengths, (const void*)weights,
                         (const void*)scores_out, (const void*)error_word})
     if (!aligned(x, 4)) return DSA_ERR_INVALID_ARGUMENT;
@@ -625,13 +667,16 @@ extern "C" dsa_status_t dsa_block_scores(const void* q, int64_t q_stride_t, int6
   p.units = (int)(groups * p.parts);
   p.slots = (int)(scores::kQueryBytes / ((uint32_t)(p.G * p.HP) * scores::kD * 2));
   if (p.slots > scores::kMaxSlots) p.slots = scores::kMaxSlots;
+  p.box_tokens = p.HP == H ? p.G : 1;
   if ((st = scores::prepare(dev.device)) != DSA_OK) return st;
+  CUtensorMap map{};
+  if ((st = scores::encode_queries(p, &map)) != DSA_OK) return st;
   const unsigned grid = (unsigned)(p.units < sms ? p.units : sms);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool whole = H % (weights ? 16 : 32) == 0 && aligned(weights, 16);
-  auto kernel = weights ? (whole ? scores::scores_kernel<true, true, 16> : scores::scores_kernel<true, false, 16>)
+  const bool whole = H % 32 == 0;
+  auto kernel = weights ? (whole ? scores::scores_kernel<true, true, 32> : scores::scores_kernel<true, false, 16>)
                         : (whole ? scores::scores_kernel<false, true, 32> : scores::scores_kernel<false, false, 16>);
-  kernel<<<grid, scores::kThreads, scores::kSmemBytes, s>>>(p);
+  kernel<<<grid, scores::kThreads, scores::kSmemBytes, s>>>(p, map);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? DSA_OK : cuda_fail(e);
 }

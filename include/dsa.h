@@ -557,14 +557,15 @@ DSA_API dsa_status_t dsa_block_pool(const void* cache, dsa_cache_kind_t kind, in
  *   scores[t, b] = sum_h w[t,h] * max(0, sm_scale * dot(q[t,h,:], summary[block_table[r, b]]))
  * for the blocks b < ceil(lengths[t] / page_size) of the token's request r; other entries of scores
  * are left as they are. w = weights, or 1 when NULL. bf16 products (exact) accumulated in fp32 on
- * the tensor cores, the sum over heads in fp32 and scaled at its end (before the scale it must stay
- * within the fp32 range). NaN passes through the maximum. A block whose page does not
+ * the tensor cores, the sum over heads in fp32 (of w * sm_scale times the products' positive
+ * part). NaN passes through the maximum. A block whose page does not
  * exist scores -inf and sets DSA_DEVERR_INDEX_OUT_OF_RANGE, as do blocks at or past max_pages or
  * width (not scored) and a request that does not exist (its token is skipped).
  * Causality: a token's own block, and with several tokens of a request in one call the blocks after
  * it, hold rows the token must not see. Blocks after it are not scored (lengths[t]); its own block
  * has to be selected whatever its score (recent >= 1 below).
- *   q             bf16 [T, H, 256], 16-byte aligned, strides multiples of 8; H 1 .. 128, T <= 2^24
+ *   q             bf16 [T, H, 256], 16-byte aligned, strides multiples of 8, at least 256 (unused for a
+ *                 single token or head) and below 2^39; H 1 .. 128, T <= 2^24
  *   summary       bf16 [num_pages, 256], 16-byte aligned
  *   req_of_token  int32 [T], or NULL: token t belongs to request t. Neighbouring tokens of one
  *                 request share the reads of its summaries.
