@@ -3,18 +3,21 @@
 //
 // Transposed products: S^T[block, head] = P Q^T with M = 128 blocks and, as N, the heads of up to
 // 256 / H neighbouring tokens (tcgen05 kind::f16, fp32 accumulators in tensor memory). A block is then a
-// lane of tensor memory, so the sum over heads stays within four threads, and what a
-// block's row holds (NaN, infinities, nothing) reaches its own scores only. Tokens of one request share the tile
-// of summaries; where a group of tokens has several requests, each run of equal ones is a product of
-// its own over its part of the query rows.
-//
-// Long prefills are bound by the tensor core, decode by HBM (a summary is read once per request).
+// lane of tensor memory, so the sum over heads stays within a thread: no shuffle, and what a block's row
+// holds (NaN, infinities, nothing) reaches its own scores only. Tokens of one request share the tile of
+// summaries; where a group of tokens has several requests, each run of equal ones is a product of its
+// own over its part of the query rows.
 //
 // One CTA per SM walks units (group of tokens, part of its block tiles). Warps 0-7 sum up and store, 8-11 load
-// summaries (cp.async, row by row: pages are scattered) in quarters of a tile's columns through a ring of
-// five, 12 issues the products, 13 has queries copied (TMA), up to four groups ahead where they are small, 14 loads weights. Two accumulators
-// let the products of a tile run while the one before it is summed up. Every wait is bounded.
-#include <cuda.h>
+// summaries (cp.async, row by row: pages are scattered), a column quarter each, through a ring of six, 12
+// issues the products, 13-14 load queries, up to four groups ahead where they are small, 15 loads weights.
+// Two accumulators let the products of a tile run while the one before it is summed up. Every wait is bounded.
+//
+// 4096 tokens of 64 heads over 2016 to 2048 blocks, 275 GFLOP, take 169 us (1.63 PFLOP/s); the products alone
+// 125 (with parts of the work left out: 131 without queries and sums, 148 without sums, 152 without queries).
+// Reading the accumulators out takes tensor memory from the products, and a group's queries, which fill
+// the room that there is for them, come in between two groups. 256 requests of up to 512 blocks, 47 MB, take
+// 21 us: chains of loads (lengths, pages, rows) at the start and of hand-offs per tile, not HBM (7 us).
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -36,8 +39,7 @@ constexpr int kBM = 128;     // blocks per tile (MMA M)
 constexpr int kMaxN = 256;   // query rows per group (MMA N)
 constexpr int kChunks = kD / 64;
 constexpr int kStages = 6;
-constexpr int kTurns = 1;  // warps per accumulator and lane quarter: they take its tokens in turn
-constexpr int kSumWarps = 8 * kTurns;
+constexpr int kSumWarps = 8;  // one per accumulator and lane quarter
 constexpr int kWarpLoad0 = kSumWarps, kLoadWarps = 4, kWarpMma = kWarpLoad0 + kLoadWarps, kWarpQuery = kWarpMma + 1,
               kQueryWarps = 2, kWarpWeights = kWarpQuery + kQueryWarps;
 constexpr int kWarps = kWarpWeights + 1;
@@ -56,7 +58,6 @@ struct Params {
   int64_t T;
   int H, HP;  // heads, rounded up to a multiple of 16
   int G;      // tokens per group
-  int box_tokens;  // tokens per query copy: the group's where its rows lie without gaps, else one
   int slots;  // groups of query rows that fit
   int parts;  // units per group
   int units;
@@ -232,7 +233,7 @@ struct Walk {
 
 // N: heads summed up per step, 16 or 32. WHOLE: they fill steps.
 template <bool WEIGHTS, bool WHOLE, int N>
-__global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p, const __grid_constant__ CUtensorMap tmap_q) {
+__global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023) & ~1023u;
@@ -241,9 +242,9 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p, con
   const uint32_t bars = base + kMiscOff;
   auto full = [&](int s) { return bars + 8 * s; };
   auto empty = [&](int s) { return bars + 8 * (kStages + s); };
-  constexpr int kQBar = 2 * kStages, kAccBar = kQBar + 2 * kMaxSlots * kChunks, kWBar = kAccBar + 4;
-  auto q_full = [&](int s, int c) { return bars + 8 * (kQBar + kChunks * s + c); };
-  auto q_empty = [&](int s, int c) { return bars + 8 * (kQBar + kChunks * (kMaxSlots + s) + c); };
+  constexpr int kQBar = 2 * kStages, kAccBar = kQBar + 2 * kMaxSlots, kWBar = kAccBar + 4;
+  auto q_full = [&](int s) { return bars + 8 * (kQBar + s); };
+  auto q_empty = [&](int s) { return bars + 8 * (kQBar + kMaxSlots + s); };
   auto acc_full = [&](int s) { return bars + 8 * (kAccBar + s); };
   auto acc_empty = [&](int s) { return bars + 8 * (kAccBar + 2 + s); };
   const uint32_t w_full = bars + 8 * kWBar, w_empty = w_full + 8;
@@ -259,14 +260,12 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p, con
       mbar_init(empty(s), 1);
     }
     for (int s = 0; s < kMaxSlots; ++s) {
-      for (int c = 0; c < kChunks; ++c) {
-        mbar_init(q_full(s, c), kQueryWarps);
-        mbar_init(q_empty(s, c), 1);
-      }
+      mbar_init(q_full(s), kQueryWarps);
+      mbar_init(q_empty(s), 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(acc_full(s), 1);
-      mbar_init(acc_empty(s), kSumWarps / 2);
+      mbar_init(acc_empty(s), 4);
     }
     mbar_init(w_full, 1);
     mbar_init(w_empty, kSumWarps);
@@ -354,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p, con
     while (k.next(p)) {
       if (k.u == last) continue;
       last = k.u;
-      if (!bar_wait(q_empty(slot, 0), phase ^ 1, abort)) {
+      if (!bar_wait(q_empty(slot), phase ^ 1, abort)) {
         give_up();
         break;
       }
@@ -370,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p, con
       asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_full(slot, 0));
+      if (lane == 0) mbar_arrive(q_full(slot));
       if (p.slots == 1 && k.u + (int)gridDim.x < p.units) {
         const int n = (int)(p.T - k.ahead_t < p.G ? p.T - k.ahead_t : p.G) * p.H;
         for (int i = w * 32 + lane; i < n; i += 32 * kQueryWarps)
@@ -419,8 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p, con
     bool ok = true, fresh = false, released = true;
     while (ok && k.next(p)) {
       if (k.u != last) {
-        if (!released && lane == 0)
-          mma_commit(q_empty(slot, 0));
+        if (!released && lane == 0) mma_commit(q_empty(slot));
         __syncwarp();
         if (++slot == p.slots) {
           slot = 0;
@@ -430,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p, con
         fresh = true;
         released = false;
       }
-      // a unit's last tile gives up its query rows quarter by quarter
+      // after a unit's last tile its query rows may go; else the next unit finds out
       const bool ends = k.m + 1 >= k.m_end && !__any_sync(0xffffffffu, lane >= k.b && k.nb > 0);
       released |= ends;
       if (!bar_wait(acc_empty(buf), acc_phase ^ 1, abort)) {
@@ -441,7 +439,10 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p, con
       const uint32_t idesc = idesc_bf16(kBM, (k.b - k.a) * p.HP, 0, 0);
       const uint32_t acc = tmem + buf * kMaxN;
       const uint32_t q0 = base + (uint32_t)slot * kChunks * row_bytes_q + (uint32_t)(k.a * p.HP) * 128;
-      if (fresh && !bar_wait(q_full(slot, 0), q_phase, abort)) { give_up(); break; }
+      if (fresh && !bar_wait(q_full(slot), q_phase, abort)) {
+        give_up();
+        break;
+      }
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         if (!bar_wait(full(stage), phase, abort)) {
@@ -460,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p, con
               mma_bf16_lohi<1>(acc, a_lo + 2 * s, d_hi, b_lo + 2 * s, d_hi, idesc);
           }
           mma_commit(empty(stage));
-          if (ends && c == kChunks - 1) mma_commit(q_empty(slot, 0));
+          if (ends && c == kChunks - 1) mma_commit(q_empty(slot));
         }
         __syncwarp();
         if (++stage == kStages) {
@@ -481,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p, con
     bar_wait(drained, 0, nullptr);
   } else {
     // ---- sums over heads: a block per lane, tiles in turn between the warps of either accumulator
-    const int buf = warp / (4 * kTurns), first = (warp >> 2) % kTurns, quarter = warp & 3;
+    const int buf = warp >> 2, quarter = warp & 3;
     uint32_t phase = 0, w_phase = 0;
     int last = -1;
     bool mine = buf != 0;
@@ -513,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p, con
       phase ^= 1;
       tc_fence_after();
       // N heads at a time; while one warp waits for its products, the others of its scheduler sum up theirs
-      for (int i = k.a + first; i < k.b; i += kTurns) {
+      for (int i = k.a; i < k.b; ++i) {
         const uint32_t col = acc0 + (i - k.a) * p.HP;
         const float4* w = reinterpret_cast<const float4*>(weights + i * p.HP);
         uint64_t sum[4] = {0, 0, 0, 0};  // chains of pairs of heads
@@ -574,38 +575,6 @@ dsa_status_t prepare(int device) {
   return DSA_OK;
 }
 
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// 3-D map over the queries, box 64 columns x H heads x p.box_tokens, 128-byte swizzle: the K-major layout the
-// products read.
-dsa_status_t encode_queries(const Params& p, CUtensorMap* map) {
-  static std::mutex mu;
-  static EncodeFn fn = nullptr;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (!fn) {
-      void* f = nullptr;
-      cudaDriverEntryPointQueryResult qres;
-      const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &qres);
-      if (e != cudaSuccess) return cuda_fail(e);
-      if (!f || qres != cudaDriverEntryPointSuccess) return cuda_fail(cudaErrorSymbolNotFound);
-      fn = reinterpret_cast<EncodeFn>(f);
-    }
-  }
-  // a dimension of one entry has no stride of its own
-  const int64_t sh = p.H > 1 ? p.q_sh : kD, st = p.T > 1 ? p.q_st : kD * (int64_t)p.H;
-  const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)p.H, (cuuint64_t)p.T};
-  const cuuint64_t strides[2] = {(cuuint64_t)sh * 2, (cuuint64_t)st * 2};
-  const cuuint32_t boxes[3] = {64, (cuuint32_t)p.H, (cuuint32_t)p.box_tokens};
-  const cuuint32_t es[3] = {1, 1, 1};
-  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(p.q), dims, strides, boxes, es,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? DSA_OK : cuda_fail(cudaErrorInvalidValue);
-}
-
 }  // namespace scores
 }  // namespace dsa
 
@@ -624,10 +593,8 @@ extern "C" dsa_status_t dsa_block_scores(const void* q, int64_t q_stride_t, int6
   if (T == 0) return DSA_OK;
   if (!q || !summary || !block_table || !lengths || !scores_out || num_requests < 1 || (!req_of_token && T > num_requests))
     return DSA_ERR_INVALID_ARGUMENT;
-  if (!aligned(q, 16) || q_stride_t < 0 || q_stride_h < 0 || q_stride_t % 8 || q_stride_h % 8 || !aligned(summary, 16) ||
-      (T > 1 && q_stride_t < scores::kD) || (H > 1 && q_stride_h < scores::kD))
+  if (!aligned(q, 16) || q_stride_t < 0 || q_stride_h < 0 || q_stride_t % 8 || q_stride_h % 8 || !aligned(summary, 16))
     return DSA_ERR_INVALID_ARGUMENT;
-  if (q_stride_t >= (int64_t)1 << 39 || q_stride_h >= (int64_t)1 << 39) return DSA_ERR_UNSUPPORTED;
   for (const void* x : {(const void*)block_table, (const void*)req_of_token, (const void*)lengths, (const void*)weights,
                         (const void*)scores_out, (const void*)error_word})
     if (!aligned(x, 4)) return DSA_ERR_INVALID_ARGUMENT;
@@ -656,27 +623,28 @@ extern "C" dsa_status_t dsa_block_scores(const void* q, int64_t q_stride_t, int6
   p.most = (int)(width < max_pages ? width : max_pages);
   const int64_t tiles = p.most > 0 ? (p.most + scores::kBM - 1) / scores::kBM : 1;
   const int sms = dev.sm_count;
-  // As many tokens in a group as an MMA takes, while there are units enough for every SM; tokens that do not
-  // name their requests have one each.
+  // As many tokens in a group as an MMA takes, while their tiles are three times the SMs: neighbours of one
+  // request share its summaries (1024 tokens of 4 requests x 1024 blocks, 32 heads: 27 us with 8 in a group, 67
+  // with 1), but a unit is as long as all its tokens' tiles (8 requests x 2048 blocks: 10.5 us with 1 and 14.4
+  // with 4). Tokens that do not name their requests have one each. Then units of a part of a group's tiles, one
+  // and a half times the SMs: each brings the queries anew (256 requests of up to 512 blocks: 21 us with 1.5
+  // times, 30 with 4).
   p.HP = (H + 15) / 16 * 16;
   p.G = req_of_token ? scores::kMaxN / p.HP : 1;
-  while (p.G > 1 && (T + p.G - 1) / p.G * tiles < 4 * sms) p.G >>= 1;
+  while (p.G > 1 && (T + p.G - 1) / p.G * tiles < 3 * sms) p.G >>= 1;
   const int64_t groups = (T + p.G - 1) / p.G;
-  int64_t parts = (4 * sms + groups - 1) / groups;
+  int64_t parts = (3 * sms / 2 + groups - 1) / groups;
   p.parts = (int)(parts < tiles ? parts : tiles);
   p.units = (int)(groups * p.parts);
   p.slots = (int)(scores::kQueryBytes / ((uint32_t)(p.G * p.HP) * scores::kD * 2));
   if (p.slots > scores::kMaxSlots) p.slots = scores::kMaxSlots;
-  p.box_tokens = p.HP == H ? p.G : 1;
   if ((st = scores::prepare(dev.device)) != DSA_OK) return st;
-  CUtensorMap map{};
-  if ((st = scores::encode_queries(p, &map)) != DSA_OK) return st;
   const unsigned grid = (unsigned)(p.units < sms ? p.units : sms);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool whole = H % 32 == 0;
   auto kernel = weights ? (whole ? scores::scores_kernel<true, true, 32> : scores::scores_kernel<true, false, 16>)
                         : (whole ? scores::scores_kernel<false, true, 32> : scores::scores_kernel<false, false, 16>);
-  kernel<<<grid, scores::kThreads, scores::kSmemBytes, s>>>(p, map);
+  kernel<<<grid, scores::kThreads, scores::kSmemBytes, s>>>(p);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? DSA_OK : cuda_fail(e);
 }

@@ -564,8 +564,7 @@ DSA_API dsa_status_t dsa_block_pool(const void* cache, dsa_cache_kind_t kind, in
  * Causality: a token's own block, and with several tokens of a request in one call the blocks after
  * it, hold rows the token must not see. Blocks after it are not scored (lengths[t]); its own block
  * has to be selected whatever its score (recent >= 1 below).
- *   q             bf16 [T, H, 256], 16-byte aligned, strides multiples of 8, at least 256 (unused for a
- *                 single token or head) and below 2^39; H 1 .. 128, T <= 2^24
+ *   q             bf16 [T, H, 256], 16-byte aligned, strides multiples of 8; H 1 .. 128, T <= 2^24
  *   summary       bf16 [num_pages, 256], 16-byte aligned
  *   req_of_token  int32 [T], or NULL: token t belongs to request t. Neighbouring tokens of one
  *                 request share the reads of its summaries.
