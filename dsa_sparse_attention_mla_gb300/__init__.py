@@ -574,6 +574,8 @@ def _ptr_on(t, name: str, dtype, index: int):
     """data_ptr() of a tensor that must be on the device, or None."""
     if t is None:
         return None
+    if t.dtype is dtype and t.get_device() == index:
+        return t.data_ptr()
     i = _cuda_index(t, name, dtype)
     if i != index:
         raise ValueError(f"{name} is on cuda:{i}, not on cuda:{index}: every tensor must be on one device")
@@ -584,6 +586,8 @@ def _vector(t, name: str, n: int, dtype, index: int):
     """data_ptr() of a contiguous tensor of n entries, or None."""
     if t is None:
         return None
+    if t.dtype is dtype and t.shape == (n,) and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
     p = _ptr_on(t, name, dtype, index)
     if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of {n} entries")
@@ -865,17 +869,15 @@ def dsa_batch_plan(lengths, new_tokens, held, block_table, free_pages, num_free,
         raise ValueError("new_tokens, held and num_free are required")
     len_ptr, held_ptr = _vector(lengths, "lengths", R, i32, index), _vector(held, "held", R, i32, index)
     free_n = _vector(num_free, "num_free", 1, i32, index)
-    # the outputs that the caller does not bring lie in two buffers
-    if cu_tokens is None or req_of_token is None or positions is None or token_lengths is None:
-        buf = torch.empty(3 * T + R + 1, dtype=i32, device=index)
-        if req_of_token is None:
-            req_of_token = buf[:T]
-        if positions is None:
-            positions = buf[T:2 * T]
-        if token_lengths is None:
-            token_lengths = buf[2 * T:3 * T]
-        if cu_tokens is None:
-            cu_tokens = buf[3 * T:]
+    # (between launches a tensor costs 2 us of host time, a view as much again: one tensor each)
+    if req_of_token is None:
+        req_of_token = torch.empty(T, dtype=i32, device=index)
+    if positions is None:
+        positions = torch.empty(T, dtype=i32, device=index)
+    if token_lengths is None:
+        token_lengths = torch.empty(T, dtype=i32, device=index)
+    if cu_tokens is None:
+        cu_tokens = torch.empty(R + 1, dtype=i32, device=index)
     if out_loc is None:
         out_loc = torch.empty(T, dtype=torch.int64, device=index)
     a = DsaPlanArgs(
@@ -912,47 +914,47 @@ def dsa_qk_norm_rope(q=None, k=None, positions=None, cos_sin=None, eps: float = 
         raise ValueError("q or k is required")
     index = _cuda_index(lead, "q" if q is not None else "k", bf16)
     T, D = lead.shape[0], d_nope + d_rope
-    a = DsaQkArgs()
-    a.T, a.d_nope, a.d_rope, a.eps, a.interleaved = T, d_nope, d_rope, eps, bool(interleaved)
+    _c_int("q_norm", q_norm)
+    _c_int("k_norm", k_norm)
+    H, q_ptr, q_st, q_sh, o_ptr, o_st, o_sh = 0, None, 0, 0, None, 0, 0
     if q is not None:
         st = q.stride()
-        if q.dim() != 3 or q.shape[2] != D or st[2] != 1:
+        shape = q.shape
+        if len(shape) != 3 or shape[2] != D or st[2] != 1:
             raise ValueError("q must be [T, H, d_nope + d_rope], contiguous along its last dimension")
-        H = q.shape[1]
-        a.H, a.q, a.q_stride_t, a.q_stride_h = H, q.data_ptr(), st[0] if T > 1 else 0, st[1] if H > 1 else 0
+        H = shape[1]
+        q_ptr, q_st, q_sh = q.data_ptr(), st[0] if T > 1 else 0, st[1] if H > 1 else 0
         if q_out is None:
             q_out = torch.empty((T, H, D), dtype=bf16, device=index)
-        a.q_out = _ptr_on(q_out, "q_out", bf16, index)
+        o_ptr = _ptr_on(q_out, "q_out", bf16, index)
         st = q_out.stride()
-        if q_out.shape != q.shape or st[2] != 1:
+        if q_out.shape != shape or st[2] != 1:
             raise ValueError("q_out must have q's shape, contiguous along its last dimension")
-        a.q_out_stride_t, a.q_out_stride_h = st[0] if T > 1 else 0, st[1] if H > 1 else 0
-        a.q_norm = _c_int("q_norm", q_norm)
-        a.q_weight = _vector(q_weight, "q_weight", q_norm, bf16, index)
+        o_st, o_sh = st[0] if T > 1 else 0, st[1] if H > 1 else 0
     elif q_out is not None:
         raise ValueError("q_out without q")
+    k_ptr, k_st, c_ptr, slots = None, 0, None, 0
     if k is not None:
         if cache is None or kind is None:
             raise ValueError("k needs cache and kind")
-        k_index = _cuda_index(k, "k", bf16)
-        if k_index != index:
-            raise ValueError(f"k is on cuda:{k_index}, not on cuda:{index}: every tensor must be on one device")
-        a.k, a.k_stride_t, _, width = _rows(k, "k", bf16, index, T)
+        k_ptr, k_st, _, width = _rows(k, "k", bf16, index, T)
         if width != D:
             raise ValueError("k must be [T, d_nope + d_rope]")
-        if T <= 1:
-            a.k_stride_t = 0
-        c_index, a.cache, a.num_slots = _cache_rows(cache, kind, D if kind == CACHE_BF16 else dsa_packed_row_bytes(d_nope, d_rope))
+        # (the packed row of geometries that the library does not know is refused there)
+        row = D if kind == CACHE_BF16 else D + d_nope // 32 + d_rope
+        c_index, c_ptr, slots = _cache_rows(cache, kind, row)
         if c_index != index:
             raise ValueError(f"cache is on cuda:{c_index}, not on cuda:{index}: every tensor must be on one device")
-        a.kind = kind
-        a.k_norm = _c_int("k_norm", k_norm)
-        a.k_weight = _vector(k_weight, "k_weight", k_norm, bf16, index)
-        a.out_loc = _vector(out_loc, "out_loc", T, torch.int64, index)
-    a.positions = _vector(positions, "positions", T, i32, index)
+    cs_ptr, cs_st, cs_n = None, 0, 0
     if cos_sin is not None:
-        a.cos_sin, a.cs_stride, a.num_positions, _ = _rows(cos_sin, "cos_sin", torch.float32, index, None, d_rope)
-    a.error_word = _ptr_on(error_word, "error_word", i32, index)
+        cs_ptr, cs_st, cs_n, _ = _rows(cos_sin, "cos_sin", torch.float32, index, None, d_rope)
+    a = DsaQkArgs(
+        T, d_nope, d_rope, q_ptr, q_st, q_sh, H, o_ptr, o_st, o_sh, q_norm,
+        None if q is None else _vector(q_weight, "q_weight", q_norm, bf16, index), k_ptr, k_st if T > 1 else 0, k_norm,
+        None if k is None else _vector(k_weight, "k_weight", k_norm, bf16, index), c_ptr, 0 if kind is None else kind, slots,
+        None if k is None else _vector(out_loc, "out_loc", T, torch.int64, index), eps,
+        _vector(positions, "positions", T, i32, index), cs_ptr, cs_st, cs_n, bool(interleaved),
+        _ptr_on(error_word, "error_word", i32, index))
     with _on_device(index):
         _check((_LIB or load_library()).dsa_qk_norm_rope(ctypes.byref(a), torch.cuda.current_stream(index).cuda_stream),
                "dsa_qk_norm_rope")
@@ -1030,11 +1032,12 @@ def dsa_block_select(scores, block_table, lengths, K: int, *, page_size: int, re
     index = _cuda_index(scores, "scores", torch.float32)
     s_ptr, s_stride, T, width = _rows(scores, "scores", torch.float32, index, None, 1)
     bt_ptr, bt_stride, R, pages = _rows(block_table, "block_table", i32, index, None, 1 if T else 0)
-    if blocks is None and table is None and K > 0:
-        buf = torch.empty((2, T, K), dtype=i32, device=index)
-        blocks, table = buf[0], buf[1]
-    elif blocks is None or table is None:
-        raise ValueError("blocks and table come together, and K is positive")
+    if K < 1:
+        raise ValueError("K must be positive")
+    if blocks is None:
+        blocks = torch.empty((T, K), dtype=i32, device=index)
+    if table is None:
+        table = torch.empty((T, K), dtype=i32, device=index)
     if lengths_out is None:
         lengths_out = torch.empty(T, dtype=i32, device=index)
     b_ptr, b_stride, _, b_width = _rows(blocks, "blocks", i32, index, T, K)

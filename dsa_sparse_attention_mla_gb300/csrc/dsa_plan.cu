@@ -6,8 +6,10 @@
 // page moved finds its request by a binary search in the sums of its chunk of requests, so a step
 // with one long prompt and one with many short ones cost the same per page.
 //
-// One block does the requests: the sums need all of them, and a decode step has a few hundred. What
-// bounds it is the chain of dependent loads (state, table, stack, table again), not bytes.
+// The sums need every request, and a decode step has a few hundred: a cluster of blocks does the step,
+// each block all the sums (for itself, so that no value has to be passed on) and its share of the pages
+// and tokens. Between the parts lies a barrier of the cluster. What bounds it is the chain of dependent
+// loads (state, table, stack, table again), not bytes.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -18,8 +20,10 @@ namespace dsa {
 namespace plan {
 
 constexpr int kThreads = 1024;     // requests of a chunk, one per thread
+constexpr int kCluster = 8;
+constexpr int kAhead = 4;          // pages a thread moves at a time, their loads in flight together
 constexpr int kFillThreads = 256;
-constexpr int64_t kMaxFill = 4096;  // tokens that the plan's own block writes
+constexpr int64_t kMaxFill = 16384;  // tokens that the plan's own blocks write
 
 struct Params {
   int64_t R;
@@ -83,27 +87,30 @@ __device__ __forceinline__ int64_t first_above(const V* a, int64_t n, int64_t i)
   return lo;
 }
 
-// The entries of token slot i. cu and the requests' new lengths were written by this block, or by an
-// earlier kernel.
-__device__ __forceinline__ void fill(const Params& p, int64_t i, int64_t total) {
-  if (i >= total) {
-    p.req[i] = 0;
-    p.pos[i] = -1;
-    p.tlen[i] = 0;
-    p.loc[i] = -1;
-    return;
-  }
-  const int64_t r = first_above(p.cu + 1, p.R, i);
-  const int pos = p.len_out[r] - p.cu[r + 1] + (int)i;
-  const int page = p.bt[r * p.bt_st + pos / p.page];
+// The entries of token slot i of request r, whose new length is `len` and whose tokens end before slot
+// `next`. The table's entries may have been written by another block of the cluster: past L1.
+__device__ __forceinline__ void fill(const Params& p, int64_t i, int64_t r, int next, int len) {
+  const int pos = len - next + (int)i;
+  const int page = __ldcg(p.bt + r * p.bt_st + pos / p.page);
   p.req[i] = (int)r;
   p.pos[i] = pos;
   p.tlen[i] = pos + 1;
   p.loc[i] = page < 0 ? -1 : (int64_t)page * p.page + pos % p.page;
 }
+__device__ __forceinline__ void fill_padding(const Params& p, int64_t i) {
+  p.req[i] = 0;
+  p.pos[i] = -1;
+  p.tlen[i] = 0;
+  p.loc[i] = -1;
+}
+
+// All blocks of the cluster: what each wrote before is seen by the others after.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 struct Want {
-  int64_t after, need;  // the request's length and pages if it is granted
+  uint32_t after, need;  // the request's length and pages if it is granted (below 2^32 both)
   int l, h;
   bool fits;
   long long back, take, tokens;
@@ -114,94 +121,159 @@ __device__ __forceinline__ Want want_of(const Params& p, int64_t r) {
   w.l = max(p.lengths[r], 0);
   w.h = min(max(p.held[r], 0), p.max_pages);
   const int n = p.add[r];
-  w.after = n < 0 ? 0 : (int64_t)w.l + n;
-  w.need = (w.after + p.page - 1) / p.page;
-  w.fits = w.need <= p.max_pages && w.after <= INT_MAX;
-  w.back = w.need < w.h ? w.h - w.need : 0;
-  w.take = w.fits && w.need > w.h ? w.need - w.h : 0;
+  w.after = n < 0 ? 0 : (uint32_t)w.l + (uint32_t)n;
+  w.need = w.after ? (w.after - 1) / (uint32_t)p.page + 1 : 0;
+  w.fits = w.need <= (uint32_t)p.max_pages && w.after <= (uint32_t)INT_MAX;
+  w.back = w.need < (uint32_t)w.h ? w.h - (int)w.need : 0;
+  w.take = w.fits && w.need > (uint32_t)w.h ? (int)w.need - w.h : 0;
   w.tokens = w.fits && n > 0 ? n : 0;
   return w;
 }
 
-__global__ void __launch_bounds__(kThreads) plan_kernel(const Params p, const int fill_here) {
+// Calls move(k, j, i) for the pages i of a chunk that this block is to move: request k of the chunk, its
+// j-th page among them. `sums`: the chunk's inclusive sums.
+template <class Load, class Store>
+__device__ __forceinline__ void each_page(const long long* sums, int64_t total, int rank, int blocks, Load load, Store store) {
+  const int64_t step = (int64_t)blocks * kThreads;
+  for (int64_t i0 = (int64_t)rank * kThreads + threadIdx.x; i0 < total; i0 += kAhead * step) {
+    int k[kAhead], v[kAhead];
+    int64_t j[kAhead];
+#pragma unroll
+    for (int z = 0; z < kAhead; ++z) {
+      const int64_t i = i0 + z * step;
+      if (i >= total) break;
+      k[z] = (int)first_above(sums, kThreads, i);
+      j[z] = i - (k[z] ? sums[k[z] - 1] : 0);
+      v[z] = load(k[z], j[z], i);
+    }
+#pragma unroll
+    for (int z = 0; z < kAhead; ++z) {
+      const int64_t i = i0 + z * step;
+      if (i >= total) break;
+      store(k[z], j[z], i, v[z]);
+    }
+  }
+}
+
+// `blocks` of the cluster (1: no cluster). More than one only where one chunk holds all requests: then no
+// block reads the requests' state after the first barrier, and it may change in place.
+__global__ void __launch_bounds__(kThreads) plan_kernel(const Params p, const int blocks, const int fill_here) {
   __shared__ longlong2 s_warp[32];
   __shared__ long long s_sum[kThreads];  // inclusive page sums of the chunk
   __shared__ int s_first[kThreads];      // first table entry that a request gives back or takes
-  const int tid = threadIdx.x;
+  __shared__ int s_cu[kThreads + 1], s_len[kThreads];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, rank = blocks > 1 ? (int)blockIdx.x : 0;
   const int64_t nf = min((int64_t)max(*p.num_free, 0), p.cap);
+  const bool one = p.R <= kThreads;
+  auto sync = [&]() {
+    if (blocks > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+  };
   int bad = 0;
   longlong2 total;
+  Want w{};
   // pages given back go onto the stack
   int64_t have = nf;
   for (int64_t r0 = 0; r0 < p.R; r0 += kThreads) {
     const int64_t r = r0 + tid;
-    Want w{};
+    w = Want{};
     if (r < p.R) w = want_of(p, r);
     const longlong2 sum = block_scan(make_longlong2(w.back, 0), s_warp, &total);
     s_sum[tid] = sum.x;
     s_first[tid] = (int)w.need;
     __syncthreads();
-    for (int64_t i = tid; i < total.x; i += kThreads) {
-      const int64_t k = first_above(s_sum, kThreads, i);
-      const int64_t j = s_first[k] + i - (k ? s_sum[k - 1] : 0);
-      if (have + i < p.cap)
-        p.stack[have + i] = p.bt[(r0 + k) * p.bt_st + j];
-      else
-        bad = DSA_DEVERR_SLOT_OUT_OF_RANGE;
-    }
+    each_page(
+        s_sum, total.x, rank, blocks,
+        [&](int k, int64_t j, int64_t) { return __ldcg(p.bt + (r0 + k) * p.bt_st + s_first[k] + j); },
+        [&](int, int64_t, int64_t i, int page) {
+          if (have + i < p.cap)
+            p.stack[have + i] = page;
+          else
+            bad = DSA_DEVERR_SLOT_OUT_OF_RANGE;
+        });
     have += total.x;
     __syncthreads();
   }
   if (have > p.cap) have = p.cap;
+  sync();
   // what is wanted, what of it is granted, and the pages taken from the top
   longlong2 wanted = make_longlong2(0, 0), granted = make_longlong2(0, 0);
   for (int64_t r0 = 0; r0 < p.R; r0 += kThreads) {
     const int64_t r = r0 + tid;
-    Want w{};
-    if (r < p.R) w = want_of(p, r);
+    if (!one) {
+      w = Want{};
+      if (r < p.R) w = want_of(p, r);
+    }
     longlong2 sum = block_scan(make_longlong2(w.take, w.tokens), s_warp, &total);
     const bool no_page = w.take > 0 && wanted.x + sum.x > have;
     const bool no_room = w.tokens > 0 && wanted.y + sum.y > p.T;
     wanted.x += total.x;
     wanted.y += total.y;
     const bool ok = w.fits && !no_page && !no_room;
-    if (r < p.R) {
+    // (a chunk that is granted whole has its sums already)
+    const bool whole = __syncthreads_and(r >= p.R || ok || (w.take == 0 && w.tokens == 0));
+    if (r < p.R && rank == 0) {
       if (!w.fits) bad |= DSA_DEVERR_INDEX_OUT_OF_RANGE;
       if (no_page) bad |= DSA_DEVERR_OUT_OF_PAGES;
       if (no_room) bad |= DSA_DEVERR_TOKEN_CAPACITY;
     }
     if (!ok) w.take = w.tokens = 0;
-    sum = block_scan(make_longlong2(w.take, w.tokens), s_warp, &total);
+    if (!whole) sum = block_scan(make_longlong2(w.take, w.tokens), s_warp, &total);
     s_sum[tid] = sum.x;
     s_first[tid] = w.h;
     if (r < p.R) {
-      p.len_out[r] = ok ? (int)w.after : w.l;
-      p.held_out[r] = w.take > 0 || w.need < w.h ? (int)w.need : w.h;
-      p.cu[r + 1] = (int)(granted.y + sum.y);
+      const int len = ok ? (int)w.after : w.l, cu = (int)(granted.y + sum.y);
+      s_cu[tid + 1] = cu;
+      s_len[tid] = len;
+      if (rank == 0) {
+        p.len_out[r] = len;
+        p.held_out[r] = w.take > 0 || w.need < (uint32_t)w.h ? (int)w.need : w.h;
+        p.cu[r + 1] = cu;
+      }
     }
     __syncthreads();
-    for (int64_t i = tid; i < total.x; i += kThreads) {
-      const int64_t k = first_above(s_sum, kThreads, i);
-      const int64_t j = s_first[k] + i - (k ? s_sum[k - 1] : 0);
-      p.bt[(r0 + k) * p.bt_st + j] = p.stack[have - 1 - granted.x - i];
-    }
+    each_page(
+        s_sum, total.x, rank, blocks,
+        [&](int, int64_t, int64_t i) { return __ldcg(p.stack + have - 1 - granted.x - i); },
+        [&](int k, int64_t j, int64_t, int page) { p.bt[(r0 + k) * p.bt_st + s_first[k] + j] = page; });
     granted.x += total.x;
     granted.y += total.y;
     __syncthreads();
   }
-  if (tid == 0) {
+  if (tid == 0 && rank == 0) {
     p.cu[0] = 0;
     *p.num_free_out = (int)(have - granted.x);
   }
   if (bad && p.err) atomicOr(p.err, bad);
   if (!fill_here) return;
-  __syncthreads();
-  for (int64_t i = tid; i < p.T; i += kThreads) fill(p, i, granted.y);
+  sync();
+  const int64_t step = (int64_t)blocks * kThreads;
+  for (int64_t i = (int64_t)rank * kThreads + tid; i < p.T; i += step) {
+    if (i >= granted.y) {
+      fill_padding(p, i);
+    } else if (one) {
+      const int r = (int)first_above(s_cu + 1, p.R, i);
+      fill(p, i, r, s_cu[r + 1], s_len[r]);
+    } else {
+      const int64_t r = first_above(p.cu + 1, p.R, i);
+      fill(p, i, r, p.cu[r + 1], p.len_out[r]);
+    }
+  }
 }
 
 __global__ void __launch_bounds__(kFillThreads) fill_kernel(const Params p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t i = (int64_t)blockIdx.x * kFillThreads + threadIdx.x;
-  if (i < p.T) fill(p, i, p.cu[p.R]);
+  if (i >= p.T) return;
+  if (i >= p.cu[p.R]) {
+    fill_padding(p, i);
+    return;
+  }
+  const int64_t r = first_above(p.cu + 1, p.R, i);
+  fill(p, i, r, p.cu[r + 1], p.len_out[r]);
 }
 
 }  // namespace plan
@@ -253,12 +325,27 @@ extern "C" dsa_status_t dsa_batch_plan(const dsa_plan_args_t* a, void* stream) {
   p.err = a->error_word;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool here = p.T <= plan::kMaxFill;
-  plan::plan_kernel<<<1, plan::kThreads, 0, s>>>(p, here);
-  cudaError_t e = cudaGetLastError();
+  // One block where it can have little to move, and where the requests take several chunks (see the kernel).
+  const bool little = p.T <= plan::kThreads && (double)p.R * p.max_pages <= plan::kAhead * plan::kThreads;
+  const int blocks = p.R <= plan::kThreads && !little ? plan::kCluster : 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(plan::kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)blocks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, plan::plan_kernel, (const plan::Params)p, blocks, (int)here);
   if (e != cudaSuccess) return cuda_fail(e);
   if (!here) {
-    plan::fill_kernel<<<(unsigned)((p.T + plan::kFillThreads - 1) / plan::kFillThreads), plan::kFillThreads, 0, s>>>(p);
-    e = cudaGetLastError();
+    cfg.gridDim = dim3((unsigned)((p.T + plan::kFillThreads - 1) / plan::kFillThreads));
+    cfg.blockDim = dim3(plan::kFillThreads);
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    e = cudaLaunchKernelEx(&cfg, plan::fill_kernel, (const plan::Params)p);
   }
   return e == cudaSuccess ? DSA_OK : cuda_fail(e);
 }

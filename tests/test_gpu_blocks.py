@@ -418,7 +418,7 @@ def test_binding_refusals(gpu):
     with pytest.raises(dsa.DsaError):
         dsa.dsa_block_scores(**{**scores, "sm_scale": -1.0})
     choice = dict(scores=s, block_table=table, lengths=one, K=2, page_size=16)
-    for name, bad in [("scores", s.double()), ("K", 0), ("K", 1 << 32), ("blocks", table), ("lengths_out", i32([1, 1], gpu)),
+    for name, bad in [("scores", s.double()), ("K", 0), ("K", 1 << 32), ("blocks", table[:, :1]), ("lengths_out", i32([1, 1], gpu)),
                       ("lengths", one.long())]:
         with pytest.raises(ValueError):
             dsa.dsa_block_select(**{**choice, name: bad})
