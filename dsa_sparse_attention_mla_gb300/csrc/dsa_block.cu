@@ -7,10 +7,9 @@
 // are joined in a fixed order. Bytes bound it.
 //
 // Select: the m-th largest key of a row decides, found bit by bit: scores map to unsigned keys of the
-// same order, blocks that are always chosen to the largest one, and 32 counts of the keys at or above
-// a trial value build it from the top bit down. The keys stay in registers, each thread holding
-// neighbours, so that the chosen blocks come out in ascending order from one prefix sum. Rows of up
-// to 512 blocks take one warp, longer ones 256 threads; what bounds it is the chain of counts.
+// same order, blocks that are always chosen to the largest one, and up to 32 counts of the keys at or
+// above a trial value build it from the top bit down. The keys stay in registers; ballots and their
+// prefix sums put the chosen blocks in ascending order. What bounds it is the chain of counts.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -171,55 +170,40 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   return u == 0xFFFFFFFFu ? 0xFFFFFFFEu : u;
 }
 
-// Sums over the group of W warps that share a row (a whole block, or one warp).
+// Sum over the group of W warps that share a row (a whole block, or one warp).
 template <int W>
-struct Group {
-  static __device__ __forceinline__ int sum(int v, int (&s)[2][32], int& turn) {
-    v = __reduce_add_sync(0xffffffffu, v);
-    if (W == 1) return v;
-    const int lane = threadIdx.x & 31;
-    if (lane == 0) s[turn][threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = lane < W ? s[turn][lane] : 0;
-    turn ^= 1;  // the next sum writes elsewhere: one barrier per sum
-    return __reduce_add_sync(0xffffffffu, v);
-  }
-  // Exclusive prefix of v over the group's threads.
-  static __device__ __forceinline__ int before(int v, int (&s)[2][32], int& turn) {
-    const int lane = threadIdx.x & 31;
-    int x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (W == 1) return x - v;
-    const int warp = threadIdx.x >> 5;
-    if (lane == 31) s[turn][warp] = x;
-    __syncthreads();
-    const int w = lane < warp && lane < W ? s[turn][lane] : 0;
-    turn ^= 1;
-    return x - v + __reduce_add_sync(0xffffffffu, w);
-  }
-};
+__device__ __forceinline__ int group_sum(int v, int (&s)[2][32], int& turn) {
+  v = __reduce_add_sync(0xffffffffu, v);
+  if (W == 1) return v;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) s[turn][threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = lane < W ? s[turn][lane] : 0;
+  turn ^= 1;  // the next sum writes elsewhere: one barrier per sum
+  return __reduce_add_sync(0xffffffffu, v);
+}
 
-// W warps per row, N neighbouring keys per thread and chunk of 32 W N blocks. A row of one chunk keeps
-// its keys in registers (ONE); a longer one reads them anew for every count.
+// W warps per row, N keys per thread and chunk of 32 W N blocks, thread g of the group holding blocks g, g + 32 W,
+// ...: loads are whole lines, and a ballot is 32 neighbouring blocks. A row of one chunk (ONE) keeps its keys in
+// registers and lists the chosen blocks in shared memory; a longer one reads them anew for every count.
 template <int W, int N, bool ONE>
 __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) select_kernel(const SelectParams p) {
+  constexpr int GT = 32 * W, CHUNK = GT * N, ROWS = W == 1 ? 4 : 1;
   __shared__ int s[2][32];
   __shared__ int s_last;
+  __shared__ int s_list[ONE ? ROWS : 1][ONE ? CHUNK : 1];
+  __shared__ uint32_t s_above[W == 1 ? 1 : N * W], s_equal[W == 1 ? 1 : N * W];    // bits of 32 blocks each
+  __shared__ int s_above0[W == 1 ? 1 : N * W], s_equal0[W == 1 ? 1 : N * W];       // and how many before them
   int turn = 0;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = W == 1 ? 0 : threadIdx.x >> 5;
   const int g = W == 1 ? lane : (int)threadIdx.x;  // thread of the group
-  constexpr int GT = 32 * W;
-  constexpr int CHUNK = GT * N;
-  const int64_t t = W == 1 ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
+  const int64_t t = W == 1 ? (int64_t)blockIdx.x * ROWS + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
   if (t >= p.T) return;  // whole warps (W == 1), or nobody
+  int* list = s_list[ONE && W == 1 ? threadIdx.x >> 5 : 0];
   const int len = max(p.lengths[t], 0);
   const int64_t r = p.req ? p.req[t] : t;
-  int64_t nb = ((int64_t)len + p.page - 1) / p.page;
-  const int64_t most = p.width < p.max_pages ? p.width : p.max_pages;
+  int nb = len > 0 ? (len - 1) / p.page + 1 : 0;
+  const int most = (int)(p.width < p.max_pages ? p.width : p.max_pages);
   bool bad = nb > most;
   const bool cut = bad;
   if (bad) nb = most;
@@ -228,7 +212,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) select_kernel(const Sel
     nb = 0;
   }
   if (bad && g == 0 && p.err) atomicOr(p.err, DSA_DEVERR_INDEX_OUT_OF_RANGE);
-  const int n = (int)nb;
+  const int n = nb;
   const int m = n < p.K ? n : p.K;
   const float* row = p.scores + t * p.score_st;
   const int32_t* pages = p.bt + (n ? r * p.bt_st : 0);
@@ -237,96 +221,152 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) select_kernel(const Sel
   auto load = [&](int c0) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int b = c0 + g * N + i;
+      const int b = c0 + i * GT + g;
       key[i] = 0;  // below every score
       if (b < n) key[i] = b < end_sink || b >= from_recent ? 0xFFFFFFFFu : key_of(row[b]);
     }
   };
   auto count = [&](uint32_t at_least) {
     int c = 0;
-    if (ONE) {
+    for (int c0 = 0; c0 < n; c0 += CHUNK) {
+      if (!ONE) load(c0);
 #pragma unroll
       for (int i = 0; i < N; ++i) c += key[i] >= at_least;
-    } else {
-      for (int c0 = 0; c0 < n; c0 += CHUNK) {
-        load(c0);
-#pragma unroll
-        for (int i = 0; i < N; ++i) c += key[i] >= at_least;
-      }
+      if (ONE) break;
     }
-    return Group<W>::sum(c, s, turn);
+    return group_sum<W>(c, s, turn);
   };
   if (ONE) load(0);
-  // the largest value that at least m keys reach: the m-th largest key
+  // The largest value that at least m keys reach is the m-th largest key, found from the top bit down; a value
+  // that exactly m keys reach ends the search. Chosen: the keys above `u`, and the first `ties` of those equal.
   uint32_t u = 0;
-  int ties = 0;  // how many of the keys equal to u are chosen
+  int ties = 0;
   if (m < n) {
-    for (int bit = 31; bit >= 0; --bit) {
+    int c = 0;
+    for (int bit = 31; bit >= 0 && c != m; --bit) {
       const uint32_t trial = u | (1u << bit);
-      if (count(trial) >= m) u = trial;
+      const int reach = count(trial);
+      if (reach >= m) {
+        u = trial;
+        c = reach;
+      }
     }
-    ties = m - (u == 0xFFFFFFFFu ? 0 : count(u + 1));
-  } else {
-    u = 1;  // every key of a block: scores map to no 0
-    ties = n;
+    if (c == m)
+      --u;  // all that reach it
+    else
+      ties = m - (u == 0xFFFFFFFFu ? 0 : count(u + 1));
   }
+  const bool all = m == n;
   if (W > 1) {
     if (threadIdx.x == 0) s_last = 0;
     __syncthreads();
   }
   bool last = false;
-  int above0 = 0, equal0 = 0;  // before the chunk
+  auto choose = [&](int b, int at) {
+    if (ONE) {
+      list[at] = b;
+    } else {
+      if (p.blocks) p.blocks[t * p.blocks_st + at] = b;
+      p.table[t * p.table_st + at] = pages[b];
+    }
+    last |= b == n - 1;
+  };
+  const uint32_t lower = (1u << lane) - 1;
+  int above0 = 0, equal0 = 0;  // before this chunk (W == 1: before these 32)
   for (int c0 = 0; c0 < n; c0 += CHUNK) {
     if (!ONE) load(c0);
-    int above = 0, equal = 0;
-    const bool all = m == n;
+    uint32_t above[N], equal[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const bool in = c0 + g * N + i < n;
-      above += in && (all || key[i] > u);
-      equal += in && !all && key[i] == u;
+      const bool in = c0 + i * GT + g < n;
+      above[i] = __ballot_sync(0xffffffffu, in && (all || key[i] > u));
+      equal[i] = __ballot_sync(0xffffffffu, in && !all && key[i] == u);
     }
-    int a = above0, e = equal0;
-    if (ONE) {
-      // a chunk's counts fit 16 bits each (at most 8192 blocks)
-      const int both = Group<W>::before(above | (equal << 16), s, turn);
-      a += both & 0xFFFF;
-      e += both >> 16;
-    } else {
-      a += Group<W>::before(above, s, turn);
-      e += Group<W>::before(equal, s, turn);
-      above0 += Group<W>::sum(above, s, turn);
-      equal0 += Group<W>::sum(equal, s, turn);
-    }
+    if (W > 1) {
+      if (lane == 0) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int b = c0 + g * N + i;
-      if (b >= n) continue;
-      const bool up = all || key[i] > u, tie = !all && key[i] == u;
-      if (up || (tie && e < ties)) {
-        const int at = a + (e < ties ? e : ties);
-        if (p.blocks) p.blocks[t * p.blocks_st + at] = b;
-        p.table[t * p.table_st + at] = pages[b];
-        last |= b == n - 1;
+        for (int i = 0; i < N; ++i) {
+          s_above[i * W + warp] = above[i];
+          s_equal[i * W + warp] = equal[i];
+        }
       }
-      a += up;
-      e += tie;
+      __syncthreads();
+      if (warp == 0) {  // N words per lane, W of which are neighbours in order
+        constexpr int PER = (N * W + 31) / 32;
+        int a = 0, e = 0;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+          const int word = lane * PER + k;
+          if (word < N * W) {
+            a += __popc(s_above[word]);
+            e += __popc(s_equal[word]);
+          }
+        }
+        int as = a, es = e;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, as, o), y = __shfl_up_sync(0xffffffffu, es, o);
+          if (lane >= o) {
+            as += x;
+            es += y;
+          }
+        }
+        as -= a;
+        es -= e;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+          const int word = lane * PER + k;
+          if (word < N * W) {
+            s_above0[word] = above0 + as;
+            s_equal0[word] = equal0 + es;
+            as += __popc(s_above[word]);
+            es += __popc(s_equal[word]);
+          }
+        }
+      }
+      __syncthreads();
     }
-  }
-  for (int i = m + g; i < p.K; i += GT) {
-    if (p.blocks) p.blocks[t * p.blocks_st + i] = -1;
-    p.table[t * p.table_st + i] = -1;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int b = c0 + i * GT + g;
+      int a, e;
+      if (W == 1) {
+        a = above0;
+        e = equal0;
+        above0 += __popc(above[i]);
+        equal0 += __popc(equal[i]);
+      } else {
+        a = s_above0[i * W + warp];
+        e = s_equal0[i * W + warp];
+      }
+      a += __popc(above[i] & lower);
+      e += __popc(equal[i] & lower);
+      const bool up = (above[i] >> lane) & 1, tie = (equal[i] >> lane) & 1;
+      if (up || (tie && e < ties)) choose(b, a + (e < ties ? e : ties));
+    }
+    if (W > 1 && !ONE) {
+      above0 = s_above0[N * W - 1] + __popc(s_above[N * W - 1]);
+      equal0 = s_equal0[N * W - 1] + __popc(s_equal[N * W - 1]);
+      __syncthreads();
+    }
+    if (ONE) break;
   }
   if (W == 1) {
     last = __any_sync(0xffffffffu, last);
+    __syncwarp();
   } else {
     if (last) s_last = 1;
     __syncthreads();
     last = s_last != 0;
   }
+  for (int i = (ONE ? 0 : m) + g; i < p.K; i += GT) {
+    const int b = ONE && i < m ? list[i] : -1;
+    if (p.blocks) p.blocks[t * p.blocks_st + i] = b;
+    p.table[t * p.table_st + i] = b < 0 ? -1 : pages[b];
+  }
   if (g == 0) {
     int64_t out = (int64_t)m * p.page;
-    if (last && !cut) out -= nb * p.page - len;
+    if (last && !cut) out -= (int64_t)nb * p.page - len;
     p.len_out[t] = (int)(out < INT_MAX ? out : INT_MAX);
   }
 }
@@ -432,14 +472,22 @@ extern "C" dsa_status_t dsa_block_select(const float* scores, int64_t score_stri
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t most = width < max_pages ? width : max_pages;
   cudaError_t e;
-  if (most <= 128)
-    e = block::launch_select<1, 4, true>(p, s);
-  else if (most <= 512)
-    e = block::launch_select<1, 16, true>(p, s);
-  else if (most <= 2048)
-    e = block::launch_select<8, 8, true>(p, s);
-  else if (most <= 8192)
-    e = block::launch_select<16, 16, true>(p, s);
+  // a warp per row up to 544 blocks, then as few warps as hold the keys (tables are a little wider than a
+  // round number of blocks as a rule)
+  if (most <= 160)
+    e = block::launch_select<1, 5, true>(p, s);
+  else if (most <= 288)
+    e = block::launch_select<1, 9, true>(p, s);
+  else if (most <= 544)
+    e = block::launch_select<1, 17, true>(p, s);
+  else if (most <= 1152)
+    e = block::launch_select<4, 9, true>(p, s);
+  else if (most <= 2304)
+    e = block::launch_select<8, 9, true>(p, s);
+  else if (most <= 4608)
+    e = block::launch_select<16, 9, true>(p, s);
+  else if (most <= 8704)
+    e = block::launch_select<16, 17, true>(p, s);
   else
     e = block::launch_select<32, 8, false>(p, s);
   return e == cudaSuccess ? DSA_OK : cuda_fail(e);
