@@ -20,7 +20,8 @@
 namespace dsa {
 namespace qk {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kBlocks = 16;  // per SM: every row in flight counts (8192 x 64 rows of 1152 bytes: 200 us with 16, 215 with 12)
 constexpr int kWarps = kThreads / 32;
 
 struct Params {
@@ -66,7 +67,7 @@ __device__ __forceinline__ uint4 narrow(const float* x) {
 }
 
 template <int KIND, int D_NOPE, int D_ROPE>
-__global__ void __launch_bounds__(kThreads) qk_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, kBlocks) qk_kernel(const Params p) {
   constexpr int NV = D_NOPE / 256;  // 16-byte pieces per lane
   constexpr int D = D_NOPE + D_ROPE;
   constexpr int TILES = D_NOPE / 128;
@@ -96,33 +97,44 @@ __global__ void __launch_bounds__(kThreads) qk_kernel(const Params p) {
     }
   }
   const uint16_t* src = is_q ? p.q + t * p.q_st + h * p.q_sh : p.k + t * p.k_st;
-  float x[NV][8], a = 0.0f, b = 0.0f;
+  // every load of the row at once; it stays in bf16 until its pieces are worked on, one after another
+  uint4 raw[NV];
+  uint32_t raw_tail = 0;
+  float2 cos = make_float2(1.0f, 1.0f), sin = make_float2(0.0f, 0.0f);  // of the lane's two RoPE columns
 #pragma unroll
-  for (int v = 0; v < NV; ++v) widen(*reinterpret_cast<const uint4*>(src + 256 * v + 8 * lane), x[v]);
+  for (int v = 0; v < NV; ++v) raw[v] = *reinterpret_cast<const uint4*>(src + 256 * v + 8 * lane);
   if (D_ROPE > 0) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(src + D_NOPE + 2 * lane);
-    a = lo_bf16(w);
-    b = hi_bf16(w);
+    raw_tail = *reinterpret_cast<const uint32_t*>(src + D_NOPE + 2 * lane);
+    if (p.cs) {
+      const float* cs = p.cs + at * p.cs_st;
+      if (p.inter) {
+        cos.x = cs[lane];
+        sin.x = cs[D_ROPE / 2 + lane];
+      } else {
+        const int i = 2 * (lane & 15);
+        cos = make_float2(cs[i], cs[i + 1]);
+        sin = make_float2(cs[D_ROPE / 2 + i], cs[D_ROPE / 2 + i + 1]);
+      }
+    }
   }
+  float a = lo_bf16(raw_tail), b = hi_bf16(raw_tail);
   const int n = is_q ? p.q_norm : p.k_norm;
+  const uint16_t* wt = nullptr;
+  float r = 1.0f;
   if (n > 0) {
     float ss = 0.0f;
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+    for (int v = 0; v < NV; ++v) {
+      float x[8];
+      widen(raw[v], x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(x[v][i], x[v][i], ss);
+      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+    }
     if (D_ROPE > 0 && n == D) ss = fmaf(a, a, fmaf(b, b, ss));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float r = rsqrtf(ss / (float)n + p.eps);
-    const uint16_t* wt = is_q ? p.q_w : p.k_w;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      float w[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
-      if (wt) widen(*reinterpret_cast<const uint4*>(wt + 256 * v + 8 * lane), w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[v][i] *= r * w[i];
-    }
+    r = rsqrtf(ss / (float)n + p.eps);
+    wt = is_q ? p.q_w : p.k_w;
     if (D_ROPE > 0 && n == D) {
       a *= r;
       b *= r;
@@ -134,35 +146,42 @@ __global__ void __launch_bounds__(kThreads) qk_kernel(const Params p) {
     }
   }
   if (D_ROPE > 0 && p.cs) {
-    const float* cs = p.cs + at * p.cs_st;
     if (p.inter) {
-      const float c = cs[lane], s = cs[D_ROPE / 2 + lane];
-      const float u = a * c - b * s;
-      b = b * c + a * s;
+      const float u = a * cos.x - b * sin.x;
+      b = b * cos.x + a * sin.x;
       a = u;
     } else {
       // lanes 0-15 hold the first halves of the pairs, lanes 16-31 the second ones
       const float pa = __shfl_xor_sync(0xffffffffu, a, 16), pb = __shfl_xor_sync(0xffffffffu, b, 16);
-      const int i = 2 * (lane & 15);
       const float sign = lane < 16 ? -1.0f : 1.0f;
-      a = a * cs[i] + sign * (pa * cs[D_ROPE / 2 + i]);
-      b = b * cs[i + 1] + sign * (pb * cs[D_ROPE / 2 + i + 1]);
+      a = a * cos.x + sign * (pa * sin.x);
+      b = b * cos.y + sign * (pb * sin.y);
     }
   }
-  if (is_q || KIND == DSA_CACHE_BF16) {
-    uint16_t* dst = is_q ? p.qo + t * p.qo_st + h * p.qo_sh : reinterpret_cast<uint16_t*>(p.cache + slot * RB);
-#pragma unroll
-    for (int v = 0; v < NV; ++v) *reinterpret_cast<uint4*>(dst + 256 * v + 8 * lane) = narrow(x[v]);
-    if (D_ROPE > 0) *reinterpret_cast<uint32_t*>(dst + D_NOPE + 2 * lane) = f32x2_to_bf16x2(a, b);
-    return;
-  }
-  // a 128-column tile is half a warp's 8-column pieces
-  uint8_t* dst = p.cache + slot * RB;
+  const bool packed = !is_q && KIND == DSA_CACHE_FP8_SCALED;
+  uint16_t* dst = is_q ? p.qo + t * p.qo_st + h * p.qo_sh : reinterpret_cast<uint16_t*>(p.cache + slot * RB);
+  uint8_t* row_out = p.cache + slot * RB;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
+    float x[8];
+    widen(raw[v], x);
+    if (wt) {
+      float w[8];
+      widen(*reinterpret_cast<const uint4*>(wt + 256 * v + 8 * lane), w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] *= r * w[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] *= r;
+    }
+    if (!packed) {
+      *reinterpret_cast<uint4*>(dst + 256 * v + 8 * lane) = narrow(x);
+      continue;
+    }
+    // a 128-column tile is half a warp's 8-column pieces
     float amax = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[v][i]));
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     float scale = 0.0f;
@@ -171,13 +190,19 @@ __global__ void __launch_bounds__(kThreads) qk_kernel(const Params p) {
       scale = __fdiv_rn(amax, 448.0f);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        code[i] = (uint32_t)f32x2_to_e4m3x2(__fdiv_rn(x[v][4 * i], scale), __fdiv_rn(x[v][4 * i + 1], scale)) |
-                  ((uint32_t)f32x2_to_e4m3x2(__fdiv_rn(x[v][4 * i + 2], scale), __fdiv_rn(x[v][4 * i + 3], scale)) << 16);
+        code[i] = (uint32_t)f32x2_to_e4m3x2(__fdiv_rn(x[4 * i], scale), __fdiv_rn(x[4 * i + 1], scale)) |
+                  ((uint32_t)f32x2_to_e4m3x2(__fdiv_rn(x[4 * i + 2], scale), __fdiv_rn(x[4 * i + 3], scale)) << 16);
     }
-    *reinterpret_cast<uint2*>(dst + 256 * v + 8 * lane) = make_uint2(code[0], code[1]);
-    if ((lane & 15) == 0) *reinterpret_cast<float*>(dst + D_NOPE + 4 * (2 * v + (lane >> 4))) = scale;
+    *reinterpret_cast<uint2*>(row_out + 256 * v + 8 * lane) = make_uint2(code[0], code[1]);
+    if ((lane & 15) == 0) *reinterpret_cast<float*>(row_out + D_NOPE + 4 * (2 * v + (lane >> 4))) = scale;
   }
-  if (D_ROPE > 0) *reinterpret_cast<uint32_t*>(dst + D_NOPE + 4 * TILES + 4 * lane) = f32x2_to_bf16x2(a, b);
+  if (D_ROPE > 0) {
+    const uint32_t tail = f32x2_to_bf16x2(a, b);
+    if (packed)
+      *reinterpret_cast<uint32_t*>(row_out + D_NOPE + 4 * TILES + 4 * lane) = tail;
+    else
+      *reinterpret_cast<uint32_t*>(dst + D_NOPE + 2 * lane) = tail;
+  }
 }
 
 template <int KIND, int D_NOPE, int D_ROPE>
