@@ -415,9 +415,11 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     int stage = 0, slot = -1, buf = 0;
     uint32_t phase = 0, q_phase = 0, acc_phase = 0;
     int last = -1;
-    bool ok = true, fresh = false, released = true;
-    while (ok && k.next(p)) {
-      if (k.u != last) {
+    bool ok = true, released = true;
+    bool more = k.next(p);
+    while (more) {
+      const bool fresh = k.u != last;
+      if (fresh) {
         if (!released && lane == 0) mma_commit(q_empty(slot));
         __syncwarp();
         if (++slot == p.slots) {
@@ -425,24 +427,19 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
           q_phase ^= 1;
         }
         last = k.u;
-        fresh = true;
         released = false;
       }
       // after a unit's last tile its query rows may go; else the next unit finds out
       const bool ends = k.m + 1 >= k.m_end && !__any_sync(0xffffffffu, lane >= k.b && k.nb > 0);
       released |= ends;
-      if (!bar_wait(acc_empty(buf), acc_phase ^ 1, abort)) {
+      const uint32_t idesc = idesc_bf16(kBM, (k.b - k.a) * p.HP, 0, 0);
+      const uint32_t acc = tmem + buf * kMaxN;
+      const uint32_t q_lo = d_lo | ((base + (uint32_t)slot * kChunks * row_bytes_q + (uint32_t)(k.a * p.HP) * 128) >> 4);
+      if (!bar_wait(acc_empty(buf), acc_phase ^ 1, abort) || (fresh && !bar_wait(q_full(slot), q_phase, abort))) {
         give_up();
         break;
       }
       tc_fence_after();
-      const uint32_t idesc = idesc_bf16(kBM, (k.b - k.a) * p.HP, 0, 0);
-      const uint32_t acc = tmem + buf * kMaxN;
-      const uint32_t q0 = base + (uint32_t)slot * kChunks * row_bytes_q + (uint32_t)(k.a * p.HP) * 128;
-      if (fresh && !bar_wait(q_full(slot), q_phase, abort)) {
-        give_up();
-        break;
-      }
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         if (!bar_wait(full(stage), phase, abort)) {
@@ -452,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
         }
         if (lane == 0) {
           const uint32_t a_lo = d_lo | ((base + kRingOff + stage * kChunkBytes) >> 4);
-          const uint32_t b_lo = d_lo | ((q0 + c * row_bytes_q) >> 4);
+          const uint32_t b_lo = q_lo + c * (row_bytes_q >> 4);
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
             if (c == 0 && s == 0)
@@ -461,18 +458,19 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
               mma_bf16_lohi<1>(acc, a_lo + 2 * s, d_hi, b_lo + 2 * s, d_hi, idesc);
           }
           mma_commit(empty(stage));
-          if (ends && c == kChunks - 1) mma_commit(q_empty(slot));
+          if (c == kChunks - 1) {
+            mma_commit(acc_full(buf));
+            if (ends) mma_commit(q_empty(slot));
+          }
         }
         __syncwarp();
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1;
         }
+        if (c == 0) more = k.next(p);  // while the products of the first quarter run
       }
       if (!ok) break;
-      fresh = false;
-      if (lane == 0) mma_commit(acc_full(buf));
-      __syncwarp();
       buf ^= 1;
       acc_phase ^= buf == 0;
     }
