@@ -841,6 +841,13 @@ def dsa_cache_evict(cache, kind: int, block_table, lengths, mass, budget=None, *
 
 
 # --------------------------------------------------------- a serving step around the paged cache --
+def _raw_stream(index: int) -> int:
+    """The current stream's handle. (torch.cuda.current_stream makes a Python object of it for a microsecond.)"""
+    import torch
+
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 def dsa_batch_plan(lengths, new_tokens, held, block_table, free_pages, num_free, tokens: int, *, page_size: int,
                    lengths_out=None, held_out=None, num_free_out=None, cu_tokens=None, req_of_token=None, positions=None,
                    token_lengths=None, out_loc=None, error_word=None):
@@ -890,7 +897,7 @@ def dsa_batch_plan(lengths, new_tokens, held, block_table, free_pages, num_free,
         _vector(positions, "positions", T, i32, index), _vector(token_lengths, "token_lengths", T, i32, index),
         _vector(out_loc, "out_loc", T, torch.int64, index), _ptr_on(error_word, "error_word", i32, index))
     with _on_device(index):
-        _check((_LIB or load_library()).dsa_batch_plan(ctypes.byref(a), torch.cuda.current_stream(index).cuda_stream),
+        _check((_LIB or load_library()).dsa_batch_plan(ctypes.byref(a), _raw_stream(index)),
                "dsa_batch_plan")
     return cu_tokens, req_of_token, positions, token_lengths, out_loc
 
@@ -956,7 +963,7 @@ def dsa_qk_norm_rope(q=None, k=None, positions=None, cos_sin=None, eps: float = 
         _vector(positions, "positions", T, i32, index), cs_ptr, cs_st, cs_n, bool(interleaved),
         _ptr_on(error_word, "error_word", i32, index))
     with _on_device(index):
-        _check((_LIB or load_library()).dsa_qk_norm_rope(ctypes.byref(a), torch.cuda.current_stream(index).cuda_stream),
+        _check((_LIB or load_library()).dsa_qk_norm_rope(ctypes.byref(a), _raw_stream(index)),
                "dsa_qk_norm_rope")
     return q_out
 
@@ -981,7 +988,7 @@ def dsa_block_pool(cache, kind: int, block_table, positions, lengths, summary, *
             cache_ptr, kind, slots, bt_ptr, bt_stride, page_size, pages, R, _vector(positions, "positions", T, i32, index),
             _vector(req_of_token, "req_of_token", T, i32, index), T, _vector(lengths, "lengths", R, i32, index), s_ptr,
             summary.shape[0], _ptr_on(error_word, "error_word", i32, index),
-            torch.cuda.current_stream(index).cuda_stream), "dsa_block_pool")
+            _raw_stream(index)), "dsa_block_pool")
     return summary
 
 
@@ -1013,7 +1020,7 @@ def dsa_block_scores(q, summary, block_table, lengths, sm_scale: float, *, page_
             q.data_ptr(), st[0] if T > 1 else 0, st[1] if H > 1 else 0, T, H, s_ptr, summary.shape[0], bt_ptr, bt_stride,
             page_size, pages, R, _vector(req_of_token, "req_of_token", T, i32, index),
             _vector(lengths, "lengths", T, i32, index), sm_scale, _ptr_on(weights, "weights", f32, index), o_ptr, o_stride,
-            width, _ptr_on(error_word, "error_word", i32, index), torch.cuda.current_stream(index).cuda_stream),
+            width, _ptr_on(error_word, "error_word", i32, index), _raw_stream(index)),
             "dsa_block_scores")
     return out
 
@@ -1047,6 +1054,6 @@ def dsa_block_select(scores, block_table, lengths, K: int, *, page_size: int, re
             s_ptr, s_stride, width, T, bt_ptr, bt_stride, page_size, pages, R,
             _vector(req_of_token, "req_of_token", T, i32, index), _vector(lengths, "lengths", T, i32, index), K, sink, recent,
             b_ptr, b_stride, t_ptr, t_stride, _vector(lengths_out, "lengths_out", T, i32, index),
-            _ptr_on(error_word, "error_word", i32, index), torch.cuda.current_stream(index).cuda_stream),
+            _ptr_on(error_word, "error_word", i32, index), _raw_stream(index)),
             "dsa_block_select")
     return blocks, table, lengths_out

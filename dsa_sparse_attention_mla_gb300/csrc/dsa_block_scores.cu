@@ -624,15 +624,22 @@ extern "C" dsa_status_t dsa_block_scores(const void* q, int64_t q_stride_t, int6
   // As many tokens in a group as an MMA takes, while their tiles are three times the SMs: neighbours of one
   // request share its summaries (1024 tokens of 4 requests x 1024 blocks, 32 heads: 27 us with 8 in a group, 67
   // with 1), but a unit is as long as all its tokens' tiles (8 requests x 2048 blocks: 10.5 us with 1 and 14.4
-  // with 4). Tokens that do not name their requests have one each. Then units of a part of a group's tiles, one
-  // and a half times the SMs: each brings the queries anew (256 requests of up to 512 blocks: 21 us with 1.5
-  // times, 30 with 4).
+  // with 4). Tokens that do not name their requests have one each.
   p.HP = (H + 15) / 16 * 16;
   p.G = req_of_token ? scores::kMaxN / p.HP : 1;
   while (p.G > 1 && (T + p.G - 1) / p.G * tiles < 3 * sms) p.G >>= 1;
   const int64_t groups = (T + p.G - 1) / p.G;
-  int64_t parts = (3 * sms / 2 + groups - 1) / groups;
-  p.parts = (int)(parts < tiles ? parts : tiles);
+  // As many parts of a group's tiles as end first, a unit's start (lengths, pages, queries) being worth a tile (256
+  // requests of up to 512 blocks: 18.7 us in one part, 21.5 in two; 64 such requests: 12.3 in one, 10.2 in two).
+  int64_t parts = 1;
+  double best = 0.0;
+  for (int64_t n = 1; n <= tiles && (n - 1) * groups <= 2 * sms; ++n) {
+    const double cost = (double)((groups * n + sms - 1) / sms) * ((double)tiles / n + 1.0);
+    if (n > 1 && cost >= best) continue;
+    best = cost;
+    parts = n;
+  }
+  p.parts = (int)parts;
   p.units = (int)(groups * p.parts);
   p.slots = (int)(scores::kQueryBytes / ((uint32_t)(p.G * p.HP) * scores::kD * 2));
   if (p.slots > scores::kMaxSlots) p.slots = scores::kMaxSlots;
