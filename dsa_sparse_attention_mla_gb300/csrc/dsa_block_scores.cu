@@ -13,11 +13,18 @@
 // issues the products, 13-14 load queries, up to four groups ahead where they are small, 15 loads weights.
 // Two accumulators let the products of a tile run while the one before it is summed up. Every wait is bounded.
 //
-// 4096 tokens of 64 heads over 2016 to 2048 blocks, 275 GFLOP, take 169 us (1.63 PFLOP/s); the products alone
-// 125 (with parts of the work left out: 131 without queries and sums, 148 without sums, 152 without queries).
-// Reading the accumulators out takes tensor memory from the products, and a group's queries, which fill
-// the room that there is for them, come in between two groups. 256 requests of up to 512 blocks, 47 MB, take
-// 21 us: chains of loads (lengths, pages, rows) at the start and of hand-offs per tile, not HBM (7 us).
+// 4096 tokens of 64 heads, half of them over 2016 to 2048 blocks and half over 909 to 941, 198 GFLOP, take 168
+// us (1.18 PFLOP/s; 103 at the tensor core's rate). Of some 3700 cycles a tile (with counters in the kernel) the
+// issuing warp spends 2034 on products, which the tensor core takes at its own rate and next to no ahead, 530 on
+// the queries between two groups (they fill the room that there is for them), 480 on waits for quarters that
+// are there, 130 on accumulators, the rest on its walk. The busiest SM has 88 tiles, the mean is 81. Shared memory has
+// little left: the products read 96 bytes a cycle of its 128, the copies write 32. With parts of the work left
+// out: 128 without queries and sums, 146 without sums, 152 without queries, 160 without weights.
+// 256 requests of up to 512 blocks, 47 MB, take 18.7 us: chains of loads (lengths, pages, rows) at the start and
+// of hand-offs per tile, not HBM (7 us).
+//
+// Two issuing warps taking tiles in turn run the products faster (113 without queries and sums) and the whole slower
+// (183 to 210): tiles that run at the same time end at the same time, and their sums then have nothing to run beside.
 #include <cuda_runtime.h>
 
 #include <climits>

@@ -217,6 +217,50 @@ def test_scores_of_a_large_batch(gpu):
     check_scores(gpu, [(0, n) for n in range(5000, 7500, 3)], 16, 64, weights=True)
 
 
+@pytest.mark.parametrize("H,page,top", [(64, 64, 8000), (64, 16, 5000), (64, 16, 2047), (128, 16, 9000), (32, 16, 6200),
+                                        (48, 16, 4100), (8, 16, 30000)])
+@pytest.mark.parametrize("weights", [False, True])
+def test_scores_of_many_groups(gpu, H, page, top, weights):
+    """Enough tokens that a group fills an MMA: units of one tile, of odd numbers of tiles and of tokens of several
+    requests follow one another, over many rounds of every ring. Run often: the warps' order differs."""
+    gen = torch.Generator(device=gpu).manual_seed(top + H)
+    T, R = 6000, 3
+    lens = torch.randint(0, top, (T,), generator=gen, device=gpu).to(torch.int32)
+    lens[:2000] = torch.arange(2000, device=gpu).to(torch.int32) + top - 2000 if top > 4000 else lens[:2000]
+    lens[3000:3500] = 0
+    req = torch.zeros(T, dtype=torch.int32, device=gpu)
+    req[2500:] = 1
+    req[5000:] = torch.randint(0, R, (1000,), generator=gen, device=gpu).to(torch.int32)
+    nb = -(-top // page)
+    table = torch.randperm(R * nb, generator=gen, device=gpu).to(torch.int32).view(R, nb)
+    summary = torch.randn((R * nb, 256), generator=gen, device=gpu).to(torch.bfloat16)
+    q = torch.randn((T, H, 256), generator=gen, device=gpu).to(torch.bfloat16)
+    w = torch.randn((T, H), generator=gen, device=gpu) if weights else None
+    err = torch.zeros(1, dtype=torch.int32, device=gpu)
+    outs = [torch.full((T, nb), 7.0, device=gpu) for _ in range(8)]
+    for out in outs:
+        dsa.dsa_block_scores(q, summary, table, lens, 0.125, page_size=page, req_of_token=req, weights=w, out=out, error_word=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    assert all(torch.equal(o, outs[0]) for o in outs)
+    step = 500
+    for a in range(0, T, step):
+        x = q[a:a + step].double()
+        for r in req[a:a + step].unique().tolist():
+            s = summary[table[r].long()].double()
+            dot = torch.einsum("thd,bd->thb", x, s).clamp_(min=0) * 0.125
+            ww = torch.ones((step, H), dtype=torch.float64, device=gpu) if w is None else w[a:a + step].double()
+            want = torch.einsum("thb,th->tb", dot, ww)
+            # |q| |s| bounds the sum of products of each head
+            size = 0.125 * (ww.abs() * x.norm(dim=2)).sum(1)[:, None] * s.norm(dim=1)[None, :]
+            tol = size * (256 * 2.0 ** -23 + (H + 2) * 2.0 ** -24)
+            mine = req[a:a + step] == r
+            live = (torch.arange(nb, device=gpu)[None] * page < lens[a:a + step, None]) & mine[:, None]
+            got = outs[0][a:a + step].double()
+            assert ((got - want).abs() <= tol)[live].all()
+            assert (got == 7.0)[~live & mine[:, None]].all()
+
+
 def test_scores_bad_entries(gpu):
     q = torch.ones((3, 4, 256), dtype=torch.bfloat16, device=gpu)
     summary = torch.ones((4, 256), dtype=torch.bfloat16, device=gpu)
