@@ -327,6 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
         if (w == 0 && now[i] < 0 && 32 * i + lane < blocks) set_err(p.err, DSA_DEVERR_INDEX_OUT_OF_RANGE);
       }
       load_pages();
+      // (one issuing warp reads the quarters in order: so the phase two rounds before, of the same parity, is past)
       if (!bar_wait(empty(stage), phase ^ 1, abort)) {
         give_up();
         break;

@@ -323,6 +323,33 @@ def test_scores_streams_and_graphs(gpu):
     assert torch.equal(out, want)
 
 
+def test_pages_past_four_gigabytes(gpu):
+    """Cache rows and summaries whose offsets pass 32 bits."""
+    page = 64
+    pages = (1 << 32) // 512 + 200
+    rows = (1 << 32) // 264 + 64 * page
+    far = rows // page - 1
+    cache = torch.zeros((rows, 264), dtype=torch.uint8, device=gpu)
+    part = make_cache(gpu, FP8, 4 * page, 3)
+    picks = [far, 0, far - 1, 7]
+    for i, p in enumerate(picks):
+        cache[p * page:(p + 1) * page] = part[i * page:(i + 1) * page]
+    summary = torch.zeros((pages, 256), dtype=torch.bfloat16, device=gpu)
+    lens = i32([4 * page], gpu)
+    table = i32([picks], gpu)
+    pos, req = i32([0, 64, 128, 192], gpu), i32([0, 0, 0, 0], gpu)
+    dsa.dsa_block_pool(cache, FP8, table, pos, lens, summary, page_size=page, req_of_token=req)
+    small = torch.zeros((4, 256), dtype=torch.bfloat16, device=gpu)
+    dsa.dsa_block_pool(part, FP8, i32([[0, 1, 2, 3]], gpu), pos, lens, small, page_size=page, req_of_token=req)
+    assert torch.equal(summary[picks], small) and small.ne(0).any(1).all()
+    ends = [pages - 1, 5, pages - 60, pages - 2]
+    summary[ends] = small
+    q = torch.randn((2, 16, 256), device=gpu).to(torch.bfloat16)
+    args = dict(lengths=i32([4 * page, 3 * page], gpu), sm_scale=0.5, page_size=page, req_of_token=i32([0, 0], gpu))
+    got = dsa.dsa_block_scores(q, summary, i32([ends], gpu), **args)
+    assert torch.equal(got, dsa.dsa_block_scores(q, small, i32([[0, 1, 2, 3]], gpu), **args))
+
+
 # -------------------------------------------------------------------------------------- choice --
 def rows_of(rng, T, width):
     s = np.exp(rng.standard_normal((T, width))).astype(np.float32)

@@ -95,7 +95,8 @@ def test_more_requests_than_one_pass(gpu, R):
     held = np.array([pages(int(n), 8) for n in lens])
     new = rng.integers(-1, 12, R)
     lens[::7] //= 2
-    check(gpu, lens.tolist(), new.tolist(), held.tolist(), int(new[new > 0].sum()), 8, width=12, spare=3 * R, inplace=False)
+    for inplace in (False, True):
+        check(gpu, lens.tolist(), new.tolist(), held.tolist(), int(new[new > 0].sum()), 8, width=12, spare=3 * R, inplace=inplace)
 
 
 def test_refusals_for_pages(gpu):
@@ -165,6 +166,67 @@ def test_graph_replays_follow_the_state(gpu):
         state = want
         assert lens.cpu().tolist() == want["lengths"] and nfree.cpu().tolist() == want["num_free"]
         assert np.array_equal(d_table.cpu().numpy(), table) and np.array_equal(d_stack.cpu().numpy(), stack)
+
+
+@pytest.mark.parametrize("R,T,most", [(300, 2000, 6), (300, 20000, 60), (1500, 9000, 5)])
+def test_graph_of_large_steps(gpu, R, T, most):
+    """The same where a cluster moves the pages, where the tokens have a launch of their own, and where the
+    requests take several passes, in place."""
+    rng = np.random.default_rng(R)
+    page, width = 4, 100
+    table, stack, free = build(rng, [0] * R, [0] * R, width, 30 * R)
+    i32 = lambda v: torch.tensor(np.asarray(v), dtype=torch.int32, device=gpu)  # noqa: E731
+    lens, held, nfree, new = i32([0] * R), i32([0] * R), i32([free]), i32([0] * R)
+    d_table, d_stack = i32(table), i32(stack)
+    state = {"lengths": [0] * R, "held": [0] * R, "num_free": [free]}
+    dsa.dsa_batch_plan(lens, new, held, d_table, d_stack, nfree, T, page_size=page)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = dsa.dsa_batch_plan(lens, new, held, d_table, d_stack, nfree, T, page_size=page)
+        tail = got[3] + 1  # what follows in the stream sees the tokens
+    for step in range(6):
+        add = rng.integers(-1, most + 1, R)
+        if step > 2:
+            shrunk = rng.random(R) < 0.3
+            now = np.where(shrunk, np.array(state["lengths"]) // 2, state["lengths"])
+            state["lengths"] = now.tolist()
+            lens.copy_(i32(now))
+        new.copy_(i32(add))
+        graph.replay()
+        torch.cuda.synchronize()
+        want, _ = S.plan(state["lengths"], add, state["held"], table, stack, state["num_free"][0], T, page)
+        for name, t in zip(NAMES, got):
+            assert t.cpu().tolist() == want[name], (step, name)
+        assert torch.equal(tail, got[3] + 1)
+        state = want
+        assert lens.cpu().tolist() == want["lengths"] and held.cpu().tolist() == want["held"]
+        assert np.array_equal(d_table.cpu().numpy(), table) and np.array_equal(d_stack.cpu().numpy(), stack)
+
+
+def test_two_plans_at_once(gpu):
+    """Two batches of their own, on two streams."""
+    i32 = lambda v: torch.tensor(np.asarray(v), dtype=torch.int32, device=gpu)  # noqa: E731
+    rng = np.random.default_rng(7)
+    streams, runs = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for s in range(2):
+        R = 400
+        lens, new = rng.integers(0, 900, R), rng.integers(-1, 30, R)
+        held = [pages(int(n), 8) for n in lens]
+        table, stack, free = build(rng, lens, held, 140, 4 * R)
+        runs.append((lens, new, held, table, stack, free, [i32(lens), i32(new), i32(held), i32(table), i32(stack), i32([free])]))
+    torch.cuda.synchronize()
+    outs = []
+    for (_, _, _, _, _, _, d), st in zip(runs, streams):
+        with torch.cuda.stream(st):
+            outs.append(dsa.dsa_batch_plan(*d, 12000, page_size=8))
+    torch.cuda.synchronize()
+    for (lens, new, held, table, stack, free, d), got in zip(runs, outs):
+        want, bits = S.plan(lens, new, held, table, stack, free, 12000, 8)
+        assert bits == 0
+        for name, t in zip(NAMES, got):
+            assert t.cpu().tolist() == want[name], name
+        assert np.array_equal(d[3].cpu().numpy(), table) and np.array_equal(d[4].cpu().numpy(), stack)
 
 
 def test_side_stream_and_given_outputs(gpu):
