@@ -143,6 +143,12 @@ __device__ __forceinline__ void wait_ld(uint32_t (&r)[32]) {
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+// One thread of the warp, chosen by the hardware.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ void set_err(int32_t* err, int bit) {
   if (err) atomicOr(err, bit);
 }
@@ -245,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t bars = base + kMiscOff;
   auto full = [&](int s) { return bars + 8 * s; };
   auto empty = [&](int s) { return bars + 8 * (kStages + s); };
@@ -418,6 +424,9 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     }
   } else if (warp == kWarpMma) {
     // ---- products
+    auto wait_all = [&](uint32_t bar, uint32_t parity, const volatile int* a) {
+      return __all_sync(0xffffffffu, bar_wait(bar, parity, a)) != 0;
+    };
     const uint64_t d0 = sw128_desc(0, 16, 1024);
     const uint32_t d_hi = (uint32_t)(d0 >> 32), d_lo = (uint32_t)d0;
     int stage = 0, slot = -1, buf = 0;
@@ -428,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     while (more) {
       const bool fresh = k.u != last;
       if (fresh) {
-        if (!released && lane == 0) mma_commit(q_empty(slot));
+        if (!released && elect_one()) mma_commit(q_empty(slot));
         __syncwarp();
         if (++slot == p.slots) {
           slot = 0;
@@ -443,19 +452,19 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
       const uint32_t idesc = idesc_bf16(kBM, (k.b - k.a) * p.HP, 0, 0);
       const uint32_t acc = tmem + buf * kMaxN;
       const uint32_t q_lo = d_lo | ((base + (uint32_t)slot * kChunks * row_bytes_q + (uint32_t)(k.a * p.HP) * 128) >> 4);
-      if (!bar_wait(acc_empty(buf), acc_phase ^ 1, abort) || (fresh && !bar_wait(q_full(slot), q_phase, abort))) {
+      if (!wait_all(acc_empty(buf), acc_phase ^ 1, abort) || (fresh && !wait_all(q_full(slot), q_phase, abort))) {
         give_up();
         break;
       }
       tc_fence_after();
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
-        if (!bar_wait(full(stage), phase, abort)) {
+        if (!wait_all(full(stage), phase, abort)) {
           give_up();
           ok = false;
           break;
         }
-        if (lane == 0) {
+        if (elect_one()) {
           const uint32_t a_lo = d_lo | ((base + kRingOff + stage * kChunkBytes) >> 4);
           const uint32_t b_lo = q_lo + c * (row_bytes_q >> 4);
 #pragma unroll
