@@ -45,8 +45,10 @@ constexpr int kMaxHeads = 128;
 constexpr int kBM = 128;     // blocks per tile (MMA M)
 constexpr int kMaxN = 256;   // query rows per group (MMA N)
 constexpr int kChunks = kD / 64;
-constexpr int kStages = 6;
-constexpr int kSumWarps = 8;  // one per accumulator and lane quarter
+constexpr int N = 16;        // heads summed up per step
+constexpr int kStages = 3;      // halves of a tile's columns
+constexpr int kTurns = 2;  // warps per accumulator and lane quarter: they take its tokens in turn
+constexpr int kSumWarps = 8 * kTurns;
 constexpr int kWarpLoad0 = kSumWarps, kLoadWarps = 4, kWarpMma = kWarpLoad0 + kLoadWarps, kWarpQuery = kWarpMma + 1,
               kQueryWarps = 2, kWarpWeights = kWarpQuery + kQueryWarps;
 constexpr int kWarps = kWarpWeights + 1;
@@ -55,7 +57,7 @@ constexpr int kMaxSlots = 4;  // query groups in shared memory, where they are s
 constexpr uint32_t kChunkBytes = kBM * 128;
 constexpr uint32_t kQueryBytes = kMaxN * kD * 2;
 constexpr uint32_t kRingOff = kQueryBytes;
-constexpr uint32_t kWeightOff = kRingOff + kStages * kChunkBytes;
+constexpr uint32_t kWeightOff = kRingOff + kStages * 2 * kChunkBytes;
 constexpr uint32_t kMiscOff = kWeightOff + kMaxN * 4;
 constexpr uint32_t kSmemBytes = kMiscOff + 512 + 1024;  // and room to align
 
@@ -104,39 +106,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-// 32 lanes x N columns of tensor memory: a lane per thread, a column per register.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-                 "=r"(r[15])
-               : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-                 "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-                 "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-                 "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-               : "r"(taddr));
-}
-// Waits for them; the registers pass through, so that no use of them moves before it.
-__device__ __forceinline__ void wait_ld(uint32_t (&r)[16]) {
+// Waits for tensor-memory loads; the registers pass through, so that no use of them moves before it.
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[N]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                 "+r"(r[15])
-               :
-               : "memory");
-}
-__device__ __forceinline__ void wait_ld(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
-                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
-                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                :
                : "memory");
 }
@@ -244,8 +218,8 @@ struct Walk {
   __device__ __forceinline__ int64_t run_req() const { return __shfl_sync(0xffffffffu, req, a); }
 };
 
-// N: heads summed up per step, 16 or 32. WHOLE: they fill steps.
-template <bool WEIGHTS, bool WHOLE, int N>
+// WHOLE: the heads fill steps of N.
+template <bool WEIGHTS, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -269,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
   float* weights = reinterpret_cast<float*>(smem + kWeightOff);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(full(s), 1);
+      mbar_init(full(s), kLoadWarps / 2);
       mbar_init(empty(s), 1);
     }
     for (int s = 0; s < kMaxSlots; ++s) {
@@ -278,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(acc_full(s), 1);
-      mbar_init(acc_empty(s), 4);
+      mbar_init(acc_empty(s), kSumWarps / 2);
     }
     mbar_init(w_full, 1);
     mbar_init(w_empty, kSumWarps);
@@ -321,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) page[i] = 32 * i + lane < blocks ? from[32 * i] : -1;
     };
-    int stage = w;
+    int stage = w >> 1;
     uint32_t phase = 0;
     load_pages();
     while (more) {
@@ -333,13 +307,13 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
         if (w == 0 && now[i] < 0 && 32 * i + lane < blocks) set_err(p.err, DSA_DEVERR_INDEX_OUT_OF_RANGE);
       }
       load_pages();
-      // (one issuing warp reads the quarters in order: so the phase two rounds before, of the same parity, is past)
+      // (one issuing warp reads the halves in order: so the phase two rounds before, of the same parity, is past)
       if (!bar_wait(empty(stage), phase ^ 1, abort)) {
         give_up();
         break;
       }
       // rows without a summary keep what the stage holds: their lanes are not read
-      const uint32_t to = base + kRingOff + stage * kChunkBytes;
+      const uint32_t to = base + kRingOff + (2 * stage + (w & 1)) * kChunkBytes;
       const uint16_t* from = p.summary + 64 * w + 8 * piece;
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
@@ -351,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(full(stage));
-      stage += kChunks;
+      stage += 2;
       if (stage >= kStages) {
         stage -= kStages;
         phase ^= 1;
@@ -458,24 +432,25 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
       }
       tc_fence_after();
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
+      for (int c = 0; c < kChunks; c += 2) {  // a half: one wait and one commit for eight products
         if (!wait_all(full(stage), phase, abort)) {
           give_up();
           ok = false;
           break;
         }
         if (elect_one()) {
-          const uint32_t a_lo = d_lo | ((base + kRingOff + stage * kChunkBytes) >> 4);
+          const uint32_t a_lo = d_lo | ((base + kRingOff + 2 * stage * kChunkBytes) >> 4);
           const uint32_t b_lo = q_lo + c * (row_bytes_q >> 4);
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {
+          for (int s = 0; s < 8; ++s) {
+            const uint32_t da = (s >> 2) * (kChunkBytes >> 4) + 2 * (s & 3), db = (s >> 2) * (row_bytes_q >> 4) + 2 * (s & 3);
             if (c == 0 && s == 0)
               mma_bf16_lohi<0>(acc, a_lo, d_hi, b_lo, d_hi, idesc);
             else
-              mma_bf16_lohi<1>(acc, a_lo + 2 * s, d_hi, b_lo + 2 * s, d_hi, idesc);
+              mma_bf16_lohi<1>(acc, a_lo + da, d_hi, b_lo + db, d_hi, idesc);
           }
           mma_commit(empty(stage));
-          if (c == kChunks - 1) {
+          if (c + 2 == kChunks) {
             mma_commit(acc_full(buf));
             if (ends) mma_commit(q_empty(slot));
           }
@@ -485,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
           stage = 0;
           phase ^= 1;
         }
-        if (c == 0) more = k.next(p);  // while the products of the first quarter run
+        if (c == 0) more = k.next(p);  // while the products of the first half run
       }
       if (!ok) break;
       buf ^= 1;
@@ -497,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     bar_wait(drained, 0, nullptr);
   } else {
     // ---- sums over heads: a block per lane, tiles in turn between the warps of either accumulator
-    const int buf = warp >> 2, quarter = warp & 3;
+    const int buf = warp / (4 * kTurns), first = (warp >> 2) % kTurns, quarter = warp & 3;
     uint32_t phase = 0, w_phase = 0;
     int last = -1;
     bool mine = buf != 0;
@@ -528,14 +503,14 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
       }
       phase ^= 1;
       tc_fence_after();
-      // N heads at a time; while one warp waits for its products, the others of its scheduler sum up theirs
-      for (int i = k.a; i < k.b; ++i) {
+      // while one warp waits for its products, the others of its scheduler sum up theirs
+      for (int i = k.a + first; i < k.b; i += kTurns) {
         const uint32_t col = acc0 + (i - k.a) * p.HP;
         const float4* w = reinterpret_cast<const float4*>(weights + i * p.HP);
         uint64_t sum[4] = {0, 0, 0, 0};  // chains of pairs of heads
         for (int h0 = 0; h0 < p.HP; h0 += N) {
           uint32_t x[N];
-          tmem_ld32(col + h0, x);
+          tmem_ld32_x16(col + h0, x);
           wait_ld(x);
 #pragma unroll
           for (int j = 0; j < N / 4; ++j) {
@@ -582,8 +557,8 @@ dsa_status_t prepare(int device) {
   std::lock_guard<std::mutex> lock(mu);
   if (done[device]) return DSA_OK;
   cudaError_t e = cudaSuccess;
-  for (const void* f : {(const void*)scores_kernel<false, false, 16>, (const void*)scores_kernel<true, false, 16>,
-                        (const void*)scores_kernel<false, true, 32>, (const void*)scores_kernel<true, true, 32>})
+  for (const void* f : {(const void*)scores_kernel<false, false>, (const void*)scores_kernel<true, false>,
+                        (const void*)scores_kernel<false, true>, (const void*)scores_kernel<true, true>})
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return cuda_fail(e);
   done[device] = true;
@@ -663,9 +638,9 @@ extern "C" dsa_status_t dsa_block_scores(const void* q, int64_t q_stride_t, int6
   if ((st = scores::prepare(dev.device)) != DSA_OK) return st;
   const unsigned grid = (unsigned)(p.units < sms ? p.units : sms);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool whole = H % 32 == 0;
-  auto kernel = weights ? (whole ? scores::scores_kernel<true, true, 32> : scores::scores_kernel<true, false, 16>)
-                        : (whole ? scores::scores_kernel<false, true, 32> : scores::scores_kernel<false, false, 16>);
+  const bool whole = H % scores::N == 0;
+  auto kernel = weights ? (whole ? scores::scores_kernel<true, true> : scores::scores_kernel<true, false>)
+                        : (whole ? scores::scores_kernel<false, true> : scores::scores_kernel<false, false>);
   kernel<<<grid, scores::kThreads, scores::kSmemBytes, s>>>(p);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? DSA_OK : cuda_fail(e);
