@@ -543,6 +543,7 @@ DSA_API dsa_status_t dsa_qk_norm_rope(const dsa_qk_args_t* args, void* stream);
  * at or past max_pages * page_size, a block without a position below lengths[r] or with rows past
  * num_slots sets DSA_DEVERR_INDEX_OUT_OF_RANGE and is skipped.
  *   cache         contiguous rows, 16-byte aligned; num_slots below 2^31
+ * (dsa_cache_evict moves rows between blocks: make the summaries of what is left anew, by positions 0 .. length - 1.)
  *   lengths       int32 [num_requests], with this step's tokens
  *   summary       bf16 [num_pages, 256], 16-byte aligned; the summaries of other pages stay as they are
  */
