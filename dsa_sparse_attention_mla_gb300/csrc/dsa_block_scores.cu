@@ -24,7 +24,7 @@
 //
 // Two issuing warps taking tiles in turn ran the products faster (113 without queries and sums) and the whole slower
 // (183 to 210): tiles that run at the same time end at the same time, and their sums then have nothing to run beside.
-// Queries by TMA: 144 for 146, for a tensor map that each call has to encode.
+// Queries by TMA: 142 to 144 for 146, for a tensor map that each call has to encode (1 us of a small call's 10).
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -620,6 +620,9 @@ extern "C" dsa_status_t dsa_block_scores(const void* q, int64_t q_stride_t, int6
   p.HP = (H + 15) / 16 * 16;
   p.G = req_of_token ? scores::kMaxN / p.HP : 1;
   while (p.G > 1 && (T + p.G - 1) / p.G * tiles < 3 * sms) p.G >>= 1;
+  // Few tiles do not cover the time that the next group's queries take: two groups must fit then (1495 tokens x 128
+  // heads x 19 blocks: 31 us for 37; 4096 x 64 x 256: 45 for 53; x 1024: 96 for 80).
+  while (p.G > 1 && tiles <= 4 && p.G * p.HP > scores::kMaxN / 2) p.G >>= 1;
   const int64_t groups = (T + p.G - 1) / p.G;
   // As many parts of a group's tiles as end first, a unit's start (lengths, pages, queries) being worth a tile (256
   // requests of up to 512 blocks: 18.7 us in one part, 21.5 in two; 64 such requests: 12.3 in one, 10.2 in two).

@@ -217,8 +217,8 @@ def test_scores_of_a_large_batch(gpu):
     check_scores(gpu, [(0, n) for n in range(5000, 7500, 3)], 16, 64, weights=True)
 
 
-@pytest.mark.parametrize("H,page,top", [(64, 64, 8000), (64, 16, 5000), (64, 16, 2047), (128, 16, 9000), (32, 16, 6200),
-                                        (48, 16, 4100), (8, 16, 30000)])
+@pytest.mark.parametrize("H,page,top", [(64, 64, 8000), (64, 16, 5000), (64, 16, 2047), (64, 16, 9000), (128, 16, 9000),
+                                        (32, 16, 6200), (48, 16, 4100), (48, 16, 12000), (8, 16, 30000)])
 @pytest.mark.parametrize("weights", [False, True])
 def test_scores_of_many_groups(gpu, H, page, top, weights):
     """Enough tokens that a group fills an MMA: units of one tile, of odd numbers of tiles and of tokens of several
@@ -228,6 +228,7 @@ def test_scores_of_many_groups(gpu, H, page, top, weights):
     lens = torch.randint(0, top, (T,), generator=gen, device=gpu).to(torch.int32)
     lens[:2000] = torch.arange(2000, device=gpu).to(torch.int32) + top - 2000 if top > 4000 else lens[:2000]
     lens[3000:3500] = 0
+    lens[3500:4200] = lens[3500:4200] % (128 * page)  # one tile, between groups of several
     req = torch.zeros(T, dtype=torch.int32, device=gpu)
     req[2500:] = 1
     req[5000:] = torch.randint(0, R, (1000,), generator=gen, device=gpu).to(torch.int32)
