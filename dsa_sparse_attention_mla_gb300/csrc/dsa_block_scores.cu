@@ -117,7 +117,7 @@ __device__ __forceinline__ void wait_ld(uint32_t (&r)[N]) {
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-// One thread of the warp, chosen by the hardware.
+// One thread of the warp, chosen by the hardware: the same one every time (a commit covers its own thread's products).
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(r));
@@ -272,6 +272,8 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     *abort = 1;
     if (lane == 0) set_err(p.err, DSA_DEVERR_TIMEOUT);
   };
+  // one answer for the warp, also where the limit runs out between two lanes' attempts
+  auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, bar_wait(bar, parity, abort)) != 0; };
   const uint32_t row_bytes_q = (uint32_t)(p.G * p.HP) * 128;  // one column quarter of a group's rows
   Walk k;
   k.start(p);
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
       }
       load_pages();
       // (one issuing warp reads the halves in order: so the phase two rounds before, of the same parity, is past)
-      if (!bar_wait(empty(stage), phase ^ 1, abort)) {
+      if (!wait(empty(stage), phase ^ 1)) {
         give_up();
         break;
       }
@@ -341,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     while (k.next(p)) {
       if (k.u == last) continue;
       last = k.u;
-      if (!bar_wait(q_empty(slot), phase ^ 1, abort)) {
+      if (!wait(q_empty(slot), phase ^ 1)) {
         give_up();
         break;
       }
@@ -386,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
         const int n = 32 * z + lane, i = n / p.HP, h = n - i * p.HP;
         v[z] = i < k.count && h < p.H ? from[i * p.H + h] : 0.0f;
       }
-      if (!bar_wait(w_empty, phase ^ 1, abort)) {
+      if (!wait(w_empty, phase ^ 1)) {
         give_up();
         break;
       }
@@ -398,9 +400,6 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     }
   } else if (warp == kWarpMma) {
     // ---- products
-    auto wait_all = [&](uint32_t bar, uint32_t parity, const volatile int* a) {
-      return __all_sync(0xffffffffu, bar_wait(bar, parity, a)) != 0;
-    };
     const uint64_t d0 = sw128_desc(0, 16, 1024);
     const uint32_t d_hi = (uint32_t)(d0 >> 32), d_lo = (uint32_t)d0;
     int stage = 0, slot = -1, buf = 0;
@@ -426,14 +425,14 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
       const uint32_t idesc = idesc_bf16(kBM, (k.b - k.a) * p.HP, 0, 0);
       const uint32_t acc = tmem + buf * kMaxN;
       const uint32_t q_lo = d_lo | ((base + (uint32_t)slot * kChunks * row_bytes_q + (uint32_t)(k.a * p.HP) * 128) >> 4);
-      if (!wait_all(acc_empty(buf), acc_phase ^ 1, abort) || (fresh && !wait_all(q_full(slot), q_phase, abort))) {
+      if (!wait(acc_empty(buf), acc_phase ^ 1) || (fresh && !wait(q_full(slot), q_phase))) {
         give_up();
         break;
       }
       tc_fence_after();
 #pragma unroll
       for (int c = 0; c < kChunks; c += 2) {  // a half: one wait and one commit for eight products
-        if (!wait_all(full(stage), phase, abort)) {
+        if (!wait(full(stage), phase)) {
           give_up();
           ok = false;
           break;
@@ -467,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
       acc_phase ^= buf == 0;
     }
     // every product ends before tensor memory is given back
-    if (lane == 0) mma_commit(drained);
+    if (elect_one()) mma_commit(drained);
     __syncwarp();
     bar_wait(drained, 0, nullptr);
   } else {
@@ -486,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
           if (lane == 0) mbar_arrive(w_empty);
         }
         last = k.u;
-        if (!bar_wait(w_full, w_phase, abort)) {
+        if (!wait(w_full, w_phase)) {
           give_up();
           break;
         }
@@ -497,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
       const int64_t r = k.run_req();
       int page = -1;
       if (row < k.blocks) page = p.bt[r * p.bt_st + row];
-      if (!bar_wait(acc_full(buf), phase, abort)) {
+      if (!wait(acc_full(buf), phase)) {
         give_up();
         break;
       }
