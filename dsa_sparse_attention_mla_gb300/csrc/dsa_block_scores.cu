@@ -22,8 +22,9 @@
 // 256 requests of up to 512 blocks, 47 MB, take 18.5 us: chains of loads (lengths, pages, rows) at the start and
 // of hand-offs per tile, not HBM (7 us).
 //
-// Two issuing warps taking tiles in turn ran the products faster (113 without queries and sums) and the whole slower
-// (183 to 210): tiles that run at the same time end at the same time, and their sums then have nothing to run beside.
+// Two issuing warps taking tiles in turn ran the products faster (111 without queries and sums) and the whole slower
+// (166 with a token between them, 183 to 210 without: tiles that run at the same time end at the same time, and their
+// sums then have nothing to run beside).
 // Queries by TMA: 142 to 144 for 146, for a tensor map that each call has to encode (1 us of a small call's 10).
 #include <cuda_runtime.h>
 
