@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W, W == 1 ? 8 : 1) select_
         }
       }
       __syncthreads();
-      if (warp == 0) {  // N words per lane, W of which are neighbours in order
+      if (warp == 0) {  // the words in order, neighbouring ones in one lane
         constexpr int PER = (N * W + 31) / 32;
         int a = 0, e = 0;
 #pragma unroll

@@ -132,8 +132,8 @@ __device__ __forceinline__ Want want_of(const Params& p, int64_t r) {
   return w;
 }
 
-// Calls move(k, j, i) for the pages i of a chunk that this block is to move: request k of the chunk, its
-// j-th page among them. `sums`: the chunk's inclusive sums.
+// Moves the pages of a chunk that are this block's share: page i is the j-th of request k of the chunk
+// (`sums`: its inclusive sums), load(k, j, i) gives it and store(k, j, i, page) takes it.
 template <class Load, class Store>
 __device__ __forceinline__ void each_page(const long long* sums, int64_t total, int rank, int blocks, Load load, Store store) {
   const int64_t step = (int64_t)blocks * kThreads;
