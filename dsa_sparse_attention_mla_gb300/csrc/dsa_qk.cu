@@ -192,6 +192,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qk_kernel(const Params p) {
       for (int i = 0; i < 2; ++i)
         code[i] = (uint32_t)f32x2_to_e4m3x2(__fdiv_rn(x[4 * i], scale), __fdiv_rn(x[4 * i + 1], scale)) |
                   ((uint32_t)f32x2_to_e4m3x2(__fdiv_rn(x[4 * i + 2], scale), __fdiv_rn(x[4 * i + 3], scale)) << 16);
+    } else {
+      // zeros, or NaN, which the maximum passes over: a norm makes a whole row of it, and zeros would hide that
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (x[i] != x[i]) code[i >> 2] |= 0x7Fu << (8 * (i & 3));
     }
     *reinterpret_cast<uint2*>(row_out + 256 * v + 8 * lane) = make_uint2(code[0], code[1]);
     if ((lane & 15) == 0) *reinterpret_cast<float*>(row_out + D_NOPE + 4 * (2 * v + (lane >> 4))) = scale;
