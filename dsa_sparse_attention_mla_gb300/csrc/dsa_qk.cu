@@ -184,16 +184,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qk_kernel(const Params p) {
     for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    float scale = 0.0f;
+    const float scale = __fdiv_rn(amax, 448.0f);
     uint32_t code[2] = {0, 0};
-    if (amax > 0.0f) {
-      scale = __fdiv_rn(amax, 448.0f);
+    if (scale > 0.0f) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         code[i] = (uint32_t)f32x2_to_e4m3x2(__fdiv_rn(x[4 * i], scale), __fdiv_rn(x[4 * i + 1], scale)) |
                   ((uint32_t)f32x2_to_e4m3x2(__fdiv_rn(x[4 * i + 2], scale), __fdiv_rn(x[4 * i + 3], scale)) << 16);
     } else {
-      // zeros, or NaN, which the maximum passes over: a norm makes a whole row of it, and zeros would hide that
+      // values below 448 * 2^-150, which count as zeros (the unrounded row can hold them), or NaN, which the maximum
+      // passes over: a norm makes a whole row of it, and zeros would hide that
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (x[i] != x[i]) code[i >> 2] |= 0x7Fu << (8 * (i & 3));

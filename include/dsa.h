@@ -497,8 +497,8 @@ DSA_API dsa_status_t dsa_batch_plan(const dsa_plan_args_t* args, void* stream);
  * with cos = cos_sin[positions[t], i] and sin = cos_sin[positions[t], d_rope / 2 + i]. Everything is
  * in fp32 and rounded once: queries to bf16, the key's row as the cache holds it (bf16, or packed as
  * dsa_quant_k_cache packs, from the unrounded row; but a tile of NaN, or of zeros and NaN, keeps its
- * NaN as codes: a NaN under the norm makes all normalised columns NaN). Sums of squares must stay
- * below the fp32 range.
+ * NaN as codes: a NaN under the norm makes all normalised columns NaN; and a tile whose scale rounds
+ * to zero, largest value below 448 * 2^-150, is zeros). Sums of squares must stay below the fp32 range.
  * A token with a negative position is padding: nothing of it is read or written. A position at or
  * past num_positions skips the token and sets DSA_DEVERR_INDEX_OUT_OF_RANGE. A key whose out_loc is
  * negative is not written; one at or past num_slots is not either and sets

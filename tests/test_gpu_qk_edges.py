@@ -60,3 +60,21 @@ def test_nan_without_a_norm(gpu):
     assert torch.equal(cache[0], dsa.dsa_quant_k_cache(k)[0])
     assert rows.isnan().sum(1).tolist() == [1, 128, 1]
     assert rows[0, 7].isnan() and rows[1, :128].isnan().all() and rows[2, 9].isnan() and (rows[2, 10:128] == 0).all()
+
+
+@pytest.mark.parametrize("value", [2.0 ** -10, 2.0 ** -7, 1.0, 200.0])
+def test_rows_below_the_smallest_scale_are_zero(gpu, value):
+    """The smallest bf16 weight makes products of a few units of the last place of fp32, whose 448th part can round
+    to no scale at all: the row is finite then, and off by less than 448 halves of the smallest fp32 number."""
+    k = torch.zeros((2, 256), dtype=torch.bfloat16, device=gpu)
+    k[0, 5], k[0, 9], k[1, 200] = value, -value / 2, value
+    w = torch.full((256,), 2.0 ** -133, dtype=torch.bfloat16, device=gpu)
+    cache, rows = packed(k, 256, 0, k_norm=256, k_weight=w, eps=1.0)
+    x = k.double()
+    want = x * (x.square().mean(1, keepdim=True) + 1).rsqrt() * 2.0 ** -133
+    codes = cache[:, :256].view(torch.float8_e4m3fn).float().double()
+    scales = cache[:, 256:].contiguous().view(torch.float32).double().repeat_interleave(128, dim=1)
+    assert codes.isfinite().all() and rows.isfinite().all()
+    # half a step of a scale of 2^-149 steps times a code, half a code's step, and the fp32 product's own half step
+    off = (codes * scales - want).abs()
+    assert (off <= 448 * 2.0 ** -150 + want.abs() * 2.0 ** -4 + 2.0 ** -149).all()
