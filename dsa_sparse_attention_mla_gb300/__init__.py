@@ -122,6 +122,8 @@ class DsaPlanArgs(ctypes.Structure):
         ("T", ctypes.c_int64), ("cu_tokens", ctypes.c_void_p), ("req_of_token", ctypes.c_void_p),
         ("positions", ctypes.c_void_p), ("token_lengths", ctypes.c_void_p), ("out_loc", ctypes.c_void_p),
         ("error_word", ctypes.c_void_p),
+        ("seen", ctypes.c_void_p), ("seen_out", ctypes.c_void_p), ("token_positions", ctypes.c_void_p),
+        ("key_positions", ctypes.c_void_p), ("kp_stride", ctypes.c_int64), ("kp_width", ctypes.c_int64),
     ]
 
 
@@ -850,7 +852,8 @@ def _raw_stream(index: int) -> int:
 
 def dsa_batch_plan(lengths, new_tokens, held, block_table, free_pages, num_free, tokens: int, *, page_size: int,
                    lengths_out=None, held_out=None, num_free_out=None, cu_tokens=None, req_of_token=None, positions=None,
-                   token_lengths=None, out_loc=None, error_word=None):
+                   token_lengths=None, out_loc=None, error_word=None, seen=None, seen_out=None, token_positions=None,
+                   key_positions=None):
     """Brings block tables int32 [R, pages] to the requests' lengths and builds the step's slot maps.
 
     Request r of ``lengths`` int32 [R] adds ``new_tokens[r]`` positions, or ends when that is negative;
@@ -859,7 +862,12 @@ def dsa_batch_plan(lengths, new_tokens, held, block_table, free_pages, num_free,
     (a captured step keeps it fixed; entries behind the last token read as padding). ``lengths``,
     ``held`` and ``num_free`` change in place, unless their ``_out`` tensors are given. Returns
     (cu_tokens int32 [R + 1], req_of_token, positions, token_lengths int32 [tokens], out_loc int64
-    [tokens])."""
+    [tokens]).
+
+    Where the cache evicts, ``seen`` int32 [R] counts each request's tokens (in place, or into ``seen_out``), and
+    token_positions int32 [tokens], returned last, are the tokens' places in their sequences, which the rotation
+    goes by; ``positions`` then are those among the cached ones. ``key_positions`` int32 [R, S] receives the place
+    at each new token's position: what dsa_paged_attn and dsa_cache_evict (as ``positions``) take."""
     import torch
 
     i32 = torch.int32
@@ -887,6 +895,14 @@ def dsa_batch_plan(lengths, new_tokens, held, block_table, free_pages, num_free,
         cu_tokens = torch.empty(R + 1, dtype=i32, device=index)
     if out_loc is None:
         out_loc = torch.empty(T, dtype=torch.int64, device=index)
+    seen_ptr = _vector(seen, "seen", R, i32, index)
+    if seen is None and seen_out is not None:
+        raise ValueError("seen_out without seen")
+    if seen is not None and token_positions is None:
+        token_positions = torch.empty(T, dtype=i32, device=index)
+    kp_ptr, kp_stride, kp_width = None, 0, 0
+    if key_positions is not None:
+        kp_ptr, kp_stride, _, kp_width = _rows(key_positions, "key_positions", i32, index, R)
     a = DsaPlanArgs(
         R, len_ptr, _vector(new_tokens, "new_tokens", R, i32, index), held_ptr, bt_ptr, bt_stride, page_size, pages,
         free_ptr, free_pages.shape[0], free_n,
@@ -895,11 +911,14 @@ def dsa_batch_plan(lengths, new_tokens, held, block_table, free_pages, num_free,
         free_n if num_free_out is None else _vector(num_free_out, "num_free_out", 1, i32, index),
         T, _vector(cu_tokens, "cu_tokens", R + 1, i32, index), _vector(req_of_token, "req_of_token", T, i32, index),
         _vector(positions, "positions", T, i32, index), _vector(token_lengths, "token_lengths", T, i32, index),
-        _vector(out_loc, "out_loc", T, torch.int64, index), _ptr_on(error_word, "error_word", i32, index))
+        _vector(out_loc, "out_loc", T, torch.int64, index), _ptr_on(error_word, "error_word", i32, index),
+        seen_ptr, seen_ptr if seen_out is None else _vector(seen_out, "seen_out", R, i32, index),
+        _vector(token_positions, "token_positions", T, i32, index), kp_ptr, kp_stride, kp_width)
     with _on_device(index):
         _check((_LIB or load_library()).dsa_batch_plan(ctypes.byref(a), _raw_stream(index)),
                "dsa_batch_plan")
-    return cu_tokens, req_of_token, positions, token_lengths, out_loc
+    got = cu_tokens, req_of_token, positions, token_lengths, out_loc
+    return got if token_positions is None else (*got, token_positions)
 
 
 def dsa_qk_norm_rope(q=None, k=None, positions=None, cos_sin=None, eps: float = 1e-6, cache=None, kind: int = None,

@@ -41,6 +41,10 @@ struct Params {
   int32_t *cu, *req, *pos, *tlen;
   int64_t* loc;
   int32_t* err;
+  const int32_t* seen;
+  int32_t *seen_out, *tok, *kpos;
+  int64_t kp_st;
+  int kp_width;  // INT_MAX without kpos
 };
 
 // Inclusive sums over the block of two values per thread; *total receives the sums over all threads.
@@ -89,21 +93,24 @@ __device__ __forceinline__ int64_t first_above(const V* a, int64_t n, int64_t i)
   return lo;
 }
 
-// The entries of token slot i of request r, whose new length is `len` and whose tokens end before slot
-// `next`. The table's entries may have been written by another block of the cluster: past L1.
-__device__ __forceinline__ void fill(const Params& p, int64_t i, int64_t r, int next, int len) {
-  const int pos = len - next + (int)i;
+// The entries of token slot i of request r, whose new length is `len`, which has been given `seen` tokens by now and
+// whose tokens end before slot `next`. The table's entries may have been written by another block of the cluster: past L1.
+__device__ __forceinline__ void fill(const Params& p, int64_t i, int64_t r, int next, int len, int seen) {
+  const int pos = len - next + (int)i, tok = seen - next + (int)i;
   const int page = __ldcg(p.bt + r * p.bt_st + pos / p.page);
   p.req[i] = (int)r;
   p.pos[i] = pos;
   p.tlen[i] = pos + 1;
   p.loc[i] = page < 0 ? -1 : (int64_t)page * p.page + pos % p.page;
+  if (p.tok) p.tok[i] = tok;
+  if (p.kpos) p.kpos[r * p.kp_st + pos] = tok;
 }
 __device__ __forceinline__ void fill_padding(const Params& p, int64_t i) {
   p.req[i] = 0;
   p.pos[i] = -1;
   p.tlen[i] = 0;
   p.loc[i] = -1;
+  if (p.tok) p.tok[i] = -1;
 }
 
 // All blocks of the cluster: what each wrote before is seen by the others after.
@@ -113,7 +120,8 @@ __device__ __forceinline__ void cluster_sync() {
 
 struct Want {
   uint32_t after, need;  // the request's length and pages if it is granted (below 2^32 both)
-  int l, h;
+  uint32_t seen_after;   // and the tokens it has been given
+  int l, h, seen;
   bool fits;
   long long back, take, tokens;
 };
@@ -125,7 +133,10 @@ __device__ __forceinline__ Want want_of(const Params& p, int64_t r) {
   const int n = p.add[r];
   w.after = n < 0 ? 0 : (uint32_t)w.l + (uint32_t)n;
   w.need = w.after ? (w.after - 1) / (uint32_t)p.page + 1 : 0;
-  w.fits = w.need <= (uint32_t)p.max_pages && w.after <= (uint32_t)INT_MAX;
+  w.seen = p.seen ? max(p.seen[r], 0) : w.l;
+  w.seen_after = n < 0 ? 0 : (uint32_t)w.seen + (uint32_t)n;
+  w.fits = w.need <= (uint32_t)p.max_pages && max(w.after, w.seen_after) <= (uint32_t)INT_MAX &&
+           (n <= 0 || w.after <= (uint32_t)p.kp_width);
   w.back = w.need < (uint32_t)w.h ? w.h - (int)w.need : 0;
   w.take = w.fits && w.need > (uint32_t)w.h ? (int)w.need - w.h : 0;
   w.tokens = w.fits && n > 0 ? n : 0;
@@ -163,7 +174,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const Params p, const in
   __shared__ longlong2 s_warp[32];
   __shared__ long long s_sum[kThreads];  // inclusive page sums of the chunk
   __shared__ int s_first[kThreads];      // first table entry that a request gives back or takes
-  __shared__ int s_cu[kThreads + 1], s_len[kThreads];
+  __shared__ int s_cu[kThreads + 1], s_len[kThreads], s_seen[kThreads];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, rank = blocks > 1 ? (int)blockIdx.x : 0;
   const int64_t nf = min((int64_t)max(*p.num_free, 0), p.cap);
@@ -227,11 +238,13 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const Params p, const in
     s_sum[tid] = sum.x;
     s_first[tid] = w.h;
     if (r < p.R) {
-      const int len = ok ? (int)w.after : w.l, cu = (int)(granted.y + sum.y);
+      const int len = ok ? (int)w.after : w.l, cu = (int)(granted.y + sum.y), seen = ok ? (int)w.seen_after : w.seen;
       s_cu[tid + 1] = cu;
       s_len[tid] = len;
+      s_seen[tid] = seen;
       if (rank == 0) {
         p.len_out[r] = len;
+        if (p.seen) p.seen_out[r] = seen;
         p.held_out[r] = w.take > 0 || w.need < (uint32_t)w.h ? (int)w.need : w.h;
         p.cu[r + 1] = cu;
       }
@@ -258,10 +271,11 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const Params p, const in
       fill_padding(p, i);
     } else if (one) {
       const int r = (int)first_above(s_cu + 1, p.R, i);
-      fill(p, i, r, s_cu[r + 1], s_len[r]);
+      fill(p, i, r, s_cu[r + 1], s_len[r], s_seen[r]);
     } else {
       const int64_t r = first_above(p.cu + 1, p.R, i);
-      fill(p, i, r, p.cu[r + 1], p.len_out[r]);
+      const int len = p.len_out[r];
+      fill(p, i, r, p.cu[r + 1], len, p.seen ? p.seen_out[r] : len);
     }
   }
 }
@@ -275,7 +289,8 @@ __global__ void __launch_bounds__(kFillThreads) fill_kernel(const Params p) {
     return;
   }
   const int64_t r = first_above(p.cu + 1, p.R, i);
-  fill(p, i, r, p.cu[r + 1], p.len_out[r]);
+  const int len = p.len_out[r];
+  fill(p, i, r, p.cu[r + 1], len, p.seen ? p.seen_out[r] : len);
 }
 
 }  // namespace plan
@@ -293,12 +308,15 @@ extern "C" dsa_status_t dsa_batch_plan(const dsa_plan_args_t* a, void* stream) {
                               (a->max_pages > 0 && !a->block_table)))
     return DSA_ERR_INVALID_ARGUMENT;
   if (a->T > 0 && (!a->req_of_token || !a->positions || !a->token_lengths || !a->out_loc)) return DSA_ERR_INVALID_ARGUMENT;
+  if (a->num_requests > 0 && a->seen && !a->seen_out) return DSA_ERR_INVALID_ARGUMENT;
+  if (a->key_positions && (a->kp_width < 0 || a->kp_stride < a->kp_width)) return DSA_ERR_INVALID_ARGUMENT;
   if (!aligned(a->out_loc, 8)) return DSA_ERR_INVALID_ARGUMENT;
   for (const void* q : {(const void*)a->lengths, (const void*)a->new_tokens, (const void*)a->held, (const void*)a->block_table,
                         (const void*)a->free_pages, (const void*)a->num_free, (const void*)a->lengths_out,
                         (const void*)a->held_out, (const void*)a->num_free_out, (const void*)a->cu_tokens,
                         (const void*)a->req_of_token, (const void*)a->positions, (const void*)a->token_lengths,
-                        (const void*)a->error_word})
+                        (const void*)a->error_word, (const void*)a->seen, (const void*)a->seen_out,
+                        (const void*)a->token_positions, (const void*)a->key_positions})
     if (!aligned(q, 4)) return DSA_ERR_INVALID_ARGUMENT;
   DeviceInfo dev;
   const dsa_status_t st = current_device(&dev);
@@ -325,6 +343,12 @@ extern "C" dsa_status_t dsa_batch_plan(const dsa_plan_args_t* a, void* stream) {
   p.tlen = a->token_lengths;
   p.loc = a->out_loc;
   p.err = a->error_word;
+  p.seen = a->seen;
+  p.seen_out = a->seen_out;
+  p.tok = a->token_positions;
+  p.kpos = a->key_positions;
+  p.kp_st = a->kp_stride;
+  p.kp_width = a->key_positions && a->kp_width < INT_MAX ? (int)a->kp_width : INT_MAX;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool here = p.T <= plan::kMaxFill;
   // One block where it can have little to move, and where the requests take several chunks (see the kernel).

@@ -431,6 +431,10 @@ DSA_API dsa_status_t dsa_cache_evict(const dsa_evict_args_t* args, void* stream)
  * of the blocks (a block = a page of positions) that each token attends to. In turn: dsa_batch_plan
  * -> dsa_qk_norm_rope -> dsa_block_pool -> dsa_block_scores -> dsa_block_select -> dsa_paged_attn
  * over the selected table; dsa_cache_evict shrinks lengths, and the next plan takes its pages back.
+ * An eviction closes the gaps it leaves, so the j-th cached position of a request holds its j-th token
+ * only until the first one. Where the cache is told by its positions (means, scores, choice, lengths),
+ * the plan's `positions` and `token_lengths` say it; where a token's place in its sequence counts (the
+ * rotation, the attention's q_positions and key_positions), `token_positions` does, with `seen`.
  * Results are bit-identical across repeated calls with the same inputs on one device.
  */
 
@@ -449,18 +453,26 @@ DSA_API dsa_status_t dsa_cache_evict(const dsa_evict_args_t* args, void* stream)
  * 2^31 - 1 (DSA_DEVERR_INDEX_OUT_OF_RANGE); or, of the requests not refused by that, when it takes
  * pages and it and those before it want more pages than there are (DSA_DEVERR_OUT_OF_PAGES), or
  * when it adds tokens and it and those before it add more than T (DSA_DEVERR_TOKEN_CAPACITY). A
- * refused request adds no token and takes no page; its length stays l, and pages past need still
+ * refused request adds no token and takes no page; its length and seen stay, and pages past need still
  * go back. Negative lengths and held count as 0, held past max_pages as max_pages, *num_free as
  * clamped to [0, free_capacity]. Pages that find no room on the stack are dropped and set
  * DSA_DEVERR_SLOT_OUT_OF_RANGE.
  * The tokens that requests add are numbered in order of requests and positions, i = 0, 1, ...:
  *   cu_tokens     [R + 1]: the first token of each request, and the number of all
- *   req_of_token  [T], positions [T] (the token's position), token_lengths [T] (position + 1: what
- *                 the token attends to), out_loc int64 [T] (the cache slot of its position; -1 for a
- *                 page < 0). Entries behind the last token: request 0, position -1, length 0, slot
- *                 -1, which every operator skips.
- * Each of lengths_out, held_out and num_free_out may be its input (in place) or disjoint; the block
- * table and the free stack change in place.
+ *   req_of_token  [T], positions [T] (the token's position among its request's cached ones),
+ *                 token_lengths [T] (position + 1: what the token attends to), out_loc int64 [T] (the
+ *                 cache slot of its position; -1 for a page < 0). Entries behind the last token: request
+ *                 0, position -1, length 0, slot -1, which every operator skips.
+ * Where an eviction has shortened requests, a token's place in its sequence is not its position any
+ * more. `seen` counts the tokens that each request has been given: the i-th of this step's has place
+ * seen + i, and seen becomes seen + n (0 when the request ends; a negative one counts as 0; l + i and
+ * l when NULL). A request whose seen + n exceeds 2^31 - 1, or that adds tokens to more than kp_width
+ * positions, is refused (DSA_DEVERR_INDEX_OUT_OF_RANGE).
+ *   token_positions  [T]: the token's place, -1 behind the last token
+ *   key_positions    [r, position] = place of every new token (the other entries stay: dsa_cache_evict
+ *                    moves them with the rows as its positions, in place)
+ * Each of lengths_out, held_out, num_free_out and seen_out may be its input (in place) or disjoint; the
+ * block table and the free stack change in place. Zero-initialise the struct, then fill.
  */
 typedef struct dsa_plan_args {
   int64_t num_requests;          /* at most 2^20 */
@@ -483,6 +495,12 @@ typedef struct dsa_plan_args {
   int32_t* token_lengths;        /* int32 [T] */
   int64_t* out_loc;              /* int64 [T] */
   int32_t* error_word;
+  const int32_t* seen;           /* int32 [num_requests] or NULL */
+  int32_t* seen_out;             /* int32 [num_requests]; unused without seen */
+  int32_t* token_positions;      /* int32 [T] or NULL */
+  int32_t* key_positions;        /* int32 [num_requests, kp_width] or NULL */
+  int64_t kp_stride;
+  int64_t kp_width;
 } dsa_plan_args_t;
 
 DSA_API dsa_status_t dsa_batch_plan(const dsa_plan_args_t* args, void* stream);
@@ -492,7 +510,8 @@ DSA_API dsa_status_t dsa_batch_plan(const dsa_plan_args_t* args, void* stream);
  * RoPE columns and the key's cache row, in one pass. A row x of d_nope + d_rope columns becomes
  *   y_d = x_d * rsqrt(mean_{d < n} x_d^2 + eps) * weight_d      for the first n columns
  * (n = q_norm for queries, k_norm for keys: 0 leaves them as they are, d_nope, or all; weight 1
- * when NULL), then, when cos_sin is given, the last d_rope columns turn by the token's angles:
+ * when NULL), then, when cos_sin is given, the last d_rope columns turn by the token's angles
+ * (positions: its place in the sequence, the plan's token_positions where the cache evicts):
  *   (a, b) -> (a cos - b sin, b cos + a sin) for the pairs (i, i + d_rope / 2), or (2 i, 2 i + 1) when interleaved,
  * with cos = cos_sin[positions[t], i] and sin = cos_sin[positions[t], d_rope / 2 + i]. Everything is
  * in fp32 and rounded once: queries to bf16, the key's row as the cache holds it (bf16, or packed as

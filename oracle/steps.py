@@ -14,8 +14,9 @@ def _pages(n: int, page: int) -> int:
     return -(-n // page)
 
 
-def plan(lengths, new, held, table, free, num_free, T, page):
-    """The plan's outputs by name, and its error bits; ``table`` and ``free`` are changed in place."""
+def plan(lengths, new, held, table, free, num_free, T, page, seen=None, key_positions=None):
+    """The plan's outputs by name, and its error bits; ``table``, ``free`` and ``key_positions`` are changed
+    in place. ``seen``: tokens given to each request so far (its length without it)."""
     R, width = table.shape
     err = 0
     lens = [max(int(x), 0) for x in lengths]
@@ -31,11 +32,13 @@ def plan(lengths, new, held, table, free, num_free, T, page):
             else:
                 err |= SLOT
     have, wanted, tokens = top, 0, 0
-    out_len, out_held, cu, req, pos = [], [], [0], [], []
+    out_len, out_held, cu, req, pos, out_seen, place = [], [], [0], [], [], [], []
+    seen = [max(int(x), 0) for x in seen] if seen is not None else lens
+    kp_width = 2 ** 31 - 1 if key_positions is None else key_positions.shape[1]
     for r in range(R):
         take, add = max(need[r] - held[r], 0), max(int(new[r]), 0)
         ok = True
-        if need[r] > width or goal[r] > 2 ** 31 - 1:
+        if need[r] > width or max(goal[r], seen[r] + add) > 2 ** 31 - 1 or (add and goal[r] > kp_width):
             err |= OUT_OF_RANGE
             ok = False
         else:
@@ -53,6 +56,10 @@ def plan(lengths, new, held, table, free, num_free, T, page):
                 table[r, j] = free[top]
             req += [r] * add
             pos += list(range(lens[r], lens[r] + add))
+            place += list(range(seen[r], seen[r] + add))
+            if add and key_positions is not None:
+                key_positions[r, lens[r]:lens[r] + add] = place[-add:]
+        out_seen.append((0 if new[r] < 0 else seen[r] + add) if ok else seen[r])
         out_len.append(goal[r] if ok else lens[r])
         out_held.append(need[r] if ok or need[r] < held[r] else held[r])
         cu.append(len(pos))
@@ -60,7 +67,7 @@ def plan(lengths, new, held, table, free, num_free, T, page):
     pad = T - len(pos)
     return {"lengths": out_len, "held": out_held, "num_free": [top], "cu": cu, "req": req + [0] * pad,
             "positions": pos + [-1] * pad, "token_lengths": [p + 1 for p in pos] + [0] * pad,
-            "out_loc": loc + [-1] * pad}, err
+            "out_loc": loc + [-1] * pad, "seen": out_seen, "token_positions": place + [-1] * pad}, err
 
 
 def norm_rope(x, n, weight, eps, angles, interleaved):
