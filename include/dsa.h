@@ -457,6 +457,12 @@ DSA_API dsa_status_t dsa_cache_evict(const dsa_evict_args_t* args, void* stream)
  * go back. Negative lengths and held count as 0, held past max_pages as max_pages, *num_free as
  * clamped to [0, free_capacity]. Pages that find no room on the stack are dropped and set
  * DSA_DEVERR_SLOT_OUT_OF_RANGE.
+ * Pages that go back must be the request's own. The plan does not look for one that another request
+ * holds too (a shared prefix): each would give it back, and it would be handed out twice, to requests
+ * that then write over each other's rows, with no error bit. A request whose first s pages are shared
+ * must keep at least s * page_size positions; to end it, set its length to that with new_tokens 0, which
+ * gives the pages behind them back, then set its length and held to 0. The shared pages go back with
+ * the last request that holds them.
  * The tokens that requests add are numbered in order of requests and positions, i = 0, 1, ...:
  *   cu_tokens     [R + 1]: the first token of each request, and the number of all
  *   req_of_token  [T], positions [T] (the token's position among its request's cached ones),
@@ -562,7 +568,8 @@ DSA_API dsa_status_t dsa_qk_norm_rope(const dsa_qk_args_t* args, void* stream);
  * every token t, page = block_table[r, block]. Rows in fp32 (FP8: code * tile scale), summed in a
  * fixed order. Negative positions are skipped. A request or page that does not exist, a position
  * at or past max_pages * page_size, a block without a position below lengths[r] or with rows past
- * num_slots sets DSA_DEVERR_INDEX_OUT_OF_RANGE and is skipped.
+ * num_slots sets DSA_DEVERR_INDEX_OUT_OF_RANGE and is skipped. Requests of one call that share a page
+ * must have equally many positions in it: it has one summary.
  *   cache         contiguous rows, 16-byte aligned; num_slots below 2^31
  * (dsa_cache_evict moves rows between blocks: make the summaries of what is left anew, by positions 0 .. length - 1.)
  *   lengths       int32 [num_requests], with this step's tokens
