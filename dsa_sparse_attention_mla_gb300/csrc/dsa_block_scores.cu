@@ -40,6 +40,7 @@ namespace dsa {
 namespace scores {
 
 using paged::bar_wait;
+using paged::bar_wait_row;
 
 constexpr int kD = 256;
 constexpr int kMaxHeads = 128;
@@ -237,10 +238,11 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
   auto acc_empty = [&](int s) { return bars + 8 * (kAccBar + 2 + s); };
   const uint32_t w_full = bars + 8 * kWBar, w_empty = w_full + 8;
   constexpr int kBars = kWBar + 3;
-  static_assert(8 * kBars + 8 <= 512, "barriers");
+  static_assert(8 * kBars + 12 <= 512, "barriers");
   const uint32_t drained = bars + 8 * (kBars - 1);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + kMiscOff + 8 * kBars);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMiscOff + 8 * kBars + 4);
+  volatile int* progress = reinterpret_cast<volatile int*>(smem + kMiscOff + 8 * kBars + 8);  // tiles issued
   float* weights = reinterpret_cast<float*>(smem + kWeightOff);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -258,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     mbar_init(w_full, 1);
     mbar_init(w_empty, kSumWarps);
     mbar_init(drained, 1);
-    *abort = 0;
+    *abort = *progress = 0;
     fence_mbar_init();
   }
   if (warp == kWarpMma) {
@@ -275,6 +277,10 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
   };
   // one answer for the warp, also where the limit runs out between two lanes' attempts
   auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, bar_wait(bar, parity, abort)) != 0; };
+  // for all tiles of a unit, however many: the limit starts anew with every tile
+  auto wait_unit = [&](uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, bar_wait_row(bar, parity, abort, progress)) != 0;
+  };
   const uint32_t row_bytes_q = (uint32_t)(p.G * p.HP) * 128;  // one column quarter of a group's rows
   Walk k;
   k.start(p);
@@ -344,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     while (k.next(p)) {
       if (k.u == last) continue;
       last = k.u;
-      if (!wait(q_empty(slot), phase ^ 1)) {
+      if (!wait_unit(q_empty(slot), phase ^ 1)) {
         give_up();
         break;
       }
@@ -389,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
         const int n = 32 * z + lane, i = n / p.HP, h = n - i * p.HP;
         v[z] = i < k.count && h < p.H ? from[i * p.H + h] : 0.0f;
       }
-      if (!wait(w_empty, phase ^ 1)) {
+      if (!wait_unit(w_empty, phase ^ 1)) {
         give_up();
         break;
       }
@@ -405,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
     const uint32_t d_hi = (uint32_t)(d0 >> 32), d_lo = (uint32_t)d0;
     int stage = 0, slot = -1, buf = 0;
     uint32_t phase = 0, q_phase = 0, acc_phase = 0;
-    int last = -1;
+    int last = -1, tiles = 0;
     bool ok = true, released = true;
     bool more = k.next(p);
     while (more) {
@@ -463,6 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_kernel(const Params p) {
         if (c == 0) more = k.next(p);  // while the products of the first half run
       }
       if (!ok) break;
+      if (lane == 0) *progress = ++tiles;
       buf ^= 1;
       acc_phase ^= buf == 0;
     }
