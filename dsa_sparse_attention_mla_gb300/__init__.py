@@ -874,8 +874,8 @@ def dsa_batch_plan(lengths, new_tokens, held, block_table, free_pages, num_free,
     _c_int("page_size", page_size)
     index = _cuda_index(lengths, "lengths", i32)
     R, T = lengths.shape[0], tokens
-    if T < 0:
-        raise ValueError("tokens must not be negative")
+    if not 0 <= T <= 1 << 30:  # before anything is allocated for them
+        raise ValueError("tokens must be 0 .. 2^30")
     bt_ptr, bt_stride, _, pages = _rows(block_table, "block_table", i32, index, R)
     free_ptr = _ptr_on(free_pages, "free_pages", i32, index)
     if free_pages.dim() != 1 or not free_pages.is_contiguous():

@@ -31,3 +31,15 @@ def test_requests_that_share_their_first_pages(gpu):
     assert step(s, [0, -1, 0]) == [3, 7, 4, 9, 2]  # the last holder
     s = state()
     assert step(s, [-1, -1, 0]) == [3, 5, 7, 4, 1, 7, 4, 9, 2]
+
+
+@pytest.mark.parametrize("tokens", [(1 << 30) + 1, (1 << 31) - 1, (1 << 40), -1])
+def test_no_room_is_made_for_a_refused_number_of_tokens(gpu, tokens):
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=gpu)  # noqa: E731
+    args = (i32([1]), i32([1]), i32([1]), i32([[0, 1]]), i32([2]), i32([1]))
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    with pytest.raises(ValueError):
+        dsa.dsa_batch_plan(*args, tokens, page_size=16)
+    assert torch.cuda.max_memory_allocated() == before
