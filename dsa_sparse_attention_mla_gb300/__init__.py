@@ -1060,6 +1060,8 @@ def dsa_block_select(scores, block_table, lengths, K: int, *, page_size: int, re
     bt_ptr, bt_stride, R, pages = _rows(block_table, "block_table", i32, index, None, 1 if T else 0)
     if K < 1:
         raise ValueError("K must be positive")
+    if K > 16384:  # before anything is allocated for it
+        raise DsaError(2, "dsa_block_select")
     if blocks is None:
         blocks = torch.empty((T, K), dtype=i32, device=index)
     if table is None:
