@@ -454,7 +454,8 @@ DSA_API dsa_status_t dsa_cache_evict(const dsa_evict_args_t* args, void* stream)
  * pages and it and those before it want more pages than there are (DSA_DEVERR_OUT_OF_PAGES), or
  * when it adds tokens and it and those before it add more than T (DSA_DEVERR_TOKEN_CAPACITY). A
  * refused request adds no token and takes no page; its length and seen stay, and pages past need still
- * go back. Negative lengths and held count as 0, held past max_pages as max_pages, *num_free as
+ * go back. What it wanted still counts for those behind it: a request too large for the step holds up
+ * every later one that takes a page or adds a token, until the caller leaves it out (new_tokens 0). Negative lengths and held count as 0, held past max_pages as max_pages, *num_free as
  * clamped to [0, free_capacity]. Pages that find no room on the stack are dropped and set
  * DSA_DEVERR_SLOT_OUT_OF_RANGE.
  * Pages that go back must be the request's own. The plan does not look for one that another request
@@ -587,7 +588,8 @@ DSA_API dsa_status_t dsa_block_pool(const void* cache, dsa_cache_kind_t kind, in
  * for the blocks b < ceil(lengths[t] / page_size) of the token's request r; other entries of scores
  * are left as they are. w = weights, or 1 when NULL. bf16 products (exact) accumulated in fp32 on
  * the tensor cores, the sum over heads in fp32 (of w * sm_scale times the products' positive
- * part). NaN passes through the maximum. A block whose page does not
+ * part). The tensor cores' sums truncate: a score is within 2^-15 * sum_h |w| sm_scale sum_d |q_d s_d|
+ * + (H + 2) * 2^-24 * sum_h |w| sm_scale max(0, q.s) of its formula. NaN passes through the maximum. A block whose page does not
  * exist scores -inf and sets DSA_DEVERR_INDEX_OUT_OF_RANGE, as do blocks at or past max_pages or
  * width (not scored) and a request that does not exist (its token is skipped).
  * Causality: a token's own block, and with several tokens of a request in one call the blocks after
