@@ -4,14 +4,17 @@
 // Pool: summary[page] = mean of the block's rows. The tokens of a step name the blocks: a token leads
 // its block when the token before it lies in another one, so no list of blocks has to be made first.
 // The leader's block of threads reads the rows, one row per warp at a time, and the warps' fp32 sums
-// are joined in a fixed order. 101739 bf16 rows in blocks of 64 (54 MB) take 13 us from a graph, 4.1 TB/s: the
-// start (positions, then table and lengths, then rows: a chain of loads), then HBM.
+// are joined in a fixed order. 101739 bf16 rows in blocks of 64 (54 MB) take 8.1 us in a graph of calls on one
+// state, whose rows lie in L2, and 15.1 after a write that takes them out of it: 3.6 TB/s, where the copy would take 8.0.
+// A leader's loads form a chain (positions, then table and lengths, then rows) with nothing of the next leader on its way.
 //
 // Select: the m-th largest key of a row decides, found bit by bit: scores map to unsigned keys of the
 // same order, blocks that are always chosen to the largest one, and up to 32 counts of the keys at or
 // above a trial value build it from the top bit down. The keys stay in registers; ballots and their
-// prefix sums put the chosen blocks in ascending order. What bounds it is the chain of counts: 8192 rows of up to
-// 512 blocks take 19 us from a graph (some 7 of it the search), 256 rows of up to 2048 8.5.
+// prefix sums put the chosen blocks in ascending order. 8192 rows of up to 512 blocks take 19.1 us in a graph of
+// calls on one state, some 7 of it the search's chain of counts, the rest not taken apart (2048 blocks of threads in 1.7
+// waves); 256 rows of up to 2048 take 8.0. With the inputs out of L2: 24.5 and 11.1. Rows of more than 8704 blocks read
+// their keys anew for every count: 64 of up to 16384 take 49 us.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -427,7 +430,8 @@ extern "C" dsa_status_t dsa_block_pool(const void* cache, dsa_cache_kind_t kind,
   p.err = error_word;
   // A decode step's tokens all lead a block: one each, spread over the device. Of a prefill's one in page_size
   // does, and blocks of threads that find none cost their start: eight per SM, of up to 32 tokens. (101739 tokens in
-  // pages of 64: 13.1 us, 19.2 with 8 tokens each; 8192 that all lead: 20.4, 61 with 32 each.)
+  // pages of 64: 13.1 us, 19.2 with 8 tokens each; 8192 that all lead: 20.4, 61 with 32 each; replays of one call,
+  // rows in L2.)
   const int64_t share = T / (8 * dev.sm_count);
   p.per_block = (int)(share < 1 ? 1 : share > 32 ? 32 : share);
   const unsigned grid = (unsigned)((T + p.per_block - 1) / p.per_block);
@@ -484,7 +488,9 @@ extern "C" dsa_status_t dsa_block_select(const float* scores, int64_t score_stri
   const int64_t most = width < max_pages ? width : max_pages;
   cudaError_t e;
   // a warp per row up to 544 blocks, then as few warps as hold the keys (tables are a little wider than a
-  // round number of blocks as a rule)
+  // round number of blocks as a rule). The table's width decides, since the lengths are on the device: rows much shorter
+  // than it pay for it (8192 rows of up to 512 blocks: 21 us in a table of 513 columns, 71 in 2052, 288 in 8208, 641 in
+  // 16416). A table sliced to the longest request's pages avoids that.
   if (most <= 160)
     e = block::launch_select<1, 5, true>(p, s);
   else if (most <= 288)

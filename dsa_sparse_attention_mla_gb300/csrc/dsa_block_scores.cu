@@ -13,14 +13,17 @@
 // tile, 20 issues the products, 21-22 load queries, up to four groups ahead where they are small, 23 loads weights.
 // Two accumulators let the products of a tile run while the one before it is summed up. Every wait is bounded.
 //
-// 4096 tokens of 64 heads, half of them over 2016 to 2048 blocks and half over 909 to 941, 198 GFLOP, take 146
-// us (1.36 PFLOP/s; 103 at the tensor core's rate). With parts of the work left out: 121 without queries and sums,
-// 129 without queries, 139 without sums. What is left of the products is the issuing warp's waits and commits
-// between them; a group's queries fill the room that there is for them, so the next ones come in between two
-// groups; the busiest SM has 88 tiles, the mean is 81. The warp that issues keeps all its state uniform and elects
+// 4096 tokens of 64 heads, half of them over 2016 to 2048 blocks and half over 909 to 941, 198 GFLOP, take 144
+// us in a graph of calls (1.37 PFLOP/s). At the measured matrix rate, 1929.7 TFLOP/s, it would be 103, 107 with the tiles'
+// empty rows, and 116 for the 88 tiles of the busiest SM (the mean is 81); by the tensor pipe's own cycles at the 1.92 GHz
+// seen here, 92 for those 88. With parts of the work left out, the whole being 146 as the replay of one call: 121
+// without queries and sums (what is above the products is waits and commits between them), 129 without queries, 139
+// without sums. A group's queries fill the room that there is for them, so the next ones come in between two
+// groups. The warp that issues keeps all its state uniform and elects
 // a thread: with a fixed thread the operands went through registers first, 168 us for 152.
-// 256 requests of up to 512 blocks, 47 MB, take 18.5 us: chains of loads (lengths, pages, rows) at the start and
-// of hand-offs per tile, not HBM (7 us).
+// 256 requests of up to 512 blocks, 47 MB, take 18.5 us, 11.6 where they lie in L2 (HBM: 7): 128 units of two tokens,
+// so 24 SMs have none and the busiest has 7 tiles of a mean of 4.6; and chains of loads (lengths, pages, rows) at
+// the start of each, and of hand-offs per tile.
 //
 // Two issuing warps taking tiles in turn ran the products faster (111 without queries and sums) and the whole slower
 // (166 with a token between them, 183 to 210 without: tiles that run at the same time end at the same time, and their
@@ -623,12 +626,15 @@ extern "C" dsa_status_t dsa_block_scores(const void* q, int64_t q_stride_t, int6
   // As many tokens in a group as an MMA takes, while their tiles are three times the SMs: neighbours of one
   // request share its summaries (1024 tokens of 4 requests x 1024 blocks, 32 heads: 27 us with 8 in a group, 67
   // with 1), but a unit is as long as all its tokens' tiles (8 requests x 2048 blocks: 10.5 us with 1 and 14.4
-  // with 4). Tokens that do not name their requests have one each.
+  // with 4). Tokens that do not name their requests have one each. These rules, and those below, go by the table's width,
+  // since the lengths are on the device: rows much shorter than it get fewer, longer units than they would bear (32
+  // requests of up to 512 blocks: 5.8 us in a table of 513 columns, 10.0 in 8208; 64: 6.6 and 9.9; 256: 11.6 and 12.9).
   p.HP = (H + 15) / 16 * 16;
   p.G = req_of_token ? scores::kMaxN / p.HP : 1;
   while (p.G > 1 && (T + p.G - 1) / p.G * tiles < 3 * sms) p.G >>= 1;
   // Few tiles do not cover the time that the next group's queries take: two groups must fit then (1495 tokens x 128
-  // heads x 19 blocks: 31 us for 37; 4096 x 64 x 256: 45 for 53; x 1024: 96 for 80).
+  // heads x 19 blocks: 31 us for 37; 4096 x 64 x 256: 45 for 53; x 1024: 96 for 80. Their floors are 15 and 21 us: the
+  // queries are waited for all the same).
   while (p.G > 1 && tiles <= 4 && p.G * p.HP > scores::kMaxN / 2) p.G >>= 1;
   const int64_t groups = (T + p.G - 1) / p.G;
   // As many parts of a group's tiles as end first, a unit's start (lengths, pages, queries) being worth a tile (256

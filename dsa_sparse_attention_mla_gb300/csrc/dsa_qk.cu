@@ -21,7 +21,9 @@ namespace dsa {
 namespace qk {
 
 constexpr int kThreads = 128;
-constexpr int kBlocks = 16;  // per SM: every row in flight counts (8192 x 64 rows of 1152 bytes: 200 us with 16, 215 with 12)
+// Per SM: every row in flight counts (8192 x 64 rows of 1152 bytes: 200 us with 16 and 215 with 12 when it was chosen; now
+// 187 in a graph, 6.6 TB/s)
+constexpr int kBlocks = 16;
 constexpr int kWarps = kThreads / 32;
 
 struct Params {

@@ -455,8 +455,9 @@ DSA_API dsa_status_t dsa_cache_evict(const dsa_evict_args_t* args, void* stream)
  * when it adds tokens and it and those before it add more than T (DSA_DEVERR_TOKEN_CAPACITY). A
  * refused request adds no token and takes no page; its length and seen stay, and pages past need still
  * go back. What it wanted still counts for those behind it: a request too large for the step holds up
- * every later one that takes a page or adds a token, until the caller leaves it out (new_tokens 0). Negative lengths and held count as 0, held past max_pages as max_pages, *num_free as
- * clamped to [0, free_capacity]. Pages that find no room on the stack are dropped and set
+ * every later one that takes a page or adds a token, until the caller leaves it out (new_tokens 0).
+ * Negative lengths and held count as 0, held past max_pages as max_pages, *num_free as clamped to
+ * [0, free_capacity]. Pages that find no room on the stack are dropped and set
  * DSA_DEVERR_SLOT_OUT_OF_RANGE.
  * Pages that go back must be the request's own. The plan does not look for one that another request
  * holds too (a shared prefix): each would give it back, and it would be handed out twice, to requests
