@@ -470,7 +470,8 @@ DSA_API dsa_status_t dsa_cache_evict(const dsa_evict_args_t* args, void* stream)
  *   req_of_token  [T], positions [T] (the token's position among its request's cached ones),
  *                 token_lengths [T] (position + 1: what the token attends to), out_loc int64 [T] (the
  *                 cache slot of its position; -1 for a page < 0). Entries behind the last token: request
- *                 0, position -1, length 0, slot -1, which every operator skips.
+ *                 0, position -1, length 0, slot -1, which every operator skips (dsa_quant_k_cache
+ *                 with its error bit for such a slot).
  * Where an eviction has shortened requests, a token's place in its sequence is not its position any
  * more. `seen` counts the tokens that each request has been given: the i-th of this step's has place
  * seen + i, and seen becomes seen + n (0 when the request ends; a negative one counts as 0; l + i and
